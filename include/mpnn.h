@@ -266,6 +266,117 @@ mpnn_status mpnn_set_graph_replay(mpnn_ctx *ctx, int32_t steps_per_replay);
  * next build). */
 mpnn_status mpnn_set_subdomains(mpnn_ctx *ctx, int32_t px, int32_t py, int32_t pz);
 
+/* ------------------------------------------------------------------------------------------------
+ * Row operators: the atom-wise parts of networks that a caller builds, trains and differentiates
+ * outside the model above (for example a deeper, routed readout on the orbital sums of
+ * mpnn_get_intermediate).  They need no neighbour list, only a context: its stream, its device
+ * scratch (one buffer, grown by the first call of a size, so a call that is to be captured into a
+ * graph runs once before) and its error text.  They enqueue work and return; nothing is copied to
+ * the host.
+ *   - Rows are row-major [n][width] of fp32 or bf16 values (mpnn_dtype); an argument ld is the
+ *     distance between rows in values (>= width), arrays without one are dense.  Arithmetic, sums
+ *     and statistics are fp32; a result is rounded once, to nearest even, to the rows' type.
+ *   - n may be 0 (arrays of n rows may then be NULL; sums over rows come out 0).
+ *   - Any alignment of a value's own size is accepted; rows that start on 16-byte boundaries and a
+ *     width that is a multiple of 16 bytes are fastest.
+ *   - Outputs must not overlap inputs, except that r may be x (ldx = width) and dx may be dr.
+ *   - No floating-point atomics: equal calls give bitwise equal results.
+ * ---------------------------------------------------------------------------------------------- */
+typedef enum { MPNN_F32 = 0, MPNN_BF16 = 1 } mpnn_dtype;
+
+/* Rows sorted by expert and back.  Row i has k slots (1..64); expert[i][s] in 0..n_experts-1 (at most
+ * 1024 experts) names the expert (an atom's species, a router's choice) of the pair p = i k + s, any
+ * other value (e.g. -1) none: the pair is dropped.
+ * mpnn_route_plan orders the n k pairs by expert, pairs of one expert in ascending order, the dropped
+ * pairs last (also ascending).  offsets[n_experts + 1]: expert e owns the places offsets[e] ..
+ * offsets[e + 1] - 1, so offsets[n_experts] pairs are routed; source[q]: the pair at place q;
+ * position[p]: the place of pair p (each the inverse of the other, over all n k pairs).
+ * MPNN_E_CAPACITY for more than 2^31-1 pairs. */
+mpnn_status mpnn_route_plan(mpnn_ctx *ctx, int64_t n, int32_t k, int32_t n_experts, const int32_t *expert,
+                            int32_t *offsets, int32_t *source, int32_t *position);
+
+/* sorted[position[i][s]] = x[i]; the rows of dropped pairs are zeros.  The gradient of x is
+ * mpnn_route_combine of the gradient of sorted without weights.  Places outside 0 .. n k - 1 are
+ * ignored here and below. */
+mpnn_status mpnn_route_scatter(mpnn_ctx *ctx, int32_t dtype, int64_t n, int32_t k, int32_t width, const void *x,
+                               int64_t ldx, const int32_t *position, const int32_t *offsets, int32_t n_experts,
+                               void *sorted);
+
+/* out[i] = sum over s, in order, of weight[i][s] sorted[position[i][s]] (weight NULL: ones).  A dropped
+ * pair adds nothing, whatever its weight and its row hold; a row without any routed pair is zero. */
+mpnn_status mpnn_route_combine(mpnn_ctx *ctx, int32_t dtype, int64_t n, int32_t k, int32_t width, const void *sorted,
+                               const int32_t *position, const int32_t *offsets, int32_t n_experts,
+                               const float *weight, void *out);
+
+/* Gradient of mpnn_route_combine: dsorted[position[i][s]] = weight[i][s] dout[i] (zeros for dropped
+ * pairs) and dweight[i][s] = sum over the columns of dout[i] sorted[position[i][s]] (fp32, 0 for dropped
+ * pairs).  dweight may be NULL; sorted is then not read and may be NULL. */
+mpnn_status mpnn_route_combine_backward(mpnn_ctx *ctx, int32_t dtype, int64_t n, int32_t k, int32_t width,
+                                        const void *dout, int64_t ld_dout, const void *sorted,
+                                        const int32_t *position, const int32_t *offsets, int32_t n_experts,
+                                        const float *weight, void *dsorted, float *dweight);
+
+/* Norms before and after a block, fused with the block's gate and residual scale:
+ *   r = x + scale * sigma(gate) * N_post(block),   h = N_pre(r),   sigma(g) = 1 / (1 + exp(-g)),
+ *   N(v) = (v - m) / sqrt(mean((v - m)^2) + eps) * weight + bias,  m = mean(v) (layer) or 0 (rms)
+ * over a row's `width` columns (at most 8192); h is taken from r before r is rounded. */
+typedef enum { MPNN_NORM_RMS = 0, MPNN_NORM_LAYER = 1 } mpnn_norm_kind;
+typedef struct {
+    int32_t dtype;              /* mpnn_dtype of every row array */
+    int32_t width;
+    int32_t kind;               /* mpnn_norm_kind of both norms */
+    int32_t gate_width;         /* with a gate: width (a value per column) or 1 (one value per row) */
+    double eps;                 /* > 0, also as fp32 */
+    const float *post_weight;   /* device [width] each, or NULL for ones (weights, scale), zeros (biases) */
+    const float *post_bias;
+    const float *scale;
+    const float *pre_weight;
+    const float *pre_bias;
+} mpnn_norm;
+
+/* block NULL: nothing is added (r = x).  gate NULL: sigma = 1.  r or h may be NULL. */
+mpnn_status mpnn_norm_residual(mpnn_ctx *ctx, const mpnn_norm *p, int64_t n, const void *x, int64_t ldx,
+                               const void *block, int64_t ld_block, const void *gate, int64_t ld_gate, void *r,
+                               void *h);
+
+/* Gradient of mpnn_norm_residual at the stored r: dr and dh are the gradients of r (from what reads r
+ * later) and of h, dense, either may be NULL.  Writes dx (may be NULL), dblock (with a block), dgate
+ * ([n][gate_width], with a gate) and, fp32 sums over the rows in a fixed order, the gradients of the
+ * five vectors (each may be NULL; written also where the vector itself is NULL). */
+mpnn_status mpnn_norm_residual_backward(mpnn_ctx *ctx, const mpnn_norm *p, int64_t n, const void *dr, const void *dh,
+                                        const void *r, int64_t ldr, const void *block, int64_t ld_block,
+                                        const void *gate, int64_t ld_gate, void *dx, void *dblock, void *dgate,
+                                        float *dpost_weight, float *dpost_bias, float *dscale, float *dpre_weight,
+                                        float *dpre_bias);
+
+/* Activation checkpoints in 8 bits: codes [n][width] and scales [n][ceil(width / 32)], one scale for 32
+ * columns of a row.  With `largest` the group's largest magnitude, m 2^E (1 <= m < 2), the step is 2^e,
+ * e = E - 6, one more if m > 127/64, within -100 .. 121; a code is the value in steps, rounded to nearest
+ * even and kept in -127 .. 127; the scale byte is e + 127.  A group with a value that is not finite gets
+ * the byte 255 and reads back as NaN.  The error is at most half a step, i.e. largest / 127 (2^-101 for
+ * the tiniest groups).  A held value has at most 7 significant bits, so it is exact in bf16 too. */
+mpnn_status mpnn_checkpoint_save(mpnn_ctx *ctx, int32_t dtype, int64_t n, int32_t width, const void *x, int64_t ldx,
+                                 int8_t *codes, uint8_t *scales);
+mpnn_status mpnn_checkpoint_load(mpnn_ctx *ctx, int32_t dtype, int64_t n, int32_t width, const int8_t *codes,
+                                 const uint8_t *scales, void *out);
+
+/* y = z / (1 + exp(-z)), the checkpoint of z and, unless y_codes and y_scales are NULL, that of y (taken
+ * before y is rounded), in one pass over z. */
+mpnn_status mpnn_checkpoint_silu(mpnn_ctx *ctx, int32_t dtype, int64_t n, int32_t width, const void *z, int64_t ldz,
+                                 void *y, int8_t *z_codes, uint8_t *z_scales, int8_t *y_codes, uint8_t *y_scales);
+
+/* dz = dy s (1 + z (1 - s)), s = sigma(z), for the z that the checkpoint holds. */
+mpnn_status mpnn_checkpoint_silu_backward(mpnn_ctx *ctx, int32_t dtype, int64_t n, int32_t width, const void *dy,
+                                          int64_t ld_dy, const int8_t *codes, const uint8_t *scales, void *dz);
+
+/* Weight gradients of one linear layer y = x W_e^T + b_e per expert, from the checkpoint of its input:
+ * dweight[e][o][c] = sum of dy[q][o] x[q][c] over the rows offsets[e] <= q < offsets[e + 1] (offsets device
+ * [n_experts + 1], as mpnn_route_plan writes them; clamped to 0 .. n), dbias[e][o] = sum of dy[q][o] (may be
+ * NULL).  fp32, as accurate as fp32 products and sums for both types; an expert without rows gets zeros. */
+mpnn_status mpnn_checkpoint_weight_grad(mpnn_ctx *ctx, int32_t dtype, int64_t n, int32_t n_out, int32_t width,
+                                        int32_t n_experts, const int32_t *offsets, const void *dy, int64_t ld_dy,
+                                        const int8_t *codes, const uint8_t *scales, float *dweight, float *dbias);
+
 /* Text of the last error on this context ("" if none); valid until the next call. */
 const char *mpnn_last_error(const mpnn_ctx *ctx);
 

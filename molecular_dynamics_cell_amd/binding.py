@@ -10,7 +10,7 @@ import re
 import numpy as np
 import torch
 
-from . import inputs
+from . import inputs, rows
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libmpnn.so")
@@ -86,6 +86,18 @@ def lib():
             "mpnn_set_profiling": ([p, i32], st),
             "mpnn_get_profile": ([p, i32, C.POINTER(C.c_char_p), C.POINTER(C.c_double),
                                   C.POINTER(C.c_int64)], st),
+            "mpnn_route_plan": ([p, i64, i32, i32, p, p, p, p], st),
+            "mpnn_route_scatter": ([p, i32, i64, i32, i32, p, i64, p, p, i32, p], st),
+            "mpnn_route_combine": ([p, i32, i64, i32, i32, p, p, p, i32, p, p], st),
+            "mpnn_route_combine_backward": ([p, i32, i64, i32, i32, p, i64, p, p, p, i32, p, p, p], st),
+            "mpnn_norm_residual": ([p, C.POINTER(rows.Norm), i64, p, i64, p, i64, p, i64, p, p], st),
+            "mpnn_norm_residual_backward": ([p, C.POINTER(rows.Norm), i64, p, p, p, i64, p, i64, p, i64, p, p, p,
+                                             p, p, p, p, p], st),
+            "mpnn_checkpoint_save": ([p, i32, i64, i32, p, i64, p, p], st),
+            "mpnn_checkpoint_load": ([p, i32, i64, i32, p, p, p], st),
+            "mpnn_checkpoint_silu": ([p, i32, i64, i32, p, i64, p, p, p, p, p], st),
+            "mpnn_checkpoint_silu_backward": ([p, i32, i64, i32, p, i64, p, p, p], st),
+            "mpnn_checkpoint_weight_grad": ([p, i32, i64, i32, i32, i32, p, p, i64, p, p, p, p], st),
             "mpnn_last_error": ([p], C.c_char_p),
         }
         for name, (args, res) in sig.items():
@@ -108,8 +120,9 @@ def _dptr(t: torch.Tensor):
     return C.c_void_p(t.data_ptr()) if t is not None else None
 
 
-class MPNN:
-    """One library context: model parameters plus one system's neighbour list and state."""
+class MPNN(rows.RowOperators):
+    """One library context: model parameters plus one system's neighbour list and state; the row
+    operators (rows.py) run on its stream."""
 
     def __init__(self, params: inputs.Params, device="cuda"):
         self.params = params

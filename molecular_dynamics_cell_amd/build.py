@@ -15,7 +15,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmpnn.so")
-SOURCES = ["api.hip", "scan.hip", "neighbors.hip", "edges.hip", "mlp.hip", "integrate.hip"]
+SOURCES = ["api.hip", "scan.hip", "neighbors.hip", "edges.hip", "mlp.hip", "integrate.hip",
+           "api_rows.hip", "routing.hip", "residual.hip", "checkpoint.hip", "weight_grad.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 FLAGS = ["-O3", "-std=c++17", "-fPIC", "--offload-arch=gfx950", "-fno-gpu-rdc",

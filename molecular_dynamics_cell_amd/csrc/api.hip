@@ -9,10 +9,6 @@
 
 #include "impl.h"
 
-struct mpnn_ctx {
-    mpnn::Context cx;
-};
-
 namespace mpnn {
 
 Status Context::grow(Buf &b, size_t bytes) {
@@ -118,7 +114,7 @@ Context::~Context() {
                   &ghost_off, &row_off, &row_len, &slab_off, &nbr, &cellpos, &t_off, &t_eid, &sp_list, &sp_off, &c, &O, &feat, &grho, &Gc,
                   &gedge, &w, &amask, &act_n, &t_act, &dact, &nact, &Frecv, &F, &Ei, &red, &flag, &tmp_a, &tmp_b, &tmp_c,
                   &tmp_d, &tmp_scan,
-                  &types_caller, &stage_pos, &stage_vel, &bak_pos, &bak_vel, &bak_F};
+                  &types_caller, &stage_pos, &stage_vel, &bak_pos, &bak_vel, &bak_F, &rows_ws};
     for (const Chunk &c : graphs) (void)hipGraphExecDestroy(c.exec);
     if (cap_stream) (void)hipStreamSynchronize(cap_stream);
     for (hipEvent_t e : cap_ev)

@@ -177,6 +177,8 @@ struct Context {
     void prof_end(int id);
     void prof_harvest();                // after a stream synchronisation
 
+    Buf rows_ws;                  // scratch of one row operator call (routing counts, partial sums)
+
     Buf types_caller;             // int32 [n] species in caller order (for rebuilds)
     Buf stage_pos, stage_vel;     // double [n][3] caller-order staging
     std::vector<float> inv_scale_host;     // 1 / s_t rounded to fp32 (arithmetic modes 0 and 2)
@@ -250,4 +252,35 @@ Status unpermute_float(Context &cx, const float *sorted, int width, int64_t np, 
 // sorted rows of `width` floats at a row stride of `stride` floats
 Status unpermute_rows(Context &cx, const float *sorted, int width, int stride, double *caller);
 
+// ---- row operators: arguments checked by api_rows.hip; `used`: device count of the pairs that have an expert ----
+// ---- routing.hip ----
+Status route_plan(Context &cx, int64_t n, int k, int n_experts, const int32_t *expert, int32_t *offsets, int32_t *source,
+                  int32_t *position);
+Status route_scatter(Context &cx, int dtype, int64_t n, int k, int width, const void *x, int64_t ldx, const int32_t *position,
+                     const int32_t *used, void *sorted);
+Status route_combine(Context &cx, int dtype, int64_t n, int k, int width, const void *sorted, const int32_t *position,
+                     const int32_t *used, const float *weight, void *out);
+Status route_combine_backward(Context &cx, int dtype, int64_t n, int k, int width, const void *dout, int64_t ld, const void *sorted,
+                              const int32_t *position, const int32_t *used, const float *weight, void *dsorted, float *dweight);
+// ---- residual.hip ----
+Status norm_residual(Context &cx, const mpnn_norm &p, int64_t n, const void *x, int64_t ldx, const void *block, int64_t ldb,
+                     const void *gate, int64_t ldg, void *r, void *h);
+// dvec: post weight, post bias, scale, pre weight, pre bias (any may be null)
+Status norm_residual_backward(Context &cx, const mpnn_norm &p, int64_t n, const void *dr, const void *dh, const void *r, int64_t ldr,
+                              const void *block, int64_t ldb, const void *gate, int64_t ldg, void *dx, void *dblock, void *dgate,
+                              float *const dvec[5]);
+// ---- checkpoint.hip ----
+Status checkpoint_save(Context &cx, int dtype, bool silu, int64_t n, int width, const void *z, int64_t ld, void *y, int8_t *codes,
+                       uint8_t *scales, int8_t *ycodes, uint8_t *yscales);
+Status checkpoint_load(Context &cx, int dtype, int64_t n, int width, const int8_t *codes, const uint8_t *scales, void *out);
+Status checkpoint_silu_backward(Context &cx, int dtype, int64_t n, int width, const void *dy, int64_t ld, const int8_t *codes,
+                                const uint8_t *scales, void *dz);
+// ---- weight_grad.hip ----
+Status weight_grad(Context &cx, int dtype, int64_t n, int out, int width, int n_experts, const int32_t *offsets, const void *dy,
+                   int64_t ld, const int8_t *codes, const uint8_t *scales, float *dweight, float *dbias);
+
 }  // namespace mpnn
+
+struct mpnn_ctx {
+    mpnn::Context cx;
+};
