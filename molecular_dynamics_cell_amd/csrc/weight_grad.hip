@@ -1,8 +1,14 @@
 // Weight gradients of one linear layer per expert from its saved input (mpnn_checkpoint_weight_grad):
 //   dW_e[o][c] = sum over the rows q of expert e of dy[q][o] x[q][c],  db_e[o] = sum of dy[q][o],
-// with x the values that the checkpoint holds.  The rows of an expert are cut into pieces of at most `rows`; each
-// piece's product is a block's own partial sum, and the pieces of an expert are added in order, so results do not
-// depend on the launch.
+// with x the values that the checkpoint holds: a product whose long axis is the rows.
+//
+// The rows of an expert are cut into pieces of at most `rows`; a block takes one piece and one BM x 128 tile of dW.
+// An expert of one piece is written at once, the pieces of the others are added afterwards in their order, so results
+// do not depend on the launch.
+//
+// Operands on the bf16 matrix cores: x is exact in bf16 (7 bits and a power of two).  A bf16 dy is one as it stands;
+// an fp32 dy is cut into three bf16 terms of 8 bits each, top, middle and last, which add up to it exactly, so that
+// every product is exact and the sums are fp32 as with fp32 products.
 #include "impl.h"
 #include "rows.h"
 
@@ -10,78 +16,326 @@ namespace mpnn {
 
 namespace {
 
-constexpr int kTile = 32;
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float floatx16 __attribute__((ext_vector_type(16)));
 
-// One block per (expert piece, 32 x 32 tile of dW): rows are read through LDS, 32 at a time.
-template <class T>
-__global__ void k_weight_grad(int out, int width, int groups, int n_experts, int64_t n, int64_t rows, int pieces,
-                              const int32_t *__restrict__ offsets, const T *__restrict__ dy, int64_t ld,
-                              const int8_t *__restrict__ codes, const uint8_t *__restrict__ scales, float *__restrict__ part) {
-    __shared__ float a[kTile][kTile + 1], b[kTile][kTile + 1];
-    const int e = blockIdx.z / pieces, piece = blockIdx.z % pieces;
-    const int64_t lo = min(max((int64_t)offsets[e], (int64_t)0), n), hi = min(max((int64_t)offsets[e + 1], lo), n);
-    const int64_t from = lo + piece * rows, to = min(hi, from + rows);
-    const int o0 = blockIdx.y * kTile, c0 = blockIdx.x * kTile;
-    const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
-    float s[4] = {}, sb[4] = {};
-    for (int64_t q0 = from; q0 < to; q0 += kTile) {
-        for (int j = ty; j < kTile; j += 8) {
-            const int64_t q = q0 + j;
-            a[j][tx] = q < to && o0 + tx < out ? to_f32(dy[q * ld + o0 + tx]) : 0.0f;
-            float v = 0.0f;
-            if (q < to && c0 + tx < width) {
-                const int byte = scales[q * groups + (c0 + tx) / 32];
-                v = (float)codes[q * width + c0 + tx] * (byte == 255 ? __uint_as_float(0x7fc00000u) : __uint_as_float((uint32_t)byte << 23));
+constexpr int kBN = 128;         // columns of x per block
+constexpr int kBK = 64;          // rows per stage: 8 chunks of 8, one matrix-core operand word each
+constexpr int kChunks = kBK / 8;
+
+// Pieces of each expert: at least one (an expert without rows writes its zeros).
+__device__ __forceinline__ int pieces_of(const int32_t *offsets, int e, int64_t n, int64_t rows, int64_t &from, int64_t &to) {
+    from = min(max((int64_t)offsets[e], (int64_t)0), n);
+    to = min(max((int64_t)offsets[e + 1], from), n);
+    return (int)max((int64_t)1, (to - from + rows - 1) / rows);
+}
+
+struct Piece {
+    int expert, piece, pieces;   // piece of its expert's pieces; expert < 0: past the last
+    int slot;                    // partial sums of the expert's first piece (pieces > 1)
+};
+
+// The piece with the given number, by one wave: a prefix sum over the experts, 64 at a time.  want_expert >= 0 looks
+// that expert up instead.
+__device__ __forceinline__ Piece find_piece(const int32_t *offsets, int n_experts, int64_t n, int64_t rows, int number, int want_expert) {
+    const int lane = threadIdx.x & 63;
+    int before = 0, slots = 0;
+    for (int base = 0; base < n_experts; base += 64) {
+        const int e = base + lane;
+        int64_t from, to;
+        const int c = e < n_experts ? pieces_of(offsets, e, n, rows, from, to) : 0;
+        const int m = c > 1 ? c : 0;
+        int s = c, t = m;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int a = __shfl_up(s, d), b = __shfl_up(t, d);
+            if (lane >= d) {
+                s += a;
+                t += b;
             }
-            b[j][tx] = v;
+        }
+        const uint64_t hit = __ballot(want_expert >= 0 ? e == want_expert : e < n_experts && number < before + s);
+        if (hit) {
+            const int l = __ffsll((unsigned long long)hit) - 1;
+            const int pc = __shfl(c, l);
+            return Piece{base + l, number - (before + __shfl(s, l) - pc), pc, slots + __shfl(t, l) - __shfl(m, l)};
+        }
+        before += __shfl(s, 63);
+        slots += __shfl(t, 63);
+    }
+    return Piece{-1, 0, 0, 0};
+}
+
+__device__ __forceinline__ uint32_t low_halves(uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x05040100u); }
+__device__ __forceinline__ uint32_t high_halves(uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x07060302u); }
+
+// Four neighbouring columns of dy in one row.
+struct Quad32 {
+    float v[4];
+    __device__ __forceinline__ float at(int j) const { return v[j]; }
+};
+struct Quad16 {
+    uint32_t v[2];
+    __device__ __forceinline__ float at(int j) const { return __uint_as_float(j & 1 ? v[j >> 1] & 0xffff0000u : v[j >> 1] << 16); }
+};
+template <class T> struct QuadOf;
+template <> struct QuadOf<float> { using type = Quad32; };
+template <> struct QuadOf<bf16> { using type = Quad16; };
+
+__device__ __forceinline__ void load_quad(Quad32 &q, const float *p, bool vec, int cols) {
+    if (vec) {
+        const float4 t = *reinterpret_cast<const float4 *>(p);
+        q.v[0] = t.x; q.v[1] = t.y; q.v[2] = t.z; q.v[3] = t.w;
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) q.v[j] = j < cols ? p[j] : 0.0f;
+    }
+}
+__device__ __forceinline__ void load_quad(Quad16 &q, const bf16 *p, bool vec, int cols) {
+    if (vec) {
+        const uint2 t = *reinterpret_cast<const uint2 *>(p);
+        q.v[0] = t.x; q.v[1] = t.y;
+    } else {
+        const uint16_t *u = reinterpret_cast<const uint16_t *>(p);
+        uint32_t h[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) h[j] = j < cols ? u[j] : 0u;
+        q.v[0] = h[0] | h[1] << 16;
+        q.v[1] = h[2] | h[3] << 16;
+    }
+}
+__device__ __forceinline__ void clear_quad(Quad32 &q) { q.v[0] = q.v[1] = q.v[2] = q.v[3] = 0.0f; }
+__device__ __forceinline__ void clear_quad(Quad16 &q) { q.v[0] = q.v[1] = 0u; }
+
+// Column j of eight rows as the operand words of each term.
+__device__ __forceinline__ void column(const Quad16 (&q)[8], int j, uint4 (&w)[1]) {
+    uint32_t p[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        p[i] = j & 1 ? high_halves(q[2 * i].v[j >> 1], q[2 * i + 1].v[j >> 1]) : low_halves(q[2 * i].v[j >> 1], q[2 * i + 1].v[j >> 1]);
+    w[0] = make_uint4(p[0], p[1], p[2], p[3]);
+}
+__device__ __forceinline__ void column(const Quad32 (&q)[8], int j, uint4 (&w)[3]) {
+    uint32_t t[3][8];
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+        const float v = q[r].v[j];
+        const uint32_t top = __float_as_uint(v) & 0xffff0000u;
+        // exact: what is left has 16 significant bits; nothing is left of an infinity
+        const float left = fabsf(v) < __uint_as_float(0x7f800000u) ? v - __uint_as_float(top) : 0.0f;
+        const uint32_t middle = __float_as_uint(left) & 0xffff0000u;
+        t[0][r] = top;
+        t[1][r] = middle;
+        t[2][r] = __float_as_uint(left - __uint_as_float(middle));   // 8 bits: its low half is zero
+    }
+#pragma unroll
+    for (int s = 0; s < 3; ++s)
+        w[s] = make_uint4(high_halves(t[s][0], t[s][1]), high_halves(t[s][2], t[s][3]), high_halves(t[s][4], t[s][5]),
+                          high_halves(t[s][6], t[s][7]));
+}
+
+// Layout.  Both operands have the rows as their slow axis, while a matrix-core operand word holds eight of them for
+// one column: a thread loads 4 neighbouring columns of 8 rows, turns them in registers and writes four 16-byte words.
+// LDS holds [chunk][position][8 rows]; column m of a tile of B columns sits at position (m % 4) (B / 4) + m / 4, so
+// that neighbouring threads write neighbouring words (no bank conflict), and the operand reads are neighbouring words
+// too.  The permutation only reorders the tile's results.
+// A wave owns 32 MT x 32 NT positions: BM = 128: 2 x 2 waves of 64 x 64; 64: 2 x 2 of 32 x 64; 32: 1 x 4 of 32 x 32.
+template <class T, int BM>
+__global__ __launch_bounds__(256, 2) void k_weight_grad(int out, int width, int groups, int n_experts, int64_t n, int64_t rows, int tiles_n,
+                                                        int tiles, const int32_t *__restrict__ offsets, const T *__restrict__ dy, int64_t ld,
+                                                        const int8_t *__restrict__ codes, const uint8_t *__restrict__ scales, int vec_dy,
+                                                        int vec_x, int64_t slots, float *__restrict__ part, float *__restrict__ dweight,
+                                                        float *__restrict__ dbias) {
+    constexpr int TERMS = sizeof(T) == 4 ? 3 : 1;
+    constexpr int WN = BM == 32 ? 4 : 2, WM = 4 / WN;
+    constexpr int MT = BM / 32 / WM, NT = kBN / 32 / WN;
+    using Quad = typename QuadOf<T>::type;
+    __shared__ uint4 A[TERMS][kChunks][BM];
+    __shared__ uint4 B[kChunks][kBN];
+    __shared__ float sums[kChunks][BM];
+
+    // blocks are dealt to the XCDs in turn: give the tiles of one piece (the same rows) to one XCD
+    const int64_t number = xcd_block();
+    const int tile = (int)(number % tiles);
+    const Piece pc = find_piece(offsets, n_experts, n, rows, (int)(number / tiles), -1);
+    if (pc.expert < 0) return;
+    int64_t from, to;
+    pieces_of(offsets, pc.expert, n, rows, from, to);
+    from += pc.piece * rows;
+    to = min(to, from + rows);
+    const int o0 = tile / tiles_n * BM, c0 = tile % tiles_n * kBN;
+
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int am = tid % (BM / 4), ak = tid / (BM / 4);       // dy: column quad, chunk (threads with ak < 8)
+    const int xm = tid % (kBN / 4), xk = tid / (kBN / 4);     // x
+    const int acols = out - o0 - 4 * am, xcols = width - c0 - 4 * xm;
+    const bool a_in = ak < kChunks && acols > 0, x_in = xcols > 0;
+    const T *ap = dy + o0 + 4 * am;
+    const int8_t *xp = codes + c0 + 4 * xm;
+    const uint8_t *sp = scales + (c0 + 4 * xm) / 32;
+
+    Quad a[8];
+    uint32_t x[8];
+    float step[8];
+    auto fetch = [&](int64_t q0) {
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+            const int64_t q = q0 + ak * 8 + r;
+            if (a_in && q < to) load_quad(a[r], ap + q * ld, vec_dy, acols);
+            else clear_quad(a[r]);
+        }
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+            const int64_t q = q0 + xk * 8 + r;
+            x[r] = 0u;
+            step[r] = 0.0f;
+            if (x_in && q < to) {
+                const int8_t *p = xp + q * width;
+                if (vec_x) {
+                    x[r] = *reinterpret_cast<const uint32_t *>(p);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) x[r] |= j < xcols ? (uint32_t)(uint8_t)p[j] << 8 * j : 0u;
+                }
+                const int byte = sp[q * groups];
+                step[r] = byte == 255 ? __uint_as_float(0x7fc00000u) : __uint_as_float((uint32_t)byte << 23);
+            }
+        }
+    };
+
+    floatx16 acc[MT][NT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) acc[i][j] = (floatx16)(0.0f);
+    float bias[4] = {};
+    const int wm = wave / WN, wn = wave % WN;
+    if (from < to) fetch(from);
+    for (int64_t q0 = from; q0 < to; q0 += kBK) {
+        __syncthreads();
+        if (ak < kChunks) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                uint4 w[TERMS];
+                column(a, j, w);
+#pragma unroll
+                for (int t = 0; t < TERMS; ++t) A[t][ak][j * (BM / 4) + am] = w[t];
+            }
+            if (c0 == 0) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                    for (int r = 0; r < 8; ++r) bias[j] += a[r].at(j);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            uint32_t v[8];
+#pragma unroll
+            for (int r = 0; r < 8; ++r)   // (code + 128) step - 128 step: exact, and NaN where the step is
+                v[r] = __float_as_uint(fmaf((float)((x[r] ^ 0x80808080u) >> 8 * j & 255u), step[r], -128.0f * step[r]));
+            B[xk][j * (kBN / 4) + xm] = make_uint4(high_halves(v[0], v[1]), high_halves(v[2], v[3]), high_halves(v[4], v[5]),
+                                                   high_halves(v[6], v[7]));
         }
         __syncthreads();
-        for (int j = 0; j < kTile; ++j)
-            for (int u = 0; u < 4; ++u) {
-                s[u] = fmaf(a[j][ty + 8 * u], b[j][tx], s[u]);
-                sb[u] += a[j][ty + 8 * u];
-            }
-        __syncthreads();
+        if (q0 + kBK < to) fetch(q0 + kBK);
+#pragma unroll
+        for (int s = 0; s < kChunks / 2; ++s) {
+            const int c = 2 * s + (lane >> 5);
+            bf16x8 bf[NT];
+#pragma unroll
+            for (int j = 0; j < NT; ++j) bf[j] = __builtin_bit_cast(bf16x8, B[c][(wn * NT + j) * 32 + (lane & 31)]);
+#pragma unroll
+            for (int t = TERMS - 1; t >= 0; --t)
+#pragma unroll
+                for (int i = 0; i < MT; ++i) {
+                    const bf16x8 af = __builtin_bit_cast(bf16x8, A[t][c][(wm * MT + i) * 32 + (lane & 31)]);
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(af, bf[j], acc[i][j], 0, 0, 0);
+                }
+        }
     }
-    float *to_p = part + (int64_t)blockIdx.z * out * (width + 1);
-    for (int u = 0; u < 4; ++u) {
-        const int o = o0 + ty + 8 * u;
-        if (o >= out) continue;
-        if (c0 + tx < width) to_p[(int64_t)o * width + c0 + tx] = s[u];
-        if (c0 == 0 && tx == 0) to_p[(int64_t)out * width + o] = sb[u];
+
+    const int64_t matrix = (int64_t)out * width;
+    const bool whole = pc.pieces == 1;
+    if (!whole && pc.slot + pc.piece >= slots) return;   // offsets that do not ascend name more pieces than there are
+    float *to_w = whole ? dweight + pc.expert * matrix : part + (int64_t)(pc.slot + pc.piece) * (matrix + out);
+    float *to_b = whole ? (dbias ? dbias + (int64_t)pc.expert * out : nullptr) : to_w + matrix;
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            const int pm = (wm * MT + i) * 32 + 8 * (r / 4) + 4 * (lane >> 5) + r % 4;
+            const int o = o0 + 4 * (pm % (BM / 4)) + pm / (BM / 4);
+            if (o >= out) continue;
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                const int pn = (wn * NT + j) * 32 + (lane & 31);
+                const int c = c0 + 4 * (pn % (kBN / 4)) + pn / (kBN / 4);
+                if (c < width) to_w[(int64_t)o * width + c] = acc[i][j][r];
+            }
+        }
+    if (c0 == 0 && to_b) {
+        if (ak < kChunks)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) sums[ak][4 * am + j] = bias[j];
+        __syncthreads();
+        if (tid < BM && o0 + tid < out) {
+            float s = 0.0f;
+#pragma unroll
+            for (int k = 0; k < kChunks; ++k) s += sums[k][tid];
+            to_b[o0 + tid] = s;
+        }
     }
 }
 
-__global__ void k_weight_grad_sum(int64_t values, int64_t matrix, int pieces, const float *__restrict__ part, float *__restrict__ dweight,
-                                  float *__restrict__ dbias) {
-    const int64_t v = (int64_t)blockIdx.x * kBlock + threadIdx.x;
-    if (v >= values) return;
-    const int64_t e = blockIdx.y;
+// The pieces of each expert that has several, added in their order.
+__global__ void k_weight_grad_sum(int n_experts, int64_t n, int64_t rows, int64_t slots, int64_t matrix, int out, const int32_t *__restrict__ offsets,
+                                  const float *__restrict__ part, float *__restrict__ dweight, float *__restrict__ dbias) {
+    const int e = blockIdx.y;
+    const Piece pc = find_piece(offsets, n_experts, n, rows, 0, e);
+    const int64_t v = (int64_t)blockIdx.x * kBlock + threadIdx.x, values = matrix + out;
+    if (pc.pieces <= 1 || v >= values || pc.slot + (int64_t)pc.pieces > slots) return;
     float s = 0.0f;
-    for (int p = 0; p < pieces; ++p) s += part[(e * pieces + p) * values + v];
+    const float *p = part + (int64_t)pc.slot * values + v;
+#pragma unroll 8
+    for (int i = 0; i < pc.pieces; ++i) s += p[i * values];
     if (v < matrix) dweight[e * matrix + v] = s;
-    else if (dbias) dbias[e * (values - matrix) + (v - matrix)] = s;
+    else if (dbias) dbias[(int64_t)e * out + (v - matrix)] = s;
+}
+
+template <class T, int BM>
+Status launch(Context &cx, int64_t n, int out, int width, int n_experts, const int32_t *offsets, const T *dy, int64_t ld,
+              const int8_t *codes, const uint8_t *scales, float *dweight, float *dbias) {
+    const int tiles_n = (width + kBN - 1) / kBN, tiles = tiles_n * ((out + BM - 1) / BM);
+    const int64_t want = std::max<int64_t>(1, 512 / tiles);
+    const int64_t rows = std::max<int64_t>(512, ((n + want - 1) / want + kBK - 1) / kBK * kBK);
+    const int64_t pieces = n / rows + n_experts;              // at most; an expert of several pieces has more than `rows` rows
+    const int64_t matrix = (int64_t)out * width, slots = n > rows ? 2 * (n / rows) : 0;   // an expert of p > 1 pieces fills p / 2 whole ones
+    MPNN_TRY(cx.grow(cx.rows_ws, sizeof(float) * (size_t)(slots * (matrix + out))));
+    const int vec_dy = out % 4 == 0 && ld % 4 == 0 && (uintptr_t)dy % (4 * sizeof(T)) == 0;
+    const int vec_x = width % 4 == 0 && (uintptr_t)codes % 4 == 0;
+    k_weight_grad<T, BM><<<grid_xcd(pieces * tiles, 1), 256, 0, cx.stream>>>(out, width, (width + 31) / 32, n_experts, n, rows, tiles_n,
+                                                                             tiles, offsets, dy, ld, codes, scales, vec_dy, vec_x, slots,
+                                                                             cx.rows_ws.as<float>(), dweight, dbias);
+    MPNN_HIP(hipGetLastError());
+    if (slots) {
+        k_weight_grad_sum<<<dim3(grid_for(matrix + out), n_experts), kBlock, 0, cx.stream>>>(n_experts, n, rows, slots, matrix, out, offsets,
+                                                                                             cx.rows_ws.as<float>(), dweight, dbias);
+        MPNN_HIP(hipGetLastError());
+    }
+    return Status::ok();
+}
+
+template <class T>
+Status weight_grad_t(Context &cx, int64_t n, int out, int width, int n_experts, const int32_t *offsets, const void *dy, int64_t ld,
+                     const int8_t *codes, const uint8_t *scales, float *dweight, float *dbias) {
+    if (out <= 32) return launch<T, 32>(cx, n, out, width, n_experts, offsets, (const T *)dy, ld, codes, scales, dweight, dbias);
+    if (out <= 64) return launch<T, 64>(cx, n, out, width, n_experts, offsets, (const T *)dy, ld, codes, scales, dweight, dbias);
+    return launch<T, 128>(cx, n, out, width, n_experts, offsets, (const T *)dy, ld, codes, scales, dweight, dbias);
 }
 
 }  // namespace
-
-template <class T>
-static Status weight_grad_t(Context &cx, int64_t n, int out, int width, int n_experts, const int32_t *offsets, const void *dy,
-                            int64_t ld, const int8_t *codes, const uint8_t *scales, float *dweight, float *dbias) {
-    const int64_t tiles = (int64_t)((width + kTile - 1) / kTile) * ((out + kTile - 1) / kTile) * n_experts;
-    const int64_t want = std::max<int64_t>(1, std::min<int64_t>((n + 255) / 256, 2048 / tiles));
-    const int64_t rows = std::max<int64_t>(1, (n + want - 1) / want);
-    const int pieces = (int)want;
-    const int64_t values = (int64_t)out * (width + 1);
-    MPNN_TRY(cx.grow(cx.rows_ws, sizeof(float) * (size_t)(values * pieces * n_experts)));
-    k_weight_grad<T><<<dim3((width + kTile - 1) / kTile, (out + kTile - 1) / kTile, (unsigned)(pieces * n_experts)), 256, 0, cx.stream>>>(
-        out, width, (width + 31) / 32, n_experts, n, rows, pieces, offsets, (const T *)dy, ld, codes, scales, cx.rows_ws.as<float>());
-    MPNN_HIP(hipGetLastError());
-    k_weight_grad_sum<<<dim3(grid_for(values), n_experts), kBlock, 0, cx.stream>>>(values, (int64_t)out * width, pieces,
-                                                                                   cx.rows_ws.as<float>(), dweight, dbias);
-    MPNN_HIP(hipGetLastError());
-    return Status::ok();
-}
 
 Status weight_grad(Context &cx, int dtype, int64_t n, int out, int width, int n_experts, const int32_t *offsets, const void *dy,
                    int64_t ld, const int8_t *codes, const uint8_t *scales, float *dweight, float *dbias) {
