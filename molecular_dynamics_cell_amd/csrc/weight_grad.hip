@@ -82,27 +82,23 @@ template <class T> struct QuadOf;
 template <> struct QuadOf<float> { using type = Quad32; };
 template <> struct QuadOf<bf16> { using type = Quad16; };
 
-__device__ __forceinline__ void load_quad(Quad32 &q, const float *p, bool vec, int cols) {
-    if (vec) {
-        const float4 t = *reinterpret_cast<const float4 *>(p);
-        q.v[0] = t.x; q.v[1] = t.y; q.v[2] = t.z; q.v[3] = t.w;
-    } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) q.v[j] = j < cols ? p[j] : 0.0f;
-    }
+// `last`: the last of the four columns that is there; those past it repeat it (their results are not written).
+__device__ __forceinline__ void load_quad(Quad32 &q, const float *p) {
+    const float4 t = *reinterpret_cast<const float4 *>(p);
+    q.v[0] = t.x; q.v[1] = t.y; q.v[2] = t.z; q.v[3] = t.w;
 }
-__device__ __forceinline__ void load_quad(Quad16 &q, const bf16 *p, bool vec, int cols) {
-    if (vec) {
-        const uint2 t = *reinterpret_cast<const uint2 *>(p);
-        q.v[0] = t.x; q.v[1] = t.y;
-    } else {
-        const uint16_t *u = reinterpret_cast<const uint16_t *>(p);
-        uint32_t h[4];
+__device__ __forceinline__ void load_quad(Quad32 &q, const float *p, int last) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) h[j] = j < cols ? u[j] : 0u;
-        q.v[0] = h[0] | h[1] << 16;
-        q.v[1] = h[2] | h[3] << 16;
-    }
+    for (int j = 0; j < 4; ++j) q.v[j] = p[min(j, last)];
+}
+__device__ __forceinline__ void load_quad(Quad16 &q, const bf16 *p) {
+    const uint2 t = *reinterpret_cast<const uint2 *>(p);
+    q.v[0] = t.x; q.v[1] = t.y;
+}
+__device__ __forceinline__ void load_quad(Quad16 &q, const bf16 *p, int last) {
+    const uint16_t *u = reinterpret_cast<const uint16_t *>(p);
+    q.v[0] = (uint32_t)u[0] | (uint32_t)u[min(1, last)] << 16;
+    q.v[1] = (uint32_t)u[min(2, last)] | (uint32_t)u[min(3, last)] << 16;
 }
 __device__ __forceinline__ void clear_quad(Quad32 &q) { q.v[0] = q.v[1] = q.v[2] = q.v[3] = 0.0f; }
 __device__ __forceinline__ void clear_quad(Quad16 &q) { q.v[0] = q.v[1] = 0u; }
@@ -168,39 +164,46 @@ __global__ __launch_bounds__(256, 2) void k_weight_grad(int out, int width, int 
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int am = tid % (BM / 4), ak = tid / (BM / 4);       // dy: column quad, chunk (threads with ak < 8)
     const int xm = tid % (kBN / 4), xk = tid / (kBN / 4);     // x
-    const int acols = out - o0 - 4 * am, xcols = width - c0 - 4 * xm;
-    const bool a_in = ak < kChunks && acols > 0, x_in = xcols > 0;
-    const T *ap = dy + o0 + 4 * am;
-    const int8_t *xp = codes + c0 + 4 * xm;
-    const uint8_t *sp = scales + (c0 + 4 * xm) / 32;
+    // columns past the last repeat it: their products are not written
+    const int ac = min(o0 + 4 * am, out - 1), xc = min(c0 + 4 * xm, width - 1);
+    const int alast = out - 1 - ac, xlast = width - 1 - xc;
+    const T *ap = dy + ac;
+    const int8_t *xp = codes + xc;
+    const uint8_t *sp = scales + xc / 32;
 
+    // The loads of a stage: rows past the last repeat it and are cleared when they are staged, so that no load waits
+    // for a condition of another.
     Quad a[8];
     uint32_t x[8];
-    float step[8];
+    uint8_t scale[8];
     auto fetch = [&](int64_t q0) {
+        int64_t qa[8], qx[8];
 #pragma unroll
         for (int r = 0; r < 8; ++r) {
-            const int64_t q = q0 + ak * 8 + r;
-            if (a_in && q < to) load_quad(a[r], ap + q * ld, vec_dy, acols);
-            else clear_quad(a[r]);
+            qa[r] = min(q0 + ak * 8 + r, to - 1);
+            qx[r] = min(q0 + xk * 8 + r, to - 1);
         }
+        if (ak < kChunks) {
+            if (vec_dy) {
 #pragma unroll
-        for (int r = 0; r < 8; ++r) {
-            const int64_t q = q0 + xk * 8 + r;
-            x[r] = 0u;
-            step[r] = 0.0f;
-            if (x_in && q < to) {
-                const int8_t *p = xp + q * width;
-                if (vec_x) {
-                    x[r] = *reinterpret_cast<const uint32_t *>(p);
-                } else {
+                for (int r = 0; r < 8; ++r) load_quad(a[r], ap + qa[r] * ld);
+            } else {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) x[r] |= j < xcols ? (uint32_t)(uint8_t)p[j] << 8 * j : 0u;
-                }
-                const int byte = sp[q * groups];
-                step[r] = byte == 255 ? __uint_as_float(0x7fc00000u) : __uint_as_float((uint32_t)byte << 23);
+                for (int r = 0; r < 8; ++r) load_quad(a[r], ap + qa[r] * ld, alast);
             }
         }
+        if (vec_x) {
+#pragma unroll
+            for (int r = 0; r < 8; ++r) x[r] = *reinterpret_cast<const uint32_t *>(xp + qx[r] * width);
+        } else {
+#pragma unroll
+            for (int r = 0; r < 8; ++r) {
+                const uint8_t *p = reinterpret_cast<const uint8_t *>(xp + qx[r] * width);
+                x[r] = (uint32_t)p[0] | (uint32_t)p[min(1, xlast)] << 8 | (uint32_t)p[min(2, xlast)] << 16 | (uint32_t)p[min(3, xlast)] << 24;
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < 8; ++r) scale[r] = sp[qx[r] * groups];
     };
 
     floatx16 acc[MT][NT];
@@ -213,6 +216,13 @@ __global__ __launch_bounds__(256, 2) void k_weight_grad(int out, int width, int 
     if (from < to) fetch(from);
     for (int64_t q0 = from; q0 < to; q0 += kBK) {
         __syncthreads();
+        if (q0 + kBK > to) {
+#pragma unroll
+            for (int r = 0; r < 8; ++r) {
+                if (q0 + ak * 8 + r >= to) clear_quad(a[r]);
+                if (q0 + xk * 8 + r >= to) scale[r] = 0;   // a step of zero
+            }
+        }
         if (ak < kChunks) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -228,6 +238,9 @@ __global__ __launch_bounds__(256, 2) void k_weight_grad(int out, int width, int 
                     for (int r = 0; r < 8; ++r) bias[j] += a[r].at(j);
             }
         }
+        float step[8];
+#pragma unroll
+        for (int r = 0; r < 8; ++r) step[r] = __uint_as_float(scale[r] == 255 ? 0x7fc00000u : (uint32_t)scale[r] << 23);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             uint32_t v[8];
