@@ -2,6 +2,8 @@
 // expert with a stable counting sort; pairs whose expert is outside 0 .. E-1 keep a place after the last segment
 // (treated as expert E), so `source` and `position` are inverse permutations of all n k pairs and every index that
 // a kernel reads from them is one it can check against n k.
+#include <type_traits>
+
 #include "impl.h"
 #include "rows.h"
 
@@ -135,62 +137,134 @@ __global__ void k_route_place(const int32_t *__restrict__ expert, int64_t pairs,
     }
 }
 
-// sorted[position[i, s]] = x[i]; a pair without an expert gets a row of zeros
-template <class T>
-__global__ void k_route_scatter(int64_t n, int k, int width, const T *__restrict__ x, int64_t ldx, const int32_t *__restrict__ position,
-                                const int32_t *__restrict__ used, T *__restrict__ sorted) {
-    const int64_t pairs = n * k;
-    const int64_t p = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    if (p >= pairs) return;
-    const int q = position[p];
-    if ((unsigned)q >= (uint64_t)pairs) return;
-    const bool live = q < *used;
-    const T *from = x + (p / k) * ldx;
-    T *to = sorted + (int64_t)q * width;
-    for (int c = threadIdx.x & 63; c < width; c += 64) to[c] = live ? from[c] : from_f32<T>(0.0f);
+// Where a chunk of a row starts: the last chunk of a row is moved back to end with the row (its first values are
+// then written twice, equally), so that every access is a whole chunk.  Rows shorter than a chunk go value by value.
+template <class T> __device__ __forceinline__ int chunk_start(int c, int width) { return min(c * Chunk<T>::W, width - Chunk<T>::W); }
+
+// sorted[position[i, s]] = x[i]; a pair without an expert gets a row of zeros.  Row-major over x, so that each row is
+// read once for its k copies.
+template <class T, bool SHORT>
+__global__ __launch_bounds__(256) void k_route_scatter(Items it, int k, int width, const T *__restrict__ x, int64_t ldx,
+                                                       const int32_t *__restrict__ position, const int32_t *__restrict__ used,
+                                                       T *__restrict__ sorted) {
+    const int64_t pairs = it.n * k;
+    const int live = *used;
+    int64_t row[kUnroll];
+    int at[kUnroll];
+    bool in[kUnroll];
+    using V = typename std::conditional<SHORT, T, Chunk<T>>::type;
+    V v[kUnroll], zero;
+    __builtin_memset(&zero, 0, sizeof zero);
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+        in[u] = item_at(it, u, row[u], at[u]);
+        if (!SHORT) at[u] = chunk_start<T>(at[u], width);
+        if (in[u]) __builtin_memcpy(&v[u], x + row[u] * ldx + at[u], sizeof(V));
+    }
+    for (int s = 0; s < k; ++s)
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            if (!in[u]) continue;
+            const int q = position[row[u] * k + s];
+            if ((unsigned)q < (uint64_t)pairs) {
+                const V w = q < live ? v[u] : zero;
+                __builtin_memcpy(sorted + (int64_t)q * width + at[u], &w, sizeof(V));
+            }
+        }
 }
 
 // out[i] = sum over s of weight[i, s] sorted[position[i, s]], in the order of the slots, in fp32
-template <class T>
-__global__ void k_route_combine(int64_t n, int k, int width, const T *__restrict__ sorted, const int32_t *__restrict__ position,
-                                const int32_t *__restrict__ used, const float *__restrict__ weight, T *__restrict__ out) {
-    const int64_t i = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    if (i >= n) return;
+template <class T, bool SHORT>
+__global__ __launch_bounds__(256) void k_route_combine(Items it, int k, int width, const T *__restrict__ sorted,
+                                                       const int32_t *__restrict__ position, const int32_t *__restrict__ used,
+                                                       const float *__restrict__ weight, T *__restrict__ out) {
+    constexpr int W = SHORT ? 1 : Chunk<T>::W, S = 4;     // S slots of a row are loaded together
     const int live = *used;
-    for (int c = threadIdx.x & 63; c < width; c += 64) {
-        float sum = 0.0f;
-        for (int s = 0; s < k; ++s) {
-            const int q = position[i * k + s];
-            if ((unsigned)q < (unsigned)live) {
-                const float v = to_f32(sorted[(int64_t)q * width + c]);
-                sum = weight ? fmaf(weight[i * k + s], v, sum) : sum + v;
+#pragma unroll 1
+    for (int u = 0; u < kUnroll; ++u) {
+        int64_t row;
+        int at;
+        if (!item_at(it, u, row, at)) continue;
+        if (!SHORT) at = chunk_start<T>(at, width);
+        float sum[W] = {};
+        for (int s0 = 0; s0 < k; s0 += S) {
+            struct { T v[W]; } y[S];
+            bool on[S];
+            float w[S];
+#pragma unroll
+            for (int j = 0; j < S; ++j) {
+                const int64_t p = row * k + min(s0 + j, k - 1);
+                const int q = position[p];
+                on[j] = s0 + j < k && (unsigned)q < (unsigned)live;
+                w[j] = weight ? weight[p] : 1.0f;
+                // a place without an expert reads another row, whose values are not used
+                __builtin_memcpy(&y[j], sorted + (int64_t)(on[j] ? q : 0) * width + at, sizeof y[j]);
             }
+#pragma unroll
+            for (int j = 0; j < S; ++j)
+#pragma unroll
+                for (int e = 0; e < W; ++e) sum[e] = on[j] ? fmaf(w[j], to_f32(y[j].v[e]), sum[e]) : sum[e];
         }
-        out[i * width + c] = from_f32<T>(sum);
+        struct { T v[W]; } o;
+#pragma unroll
+        for (int e = 0; e < W; ++e) o.v[e] = from_f32<T>(sum[e]);
+        __builtin_memcpy(out + row * width + at, &o, sizeof o);
     }
 }
 
-// dsorted[q] = weight dout[i] and dweight = <dout[i], sorted[q]> for q = position[i, s]; zeros without an expert
-template <class T>
-__global__ void k_route_combine_back(int64_t n, int k, int width, const T *__restrict__ dout, int64_t ld, const T *__restrict__ sorted,
-                                     const int32_t *__restrict__ position, const int32_t *__restrict__ used,
-                                     const float *__restrict__ weight, T *__restrict__ dsorted, float *__restrict__ dweight) {
+// dsorted[q] = weight dout[i] and dweight = <dout[i], sorted[q]> for q = position[i, s]; zeros without an expert.
+// G lanes take a row and kBackSlots of its slots, so that a chunk of dout is read once for them.
+constexpr int kBackSlots = 4;
+template <class T, int G>
+__global__ __launch_bounds__(256) void k_route_combine_back(int64_t n, int k, int batches, int width, const T *__restrict__ dout, int64_t ld,
+                                                            const T *__restrict__ sorted, const int32_t *__restrict__ position,
+                                                            const int32_t *__restrict__ used, const float *__restrict__ weight,
+                                                            T *__restrict__ dsorted, float *__restrict__ dweight) {
+    constexpr int W = Chunk<T>::W, S = kBackSlots;
     const int64_t pairs = n * k;
-    const int64_t p = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    if (p >= pairs) return;
-    const int q = position[p];
-    const bool in = (unsigned)q < (uint64_t)pairs, live = in && q < *used;
-    const float w = live && weight ? weight[p] : 1.0f;
-    const T *from = dout + (p / k) * ld;
-    float dot = 0.0f;
-    for (int c = threadIdx.x & 63; c < width && in; c += 64) {
-        const int64_t at = (int64_t)q * width + c;
-        const float d = live ? to_f32(from[c]) : 0.0f;
-        if (live && dweight) dot = fmaf(d, to_f32(sorted[at]), dot);   // without dweight there may be no sorted rows
-        dsorted[at] = from_f32<T>(live ? w * d : 0.0f);
+    const int64_t job = (int64_t)blockIdx.x * (256 / G) + threadIdx.x / G;
+    const int64_t i = batches == 1 ? job : job / batches;
+    if (i >= n) return;                                   // a whole group of lanes
+    const int s0 = batches == 1 ? 0 : (int)(job - i * batches) * S;
+    const int lane = threadIdx.x % G, live = *used;
+    int q[S];
+    bool in[S], on[S];
+    float w[S], dot[S] = {};
+#pragma unroll
+    for (int j = 0; j < S; ++j) {
+        const int64_t p = i * k + min(s0 + j, k - 1);
+        q[j] = position[p];
+        in[j] = s0 + j < k && (unsigned)q[j] < (uint64_t)pairs;
+        on[j] = in[j] && q[j] < live;
+        w[j] = weight ? weight[p] : 1.0f;
     }
-    dot = wave_sum(dot);
-    if (dweight && (threadIdx.x & 63) == 0) dweight[p] = live ? dot : 0.0f;
+    for (int c = lane * W; c < width; c += G * W) {
+        const int left = width - c;
+        const Chunk<T> d = load_chunk(dout + i * ld + c, left);
+        Chunk<T> y[S];
+        if (dweight) {
+#pragma unroll
+            for (int j = 0; j < S; ++j) y[j] = load_chunk(sorted + (int64_t)(on[j] ? q[j] : 0) * width + c, left);
+        }
+#pragma unroll
+        for (int j = 0; j < S; ++j) {
+            Chunk<T> o;
+#pragma unroll
+            for (int e = 0; e < W; ++e) {
+                const float v = to_f32(d.v[e]);
+                if (dweight) dot[j] = fmaf(v, to_f32(y[j].v[e]), dot[j]);
+                o.v[e] = from_f32<T>(on[j] ? w[j] * v : 0.0f);
+            }
+            if (in[j]) store_chunk(dsorted + (int64_t)q[j] * width + c, o, left);
+        }
+    }
+    if (dweight) {
+#pragma unroll
+        for (int j = 0; j < S; ++j) {
+            const float t = lanes_sum<G>(dot[j]);
+            if (lane == 0 && s0 + j < k) dweight[i * k + s0 + j] = on[j] ? t : 0.0f;
+        }
+    }
 }
 
 }  // namespace
@@ -219,7 +293,10 @@ Status route_plan(Context &cx, int64_t n, int k, int n_experts, const int32_t *e
 template <class T>
 static Status scatter_t(Context &cx, int64_t n, int k, int width, const void *x, int64_t ldx, const int32_t *position,
                         const int32_t *used, void *sorted) {
-    k_route_scatter<T><<<grid_for(n * k, 4), 256, 0, cx.stream>>>(n, k, width, (const T *)x, ldx, position, used, (T *)sorted);
+    constexpr int W = Chunk<T>::W;
+    const Items it = items_of(n, width < W ? width : (width + W - 1) / W);
+    auto *kernel = width < W ? k_route_scatter<T, true> : k_route_scatter<T, false>;
+    kernel<<<grid_of(it), 256, 0, cx.stream>>>(it, k, width, (const T *)x, ldx, position, used, (T *)sorted);
     MPNN_HIP(hipGetLastError());
     return Status::ok();
 }
@@ -234,7 +311,10 @@ Status route_scatter(Context &cx, int dtype, int64_t n, int k, int width, const 
 template <class T>
 static Status combine_t(Context &cx, int64_t n, int k, int width, const void *sorted, const int32_t *position, const int32_t *used,
                         const float *weight, void *out) {
-    k_route_combine<T><<<grid_for(n, 4), 256, 0, cx.stream>>>(n, k, width, (const T *)sorted, position, used, weight, (T *)out);
+    constexpr int W = Chunk<T>::W;
+    const Items it = items_of(n, width < W ? width : (width + W - 1) / W);
+    auto *kernel = width < W ? k_route_combine<T, true> : k_route_combine<T, false>;
+    kernel<<<grid_of(it), 256, 0, cx.stream>>>(it, k, width, (const T *)sorted, position, used, weight, (T *)out);
     MPNN_HIP(hipGetLastError());
     return Status::ok();
 }
@@ -249,10 +329,17 @@ Status route_combine(Context &cx, int dtype, int64_t n, int k, int width, const 
 template <class T>
 static Status combine_back_t(Context &cx, int64_t n, int k, int width, const void *dout, int64_t ld, const void *sorted,
                              const int32_t *position, const int32_t *used, const float *weight, void *dsorted, float *dweight) {
-    k_route_combine_back<T><<<grid_for(n * k, 4), 256, 0, cx.stream>>>(n, k, width, (const T *)dout, ld, (const T *)sorted, position,
-                                                                       used, weight, (T *)dsorted, dweight);
-    MPNN_HIP(hipGetLastError());
-    return Status::ok();
+    const int chunks = (width + Chunk<T>::W - 1) / Chunk<T>::W, batches = (k + kBackSlots - 1) / kBackSlots;
+    auto run = [&](auto *kernel, int lanes) -> Status {
+        kernel<<<grid_for(n * batches, 256 / lanes), 256, 0, cx.stream>>>(n, k, batches, width, (const T *)dout, ld, (const T *)sorted,
+                                                                          position, used, weight, (T *)dsorted, dweight);
+        MPNN_HIP(hipGetLastError());
+        return Status::ok();
+    };
+    if (chunks <= 8) return run(k_route_combine_back<T, 8>, 8);
+    if (chunks <= 16) return run(k_route_combine_back<T, 16>, 16);
+    if (chunks <= 32) return run(k_route_combine_back<T, 32>, 32);
+    return run(k_route_combine_back<T, 64>, 64);
 }
 
 Status route_combine_backward(Context &cx, int dtype, int64_t n, int k, int width, const void *dout, int64_t ld, const void *sorted,

@@ -11,10 +11,90 @@ using bf16 = __bf16;
 template <class T> __device__ __forceinline__ float to_f32(T v) { return (float)v; }
 template <class T> __device__ __forceinline__ T from_f32(float v) { return (T)v; }
 
-__device__ __forceinline__ float wave_sum(float v) {
+// 16 bytes of a row.  Rows may start on any value's boundary (odd widths, column blocks of wider rows): the access is
+// declared with the value's alignment, and gfx950's global loads and stores take it in one instruction all the same.
+template <class T>
+struct Chunk {
+    static constexpr int W = 16 / sizeof(T);
+    T v[W];
+};
+template <class T> __device__ __forceinline__ Chunk<T> load_chunk(const T *p) {
+    Chunk<T> c;
+    __builtin_memcpy(&c, p, sizeof c);
+    return c;
+}
+template <class T> __device__ __forceinline__ void store_chunk(T *p, const Chunk<T> &c) { __builtin_memcpy(p, &c, sizeof c); }
+
+// The first `in` values of a chunk (all of them from W on), zeros after them.
+template <class T> __device__ __forceinline__ Chunk<T> load_chunk(const T *p, int in) {
+    if (in >= Chunk<T>::W) return load_chunk(p);
+    Chunk<T> c;
 #pragma unroll
-    for (int d = 32; d >= 1; d >>= 1) v += __shfl_xor(v, d);
+    for (int j = 0; j < Chunk<T>::W; ++j) c.v[j] = j < in ? p[j] : from_f32<T>(0.0f);
+    return c;
+}
+template <class T> __device__ __forceinline__ void store_chunk(T *p, const Chunk<T> &c, int in) {
+    if (in >= Chunk<T>::W) {
+        store_chunk(p, c);
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < Chunk<T>::W; ++j)
+        if (j < in) p[j] = c.v[j];
+}
+
+// Sum over G = 4 .. 64 neighbouring lanes, the same bits in each of them: exchanges inside 16 lanes by data-parallel
+// primitives (neighbours, pairs, mirrored halves), across them by the lane swaps.
+template <int CTRL> __device__ __forceinline__ float dpp(float v) {
+    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xf, 0xf, true));
+}
+template <int G> __device__ __forceinline__ float lanes_sum(float v) {
+    v += dpp<0xb1>(v);                       // quad_perm 1 0 3 2
+    v += dpp<0x4e>(v);                       // quad_perm 2 3 0 1
+    if (G >= 8) v += dpp<0x141>(v);          // row_half_mirror
+    if (G >= 16) v += dpp<0x140>(v);         // row_mirror
+    if (G >= 32) {
+        const auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+        v = __uint_as_float(p[0]) + __uint_as_float(p[1]);
+    }
+    if (G >= 64) {
+        const auto p = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+        v = __uint_as_float(p[0]) + __uint_as_float(p[1]);
+    }
     return v;
+}
+
+__device__ __forceinline__ float wave_sum(float v) { return lanes_sum<64>(v); }
+
+// Items of a row operator without sums along the rows: `per` chunks a row.  A block takes `rows` whole rows, or, of
+// rows longer than kItems chunks, one stretch (blockIdx.y); a thread takes every 256th item, kUnroll of them at a time
+// so that their loads are in flight together.
+constexpr int kItems = 1024, kUnroll = 4;
+struct Items {
+    int64_t n;
+    int per, rows;
+    float inv;      // 1 / per
+};
+inline Items items_of(int64_t n, int per) {
+    const int rows = per < kItems ? kItems / per : 1;
+    return Items{n, per, rows, 1.0f / (float)per};
+}
+inline dim3 grid_of(const Items &it) { return dim3((unsigned)((it.n + it.rows - 1) / it.rows), (unsigned)((it.per + kItems - 1) / kItems)); }
+
+// The block's u-th item of this thread: its row and chunk; false past the last.
+__device__ __forceinline__ bool item_at(const Items &it, int u, int64_t &row, int &c) {
+    const int l = u * 256 + threadIdx.x;
+    if (it.rows == 1) {
+        row = blockIdx.x;
+        c = blockIdx.y * kItems + l;
+        return c < it.per;
+    }
+    int q = (int)((float)l * it.inv);      // off by one at most
+    q -= q * it.per > l;
+    q += (q + 1) * it.per <= l;
+    row = (int64_t)blockIdx.x * it.rows + q;
+    c = l - q * it.per;
+    return q < it.rows && row < it.n;
 }
 
 }  // namespace mpnn
