@@ -3,6 +3,15 @@
 //   N(v) = (v - mean) / sqrt(mean((v - mean)^2) + eps) * weight + bias   (rms: without the mean)
 // h comes from the unrounded r.  The reverse pass takes the statistics again from the rows it reads anyway, so the
 // forward pass stores none.
+//
+// One pass over the rows: G lanes hold a row in registers, CH 16-byte chunks each (G = 8 .. 64 inside a wave, or
+// waves of one block for wide rows), so that means and mean squares are taken from registers (the mean first, then
+// the squares about it) and every array is read and written once.  Groups walk over the rows with their columns'
+// weights in registers, and in the reverse pass with their columns' sums; the sums of all groups are added at the end
+// in a fixed order.
+#include <algorithm>
+#include <type_traits>
+
 #include "impl.h"
 #include "rows.h"
 
@@ -13,222 +22,406 @@ namespace {
 struct NormArgs {
     int64_t n;
     int width, layer;
-    int gate_width;
-    float eps;
+    int gate_width;        // 0: no gate
+    float eps, inv_width;
     const float *post_weight, *post_bias, *scale, *pre_weight, *pre_bias;
 };
 
-__device__ __forceinline__ float at_or(const float *p, int c, float otherwise) { return p ? p[c] : otherwise; }
-__device__ __forceinline__ float sigmoid(float g) { return 1.0f / (1.0f + expf(-g)); }
+__device__ __forceinline__ float sigmoid(float g) { return __builtin_amdgcn_rcpf(1.0f + expf(-g)); }
 
-// mean (0 for rms) and 1 / sqrt(mean square + eps) of a row, by one wave
-template <class F>
-__device__ __forceinline__ void row_stats(const NormArgs &a, int lane, F value, float &mean, float &inv) {
-    mean = 0.0f;
-    if (a.layer) {
-        float s = 0.0f;
-        for (int c = lane; c < a.width; c += 64) s += value(c);
-        mean = wave_sum(s) / a.width;
+// A row's place in the block's registers.
+template <class T, int G, int CH>
+struct Lanes {
+    static constexpr int W = Chunk<T>::W, E = CH * W;      // values of a row per lane
+    static constexpr int kThreads = G > 64 ? G : 256, kGroups = kThreads / G;   // several waves a row: one row a block
+    static constexpr int kWaves = G / 64;                  // waves of a row (0: part of one)
+    int lane, group;
+    int width;
+    __device__ __forceinline__ Lanes(int w) : lane(threadIdx.x % G), group(threadIdx.x / G), width(w) {}
+    __device__ __forceinline__ int column(int c) const { return (c * G + lane) * W; }
+    __device__ __forceinline__ void load(float (&v)[E], const T *row) const {
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            Chunk<T> t;
+            const int left = width - column(c);
+            if (left > 0) t = load_chunk(row + column(c), left);
+            else
+#pragma unroll
+                for (int j = 0; j < W; ++j) t.v[j] = from_f32<T>(0.0f);
+#pragma unroll
+            for (int j = 0; j < W; ++j) v[c * W + j] = to_f32(t.v[j]);
+        }
     }
-    float q = 0.0f;
-    for (int c = lane; c < a.width; c += 64) {
-        const float v = value(c) - mean;
-        q = fmaf(v, v, q);
+    __device__ __forceinline__ void store(T *row, const float (&v)[E]) const {
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            Chunk<T> t;
+#pragma unroll
+            for (int j = 0; j < W; ++j) t.v[j] = from_f32<T>(v[c * W + j]);
+            const int left = width - column(c);
+            if (left > 0) store_chunk(row + column(c), t, left);
+        }
     }
-    inv = rsqrtf(wave_sum(q) / a.width + a.eps);
+    // Wide rows: the vectors are read again for each row, from the caches, where the registers do not hold them beside
+    // the sums.  The offset is zero, but not to the compiler, which would move the loads out of the loop.
+    static constexpr bool kKeep = E <= 8;
+    __device__ __forceinline__ static int again() {
+        int z = 0;
+        if (!kKeep) asm volatile("" : "+s"(z));
+        return z;
+    }
+    // a vector's values of this lane's columns; zeros past the width
+    __device__ __forceinline__ void vector(float (&v)[E], const float *p, float otherwise) const {
+#pragma unroll
+        for (int c = 0; c < CH; ++c)
+#pragma unroll
+            for (int j = 0; j < W; ++j) {
+                const int at = column(c) + j;
+                v[c * W + j] = at < width ? (p ? p[at] : otherwise) : 0.0f;
+            }
+    }
+    // sums over the row's lanes, the same bits in each
+    template <int N, int M> __device__ __forceinline__ void sums(float (&s)[N], float (&sh)[2][M], int &turn) const {
+        if constexpr (kWaves <= 1) {
+#pragma unroll
+            for (int q = 0; q < N; ++q) s[q] = lanes_sum<G>(s[q]);
+        } else {
+            static_assert(M >= N * kWaves, "room for the waves' sums");
+            // the waves' sums through LDS; two buffers in turn, so that one barrier a sum is enough
+            float *b = sh[turn];
+            turn ^= 1;
+#pragma unroll
+            for (int q = 0; q < N; ++q) {
+                s[q] = lanes_sum<64>(s[q]);
+                if ((threadIdx.x & 63) == 0) b[q * kWaves + (lane >> 6)] = s[q];
+            }
+            __syncthreads();
+#pragma unroll
+            for (int q = 0; q < N; ++q) {
+                s[q] = 0.0f;
+#pragma unroll
+                for (int w = 0; w < kWaves; ++w) s[q] += b[q * kWaves + w];
+            }
+        }
+    }
+    // v becomes its distance from m (0 past the width)
+    __device__ __forceinline__ void centre(float (&v)[E], float m) const {
+#pragma unroll
+        for (int c = 0; c < CH; ++c)
+#pragma unroll
+            for (int j = 0; j < W; ++j) v[c * W + j] = column(c) + j < width ? v[c * W + j] - m : 0.0f;
+    }
+};
+
+template <int E> __device__ __forceinline__ float sum_of(const float (&v)[E]) {
+    float s = 0.0f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) s += v[e];
+    return s;
+}
+template <int E> __device__ __forceinline__ float dot_of(const float (&v)[E], const float (&w)[E]) {
+    float s = 0.0f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) s = fmaf(v[e], w[e], s);
+    return s;
 }
 
-template <class T>
-__global__ void k_norm_residual(NormArgs a, const T *__restrict__ x, int64_t ldx, const T *__restrict__ block, int64_t ldb,
-                                const T *__restrict__ gate, int64_t ldg, T *r, T *__restrict__ h) {
-    const int64_t i = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    if (i >= a.n) return;
-    const int lane = threadIdx.x & 63;
-    float bm = 0.0f, bi = 0.0f;
-    if (block) row_stats(a, lane, [&](int c) { return to_f32(block[i * ldb + c]); }, bm, bi);
-    auto sum = [&](int c) {
-        float v = to_f32(x[i * ldx + c]);
-        if (block) {
-            const float u = (to_f32(block[i * ldb + c]) - bm) * bi * at_or(a.post_weight, c, 1.0f) + at_or(a.post_bias, c, 0.0f);
-            const float g = gate ? sigmoid(to_f32(gate[i * ldg + (a.gate_width == 1 ? 0 : c)])) : 1.0f;
-            v += at_or(a.scale, c, 1.0f) * g * u;
+// In a group of several waves all waves of the block take the same row, so barriers inside the row loop are uniform.
+template <class T, int G, int CH>
+__global__ __launch_bounds__((Lanes<T, G, CH>::kThreads)) void k_norm_residual(NormArgs a, const T *__restrict__ x, int64_t ldx,
+                                                                             const T *__restrict__ block, int64_t ldb,
+                                                                             const T *__restrict__ gate, int64_t ldg, T *r,
+                                                                             T *__restrict__ h) {
+    using L = Lanes<T, G, CH>;
+    constexpr int E = L::E;
+    __shared__ float sh[2][L::kWaves > 1 ? L::kWaves : 1];
+    int turn = 0;
+    const L at(a.width);
+    float pw[E], pb[E], qw[E], qb[E];
+    if (block) {
+        float sc[E];
+        at.vector(pw, a.post_weight, 1.0f);
+        at.vector(pb, a.post_bias, 0.0f);
+        at.vector(sc, a.scale, 1.0f);
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            pw[e] *= sc[e];
+            pb[e] *= sc[e];
         }
-        return v;
-    };
-    float rm, ri;
-    if (h) {
-        row_stats(a, lane, sum, rm, ri);
-        for (int c = lane; c < a.width; c += 64)
-            h[i * a.width + c] = from_f32<T>((sum(c) - rm) * ri * at_or(a.pre_weight, c, 1.0f) + at_or(a.pre_bias, c, 0.0f));
     }
-    if (r)
-        for (int c = lane; c < a.width; c += 64) r[i * a.width + c] = from_f32<T>(sum(c));
+    if (h) {
+        at.vector(qw, a.pre_weight, 1.0f);
+        at.vector(qb, a.pre_bias, 0.0f);
+    }
+    auto normalise = [&](float (&v)[E]) {
+        if (a.layer) {
+            float m[1] = {sum_of(v)};
+            at.sums(m, sh, turn);
+            at.centre(v, m[0] * a.inv_width);
+        }
+        float q[1] = {dot_of(v, v)};
+        at.sums(q, sh, turn);
+        const float inv = rsqrtf(q[0] * a.inv_width + a.eps);
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[e] *= inv;
+    };
+    for (int64_t i = (int64_t)blockIdx.x * L::kGroups + at.group; i < a.n; i += (int64_t)gridDim.x * L::kGroups) {
+        float v[E];
+        at.load(v, x + i * ldx);
+        if (block) {
+            float b[E], g[E];
+            at.load(b, block + i * ldb);
+            if (a.gate_width > 1) at.load(g, gate + i * ldg);
+            else if (a.gate_width == 1) g[0] = to_f32(gate[i * ldg]);
+            normalise(b);
+            if (a.gate_width > 1) {
+#pragma unroll
+                for (int e = 0; e < E; ++e) v[e] = fmaf(sigmoid(g[e]), fmaf(b[e], pw[e], pb[e]), v[e]);
+            } else {
+                const float s = a.gate_width == 1 ? sigmoid(g[0]) : 1.0f;
+#pragma unroll
+                for (int e = 0; e < E; ++e) v[e] = fmaf(s, fmaf(b[e], pw[e], pb[e]), v[e]);
+            }
+        }
+        if (r) at.store(r + i * a.width, v);
+        if (h) {
+            normalise(v);
+#pragma unroll
+            for (int e = 0; e < E; ++e) v[e] = fmaf(v[e], qw[e], qb[e]);
+            at.store(h + i * a.width, v);
+        }
+    }
 }
 
 // Gradients of the rows.  total = dr + N_pre'(dh), dx = total, and with u = N_post(block):
 //   dgate = total scale u sigma'(gate), du = total scale sigma(gate), dblock = N_post'(du),
 //   N'(d) = inv (a - mean(a) - hat mean(a hat)), a = d weight   (rms: without mean(a))
-// The row's statistics and sums go to stats[i][kStats] for the columns' pass.
-constexpr int kStats = 6;   // block mean, block inverse, r mean, r inverse, mean(a_pre), mean(a_pre hat)
-
-template <class T>
-__global__ void k_norm_residual_back(NormArgs a, const T *__restrict__ dr, const T *__restrict__ dh, const T *__restrict__ r,
-                                     int64_t ldr, const T *__restrict__ block, int64_t ldb, const T *__restrict__ gate, int64_t ldg,
-                                     T *dx, T *__restrict__ dblock, T *__restrict__ dgate, float *__restrict__ stats) {
-    const int64_t i = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    if (i >= a.n) return;
-    const int lane = threadIdx.x & 63;
-    float bm = 0, bi = 0, rm = 0, ri = 0, m1 = 0, m2 = 0;
-    if (dh) {
-        row_stats(a, lane, [&](int c) { return to_f32(r[i * ldr + c]); }, rm, ri);
-        for (int c = lane; c < a.width; c += 64) {
-            const float w = to_f32(dh[i * a.width + c]) * at_or(a.pre_weight, c, 1.0f);
-            m1 += w;
-            m2 = fmaf(w, (to_f32(r[i * ldr + c]) - rm) * ri, m2);
-        }
-        m1 = a.layer ? wave_sum(m1) / a.width : 0.0f;
-        m2 = wave_sum(m2) / a.width;
-    }
-    auto total = [&](int c) {
-        float v = dr ? to_f32(dr[i * a.width + c]) : 0.0f;
-        if (dh) {
-            const float hat = (to_f32(r[i * ldr + c]) - rm) * ri;
-            v += ri * (to_f32(dh[i * a.width + c]) * at_or(a.pre_weight, c, 1.0f) - m1 - hat * m2);
-        }
-        return v;
+// and of the vectors, summed over the group's rows:
+//   post weight: du hat_b, post bias: du, scale: total sigma(gate) u, pre weight: dh hat_r, pre bias: dh
+template <class T, int G, int CH>
+__global__ __launch_bounds__((Lanes<T, G, CH>::kThreads)) void k_norm_residual_back(NormArgs a, const T *dr, const T *__restrict__ dh,
+                                                                                  const T *__restrict__ r, int64_t ldr,
+                                                                                  const T *__restrict__ block, int64_t ldb,
+                                                                                  const T *__restrict__ gate, int64_t ldg, T *dx,
+                                                                                  T *__restrict__ dblock, T *__restrict__ dgate,
+                                                                                  float *__restrict__ part) {
+    using L = Lanes<T, G, CH>;
+    constexpr int E = L::E;
+    constexpr int kShared = L::kWaves > 1 ? 3 * L::kWaves : 1;
+    __shared__ float sh1[2][L::kWaves > 1 ? L::kWaves : 1], sh2[2][L::kWaves > 1 ? 2 * L::kWaves : 1], sh3[2][kShared];
+    __shared__ float columns[L::kGroups > 1 ? L::kGroups * G * E : 1];
+    int turn1 = 0, turn2 = 0, turn3 = 0;
+    const L at(a.width);
+    float pw[E], pb[E], sc[E], qw[E];
+    auto after = [&](const float *p) { return p ? p + L::again() : p; };
+    auto post_vectors = [&]() {
+        at.vector(pw, after(a.post_weight), 1.0f);
+        at.vector(pb, after(a.post_bias), 0.0f);
+        at.vector(sc, after(a.scale), 1.0f);
     };
-    if (block) {
-        row_stats(a, lane, [&](int c) { return to_f32(block[i * ldb + c]); }, bm, bi);
-        float n1 = 0, n2 = 0, gs = 0;
-        auto sig = [&](int c) { return gate ? sigmoid(to_f32(gate[i * ldg + (a.gate_width == 1 ? 0 : c)])) : 1.0f; };
-        for (int c = lane; c < a.width; c += 64) {
-            const float t = total(c) * at_or(a.scale, c, 1.0f), hat = (to_f32(block[i * ldb + c]) - bm) * bi;
-            const float g = sig(c), d = t * g * at_or(a.post_weight, c, 1.0f);
-            n1 += d;
-            n2 = fmaf(d, hat, n2);
-            const float dg = t * (hat * at_or(a.post_weight, c, 1.0f) + at_or(a.post_bias, c, 0.0f)) * g * (1.0f - g);
-            if (gate && a.gate_width != 1) dgate[i * a.width + c] = from_f32<T>(dg);
-            gs += dg;
-        }
-        n1 = a.layer ? wave_sum(n1) / a.width : 0.0f;
-        n2 = wave_sum(n2) / a.width;
-        gs = wave_sum(gs);
-        if (gate && a.gate_width == 1 && lane == 0) dgate[i] = from_f32<T>(gs);
-        for (int c = lane; c < a.width; c += 64) {
-            const float hat = (to_f32(block[i * ldb + c]) - bm) * bi;
-            const float d = total(c) * at_or(a.scale, c, 1.0f) * sig(c) * at_or(a.post_weight, c, 1.0f);
-            dblock[i * a.width + c] = from_f32<T>(bi * (d - n1 - hat * n2));
-        }
+    if (L::kKeep) {
+        post_vectors();
+        at.vector(qw, a.pre_weight, 1.0f);
     }
-    if (stats && lane == 0) {
-        const float v[kStats] = {bm, bi, rm, ri, m1, m2};
-        for (int q = 0; q < kStats; ++q) stats[i * kStats + q] = v[q];
-    }
-    if (dx)
-        for (int c = lane; c < a.width; c += 64) dx[i * a.width + c] = from_f32<T>(total(c));
-}
-
-// Sums over the rows, for the five vectors: one thread per column and block of rows, then one per column.
-template <class T>
-__global__ void k_norm_columns(NormArgs a, const T *__restrict__ dr, const T *__restrict__ dh, const T *__restrict__ r, int64_t ldr,
-                               const T *__restrict__ block, int64_t ldb, const T *__restrict__ gate, int64_t ldg,
-                               const float *__restrict__ stats, int64_t rows, float *__restrict__ part) {
-    const int c = blockIdx.y * 64 + threadIdx.x;
-    if (c >= a.width) return;
-    const int64_t end = min(a.n, (int64_t)(blockIdx.x + 1) * rows);
-    float s[5] = {};
-    for (int64_t i = (int64_t)blockIdx.x * rows; i < end; ++i) {
-        const float *st = stats + i * kStats;
-        float total = dr ? to_f32(dr[i * a.width + c]) : 0.0f;
-        if (dh) {
-            const float hat = (to_f32(r[i * ldr + c]) - st[2]) * st[3], d = to_f32(dh[i * a.width + c]);
-            total += st[3] * (d * at_or(a.pre_weight, c, 1.0f) - st[4] - hat * st[5]);
-            s[3] = fmaf(d, hat, s[3]);
-            s[4] += d;
+    float s0[E] = {}, s1[E] = {}, s2[E] = {}, s3[E] = {}, s4[E] = {};
+    // v becomes its normed values; returns one over the root
+    auto normalise = [&](float (&v)[E]) {
+        if (a.layer) {
+            float m[1] = {sum_of(v)};
+            at.sums(m, sh1, turn1);
+            at.centre(v, m[0] * a.inv_width);
         }
+        float q[1] = {dot_of(v, v)};
+        at.sums(q, sh1, turn1);
+        const float inv = rsqrtf(q[0] * a.inv_width + a.eps);
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[e] *= inv;
+        return inv;
+    };
+    for (int64_t i = (int64_t)blockIdx.x * L::kGroups + at.group; i < a.n; i += (int64_t)gridDim.x * L::kGroups) {
+        float t[E];
+        if (dr) at.load(t, dr + i * a.width);
+        else
+#pragma unroll
+            for (int e = 0; e < E; ++e) t[e] = 0.0f;
+        float b[E], g[E];
         if (block) {
-            const float hat = (to_f32(block[i * ldb + c]) - st[0]) * st[1];
-            const float g = gate ? sigmoid(to_f32(gate[i * ldg + (a.gate_width == 1 ? 0 : c)])) : 1.0f;
-            const float du = total * at_or(a.scale, c, 1.0f) * g;
-            s[0] = fmaf(du, hat, s[0]);
-            s[1] += du;
-            s[2] = fmaf(total * g, hat * at_or(a.post_weight, c, 1.0f) + at_or(a.post_bias, c, 0.0f), s[2]);
+            at.load(b, block + i * ldb);
+            if (a.gate_width > 1) at.load(g, gate + i * ldg);
+            else if (a.gate_width == 1) g[0] = to_f32(gate[i * ldg]);
+        }
+        if (dh) {
+            float hat[E], d[E];
+            at.load(hat, r + i * ldr);
+            at.load(d, dh + i * a.width);
+            const float inv = normalise(hat);
+            if (!L::kKeep) at.vector(qw, after(a.pre_weight), 1.0f);
+            float m[2] = {0.0f, 0.0f};
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                s3[e] = fmaf(d[e], hat[e], s3[e]);
+                s4[e] += d[e];
+                d[e] *= qw[e];
+                m[0] += d[e];
+                m[1] = fmaf(d[e], hat[e], m[1]);
+            }
+            at.sums(m, sh2, turn2);
+            const float m1 = a.layer ? m[0] * a.inv_width : 0.0f, m2 = m[1] * a.inv_width;
+#pragma unroll
+            for (int e = 0; e < E; ++e) t[e] = fmaf(inv, d[e] - m1 - hat[e] * m2, t[e]);
+        }
+        if (dx) at.store(dx + i * a.width, t);
+        if (block) {
+            const float inv = normalise(b);
+            if (!L::kKeep) post_vectors();
+            float m[3] = {0.0f, 0.0f, 0.0f};
+            if (a.gate_width == 1) g[0] = sigmoid(g[0]);
+            float du[E], dg[E];
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const float s = a.gate_width > 1 ? sigmoid(g[e]) : a.gate_width == 1 ? g[0] : 1.0f;
+                const float u = fmaf(b[e], pw[e], pb[e]), ts = t[e] * s;
+                s2[e] = fmaf(ts, u, s2[e]);
+                dg[e] = ts * sc[e] * u * (1.0f - s);
+                du[e] = ts * sc[e];
+                s0[e] = fmaf(du[e], b[e], s0[e]);
+                s1[e] += du[e];
+                du[e] *= pw[e];
+                m[0] += du[e];
+                m[1] = fmaf(du[e], b[e], m[1]);
+                m[2] += dg[e];
+            }
+            if (a.gate_width > 1) at.store(dgate + i * a.width, dg);
+            at.sums(m, sh3, turn3);
+            if (a.gate_width == 1 && at.lane == 0) dgate[i] = from_f32<T>(m[2]);
+            const float m1 = a.layer ? m[0] * a.inv_width : 0.0f, m2 = m[1] * a.inv_width;
+#pragma unroll
+            for (int e = 0; e < E; ++e) du[e] = inv * (du[e] - m1 - b[e] * m2);
+            at.store(dblock + i * a.width, du);
         }
     }
-    for (int q = 0; q < 5; ++q) part[((int64_t)blockIdx.x * 5 + q) * a.width + c] = s[q];
+    if (!part) return;
+    // the block's sums of each column, its groups in order: part[block][5][width]
+    auto write = [&](int q, const float (&s)[E]) {
+        float *to = part + ((int64_t)blockIdx.x * 5 + q) * a.width;
+        if constexpr (L::kGroups == 1) {
+#pragma unroll
+            for (int c = 0; c < CH; ++c)
+#pragma unroll
+                for (int j = 0; j < L::W; ++j)
+                    if (at.column(c) + j < a.width) to[at.column(c) + j] = s[c * L::W + j];
+        } else {
+            constexpr int kRow = G * E;
+#pragma unroll
+            for (int c = 0; c < CH; ++c)
+#pragma unroll
+                for (int j = 0; j < L::W; ++j) columns[at.group * kRow + at.column(c) + j] = s[c * L::W + j];
+            __syncthreads();
+            for (int c = threadIdx.x; c < a.width; c += L::kThreads) {
+                float v = 0.0f;
+#pragma unroll
+                for (int g = 0; g < L::kGroups; ++g) v += columns[g * kRow + c];
+                to[c] = v;
+            }
+            __syncthreads();
+        }
+    };
+    write(0, s0);
+    write(1, s1);
+    write(2, s2);
+    write(3, s3);
+    write(4, s4);
 }
 
-__global__ void k_norm_columns_sum(int width, int parts, const float *__restrict__ part, float *o0, float *o1, float *o2, float *o3,
-                                   float *o4) {
-    const int c = blockIdx.x * 64 + threadIdx.x, q = blockIdx.y;
-    float *o = q == 0 ? o0 : q == 1 ? o1 : q == 2 ? o2 : q == 3 ? o3 : o4;
-    if (c >= width || !o) return;
+// The blocks' sums of one vector's 16 columns: 64 threads a column take every 64th block, then their sums in order.
+struct Vectors {
+    float *v[5];
+};
+__global__ __launch_bounds__(1024) void k_norm_columns(int width, int parts, const float *__restrict__ part, Vectors out) {
+    __shared__ float sh[64][17];
+    const int c = blockIdx.x * 16 + (threadIdx.x & 15), slice = threadIdx.x >> 4;
+    float *o = out.v[blockIdx.y];
+    if (!o) return;
     float s = 0.0f;
-    for (int b = 0; b < parts; ++b) s += part[((int64_t)b * 5 + q) * width + c];
-    o[c] = s;
+    if (c < width)
+#pragma unroll 8
+        for (int b = slice; b < parts; b += 64) s += part[((int64_t)b * 5 + blockIdx.y) * width + c];
+    sh[slice][threadIdx.x & 15] = s;
+    __syncthreads();
+    if (slice == 0 && c < width) {
+        float v = 0.0f;
+#pragma unroll
+        for (int b = 0; b < 64; ++b) v += sh[b][threadIdx.x];
+        o[c] = v;
+    }
 }
 
 NormArgs args_of(const mpnn_norm &p, int64_t n, bool gate) {
-    return NormArgs{n, p.width, p.kind == MPNN_NORM_LAYER, gate ? p.gate_width : 0, (float)p.eps,
+    return NormArgs{n, p.width, p.kind == MPNN_NORM_LAYER, gate ? p.gate_width : 0, (float)p.eps, 1.0f / (float)p.width,
                     p.post_weight, p.post_bias, p.scale, p.pre_weight, p.pre_bias};
 }
 
-template <class T>
-Status forward_t(Context &cx, const mpnn_norm &p, int64_t n, const void *x, int64_t ldx, const void *block, int64_t ldb,
-                 const void *gate, int64_t ldg, void *r, void *h) {
-    k_norm_residual<T><<<grid_for(n, 4), 256, 0, cx.stream>>>(args_of(p, n, gate), (const T *)x, ldx, (const T *)block, ldb,
-                                                              (const T *)gate, ldg, (T *)r, (T *)h);
-    MPNN_HIP(hipGetLastError());
-    return Status::ok();
+// Lanes of a row: the fewest that hold it with 8 values a lane (two chunks of fp32, one of bf16), which leaves room for
+// the reverse pass's five sums a column in registers; 16 values for the widest rows, whose 1,024 lanes would leave only
+// 128 registers each.
+template <class F>
+Status by_width(int dtype, int width, F run) {
+#define MPNN_ROW(limit, lanes, chunks_f32, chunks_bf16)                                          \
+    if (width <= limit)                                                                          \
+        return dtype == MPNN_BF16 ? run(bf16{}, std::integral_constant<int, lanes>{}, std::integral_constant<int, chunks_bf16>{}) \
+                                  : run(float{}, std::integral_constant<int, lanes>{}, std::integral_constant<int, chunks_f32>{});
+    MPNN_ROW(64, 8, 2, 1)
+    MPNN_ROW(128, 16, 2, 1)
+    MPNN_ROW(256, 32, 2, 1)
+    MPNN_ROW(512, 64, 2, 1)
+    MPNN_ROW(1024, 128, 2, 1)
+    MPNN_ROW(2048, 256, 2, 1)
+    MPNN_ROW(4096, 512, 2, 1)
+    MPNN_ROW(8192, 512, 4, 2)
+#undef MPNN_ROW
+    return Status::err(MPNN_E_INVALID_ARG, "bad width");
 }
 
-template <class T>
-Status backward_t(Context &cx, const mpnn_norm &p, int64_t n, const void *dr, const void *dh, const void *r, int64_t ldr,
-                  const void *block, int64_t ldb, const void *gate, int64_t ldg, void *dx, void *dblock, void *dgate,
-                  float *const dvec[5]) {
-    const NormArgs a = args_of(p, n, gate);
-    const bool columns = dvec[0] || dvec[1] || dvec[2] || dvec[3] || dvec[4];
-    const int64_t rows = std::max<int64_t>(16, (n + 1023) / 1024);
-    const int64_t parts = (n + rows - 1) / rows;
-    float *stats = nullptr, *part = nullptr;
-    if (columns) {
-        MPNN_TRY(cx.grow(cx.rows_ws, sizeof(float) * (size_t)(n * kStats + parts * 5 * p.width)));
-        stats = cx.rows_ws.as<float>();
-        part = stats + n * kStats;
-    }
-    if (n > 0) {
-        k_norm_residual_back<T><<<grid_for(n, 4), 256, 0, cx.stream>>>(a, (const T *)dr, (const T *)dh, (const T *)r, ldr,
-                                                                       (const T *)block, ldb, (const T *)gate, ldg, (T *)dx,
-                                                                       (T *)dblock, (T *)dgate, stats);
-        MPNN_HIP(hipGetLastError());
-    }
-    if (columns) {
-        if (parts > 0) {
-            k_norm_columns<T><<<dim3((unsigned)parts, (p.width + 63) / 64), 64, 0, cx.stream>>>(
-                a, (const T *)dr, (const T *)dh, (const T *)r, ldr, (const T *)block, ldb, (const T *)gate, ldg, stats, rows, part);
-            MPNN_HIP(hipGetLastError());
-        }
-        k_norm_columns_sum<<<dim3((p.width + 63) / 64, 5), 64, 0, cx.stream>>>(p.width, (int)parts, part, dvec[0], dvec[1], dvec[2],
-                                                                              dvec[3], dvec[4]);
-        MPNN_HIP(hipGetLastError());
-    }
-    return Status::ok();
-}
+constexpr int64_t kForwardBlocks = 2048, kBackBlocks = 1024;
 
 }  // namespace
 
 Status norm_residual(Context &cx, const mpnn_norm &p, int64_t n, const void *x, int64_t ldx, const void *block, int64_t ldb,
                      const void *gate, int64_t ldg, void *r, void *h) {
     if (n == 0) return Status::ok();
-    return p.dtype == MPNN_BF16 ? forward_t<bf16>(cx, p, n, x, ldx, block, ldb, gate, ldg, r, h)
-                                : forward_t<float>(cx, p, n, x, ldx, block, ldb, gate, ldg, r, h);
+    return by_width(p.dtype, p.width, [&](auto type, auto lanes, auto chunks) -> Status {
+        using T = decltype(type);
+        using L = Lanes<T, lanes(), chunks()>;
+        const int64_t blocks = std::min<int64_t>((n + L::kGroups - 1) / L::kGroups, kForwardBlocks);
+        k_norm_residual<T, lanes(), chunks()><<<(unsigned)blocks, L::kThreads, 0, cx.stream>>>(
+            args_of(p, n, gate), (const T *)x, ldx, (const T *)block, ldb, (const T *)gate, ldg, (T *)r, (T *)h);
+        MPNN_HIP(hipGetLastError());
+        return Status::ok();
+    });
 }
 
 Status norm_residual_backward(Context &cx, const mpnn_norm &p, int64_t n, const void *dr, const void *dh, const void *r, int64_t ldr,
                               const void *block, int64_t ldb, const void *gate, int64_t ldg, void *dx, void *dblock, void *dgate,
                               float *const dvec[5]) {
-    return p.dtype == MPNN_BF16 ? backward_t<bf16>(cx, p, n, dr, dh, r, ldr, block, ldb, gate, ldg, dx, dblock, dgate, dvec)
-                                : backward_t<float>(cx, p, n, dr, dh, r, ldr, block, ldb, gate, ldg, dx, dblock, dgate, dvec);
+    return by_width(p.dtype, p.width, [&](auto type, auto lanes, auto chunks) -> Status {
+        using T = decltype(type);
+        using L = Lanes<T, lanes(), chunks()>;
+        const int64_t blocks = std::min<int64_t>((n + L::kGroups - 1) / L::kGroups, kBackBlocks * 256 / L::kThreads);
+        const bool columns = dvec[0] || dvec[1] || dvec[2] || dvec[3] || dvec[4];
+        if (columns) MPNN_TRY(cx.grow(cx.rows_ws, sizeof(float) * (size_t)(blocks * 5 * p.width)));
+        if (n > 0) {
+            k_norm_residual_back<T, lanes(), chunks()><<<(unsigned)blocks, L::kThreads, 0, cx.stream>>>(
+                args_of(p, n, gate), (const T *)dr, (const T *)dh, (const T *)r, ldr, (const T *)block, ldb, (const T *)gate, ldg,
+                (T *)dx, (T *)dblock, (T *)dgate, columns ? cx.rows_ws.as<float>() : nullptr);
+            MPNN_HIP(hipGetLastError());
+        }
+        if (columns) {
+            k_norm_columns<<<dim3((p.width + 15) / 16, 5), 1024, 0, cx.stream>>>(
+                p.width, (int)blocks, cx.rows_ws.as<float>(), Vectors{{dvec[0], dvec[1], dvec[2], dvec[3], dvec[4]}});
+            MPNN_HIP(hipGetLastError());
+        }
+        return Status::ok();
+    });
 }
 
 }  // namespace mpnn
