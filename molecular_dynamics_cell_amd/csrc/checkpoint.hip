@@ -22,64 +22,133 @@ __device__ __forceinline__ int scale_byte(float largest) {
     return min(max(e, kStepMin), kStepMax) + 127;
 }
 __device__ __forceinline__ float step_of(int byte) { return byte == 255 ? __uint_as_float(0x7fc00000u) : __uint_as_float((uint32_t)byte << 23); }
-__device__ __forceinline__ int code_of(float v, int byte) {
-    if (byte == 255) return 0;
-    const float q = rintf(v * __uint_as_float((uint32_t)(254 - byte) << 23));   // 2^-e
-    return (int)fminf(fmaxf(q, -127.0f), 127.0f);
-}
+// Lanes of a group: each holds one 16-byte chunk.
+template <class T> constexpr int kGroupLanes = kGroup / Chunk<T>::W;
 
-// largest magnitude of a group; a NaN counts as the largest
-__device__ __forceinline__ float group_max(float v) {
-    uint32_t u = __float_as_uint(v) & 0x7fffffffu;   // magnitudes order as integers, NaN above infinity
+// Largest magnitude of a group from its lanes' values.  Magnitudes order as integers, a NaN above infinity.
+template <class T> __device__ __forceinline__ float group_max(const float (&v)[Chunk<T>::W]) {
+    uint32_t u = 0;
 #pragma unroll
-    for (int d = 16; d >= 1; d >>= 1) u = max(u, (uint32_t)__shfl_xor((int)u, d));
-    return __uint_as_float(u);
+    for (int j = 0; j < Chunk<T>::W; ++j) u = max(u, __float_as_uint(v[j]) & 0x7fffffffu);
+    float f = __uint_as_float(u);
+    auto step = [&](float o) { f = __uint_as_float(max(__float_as_uint(f), __float_as_uint(o))); };
+    step(dpp<0xb1>(f));
+    step(dpp<0x4e>(f));
+    if (kGroupLanes<T> == 8) step(dpp<0x141>(f));
+    return f;
 }
 
-// One lane per channel, 32 lanes per group.
+// The codes of one chunk and, by the group's first lane, the scale.
+template <class T>
+__device__ __forceinline__ void save_chunk(const float (&v)[Chunk<T>::W], int in, int8_t *codes, uint8_t *scale, bool first) {
+    constexpr int W = Chunk<T>::W;
+    const int b = scale_byte(group_max<T>(v));
+    const float to = b == 255 ? 0.0f : __uint_as_float((uint32_t)(254 - b) << 23);   // 2^-e
+    int8_t q[W];
+#pragma unroll
+    for (int j = 0; j < W; ++j) {
+        // the clamp's order sends NaN (0 times an infinity, or a NaN) to -127; such a group's codes are not used, but defined
+        const float r = fminf(fmaxf(rintf(v[j] * to), -127.0f), 127.0f);
+        q[j] = b == 255 ? 0 : (int8_t)(int)r;
+    }
+    if (in >= W) {
+        __builtin_memcpy(codes, q, W);
+    } else {
+#pragma unroll
+        for (int j = 0; j < W; ++j)
+            if (j < in) codes[j] = q[j];
+    }
+    if (first) *scale = (uint8_t)b;
+}
+
+// A lane per chunk of a whole number of groups (chunks past the row's end hold zeros), kUnroll chunks in flight.
 template <class T, bool SILU>
-__global__ void k_checkpoint_save(int64_t items, int groups, int width, const T *__restrict__ z, int64_t ld, T *__restrict__ y,
-                                  int8_t *__restrict__ codes, uint8_t *__restrict__ scales, int8_t *__restrict__ ycodes,
-                                  uint8_t *__restrict__ yscales) {
-    const int64_t g = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-    if (g >= items) return;
-    const int64_t i = g / groups;
-    const int c = (int)(g - i * groups) * kGroup + (threadIdx.x & 31);
-    const bool in = c < width;
-    const float v = in ? to_f32(z[i * ld + c]) : 0.0f;
-    int b = scale_byte(group_max(v));
-    if (in) codes[i * width + c] = (int8_t)code_of(v, b);
-    if ((threadIdx.x & 31) == 0) scales[g] = (uint8_t)b;
-    if (SILU) {
-        const float o = v / (1.0f + expf(-v));
-        if (in) y[i * width + c] = from_f32<T>(o);
-        if (ycodes) {
-            b = scale_byte(group_max(o));
-            if (in) ycodes[i * width + c] = (int8_t)code_of(o, b);
-            if ((threadIdx.x & 31) == 0) yscales[g] = (uint8_t)b;
+__global__ __launch_bounds__(256) void k_checkpoint_save(Items it, int groups, int width, const T *__restrict__ z, int64_t ld,
+                                                         T *__restrict__ y, int8_t *__restrict__ codes, uint8_t *__restrict__ scales,
+                                                         int8_t *__restrict__ ycodes, uint8_t *__restrict__ yscales) {
+    constexpr int W = Chunk<T>::W, L = kGroupLanes<T>;
+    int64_t row[kUnroll];
+    int c[kUnroll];
+    bool in[kUnroll];
+    Chunk<T> v[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+        in[u] = item_at(it, u, row[u], c[u]);
+        const int left = in[u] ? width - c[u] * W : 0;
+        if (left > 0) v[u] = load_chunk(z + row[u] * ld + c[u] * W, left);
+        else __builtin_memset(&v[u], 0, sizeof v[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+        if (!in[u]) continue;      // a group's lanes go together
+        const int left = width - c[u] * W;
+        const int64_t at = row[u] * width + c[u] * W, g = row[u] * groups + c[u] / L;
+        float f[W];
+#pragma unroll
+        for (int j = 0; j < W; ++j) f[j] = to_f32(v[u].v[j]);
+        save_chunk<T>(f, left, codes + at, scales + g, c[u] % L == 0);
+        if (SILU) {
+            Chunk<T> o;
+#pragma unroll
+            for (int j = 0; j < W; ++j) {
+                f[j] = f[j] / (1.0f + expf(-f[j]));
+                o.v[j] = from_f32<T>(f[j]);
+            }
+            if (left > 0) store_chunk(y + at, o, left);
+            if (ycodes) save_chunk<T>(f, left, ycodes + at, yscales + g, c[u] % L == 0);
         }
     }
 }
 
+// The values of one chunk of a checkpoint.
 template <class T>
-__global__ void k_checkpoint_load(int64_t n, int groups, int width, const int8_t *__restrict__ codes, const uint8_t *__restrict__ scales,
-                                  T *__restrict__ out) {
-    const int64_t i = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    if (i >= n) return;
-    for (int c = threadIdx.x & 63; c < width; c += 64)
-        out[i * width + c] = from_f32<T>((float)codes[i * width + c] * step_of(scales[i * groups + c / kGroup]));
+__device__ __forceinline__ void held_chunk(const int8_t *codes, const uint8_t *scale, int left, float (&z)[Chunk<T>::W]) {
+    constexpr int W = Chunk<T>::W;
+    int8_t q[W];
+    if (left >= W) {
+        __builtin_memcpy(q, codes, W);
+    } else {
+#pragma unroll
+        for (int j = 0; j < W; ++j) q[j] = j < left ? codes[j] : (int8_t)0;
+    }
+    const float step = step_of(*scale);
+#pragma unroll
+    for (int j = 0; j < W; ++j) z[j] = (float)q[j] * step;
 }
 
-// dz = dy s (1 + z (1 - s)), s = sigma(z), for the z that the checkpoint holds
-template <class T>
-__global__ void k_checkpoint_silu_back(int64_t n, int groups, int width, const T *__restrict__ dy, int64_t ld,
-                                       const int8_t *__restrict__ codes, const uint8_t *__restrict__ scales, T *__restrict__ dz) {
-    const int64_t i = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    if (i >= n) return;
-    for (int c = threadIdx.x & 63; c < width; c += 64) {
-        const float z = (float)codes[i * width + c] * step_of(scales[i * groups + c / kGroup]);
-        const float s = 1.0f / (1.0f + expf(-z));
-        dz[i * width + c] = from_f32<T>(to_f32(dy[i * ld + c]) * s * fmaf(z, 1.0f - s, 1.0f));
+// out = the held values, or with dy the gradient dz = dy s (1 + z (1 - s)), s = sigma(z), at the held z
+template <class T, bool BACK>
+__global__ __launch_bounds__(256) void k_checkpoint_use(Items it, int groups, int width, const T *__restrict__ dy, int64_t ld,
+                                                        const int8_t *__restrict__ codes, const uint8_t *__restrict__ scales,
+                                                        T *__restrict__ out) {
+    constexpr int W = Chunk<T>::W, L = kGroupLanes<T>;
+    int64_t row[kUnroll];
+    int c[kUnroll];
+    bool in[kUnroll];
+    Chunk<T> d[kUnroll];
+    float z[kUnroll][W];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+        in[u] = item_at(it, u, row[u], c[u]);
+        if (!in[u]) continue;
+        const int left = width - c[u] * W;
+        if (BACK) d[u] = load_chunk(dy + row[u] * ld + c[u] * W, left);
+        held_chunk<T>(codes + row[u] * width + c[u] * W, scales + row[u] * groups + c[u] / L, left, z[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+        if (!in[u]) continue;
+        Chunk<T> o;
+#pragma unroll
+        for (int j = 0; j < W; ++j) {
+            float v = z[u][j];
+            if (BACK) {
+                const float s = __builtin_amdgcn_rcpf(1.0f + expf(-v));
+                v = to_f32(d[u].v[j]) * s * fmaf(v, 1.0f - s, 1.0f);
+            }
+            o.v[j] = from_f32<T>(v);
+        }
+        store_chunk(out + row[u] * width + c[u] * W, o, width - c[u] * W);
     }
 }
 
@@ -89,13 +158,9 @@ template <class T>
 static Status save_t(Context &cx, bool silu, int64_t n, int width, const void *z, int64_t ld, void *y, int8_t *codes, uint8_t *scales,
                      int8_t *ycodes, uint8_t *yscales) {
     const int groups = (width + kGroup - 1) / kGroup;
-    const int64_t items = n * groups;
-    if (silu)
-        k_checkpoint_save<T, true><<<grid_for(items, 8), 256, 0, cx.stream>>>(items, groups, width, (const T *)z, ld, (T *)y, codes,
-                                                                              scales, ycodes, yscales);
-    else
-        k_checkpoint_save<T, false><<<grid_for(items, 8), 256, 0, cx.stream>>>(items, groups, width, (const T *)z, ld, nullptr, codes,
-                                                                               scales, nullptr, nullptr);
+    const Items it = items_of(n, groups * kGroupLanes<T>);
+    auto *kernel = silu ? k_checkpoint_save<T, true> : k_checkpoint_save<T, false>;
+    kernel<<<grid_of(it), 256, 0, cx.stream>>>(it, groups, width, (const T *)z, ld, (T *)y, codes, scales, ycodes, yscales);
     MPNN_HIP(hipGetLastError());
     return Status::ok();
 }
@@ -107,29 +172,27 @@ Status checkpoint_save(Context &cx, int dtype, bool silu, int64_t n, int width, 
                               : save_t<float>(cx, silu, n, width, z, ld, y, codes, scales, ycodes, yscales);
 }
 
-Status checkpoint_load(Context &cx, int dtype, int64_t n, int width, const int8_t *codes, const uint8_t *scales, void *out) {
-    if (n == 0) return Status::ok();
-    const int groups = (width + kGroup - 1) / kGroup;
-    if (dtype == MPNN_BF16)
-        k_checkpoint_load<bf16><<<grid_for(n, 4), 256, 0, cx.stream>>>(n, groups, width, codes, scales, (bf16 *)out);
-    else
-        k_checkpoint_load<float><<<grid_for(n, 4), 256, 0, cx.stream>>>(n, groups, width, codes, scales, (float *)out);
+template <class T, bool BACK>
+static Status use_t(Context &cx, int64_t n, int width, const void *dy, int64_t ld, const int8_t *codes, const uint8_t *scales,
+                    void *out) {
+    const Items it = items_of(n, (width + Chunk<T>::W - 1) / Chunk<T>::W);
+    k_checkpoint_use<T, BACK><<<grid_of(it), 256, 0, cx.stream>>>(it, (width + kGroup - 1) / kGroup, width, (const T *)dy, ld, codes,
+                                                                  scales, (T *)out);
     MPNN_HIP(hipGetLastError());
     return Status::ok();
+}
+
+Status checkpoint_load(Context &cx, int dtype, int64_t n, int width, const int8_t *codes, const uint8_t *scales, void *out) {
+    if (n == 0) return Status::ok();
+    return dtype == MPNN_BF16 ? use_t<bf16, false>(cx, n, width, nullptr, 0, codes, scales, out)
+                              : use_t<float, false>(cx, n, width, nullptr, 0, codes, scales, out);
 }
 
 Status checkpoint_silu_backward(Context &cx, int dtype, int64_t n, int width, const void *dy, int64_t ld, const int8_t *codes,
                                 const uint8_t *scales, void *dz) {
     if (n == 0) return Status::ok();
-    const int groups = (width + kGroup - 1) / kGroup;
-    if (dtype == MPNN_BF16)
-        k_checkpoint_silu_back<bf16><<<grid_for(n, 4), 256, 0, cx.stream>>>(n, groups, width, (const bf16 *)dy, ld, codes, scales,
-                                                                            (bf16 *)dz);
-    else
-        k_checkpoint_silu_back<float><<<grid_for(n, 4), 256, 0, cx.stream>>>(n, groups, width, (const float *)dy, ld, codes, scales,
-                                                                             (float *)dz);
-    MPNN_HIP(hipGetLastError());
-    return Status::ok();
+    return dtype == MPNN_BF16 ? use_t<bf16, true>(cx, n, width, dy, ld, codes, scales, dz)
+                              : use_t<float, true>(cx, n, width, dy, ld, codes, scales, dz);
 }
 
 }  // namespace mpnn
