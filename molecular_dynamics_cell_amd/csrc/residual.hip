@@ -27,7 +27,9 @@ struct NormArgs {
     const float *post_weight, *post_bias, *scale, *pre_weight, *pre_bias;
 };
 
-__device__ __forceinline__ float sigmoid(float g) { return __builtin_amdgcn_rcpf(1.0f + expf(-g)); }
+// 1 / (1 + 2^(-g log2 e)).  The exponent's rounding is off by |g| 2^-24 relative, which s (1 - s) |g| < 0.23 keeps
+// below half an ulp of 1 in the result; infinities and NaN come out as the formula has them.
+__device__ __forceinline__ float sigmoid(float g) { return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504f * g)); }
 
 // A row's place in the block's registers.
 template <class T, int G, int CH>
@@ -37,20 +39,32 @@ struct Lanes {
     static constexpr int kWaves = G / 64;                  // waves of a row (0: part of one)
     int lane, group;
     int width;
-    __device__ __forceinline__ Lanes(int w) : lane(threadIdx.x % G), group(threadIdx.x / G), width(w) {}
+    bool whole;            // a row is whole chunks: each is all inside it or all outside
+    __device__ __forceinline__ Lanes(int w) : lane(threadIdx.x % G), group(threadIdx.x / G), width(w), whole(w % W == 0) {}
     __device__ __forceinline__ int column(int c) const { return (c * G + lane) * W; }
-    __device__ __forceinline__ void load(float (&v)[E], const T *row) const {
+    // A row as it is in memory; zeros past its end.
+    struct Raw {
+        Chunk<T> c[CH];
+    };
+    __device__ __forceinline__ void fetch(Raw &t, const T *row) const {
+        __builtin_memset(&t, 0, sizeof t);
+        if (whole) {
 #pragma unroll
-        for (int c = 0; c < CH; ++c) {
-            Chunk<T> t;
-            const int left = width - column(c);
-            if (left > 0) t = load_chunk(row + column(c), left);
-            else
+            for (int c = 0; c < CH; ++c)
+                if (column(c) < width) t.c[c] = load_chunk(row + column(c));
+        } else {
 #pragma unroll
-                for (int j = 0; j < W; ++j) t.v[j] = from_f32<T>(0.0f);
-#pragma unroll
-            for (int j = 0; j < W; ++j) v[c * W + j] = to_f32(t.v[j]);
+            for (int c = 0; c < CH; ++c) {
+                const int left = width - column(c);
+                if (left > 0) t.c[c] = load_chunk(row + column(c), left);
+            }
         }
+    }
+    __device__ __forceinline__ void values(float (&v)[E], const Raw &t) const {
+#pragma unroll
+        for (int c = 0; c < CH; ++c)
+#pragma unroll
+            for (int j = 0; j < W; ++j) v[c * W + j] = to_f32(t.c[c].v[j]);
     }
     __device__ __forceinline__ void store(T *row, const float (&v)[E]) const {
 #pragma unroll
@@ -59,12 +73,16 @@ struct Lanes {
 #pragma unroll
             for (int j = 0; j < W; ++j) t.v[j] = from_f32<T>(v[c * W + j]);
             const int left = width - column(c);
-            if (left > 0) store_chunk(row + column(c), t, left);
+            if (whole) {
+                if (left > 0) store_chunk(row + column(c), t);
+            } else {
+                if (left > 0) store_chunk(row + column(c), t, left);
+            }
         }
     }
     // Wide rows: the vectors are read again for each row, from the caches, where the registers do not hold them beside
     // the sums.  The offset is zero, but not to the compiler, which would move the loads out of the loop.
-    static constexpr bool kKeep = E <= 8;
+    static constexpr bool kKeep = E <= 12;
     __device__ __forceinline__ static int again() {
         int z = 0;
         if (!kKeep) asm volatile("" : "+s"(z));
@@ -73,12 +91,19 @@ struct Lanes {
     // a vector's values of this lane's columns; zeros past the width
     __device__ __forceinline__ void vector(float (&v)[E], const float *p, float otherwise) const {
 #pragma unroll
-        for (int c = 0; c < CH; ++c)
+        for (int e = 0; e < E; ++e) v[e] = p ? 0.0f : column(e / W) + e % W < width ? otherwise : 0.0f;
+        if (!p) return;
+        if (whole) {
 #pragma unroll
-            for (int j = 0; j < W; ++j) {
-                const int at = column(c) + j;
-                v[c * W + j] = at < width ? (p ? p[at] : otherwise) : 0.0f;
-            }
+            for (int c = 0; c < CH; ++c)
+                if (column(c) < width) __builtin_memcpy(&v[c * W], p + column(c), W * sizeof(float));
+        } else {
+#pragma unroll
+            for (int c = 0; c < CH; ++c)
+#pragma unroll
+                for (int j = 0; j < W; ++j)
+                    if (column(c) + j < width) v[c * W + j] = p[column(c) + j];
+        }
     }
     // sums over the row's lanes, the same bits in each
     template <int N, int M> __device__ __forceinline__ void sums(float (&s)[N], float (&sh)[2][M], int &turn) const {
@@ -107,9 +132,18 @@ struct Lanes {
     // v becomes its distance from m (0 past the width)
     __device__ __forceinline__ void centre(float (&v)[E], float m) const {
 #pragma unroll
-        for (int c = 0; c < CH; ++c)
+        for (int c = 0; c < CH; ++c) {
+            const float mc = column(c) < width ? m : 0.0f;      // a chunk outside holds zeros
 #pragma unroll
-            for (int j = 0; j < W; ++j) v[c * W + j] = column(c) + j < width ? v[c * W + j] - m : 0.0f;
+            for (int j = 0; j < W; ++j) v[c * W + j] -= mc;
+        }
+        if (!whole) {
+#pragma unroll
+            for (int c = 0; c < CH; ++c)
+#pragma unroll
+                for (int j = 0; j < W; ++j)
+                    if (column(c) + j >= width) v[c * W + j] = 0.0f;
+        }
     }
 };
 
@@ -165,14 +199,30 @@ __global__ __launch_bounds__((Lanes<T, G, CH>::kThreads)) void k_norm_residual(N
 #pragma unroll
         for (int e = 0; e < E; ++e) v[e] *= inv;
     };
-    for (int64_t i = (int64_t)blockIdx.x * L::kGroups + at.group; i < a.n; i += (int64_t)gridDim.x * L::kGroups) {
-        float v[E];
-        at.load(v, x + i * ldx);
+    // the next row's loads are under way while a row is worked on
+    typename L::Raw rx, rb, rg;
+    T row_gate{};
+    auto fetch = [&](int64_t i) {
+        at.fetch(rx, x + i * ldx);
         if (block) {
-            float b[E], g[E];
-            at.load(b, block + i * ldb);
-            if (a.gate_width > 1) at.load(g, gate + i * ldg);
-            else if (a.gate_width == 1) g[0] = to_f32(gate[i * ldg]);
+            at.fetch(rb, block + i * ldb);
+            if (a.gate_width > 1) at.fetch(rg, gate + i * ldg);
+            else if (a.gate_width == 1) row_gate = gate[i * ldg];
+        }
+    };
+    const int64_t stride = (int64_t)gridDim.x * L::kGroups;
+    int64_t i = (int64_t)blockIdx.x * L::kGroups + at.group;
+    if (i < a.n) fetch(i);
+    for (; i < a.n; i += stride) {
+        float v[E], b[E], g[E];
+        at.values(v, rx);
+        if (block) {
+            at.values(b, rb);
+            if (a.gate_width > 1) at.values(g, rg);
+            else g[0] = to_f32(row_gate);
+        }
+        if (i + stride < a.n) fetch(i + stride);
+        if (block) {
             normalise(b);
             if (a.gate_width > 1) {
 #pragma unroll
@@ -238,22 +288,42 @@ __global__ __launch_bounds__((Lanes<T, G, CH>::kThreads)) void k_norm_residual_b
         for (int e = 0; e < E; ++e) v[e] *= inv;
         return inv;
     };
-    for (int64_t i = (int64_t)blockIdx.x * L::kGroups + at.group; i < a.n; i += (int64_t)gridDim.x * L::kGroups) {
+    // the next row's loads are under way while a row is worked on
+    typename L::Raw rdr, rdh, rr, rb, rg;
+    T row_gate{};
+    auto fetch_pre = [&](int64_t i) {
+        if (dr) at.fetch(rdr, dr + i * a.width);
+        if (dh) {
+            at.fetch(rr, r + i * ldr);
+            at.fetch(rdh, dh + i * a.width);
+        }
+    };
+    auto fetch_post = [&](int64_t i) {
+        if (!block) return;
+        at.fetch(rb, block + i * ldb);
+        if (a.gate_width > 1) at.fetch(rg, gate + i * ldg);
+        else if (a.gate_width == 1) row_gate = gate[i * ldg];
+    };
+    constexpr bool kAhead = L::kKeep;      // the widest rows have no registers for it
+    const int64_t stride = (int64_t)gridDim.x * L::kGroups;
+    int64_t i = (int64_t)blockIdx.x * L::kGroups + at.group;
+    if (kAhead && i < a.n) {
+        fetch_pre(i);
+        fetch_post(i);
+    }
+    for (; i < a.n; i += stride) {
+        const int64_t next = i + stride;
+        if (!kAhead) fetch_pre(i);
         float t[E];
-        if (dr) at.load(t, dr + i * a.width);
+        if (dr) at.values(t, rdr);
         else
 #pragma unroll
             for (int e = 0; e < E; ++e) t[e] = 0.0f;
-        float b[E], g[E];
-        if (block) {
-            at.load(b, block + i * ldb);
-            if (a.gate_width > 1) at.load(g, gate + i * ldg);
-            else if (a.gate_width == 1) g[0] = to_f32(gate[i * ldg]);
-        }
         if (dh) {
             float hat[E], d[E];
-            at.load(hat, r + i * ldr);
-            at.load(d, dh + i * a.width);
+            at.values(hat, rr);
+            at.values(d, rdh);
+            if (kAhead && next < a.n) fetch_pre(next);
             const float inv = normalise(hat);
             if (!L::kKeep) at.vector(qw, after(a.pre_weight), 1.0f);
             float m[2] = {0.0f, 0.0f};
@@ -270,8 +340,15 @@ __global__ __launch_bounds__((Lanes<T, G, CH>::kThreads)) void k_norm_residual_b
 #pragma unroll
             for (int e = 0; e < E; ++e) t[e] = fmaf(inv, d[e] - m1 - hat[e] * m2, t[e]);
         }
+        if (!dh && kAhead && next < a.n) fetch_pre(next);
         if (dx) at.store(dx + i * a.width, t);
         if (block) {
+            if (!kAhead) fetch_post(i);
+            float b[E], g[E];
+            at.values(b, rb);
+            if (a.gate_width > 1) at.values(g, rg);
+            else g[0] = to_f32(row_gate);
+            if (kAhead && next < a.n) fetch_post(next);
             const float inv = normalise(b);
             if (!L::kKeep) post_vectors();
             float m[3] = {0.0f, 0.0f, 0.0f};
@@ -361,23 +438,38 @@ NormArgs args_of(const mpnn_norm &p, int64_t n, bool gate) {
                     p.post_weight, p.post_bias, p.scale, p.pre_weight, p.pre_bias};
 }
 
-// Lanes of a row: the fewest that hold it with 8 values a lane (two chunks of fp32, one of bf16), which leaves room for
+// Lanes of a row and chunks of a lane: the fewest slots that hold the row's chunks (312 fp32 values are 78 chunks: 32
+// lanes of 3 waste 18 of 96 slots, 64 lanes of 2 would waste 50 of 128), up to 12 values a lane, which leaves room for
 // the reverse pass's five sums a column in registers; 16 values for the widest rows, whose 1,024 lanes would leave only
 // 128 registers each.
 template <class F>
 Status by_width(int dtype, int width, F run) {
-#define MPNN_ROW(limit, lanes, chunks_f32, chunks_bf16)                                          \
-    if (width <= limit)                                                                          \
-        return dtype == MPNN_BF16 ? run(bf16{}, std::integral_constant<int, lanes>{}, std::integral_constant<int, chunks_bf16>{}) \
-                                  : run(float{}, std::integral_constant<int, lanes>{}, std::integral_constant<int, chunks_f32>{});
-    MPNN_ROW(64, 8, 2, 1)
-    MPNN_ROW(128, 16, 2, 1)
-    MPNN_ROW(256, 32, 2, 1)
-    MPNN_ROW(512, 64, 2, 1)
-    MPNN_ROW(1024, 128, 2, 1)
-    MPNN_ROW(2048, 256, 2, 1)
-    MPNN_ROW(4096, 512, 2, 1)
-    MPNN_ROW(8192, 512, 4, 2)
+#define MPNN_ROW(type, limit, lanes, chunks) \
+    if (width <= limit) return run(type{}, std::integral_constant<int, lanes>{}, std::integral_constant<int, chunks>{});
+    if (dtype == MPNN_BF16) {
+        MPNN_ROW(bf16, 64, 8, 1)
+        MPNN_ROW(bf16, 128, 16, 1)
+        MPNN_ROW(bf16, 256, 32, 1)
+        MPNN_ROW(bf16, 512, 64, 1)
+        MPNN_ROW(bf16, 1024, 128, 1)
+        MPNN_ROW(bf16, 2048, 256, 1)
+        MPNN_ROW(bf16, 4096, 512, 1)
+        MPNN_ROW(bf16, 8192, 512, 2)
+    } else {
+        MPNN_ROW(float, 32, 8, 1)
+        MPNN_ROW(float, 64, 8, 2)
+        MPNN_ROW(float, 96, 8, 3)
+        MPNN_ROW(float, 128, 16, 2)
+        MPNN_ROW(float, 192, 16, 3)
+        MPNN_ROW(float, 256, 32, 2)
+        MPNN_ROW(float, 384, 32, 3)
+        MPNN_ROW(float, 512, 64, 2)
+        MPNN_ROW(float, 768, 64, 3)
+        MPNN_ROW(float, 1024, 128, 2)
+        MPNN_ROW(float, 2048, 256, 2)
+        MPNN_ROW(float, 4096, 512, 2)
+        MPNN_ROW(float, 8192, 512, 4)
+    }
 #undef MPNN_ROW
     return Status::err(MPNN_E_INVALID_ARG, "bad width");
 }
