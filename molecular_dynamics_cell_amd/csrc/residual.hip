@@ -80,14 +80,6 @@ struct Lanes {
             }
         }
     }
-    // Wide rows: the vectors are read again for each row, from the caches, where the registers do not hold them beside
-    // the sums.  The offset is zero, but not to the compiler, which would move the loads out of the loop.
-    static constexpr bool kKeep = E <= 12;
-    __device__ __forceinline__ static int again() {
-        int z = 0;
-        if (!kKeep) asm volatile("" : "+s"(z));
-        return z;
-    }
     // a vector's values of this lane's columns; zeros past the width
     __device__ __forceinline__ void vector(float (&v)[E], const float *p, float otherwise) const {
 #pragma unroll
@@ -104,6 +96,23 @@ struct Lanes {
                 for (int j = 0; j < W; ++j)
                     if (column(c) + j < width) v[c * W + j] = p[column(c) + j];
         }
+    }
+    // The reverse pass keeps its vectors in LDS (zeros past the width), whose registers its sums need.  The offset is
+    // zero, but not to the compiler, which would move the reads out of the row loop, into registers.
+    static constexpr int kSlots = G * E;
+    __device__ __forceinline__ void keep(float *sh, const float *p, float otherwise) const {
+        for (int c = threadIdx.x; c < kSlots; c += kThreads) sh[c] = c < width ? (p ? p[c] : otherwise) : 0.0f;
+    }
+    __device__ __forceinline__ void kept(float (&v)[E], const float *sh) const {
+        int z = 0;
+        asm volatile("" : "+v"(z));
+#pragma unroll
+        for (int c = 0; c < CH; ++c)
+#pragma unroll
+            for (int j = 0; j < W; j += 4) {
+                const float4 t = *reinterpret_cast<const float4 *>(sh + column(c) + j + z);
+                v[c * W + j] = t.x; v[c * W + j + 1] = t.y; v[c * W + j + 2] = t.z; v[c * W + j + 3] = t.w;
+            }
     }
     // sums over the row's lanes, the same bits in each
     template <int N, int M> __device__ __forceinline__ void sums(float (&s)[N], float (&sh)[2][M], int &turn) const {
@@ -248,6 +257,11 @@ __global__ __launch_bounds__((Lanes<T, G, CH>::kThreads)) void k_norm_residual(N
 //   N'(d) = inv (a - mean(a) - hat mean(a hat)), a = d weight   (rms: without mean(a))
 // and of the vectors, summed over the group's rows:
 //   post weight: du hat_b, post bias: du, scale: total sigma(gate) u, pre weight: dh hat_r, pre bias: dh
+// The first three are combinations of two sums, of total sigma hat_b (P) and of total sigma (Q), by the column's own
+// values: scale P, scale Q and weight P + bias Q.
+#ifndef AHEAD
+#define AHEAD true
+#endif
 template <class T, int G, int CH>
 __global__ __launch_bounds__((Lanes<T, G, CH>::kThreads)) void k_norm_residual_back(NormArgs a, const T *dr, const T *__restrict__ dh,
                                                                                   const T *__restrict__ r, int64_t ldr,
@@ -262,18 +276,14 @@ __global__ __launch_bounds__((Lanes<T, G, CH>::kThreads)) void k_norm_residual_b
     __shared__ float columns[L::kGroups > 1 ? L::kGroups * G * E : 1];
     int turn1 = 0, turn2 = 0, turn3 = 0;
     const L at(a.width);
-    float pw[E], pb[E], sc[E], qw[E];
-    auto after = [&](const float *p) { return p ? p + L::again() : p; };
-    auto post_vectors = [&]() {
-        at.vector(pw, after(a.post_weight), 1.0f);
-        at.vector(pb, after(a.post_bias), 0.0f);
-        at.vector(sc, after(a.scale), 1.0f);
-    };
-    if (L::kKeep) {
-        post_vectors();
-        at.vector(qw, a.pre_weight, 1.0f);
-    }
-    float s0[E] = {}, s1[E] = {}, s2[E] = {}, s3[E] = {}, s4[E] = {};
+    __shared__ __attribute__((aligned(16))) float vectors[4][L::kSlots];
+    at.keep(vectors[0], a.post_weight, 1.0f);
+    at.keep(vectors[1], a.post_bias, 0.0f);
+    at.keep(vectors[2], a.scale, 1.0f);
+    at.keep(vectors[3], a.pre_weight, 1.0f);
+    __syncthreads();
+    // sums over the group's rows: total sigma hat_b, total sigma, dh hat_r, dh
+    float s0[E] = {}, s1[E] = {}, s3[E] = {}, s4[E] = {};
     // v becomes its normed values; returns one over the root
     auto normalise = [&](float (&v)[E]) {
         if (a.layer) {
@@ -304,7 +314,7 @@ __global__ __launch_bounds__((Lanes<T, G, CH>::kThreads)) void k_norm_residual_b
         if (a.gate_width > 1) at.fetch(rg, gate + i * ldg);
         else if (a.gate_width == 1) row_gate = gate[i * ldg];
     };
-    constexpr bool kAhead = L::kKeep;      // the widest rows have no registers for it
+    constexpr bool kAhead = AHEAD;
     const int64_t stride = (int64_t)gridDim.x * L::kGroups;
     int64_t i = (int64_t)blockIdx.x * L::kGroups + at.group;
     if (kAhead && i < a.n) {
@@ -325,7 +335,8 @@ __global__ __launch_bounds__((Lanes<T, G, CH>::kThreads)) void k_norm_residual_b
             at.values(d, rdh);
             if (kAhead && next < a.n) fetch_pre(next);
             const float inv = normalise(hat);
-            if (!L::kKeep) at.vector(qw, after(a.pre_weight), 1.0f);
+            float qw[E];
+            at.kept(qw, vectors[3]);
             float m[2] = {0.0f, 0.0f};
 #pragma unroll
             for (int e = 0; e < E; ++e) {
@@ -350,19 +361,21 @@ __global__ __launch_bounds__((Lanes<T, G, CH>::kThreads)) void k_norm_residual_b
             else g[0] = to_f32(row_gate);
             if (kAhead && next < a.n) fetch_post(next);
             const float inv = normalise(b);
-            if (!L::kKeep) post_vectors();
+            float pw[E], pb[E], sc[E];
+            at.kept(pw, vectors[0]);
+            at.kept(pb, vectors[1]);
+            at.kept(sc, vectors[2]);
             float m[3] = {0.0f, 0.0f, 0.0f};
             if (a.gate_width == 1) g[0] = sigmoid(g[0]);
             float du[E], dg[E];
 #pragma unroll
             for (int e = 0; e < E; ++e) {
                 const float s = a.gate_width > 1 ? sigmoid(g[e]) : a.gate_width == 1 ? g[0] : 1.0f;
-                const float u = fmaf(b[e], pw[e], pb[e]), ts = t[e] * s;
-                s2[e] = fmaf(ts, u, s2[e]);
-                dg[e] = ts * sc[e] * u * (1.0f - s);
+                const float ts = t[e] * s;
+                s0[e] = fmaf(ts, b[e], s0[e]);
+                s1[e] += ts;
                 du[e] = ts * sc[e];
-                s0[e] = fmaf(du[e], b[e], s0[e]);
-                s1[e] += du[e];
+                dg[e] = du[e] * fmaf(b[e], pw[e], pb[e]) * (1.0f - s);
                 du[e] *= pw[e];
                 m[0] += du[e];
                 m[1] = fmaf(du[e], b[e], m[1]);
@@ -378,9 +391,9 @@ __global__ __launch_bounds__((Lanes<T, G, CH>::kThreads)) void k_norm_residual_b
         }
     }
     if (!part) return;
-    // the block's sums of each column, its groups in order: part[block][5][width]
+    // the block's sums of each column, its groups in order: part[block][4][width]
     auto write = [&](int q, const float (&s)[E]) {
-        float *to = part + ((int64_t)blockIdx.x * 5 + q) * a.width;
+        float *to = part + ((int64_t)blockIdx.x * 4 + q) * a.width;
         if constexpr (L::kGroups == 1) {
 #pragma unroll
             for (int c = 0; c < CH; ++c)
@@ -405,31 +418,44 @@ __global__ __launch_bounds__((Lanes<T, G, CH>::kThreads)) void k_norm_residual_b
     };
     write(0, s0);
     write(1, s1);
-    write(2, s2);
-    write(3, s3);
-    write(4, s4);
+    write(2, s3);
+    write(3, s4);
 }
 
-// The blocks' sums of one vector's 16 columns: 64 threads a column take every 64th block, then their sums in order.
+// The blocks' sums of 16 columns (blockIdx.y 0: P and Q, 1: the pre norm's two): 64 threads a column take every 64th
+// block, then their sums in order.
 struct Vectors {
     float *v[5];
 };
-__global__ __launch_bounds__(1024) void k_norm_columns(int width, int parts, const float *__restrict__ part, Vectors out) {
-    __shared__ float sh[64][17];
+__global__ __launch_bounds__(1024) void k_norm_columns(NormArgs a, int parts, const float *__restrict__ part, Vectors out) {
+    __shared__ float sh[2][64][17];
     const int c = blockIdx.x * 16 + (threadIdx.x & 15), slice = threadIdx.x >> 4;
-    float *o = out.v[blockIdx.y];
-    if (!o) return;
-    float s = 0.0f;
-    if (c < width)
+    float s[2] = {};
+    if (c < a.width)
 #pragma unroll 8
-        for (int b = slice; b < parts; b += 64) s += part[((int64_t)b * 5 + blockIdx.y) * width + c];
-    sh[slice][threadIdx.x & 15] = s;
+        for (int b = slice; b < parts; b += 64) {
+            const float *p = part + ((int64_t)b * 4 + blockIdx.y * 2) * a.width + c;
+            s[0] += p[0];
+            s[1] += p[a.width];
+        }
+    sh[0][slice][threadIdx.x & 15] = s[0];
+    sh[1][slice][threadIdx.x & 15] = s[1];
     __syncthreads();
-    if (slice == 0 && c < width) {
-        float v = 0.0f;
+    if (slice != 0 || c >= a.width) return;
+    float p = 0.0f, q = 0.0f;
 #pragma unroll
-        for (int b = 0; b < 64; ++b) v += sh[b][threadIdx.x];
-        o[c] = v;
+    for (int b = 0; b < 64; ++b) {
+        p += sh[0][b][threadIdx.x];
+        q += sh[1][b][threadIdx.x];
+    }
+    if (blockIdx.y == 0) {
+        const float sc = a.scale ? a.scale[c] : 1.0f, w = a.post_weight ? a.post_weight[c] : 1.0f, b = a.post_bias ? a.post_bias[c] : 0.0f;
+        if (out.v[0]) out.v[0][c] = sc * p;
+        if (out.v[1]) out.v[1][c] = sc * q;
+        if (out.v[2]) out.v[2][c] = fmaf(w, p, b * q);
+    } else {
+        if (out.v[3]) out.v[3][c] = p;
+        if (out.v[4]) out.v[4][c] = q;
     }
 }
 
@@ -500,7 +526,7 @@ Status norm_residual_backward(Context &cx, const mpnn_norm &p, int64_t n, const 
         using L = Lanes<T, lanes(), chunks()>;
         const int64_t blocks = std::min<int64_t>((n + L::kGroups - 1) / L::kGroups, kBackBlocks * 256 / L::kThreads);
         const bool columns = dvec[0] || dvec[1] || dvec[2] || dvec[3] || dvec[4];
-        if (columns) MPNN_TRY(cx.grow(cx.rows_ws, sizeof(float) * (size_t)(blocks * 5 * p.width)));
+        if (columns) MPNN_TRY(cx.grow(cx.rows_ws, sizeof(float) * (size_t)(blocks * 4 * p.width)));
         if (n > 0) {
             k_norm_residual_back<T, lanes(), chunks()><<<(unsigned)blocks, L::kThreads, 0, cx.stream>>>(
                 args_of(p, n, gate), (const T *)dr, (const T *)dh, (const T *)r, ldr, (const T *)block, ldb, (const T *)gate, ldg,
@@ -508,8 +534,8 @@ Status norm_residual_backward(Context &cx, const mpnn_norm &p, int64_t n, const 
             MPNN_HIP(hipGetLastError());
         }
         if (columns) {
-            k_norm_columns<<<dim3((p.width + 15) / 16, 5), 1024, 0, cx.stream>>>(
-                p.width, (int)blocks, cx.rows_ws.as<float>(), Vectors{{dvec[0], dvec[1], dvec[2], dvec[3], dvec[4]}});
+            k_norm_columns<<<dim3((p.width + 15) / 16, 2), 1024, 0, cx.stream>>>(
+                args_of(p, n, gate), (int)blocks, cx.rows_ws.as<float>(), Vectors{{dvec[0], dvec[1], dvec[2], dvec[3], dvec[4]}});
             MPNN_HIP(hipGetLastError());
         }
         return Status::ok();
