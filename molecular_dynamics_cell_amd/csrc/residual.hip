@@ -31,15 +31,21 @@ struct NormArgs {
 // below half an ulp of 1 in the result; infinities and NaN come out as the formula has them.
 __device__ __forceinline__ float sigmoid(float g) { return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504f * g)); }
 
+// What a launch is compiled for.  kAny: any width up to the lanes' slots, any of the optional arrays missing.  The
+// others: rows that fill the slots exactly, every array there, and the gate of that kind.  Their row loop has no
+// condition around a load or a store, so a wait for a load is a wait for that load alone; with conditions it waits for
+// all that is under way, the stores of the row before among it (gradient of 8,192 x 4,096 bf16: 242 us, 140 us without).
+enum Mode { kAny = -1, kNoGate = 0, kRowGate = 1, kElementGate = 2 };
+
 // A row's place in the block's registers.
-template <class T, int G, int CH>
+template <class T, int G, int CH, bool EXACT>
 struct Lanes {
     static constexpr int W = Chunk<T>::W, E = CH * W;      // values of a row per lane
     static constexpr int kThreads = G > 64 ? G : 256, kGroups = kThreads / G;   // several waves a row: one row a block
     static constexpr int kWaves = G / 64;                  // waves of a row (0: part of one)
     int lane, group;
     int width;
-    bool whole;            // a row is whole chunks: each is all inside it or all outside
+    bool whole;            // a row is whole chunks: each is all inside it or all outside (EXACT: inside)
     __device__ __forceinline__ Lanes(int w) : lane(threadIdx.x % G), group(threadIdx.x / G), width(w), whole(w % W == 0) {}
     __device__ __forceinline__ int column(int c) const { return (c * G + lane) * W; }
     // A row as it is in memory; zeros past its end.
@@ -47,6 +53,11 @@ struct Lanes {
         Chunk<T> c[CH];
     };
     __device__ __forceinline__ void fetch(Raw &t, const T *row) const {
+        if (EXACT) {
+#pragma unroll
+            for (int c = 0; c < CH; ++c) t.c[c] = load_chunk(row + column(c));
+            return;
+        }
         __builtin_memset(&t, 0, sizeof t);
         if (whole) {
 #pragma unroll
@@ -73,7 +84,9 @@ struct Lanes {
 #pragma unroll
             for (int j = 0; j < W; ++j) t.v[j] = from_f32<T>(v[c * W + j]);
             const int left = width - column(c);
-            if (whole) {
+            if (EXACT) {
+                store_chunk(row + column(c), t);
+            } else if (whole) {
                 if (left > 0) store_chunk(row + column(c), t);
             } else {
                 if (left > 0) store_chunk(row + column(c), t, left);
@@ -142,11 +155,11 @@ struct Lanes {
     __device__ __forceinline__ void centre(float (&v)[E], float m) const {
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
-            const float mc = column(c) < width ? m : 0.0f;      // a chunk outside holds zeros
+            const float mc = EXACT || column(c) < width ? m : 0.0f;      // a chunk outside holds zeros
 #pragma unroll
             for (int j = 0; j < W; ++j) v[c * W + j] -= mc;
         }
-        if (!whole) {
+        if (!EXACT && !whole) {
 #pragma unroll
             for (int c = 0; c < CH; ++c)
 #pragma unroll
@@ -170,18 +183,21 @@ template <int E> __device__ __forceinline__ float dot_of(const float (&v)[E], co
 }
 
 // In a group of several waves all waves of the block take the same row, so barriers inside the row loop are uniform.
-template <class T, int G, int CH>
-__global__ __launch_bounds__((Lanes<T, G, CH>::kThreads)) void k_norm_residual(NormArgs a, const T *__restrict__ x, int64_t ldx,
+template <class T, int G, int CH, int MODE>
+__global__ __launch_bounds__((Lanes<T, G, CH, false>::kThreads)) void k_norm_residual(NormArgs a, const T *__restrict__ x, int64_t ldx,
                                                                              const T *__restrict__ block, int64_t ldb,
                                                                              const T *__restrict__ gate, int64_t ldg, T *r,
                                                                              T *__restrict__ h) {
-    using L = Lanes<T, G, CH>;
+    constexpr bool EXACT = MODE != kAny;
+    using L = Lanes<T, G, CH, EXACT>;
     constexpr int E = L::E;
     __shared__ float sh[2][L::kWaves > 1 ? L::kWaves : 1];
     int turn = 0;
     const L at(a.width);
+    const int gate_kind = EXACT ? (int)MODE : a.gate_width > 1 ? (int)kElementGate : a.gate_width;   // widths of 1 count as one gate a row
+    const bool has_block = EXACT || block, has_r = EXACT || r, has_h = EXACT || h;
     float pw[E], pb[E], qw[E], qb[E];
-    if (block) {
+    if (has_block) {
         float sc[E];
         at.vector(pw, a.post_weight, 1.0f);
         at.vector(pb, a.post_bias, 0.0f);
@@ -192,7 +208,7 @@ __global__ __launch_bounds__((Lanes<T, G, CH>::kThreads)) void k_norm_residual(N
             pb[e] *= sc[e];
         }
     }
-    if (h) {
+    if (has_h) {
         at.vector(qw, a.pre_weight, 1.0f);
         at.vector(qb, a.pre_bias, 0.0f);
     }
@@ -213,10 +229,10 @@ __global__ __launch_bounds__((Lanes<T, G, CH>::kThreads)) void k_norm_residual(N
     T row_gate{};
     auto fetch = [&](int64_t i) {
         at.fetch(rx, x + i * ldx);
-        if (block) {
+        if (has_block) {
             at.fetch(rb, block + i * ldb);
-            if (a.gate_width > 1) at.fetch(rg, gate + i * ldg);
-            else if (a.gate_width == 1) row_gate = gate[i * ldg];
+            if (gate_kind == kElementGate) at.fetch(rg, gate + i * ldg);
+            else if (gate_kind == kRowGate) row_gate = gate[i * ldg];
         }
     };
     const int64_t stride = (int64_t)gridDim.x * L::kGroups;
@@ -225,25 +241,25 @@ __global__ __launch_bounds__((Lanes<T, G, CH>::kThreads)) void k_norm_residual(N
     for (; i < a.n; i += stride) {
         float v[E], b[E], g[E];
         at.values(v, rx);
-        if (block) {
+        if (has_block) {
             at.values(b, rb);
-            if (a.gate_width > 1) at.values(g, rg);
+            if (gate_kind == kElementGate) at.values(g, rg);
             else g[0] = to_f32(row_gate);
         }
         if (i + stride < a.n) fetch(i + stride);
-        if (block) {
+        if (has_block) {
             normalise(b);
-            if (a.gate_width > 1) {
+            if (gate_kind == kElementGate) {
 #pragma unroll
                 for (int e = 0; e < E; ++e) v[e] = fmaf(sigmoid(g[e]), fmaf(b[e], pw[e], pb[e]), v[e]);
             } else {
-                const float s = a.gate_width == 1 ? sigmoid(g[0]) : 1.0f;
+                const float s = gate_kind == kRowGate ? sigmoid(g[0]) : 1.0f;
 #pragma unroll
                 for (int e = 0; e < E; ++e) v[e] = fmaf(s, fmaf(b[e], pw[e], pb[e]), v[e]);
             }
         }
-        if (r) at.store(r + i * a.width, v);
-        if (h) {
+        if (has_r) at.store(r + i * a.width, v);
+        if (has_h) {
             normalise(v);
 #pragma unroll
             for (int e = 0; e < E; ++e) v[e] = fmaf(v[e], qw[e], qb[e]);
@@ -259,23 +275,23 @@ __global__ __launch_bounds__((Lanes<T, G, CH>::kThreads)) void k_norm_residual(N
 //   post weight: du hat_b, post bias: du, scale: total sigma(gate) u, pre weight: dh hat_r, pre bias: dh
 // The first three are combinations of two sums, of total sigma hat_b (P) and of total sigma (Q), by the column's own
 // values: scale P, scale Q and weight P + bias Q.
-#ifndef AHEAD
-#define AHEAD true
-#endif
-template <class T, int G, int CH>
-__global__ __launch_bounds__((Lanes<T, G, CH>::kThreads)) void k_norm_residual_back(NormArgs a, const T *dr, const T *__restrict__ dh,
+template <class T, int G, int CH, int MODE>
+__global__ __launch_bounds__((Lanes<T, G, CH, false>::kThreads)) void k_norm_residual_back(NormArgs a, const T *dr, const T *__restrict__ dh,
                                                                                   const T *__restrict__ r, int64_t ldr,
                                                                                   const T *__restrict__ block, int64_t ldb,
                                                                                   const T *__restrict__ gate, int64_t ldg, T *dx,
                                                                                   T *__restrict__ dblock, T *__restrict__ dgate,
                                                                                   float *__restrict__ part) {
-    using L = Lanes<T, G, CH>;
+    constexpr bool EXACT = MODE != kAny;
+    using L = Lanes<T, G, CH, EXACT>;
     constexpr int E = L::E;
     constexpr int kShared = L::kWaves > 1 ? 3 * L::kWaves : 1;
     __shared__ float sh1[2][L::kWaves > 1 ? L::kWaves : 1], sh2[2][L::kWaves > 1 ? 2 * L::kWaves : 1], sh3[2][kShared];
     __shared__ float columns[L::kGroups > 1 ? L::kGroups * G * E : 1];
     int turn1 = 0, turn2 = 0, turn3 = 0;
     const L at(a.width);
+    const int gate_kind = EXACT ? (int)MODE : a.gate_width > 1 ? (int)kElementGate : a.gate_width;   // widths of 1 count as one gate a row
+    const bool has_dr = EXACT || dr, has_dh = EXACT || dh, has_block = EXACT || block;
     __shared__ __attribute__((aligned(16))) float vectors[4][L::kSlots];
     at.keep(vectors[0], a.post_weight, 1.0f);
     at.keep(vectors[1], a.post_bias, 0.0f);
@@ -302,19 +318,19 @@ __global__ __launch_bounds__((Lanes<T, G, CH>::kThreads)) void k_norm_residual_b
     typename L::Raw rdr, rdh, rr, rb, rg;
     T row_gate{};
     auto fetch_pre = [&](int64_t i) {
-        if (dr) at.fetch(rdr, dr + i * a.width);
-        if (dh) {
+        if (has_dr) at.fetch(rdr, dr + i * a.width);
+        if (has_dh) {
             at.fetch(rr, r + i * ldr);
             at.fetch(rdh, dh + i * a.width);
         }
     };
     auto fetch_post = [&](int64_t i) {
-        if (!block) return;
+        if (!has_block) return;
         at.fetch(rb, block + i * ldb);
-        if (a.gate_width > 1) at.fetch(rg, gate + i * ldg);
-        else if (a.gate_width == 1) row_gate = gate[i * ldg];
+        if (gate_kind == kElementGate) at.fetch(rg, gate + i * ldg);
+        else if (gate_kind == kRowGate) row_gate = gate[i * ldg];
     };
-    constexpr bool kAhead = AHEAD;
+    constexpr bool kAhead = !EXACT;      // without conditions the block's other waves hide the loads, in fewer registers
     const int64_t stride = (int64_t)gridDim.x * L::kGroups;
     int64_t i = (int64_t)blockIdx.x * L::kGroups + at.group;
     if (kAhead && i < a.n) {
@@ -325,11 +341,11 @@ __global__ __launch_bounds__((Lanes<T, G, CH>::kThreads)) void k_norm_residual_b
         const int64_t next = i + stride;
         if (!kAhead) fetch_pre(i);
         float t[E];
-        if (dr) at.values(t, rdr);
+        if (has_dr) at.values(t, rdr);
         else
 #pragma unroll
             for (int e = 0; e < E; ++e) t[e] = 0.0f;
-        if (dh) {
+        if (has_dh) {
             float hat[E], d[E];
             at.values(hat, rr);
             at.values(d, rdh);
@@ -351,13 +367,13 @@ __global__ __launch_bounds__((Lanes<T, G, CH>::kThreads)) void k_norm_residual_b
 #pragma unroll
             for (int e = 0; e < E; ++e) t[e] = fmaf(inv, d[e] - m1 - hat[e] * m2, t[e]);
         }
-        if (!dh && kAhead && next < a.n) fetch_pre(next);
-        if (dx) at.store(dx + i * a.width, t);
-        if (block) {
+        if (!has_dh && kAhead && next < a.n) fetch_pre(next);
+        if (EXACT || dx) at.store(dx + i * a.width, t);
+        if (has_block) {
             if (!kAhead) fetch_post(i);
             float b[E], g[E];
             at.values(b, rb);
-            if (a.gate_width > 1) at.values(g, rg);
+            if (gate_kind == kElementGate) at.values(g, rg);
             else g[0] = to_f32(row_gate);
             if (kAhead && next < a.n) fetch_post(next);
             const float inv = normalise(b);
@@ -366,11 +382,11 @@ __global__ __launch_bounds__((Lanes<T, G, CH>::kThreads)) void k_norm_residual_b
             at.kept(pb, vectors[1]);
             at.kept(sc, vectors[2]);
             float m[3] = {0.0f, 0.0f, 0.0f};
-            if (a.gate_width == 1) g[0] = sigmoid(g[0]);
+            if (gate_kind == kRowGate) g[0] = sigmoid(g[0]);
             float du[E], dg[E];
 #pragma unroll
             for (int e = 0; e < E; ++e) {
-                const float s = a.gate_width > 1 ? sigmoid(g[e]) : a.gate_width == 1 ? g[0] : 1.0f;
+                const float s = gate_kind == kElementGate ? sigmoid(g[e]) : gate_kind == kRowGate ? g[0] : 1.0f;
                 const float ts = t[e] * s;
                 s0[e] = fmaf(ts, b[e], s0[e]);
                 s1[e] += ts;
@@ -381,9 +397,9 @@ __global__ __launch_bounds__((Lanes<T, G, CH>::kThreads)) void k_norm_residual_b
                 m[1] = fmaf(du[e], b[e], m[1]);
                 m[2] += dg[e];
             }
-            if (a.gate_width > 1) at.store(dgate + i * a.width, dg);
+            if (gate_kind == kElementGate) at.store(dgate + i * a.width, dg);
             at.sums(m, sh3, turn3);
-            if (a.gate_width == 1 && at.lane == 0) dgate[i] = from_f32<T>(m[2]);
+            if (gate_kind == kRowGate && at.lane == 0) dgate[i] = from_f32<T>(m[2]);
             const float m1 = a.layer ? m[0] * a.inv_width : 0.0f, m2 = m[1] * a.inv_width;
 #pragma unroll
             for (int e = 0; e < E; ++e) du[e] = inv * (du[e] - m1 - b[e] * m2);
@@ -502,40 +518,56 @@ Status by_width(int dtype, int width, F run) {
 
 constexpr int64_t kForwardBlocks = 2048, kBackBlocks = 1024;
 
+// The kernel for a call: run gets the mode as a constant.
+template <class F>
+Status by_mode(bool exact, int gate_width, F run) {
+    if (!exact) return run(std::integral_constant<int, kAny>{});
+    if (gate_width == 0) return run(std::integral_constant<int, kNoGate>{});
+    if (gate_width == 1) return run(std::integral_constant<int, kRowGate>{});
+    return run(std::integral_constant<int, kElementGate>{});
+}
+
 }  // namespace
 
 Status norm_residual(Context &cx, const mpnn_norm &p, int64_t n, const void *x, int64_t ldx, const void *block, int64_t ldb,
                      const void *gate, int64_t ldg, void *r, void *h) {
     if (n == 0) return Status::ok();
+    const NormArgs a = args_of(p, n, gate);
     return by_width(p.dtype, p.width, [&](auto type, auto lanes, auto chunks) -> Status {
         using T = decltype(type);
-        using L = Lanes<T, lanes(), chunks()>;
+        using L = Lanes<T, lanes(), chunks(), false>;
         const int64_t blocks = std::min<int64_t>((n + L::kGroups - 1) / L::kGroups, kForwardBlocks);
-        k_norm_residual<T, lanes(), chunks()><<<(unsigned)blocks, L::kThreads, 0, cx.stream>>>(
-            args_of(p, n, gate), (const T *)x, ldx, (const T *)block, ldb, (const T *)gate, ldg, (T *)r, (T *)h);
-        MPNN_HIP(hipGetLastError());
-        return Status::ok();
+        return by_mode(p.width == L::kSlots && block && r && h, a.gate_width, [&](auto mode) -> Status {
+            k_norm_residual<T, lanes(), chunks(), mode()><<<(unsigned)blocks, L::kThreads, 0, cx.stream>>>(
+                a, (const T *)x, ldx, (const T *)block, ldb, (const T *)gate, ldg, (T *)r, (T *)h);
+            MPNN_HIP(hipGetLastError());
+            return Status::ok();
+        });
     });
 }
 
 Status norm_residual_backward(Context &cx, const mpnn_norm &p, int64_t n, const void *dr, const void *dh, const void *r, int64_t ldr,
                               const void *block, int64_t ldb, const void *gate, int64_t ldg, void *dx, void *dblock, void *dgate,
                               float *const dvec[5]) {
+    const NormArgs a = args_of(p, n, gate);
     return by_width(p.dtype, p.width, [&](auto type, auto lanes, auto chunks) -> Status {
         using T = decltype(type);
-        using L = Lanes<T, lanes(), chunks()>;
+        using L = Lanes<T, lanes(), chunks(), false>;
         const int64_t blocks = std::min<int64_t>((n + L::kGroups - 1) / L::kGroups, kBackBlocks * 256 / L::kThreads);
         const bool columns = dvec[0] || dvec[1] || dvec[2] || dvec[3] || dvec[4];
         if (columns) MPNN_TRY(cx.grow(cx.rows_ws, sizeof(float) * (size_t)(blocks * 4 * p.width)));
-        if (n > 0) {
-            k_norm_residual_back<T, lanes(), chunks()><<<(unsigned)blocks, L::kThreads, 0, cx.stream>>>(
-                args_of(p, n, gate), (const T *)dr, (const T *)dh, (const T *)r, ldr, (const T *)block, ldb, (const T *)gate, ldg,
-                (T *)dx, (T *)dblock, (T *)dgate, columns ? cx.rows_ws.as<float>() : nullptr);
-            MPNN_HIP(hipGetLastError());
-        }
+        float *part = columns ? cx.rows_ws.as<float>() : nullptr;
+        if (n > 0)
+            MPNN_TRY(by_mode(p.width == L::kSlots && dr && dh && block && dx, a.gate_width, [&](auto mode) -> Status {
+                k_norm_residual_back<T, lanes(), chunks(), mode()><<<(unsigned)blocks, L::kThreads, 0, cx.stream>>>(
+                    a, (const T *)dr, (const T *)dh, (const T *)r, ldr, (const T *)block, ldb, (const T *)gate, ldg, (T *)dx,
+                    (T *)dblock, (T *)dgate, part);
+                MPNN_HIP(hipGetLastError());
+                return Status::ok();
+            }));
         if (columns) {
-            k_norm_columns<<<dim3((p.width + 15) / 16, 2), 1024, 0, cx.stream>>>(
-                args_of(p, n, gate), (int)blocks, cx.rows_ws.as<float>(), Vectors{{dvec[0], dvec[1], dvec[2], dvec[3], dvec[4]}});
+            k_norm_columns<<<dim3((p.width + 15) / 16, 2), 1024, 0, cx.stream>>>(a, (int)blocks, part,
+                                                                                 Vectors{{dvec[0], dvec[1], dvec[2], dvec[3], dvec[4]}});
             MPNN_HIP(hipGetLastError());
         }
         return Status::ok();
