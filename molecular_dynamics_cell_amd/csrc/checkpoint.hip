@@ -62,26 +62,29 @@ __device__ __forceinline__ void save_chunk(const float (&v)[Chunk<T>::W], int in
 }
 
 // A lane per chunk of a whole number of groups (chunks past the row's end hold zeros), kUnroll chunks in flight.
-template <class T, bool SILU>
+// FULL: the rows are whole groups.
+template <class T, bool SILU, bool FULL>
 __global__ __launch_bounds__(256) void k_checkpoint_save(Items it, int groups, int width, const T *__restrict__ z, int64_t ld,
                                                          T *__restrict__ y, int8_t *__restrict__ codes, uint8_t *__restrict__ scales,
                                                          int8_t *__restrict__ ycodes, uint8_t *__restrict__ yscales) {
     constexpr int W = Chunk<T>::W, L = kGroupLanes<T>;
+    const int64_t block = xcd_block();
+    const int units = it.items / 256;
     int64_t row[kUnroll];
     int c[kUnroll];
-    bool in[kUnroll];
     Chunk<T> v[kUnroll];
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-        in[u] = item_at(it, u, row[u], c[u]);
-        const int left = in[u] ? width - c[u] * W : 0;
-        if (left > 0) v[u] = load_chunk(z + row[u] * ld + c[u] * W, left);
+        if (u >= units) break;
+        item_at<L>(it, block, u, row[u], c[u]);
+        const int left = FULL ? W : width - c[u] * W;
+        if (FULL || left > 0) v[u] = load_chunk(z + row[u] * ld + c[u] * W, left);
         else __builtin_memset(&v[u], 0, sizeof v[u]);
     }
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-        if (!in[u]) continue;      // a group's lanes go together
-        const int left = width - c[u] * W;
+        if (u >= units) break;
+        const int left = FULL ? W : width - c[u] * W;
         const int64_t at = row[u] * width + c[u] * W, g = row[u] * groups + c[u] / L;
         float f[W];
 #pragma unroll
@@ -94,61 +97,63 @@ __global__ __launch_bounds__(256) void k_checkpoint_save(Items it, int groups, i
                 f[j] = f[j] / (1.0f + expf(-f[j]));
                 o.v[j] = from_f32<T>(f[j]);
             }
-            if (left > 0) store_chunk(y + at, o, left);
+            if (FULL || left > 0) store_chunk(y + at, o, left);
             if (ycodes) save_chunk<T>(f, left, ycodes + at, yscales + g, c[u] % L == 0);
         }
     }
 }
 
-// The values of one chunk of a checkpoint.
-template <class T>
-__device__ __forceinline__ void held_chunk(const int8_t *codes, const uint8_t *scale, int left, float (&z)[Chunk<T>::W]) {
-    constexpr int W = Chunk<T>::W;
-    int8_t q[W];
-    if (left >= W) {
-        __builtin_memcpy(q, codes, W);
-    } else {
+// One chunk of a checkpoint as it is in memory.
+template <int W>
+struct Held {
+    int8_t code[W];
+    uint8_t scale;
+    __device__ __forceinline__ void load(const int8_t *codes, const uint8_t *scales, int left) {
+        if (left >= W) {
+            __builtin_memcpy(code, codes, W);
+        } else {
 #pragma unroll
-        for (int j = 0; j < W; ++j) q[j] = j < left ? codes[j] : (int8_t)0;
+            for (int j = 0; j < W; ++j) code[j] = j < left ? codes[j] : (int8_t)0;
+        }
+        scale = *scales;
     }
-    const float step = step_of(*scale);
-#pragma unroll
-    for (int j = 0; j < W; ++j) z[j] = (float)q[j] * step;
-}
+};
 
 // out = the held values, or with dy the gradient dz = dy s (1 + z (1 - s)), s = sigma(z), at the held z
-template <class T, bool BACK>
+template <class T, bool BACK, bool FULL>
 __global__ __launch_bounds__(256) void k_checkpoint_use(Items it, int groups, int width, const T *__restrict__ dy, int64_t ld,
                                                         const int8_t *__restrict__ codes, const uint8_t *__restrict__ scales,
                                                         T *__restrict__ out) {
     constexpr int W = Chunk<T>::W, L = kGroupLanes<T>;
+    const int64_t block = xcd_block();
+    const int units = it.items / 256;
     int64_t row[kUnroll];
     int c[kUnroll];
-    bool in[kUnroll];
     Chunk<T> d[kUnroll];
-    float z[kUnroll][W];
+    Held<W> z[kUnroll];
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-        in[u] = item_at(it, u, row[u], c[u]);
-        if (!in[u]) continue;
-        const int left = width - c[u] * W;
+        if (u >= units) break;
+        item_at(it, block, u, row[u], c[u]);
+        const int left = FULL ? W : width - c[u] * W;
         if (BACK) d[u] = load_chunk(dy + row[u] * ld + c[u] * W, left);
-        held_chunk<T>(codes + row[u] * width + c[u] * W, scales + row[u] * groups + c[u] / L, left, z[u]);
+        z[u].load(codes + row[u] * width + c[u] * W, scales + row[u] * groups + c[u] / L, left);
     }
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-        if (!in[u]) continue;
+        if (u >= units) break;
         Chunk<T> o;
+        const float step = step_of(z[u].scale);
 #pragma unroll
         for (int j = 0; j < W; ++j) {
-            float v = z[u][j];
+            float v = (float)z[u].code[j] * step;
             if (BACK) {
                 const float s = __builtin_amdgcn_rcpf(1.0f + expf(-v));
                 v = to_f32(d[u].v[j]) * s * fmaf(v, 1.0f - s, 1.0f);
             }
             o.v[j] = from_f32<T>(v);
         }
-        store_chunk(out + row[u] * width + c[u] * W, o, width - c[u] * W);
+        store_chunk(out + row[u] * width + c[u] * W, o, FULL ? W : width - c[u] * W);
     }
 }
 
@@ -159,7 +164,9 @@ static Status save_t(Context &cx, bool silu, int64_t n, int width, const void *z
                      int8_t *ycodes, uint8_t *yscales) {
     const int groups = (width + kGroup - 1) / kGroup;
     const Items it = items_of(n, groups * kGroupLanes<T>);
-    auto *kernel = silu ? k_checkpoint_save<T, true> : k_checkpoint_save<T, false>;
+    const bool full = width % kGroup == 0;
+    auto *kernel = silu ? (full ? k_checkpoint_save<T, true, true> : k_checkpoint_save<T, true, false>)
+                        : (full ? k_checkpoint_save<T, false, true> : k_checkpoint_save<T, false, false>);
     kernel<<<grid_of(it), 256, 0, cx.stream>>>(it, groups, width, (const T *)z, ld, (T *)y, codes, scales, ycodes, yscales);
     MPNN_HIP(hipGetLastError());
     return Status::ok();
@@ -176,7 +183,8 @@ template <class T, bool BACK>
 static Status use_t(Context &cx, int64_t n, int width, const void *dy, int64_t ld, const int8_t *codes, const uint8_t *scales,
                     void *out) {
     const Items it = items_of(n, (width + Chunk<T>::W - 1) / Chunk<T>::W);
-    k_checkpoint_use<T, BACK><<<grid_of(it), 256, 0, cx.stream>>>(it, (width + kGroup - 1) / kGroup, width, (const T *)dy, ld, codes,
+    auto *kernel = width % Chunk<T>::W == 0 ? k_checkpoint_use<T, BACK, true> : k_checkpoint_use<T, BACK, false>;
+    kernel<<<grid_of(it), 256, 0, cx.stream>>>(it, (width + kGroup - 1) / kGroup, width, (const T *)dy, ld, codes,
                                                                   scales, (T *)out);
     MPNN_HIP(hipGetLastError());
     return Status::ok();

@@ -2,6 +2,7 @@
 // expert with a stable counting sort; pairs whose expert is outside 0 .. E-1 keep a place after the last segment
 // (treated as expert E), so `source` and `position` are inverse permutations of all n k pairs and every index that
 // a kernel reads from them is one it can check against n k.
+#include <algorithm>
 #include <type_traits>
 
 #include "impl.h"
@@ -13,24 +14,27 @@ namespace {
 
 constexpr int kPlanThreads = 256;
 constexpr int kPlanWaves = kPlanThreads / 64;
-constexpr int kPlanItems = 16;                             // pairs per lane
-constexpr int kPlanChunk = kPlanThreads * kPlanItems;      // pairs per block, contiguous
 constexpr int kMaxBins = 1024 + 1;                         // experts and the dropped pairs
 
 __device__ __forceinline__ int bin_of(int e, int n_experts) { return (unsigned)e < (unsigned)n_experts ? e : n_experts; }
 
-// counts[bin][block]: pairs of each bin in the block's chunk (integer adds: the order does not matter)
-__global__ void k_route_count(const int32_t *__restrict__ expert, int64_t pairs, int n_experts, int32_t *__restrict__ counts) {
+// counts[block][bin]: pairs of each bin among the block's 256 ITEMS ones (integer adds: the order does not matter)
+template <int ITEMS>
+__global__ __launch_bounds__(kPlanThreads) void k_route_count(const int32_t *__restrict__ expert, int64_t pairs, int n_experts,
+                                                              int32_t *__restrict__ counts) {
     __shared__ int32_t h[kMaxBins];
-    for (int b = threadIdx.x; b <= n_experts; b += kPlanThreads) h[b] = 0;
+    const int bins = n_experts + 1;
+    const int64_t base = (int64_t)blockIdx.x * (kPlanThreads * ITEMS);
+    int e[ITEMS];
+#pragma unroll
+    for (int j = 0; j < ITEMS; ++j) e[j] = expert[min(base + j * kPlanThreads + threadIdx.x, pairs - 1)];
+    for (int b = threadIdx.x; b < bins; b += kPlanThreads) h[b] = 0;
     __syncthreads();
-    const int64_t base = (int64_t)blockIdx.x * kPlanChunk;
-    for (int j = 0; j < kPlanItems; ++j) {
-        const int64_t p = base + j * kPlanThreads + threadIdx.x;
-        if (p < pairs) atomicAdd(&h[bin_of(expert[p], n_experts)], 1);
-    }
+#pragma unroll
+    for (int j = 0; j < ITEMS; ++j)
+        if (base + j * kPlanThreads + threadIdx.x < pairs) atomicAdd(&h[bin_of(e[j], n_experts)], 1);
     __syncthreads();
-    for (int b = threadIdx.x; b <= n_experts; b += kPlanThreads) counts[(int64_t)b * gridDim.x + blockIdx.x] = h[b];
+    for (int b = threadIdx.x; b < bins; b += kPlanThreads) counts[(int64_t)blockIdx.x * bins + b] = h[b];
 }
 
 // Inclusive prefix sum over the block's threads (kPlanThreads of them).
@@ -48,49 +52,95 @@ __device__ __forceinline__ int block_scan(int v, int32_t *sh) {
     return v;
 }
 
-// One block per bin: the counts of the bin become their exclusive prefix over the blocks; total[bin] the sum.
-__global__ void k_route_scan(int32_t *__restrict__ counts, int blocks, int32_t *__restrict__ total) {
-    __shared__ int32_t sh[kPlanWaves];
-    __shared__ int32_t carry;
-    int32_t *c = counts + (int64_t)blockIdx.x * blocks;
-    if (threadIdx.x == 0) carry = 0;
+// Many blocks: the counts of 16 bins become their exclusive prefixes over the blocks, and total[bin] their sums.  64
+// threads a bin take a stretch of the blocks each.
+__global__ __launch_bounds__(1024) void k_route_scan(int32_t *__restrict__ counts, int blocks, int bins, int32_t *__restrict__ total) {
+    __shared__ int32_t sh[64][17];
+    const int lb = threadIdx.x & 15, slice = threadIdx.x >> 4, b = blockIdx.x * 16 + lb;
+    const int each = (blocks + 63) / 64, from = min(slice * each, blocks), to = min(from + each, blocks);
+    int s = 0;
+    if (b < bins)
+#pragma unroll 8
+        for (int i = from; i < to; ++i) s += counts[(int64_t)i * bins + b];
+    sh[slice][lb] = s;
     __syncthreads();
-    for (int base = 0; base < blocks; base += kPlanThreads) {
-        const int i = base + threadIdx.x;
-        const int v = i < blocks ? c[i] : 0;
-        const int s = block_scan(v, sh) + carry;
-        __syncthreads();
-        if (i < blocks) c[i] = s - v;
-        if (threadIdx.x == kPlanThreads - 1) carry = s;
-        __syncthreads();
+    int run = 0, all = 0;
+    for (int i = 0; i < 64; ++i) {
+        run += i < slice ? sh[i][lb] : 0;
+        all += sh[i][lb];
     }
-    if (threadIdx.x == 0) total[blockIdx.x] = carry;
+    if (b >= bins) return;
+    if (slice == 0) total[b] = all;
+#pragma unroll 8
+    for (int i = from; i < to; ++i) {
+        const int c = counts[(int64_t)i * bins + b];
+        counts[(int64_t)i * bins + b] = run;
+        run += c;
+    }
 }
 
-// Each wave takes a contiguous quarter of the block's chunk, 64 pairs at a time.  A pair's place is its bin's
-// start, the bin's pairs in earlier blocks and in the block's earlier waves, and its rank among the wave's own pairs
-// of the bin: those before this iteration, and the lower lanes of equal bin (one ballot per bit of the bin).
-// Without earlier blocks (counts = nullptr, one block) the bins' totals come from the wave counts themselves.
-__global__ void k_route_place(const int32_t *__restrict__ expert, int64_t pairs, int n_experts, const int32_t *__restrict__ counts,
-                              const int32_t *__restrict__ total, int32_t *__restrict__ offsets, int32_t *__restrict__ source,
-                              int32_t *__restrict__ position) {
+// Each wave takes a contiguous quarter of the block's pairs, 64 at a time.  A pair's place is its bin's start, the bin's
+// pairs in earlier blocks and in the block's earlier waves, and its rank among the wave's own pairs of the bin: those
+// before this iteration, and the lower lanes of equal bin (one ballot per bit of the bin).
+// The bins' totals and what earlier blocks hold of them: of one block from its own counts, of up to kSumCounts
+// counts from all blocks' counts, which every block adds up for itself (a launch less), else from k_route_scan (`total`).
+constexpr int kSumCounts = 16384;
+template <int ITEMS>
+__global__ __launch_bounds__(kPlanThreads) void k_route_place(const int32_t *__restrict__ expert, int64_t pairs, int n_experts,
+                                                              const int32_t *__restrict__ counts, const int32_t *__restrict__ total,
+                                                              int32_t *__restrict__ offsets, int32_t *__restrict__ source,
+                                                              int32_t *__restrict__ position) {
     __shared__ int32_t h[kPlanWaves][kMaxBins];
+    __shared__ int32_t before[kMaxBins], sums[kMaxBins];
+    __shared__ int32_t part[2][kPlanThreads];
     __shared__ int32_t sh[kPlanWaves];
     __shared__ int32_t carry;
-    const int bins = n_experts + 1;
+    const int bins = n_experts + 1, blocks = gridDim.x;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t base = (int64_t)blockIdx.x * (kPlanThreads * ITEMS) + wave * (64 * ITEMS);
+    int bin[ITEMS];
+#pragma unroll
+    for (int j = 0; j < ITEMS; ++j) {
+        const int64_t p = base + j * 64 + lane;
+        bin[j] = pairs > 0 ? expert[min(p, pairs - 1)] : 0;
+    }
+#pragma unroll
+    for (int j = 0; j < ITEMS; ++j) bin[j] = base + j * 64 + lane < pairs ? bin_of(bin[j], n_experts) : -1;
     for (int b = threadIdx.x; b < bins; b += kPlanThreads)
         for (int w = 0; w < kPlanWaves; ++w) h[w][b] = 0;
     if (threadIdx.x == 0) carry = 0;
-    __syncthreads();
-    const int64_t base = (int64_t)blockIdx.x * kPlanChunk + wave * (64 * kPlanItems);
-    int bin[kPlanItems];
-#pragma unroll
-    for (int j = 0; j < kPlanItems; ++j) {
-        const int64_t p = base + j * 64 + lane;
-        bin[j] = p < pairs ? bin_of(expert[p], n_experts) : -1;
-        if (bin[j] >= 0) atomicAdd(&h[wave][bin[j]], 1);
+    if (counts && !total) {
+        // lanes of a column of bins, slices of the blocks
+        const int columns = bins > 32 ? 64 : bins > 16 ? 32 : bins > 8 ? 16 : 8, slices = kPlanThreads / columns;
+        const int column = threadIdx.x % columns, slice = threadIdx.x / columns;
+        for (int b0 = 0; b0 < bins; b0 += columns) {
+            const int b = b0 + column;
+            int all = 0, early = 0;
+            if (b < bins)
+#pragma unroll 8
+                for (int i = slice; i < blocks; i += slices) {
+                    const int c = counts[(int64_t)i * bins + b];
+                    all += c;
+                    early += i < (int)blockIdx.x ? c : 0;
+                }
+            __syncthreads();
+            part[0][threadIdx.x] = all;
+            part[1][threadIdx.x] = early;
+            __syncthreads();
+            if (slice == 0 && b < bins) {
+                for (int i = 1; i < slices; ++i) {
+                    all += part[0][i * columns + column];
+                    early += part[1][i * columns + column];
+                }
+                sums[b] = all;
+                before[b] = early;
+            }
+        }
     }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < ITEMS; ++j)
+        if (bin[j] >= 0) atomicAdd(&h[wave][bin[j]], 1);
     __syncthreads();
     for (int b0 = 0; b0 < bins; b0 += kPlanThreads) {
         const int b = b0 + threadIdx.x;
@@ -98,7 +148,10 @@ __global__ void k_route_place(const int32_t *__restrict__ expert, int64_t pairs,
         if (b < bins) {
             if (total) {
                 all = total[b];
-                mine = counts[(int64_t)b * gridDim.x + blockIdx.x];
+                mine = counts[(int64_t)blockIdx.x * bins + b];
+            } else if (counts) {
+                all = sums[b];
+                mine = before[b];
             } else {
                 for (int w = 0; w < kPlanWaves; ++w) all += h[w][b];
             }
@@ -119,7 +172,8 @@ __global__ void k_route_place(const int32_t *__restrict__ expert, int64_t pairs,
     }
     const int bits = 32 - __clz(n_experts);   // bins 0 .. n_experts
 #pragma unroll
-    for (int j = 0; j < kPlanItems; ++j) {
+    for (int j = 0; j < ITEMS; ++j) {
+        if (base + j * 64 >= pairs) break;    // all of the wave's
         const int64_t p = base + j * 64 + lane;
         uint64_t same = __ballot(bin[j] >= 0);
         for (int t = 0; t < bits; ++t) {
@@ -137,126 +191,165 @@ __global__ void k_route_place(const int32_t *__restrict__ expert, int64_t pairs,
     }
 }
 
-// Where a chunk of a row starts: the last chunk of a row is moved back to end with the row (its first values are
-// then written twice, equally), so that every access is a whole chunk.  Rows shorter than a chunk go value by value.
-template <class T> __device__ __forceinline__ int chunk_start(int c, int width) { return min(c * Chunk<T>::W, width - Chunk<T>::W); }
+// A chunk of a row: the last one of a row is moved back to end with the row (its first values are then written twice,
+// equally), so that every access is a whole chunk.  Rows shorter than a chunk go value by value (SHORT).
+template <class T, bool SHORT>
+struct Piece {
+    static constexpr int W = SHORT ? 1 : Chunk<T>::W;
+    T v[W];
+    __device__ __forceinline__ static int start(int c, int width) { return SHORT ? c : min(c * W, width - W); }
+    __device__ __forceinline__ void load(const T *p) { __builtin_memcpy(this, p, sizeof *this); }
+    __device__ __forceinline__ void store(T *p) const { __builtin_memcpy(p, this, sizeof *this); }
+};
+template <class T> int chunks_of(int width) { return width < Chunk<T>::W ? width : (width + Chunk<T>::W - 1) / Chunk<T>::W; }
 
 // sorted[position[i, s]] = x[i]; a pair without an expert gets a row of zeros.  Row-major over x, so that each row is
-// read once for its k copies.
-template <class T, bool SHORT>
+// read once for its k copies; the places of S slots are read together.
+template <class T, bool SHORT, int S>
 __global__ __launch_bounds__(256) void k_route_scatter(Items it, int k, int width, const T *__restrict__ x, int64_t ldx,
                                                        const int32_t *__restrict__ position, const int32_t *__restrict__ used,
                                                        T *__restrict__ sorted) {
-    const int64_t pairs = it.n * k;
-    const int live = *used;
+    using P = Piece<T, SHORT>;
+    const int64_t pairs = it.n * k, block = xcd_block();
+    const int live = *used, units = it.items / 256;
     int64_t row[kUnroll];
     int at[kUnroll];
-    bool in[kUnroll];
-    using V = typename std::conditional<SHORT, T, Chunk<T>>::type;
-    V v[kUnroll], zero;
+    P v[kUnroll], zero;
     __builtin_memset(&zero, 0, sizeof zero);
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-        in[u] = item_at(it, u, row[u], at[u]);
-        if (!SHORT) at[u] = chunk_start<T>(at[u], width);
-        if (in[u]) __builtin_memcpy(&v[u], x + row[u] * ldx + at[u], sizeof(V));
+        if (u >= units) break;
+        item_at(it, block, u, row[u], at[u]);
+        at[u] = P::start(at[u], width);
+        v[u].load(x + row[u] * ldx + at[u]);
     }
-    for (int s = 0; s < k; ++s)
+    for (int s0 = 0; s0 < k; s0 += S) {
+        int q[kUnroll][S];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u)
+#pragma unroll
+            for (int j = 0; j < S; ++j)
+                if (u < units) q[u][j] = position[row[u] * k + min(s0 + j, k - 1)];
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
-            if (!in[u]) continue;
-            const int q = position[row[u] * k + s];
-            if ((unsigned)q < (uint64_t)pairs) {
-                const V w = q < live ? v[u] : zero;
-                __builtin_memcpy(sorted + (int64_t)q * width + at[u], &w, sizeof(V));
-            }
+            if (u >= units) break;
+#pragma unroll
+            for (int j = 0; j < S; ++j)
+                if ((unsigned)q[u][j] < (uint64_t)pairs) (q[u][j] < live ? v[u] : zero).store(sorted + (int64_t)q[u][j] * width + at[u]);
         }
+    }
 }
 
-// out[i] = sum over s of weight[i, s] sorted[position[i, s]], in the order of the slots, in fp32
-template <class T, bool SHORT>
+// out[i] = sum over s of weight[i, s] sorted[position[i, s]], in the order of the slots, in fp32.  S slots of kUnroll / S
+// items are loaded together.
+template <class T, bool SHORT, int S>
 __global__ __launch_bounds__(256) void k_route_combine(Items it, int k, int width, const T *__restrict__ sorted,
                                                        const int32_t *__restrict__ position, const int32_t *__restrict__ used,
                                                        const float *__restrict__ weight, T *__restrict__ out) {
-    constexpr int W = SHORT ? 1 : Chunk<T>::W, S = 4;     // S slots of a row are loaded together
-    const int live = *used;
+    using P = Piece<T, SHORT>;
+    constexpr int W = P::W, U = kUnroll / S;
+    const int64_t block = xcd_block();
+    const int live = *used, units = it.items / 256;
 #pragma unroll 1
-    for (int u = 0; u < kUnroll; ++u) {
-        int64_t row;
-        int at;
-        if (!item_at(it, u, row, at)) continue;
-        if (!SHORT) at = chunk_start<T>(at, width);
-        float sum[W] = {};
-        for (int s0 = 0; s0 < k; s0 += S) {
-            struct { T v[W]; } y[S];
-            bool on[S];
-            float w[S];
+    for (int u0 = 0; u0 < units; u0 += U) {
+        int64_t row[U];
+        int at[U];
+        float sum[U][W] = {};
 #pragma unroll
-            for (int j = 0; j < S; ++j) {
-                const int64_t p = row * k + min(s0 + j, k - 1);
-                const int q = position[p];
-                on[j] = s0 + j < k && (unsigned)q < (unsigned)live;
-                w[j] = weight ? weight[p] : 1.0f;
-                // a place without an expert reads another row, whose values are not used
-                __builtin_memcpy(&y[j], sorted + (int64_t)(on[j] ? q : 0) * width + at, sizeof y[j]);
-            }
-#pragma unroll
-            for (int j = 0; j < S; ++j)
-#pragma unroll
-                for (int e = 0; e < W; ++e) sum[e] = on[j] ? fmaf(w[j], to_f32(y[j].v[e]), sum[e]) : sum[e];
+        for (int u = 0; u < U; ++u) {
+            item_at(it, block, min(u0 + u, units - 1), row[u], at[u]);
+            at[u] = P::start(at[u], width);
         }
-        struct { T v[W]; } o;
+        for (int s0 = 0; s0 < k; s0 += S) {
+            P y[U][S];
+            bool on[U][S];
+            float w[U][S];
 #pragma unroll
-        for (int e = 0; e < W; ++e) o.v[e] = from_f32<T>(sum[e]);
-        __builtin_memcpy(out + row * width + at, &o, sizeof o);
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int j = 0; j < S; ++j) {
+                    const int64_t p = row[u] * k + min(s0 + j, k - 1);
+                    const int q = position[p];
+                    on[u][j] = s0 + j < k && (unsigned)q < (unsigned)live;
+                    w[u][j] = weight ? weight[p] : 1.0f;
+                    // a place without an expert reads another row, whose values are not used
+                    y[u][j].load(sorted + (int64_t)(on[u][j] ? q : 0) * width + at[u]);
+                }
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int j = 0; j < S; ++j)
+#pragma unroll
+                    for (int e = 0; e < W; ++e)
+                        sum[u][e] = on[u][j] ? fmaf(w[u][j], to_f32(y[u][j].v[e]), sum[u][e]) : sum[u][e];
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            P o;
+#pragma unroll
+            for (int e = 0; e < W; ++e) o.v[e] = from_f32<T>(sum[u][e]);
+            o.store(out + row[u] * width + at[u]);
+        }
     }
 }
 
 // dsorted[q] = weight dout[i] and dweight = <dout[i], sorted[q]> for q = position[i, s]; zeros without an expert.
-// G lanes take a row and kBackSlots of its slots, so that a chunk of dout is read once for them.
-constexpr int kBackSlots = 4;
-template <class T, int G>
+// G lanes take a row and S of its slots, so that a chunk of dout is read once for them; lanes past the row's last chunk
+// repeat it without counting it in the sums.
+template <class T, bool SHORT, int G, int S>
 __global__ __launch_bounds__(256) void k_route_combine_back(int64_t n, int k, int batches, int width, const T *__restrict__ dout, int64_t ld,
                                                             const T *__restrict__ sorted, const int32_t *__restrict__ position,
                                                             const int32_t *__restrict__ used, const float *__restrict__ weight,
                                                             T *__restrict__ dsorted, float *__restrict__ dweight) {
-    constexpr int W = Chunk<T>::W, S = kBackSlots;
+    using P = Piece<T, SHORT>;
+    constexpr int W = P::W;
     const int64_t pairs = n * k;
-    const int64_t job = (int64_t)blockIdx.x * (256 / G) + threadIdx.x / G;
+    const int64_t job = xcd_block() * (256 / G) + threadIdx.x / G;
     const int64_t i = batches == 1 ? job : job / batches;
     if (i >= n) return;                                   // a whole group of lanes
     const int s0 = batches == 1 ? 0 : (int)(job - i * batches) * S;
-    const int lane = threadIdx.x % G, live = *used;
+    const int lane = threadIdx.x % G, live = *used, chunks = (width + W - 1) / W;
     int q[S];
-    bool in[S], on[S];
+    bool in[S], on[S], all_in = true;
     float w[S], dot[S] = {};
 #pragma unroll
     for (int j = 0; j < S; ++j) {
-        const int64_t p = i * k + min(s0 + j, k - 1);
+        const int64_t p = i * k + min(s0 + j, k - 1);     // slots past the last repeat it
         q[j] = position[p];
-        in[j] = s0 + j < k && (unsigned)q[j] < (uint64_t)pairs;
+        in[j] = (unsigned)q[j] < (uint64_t)pairs;
+        all_in = all_in && in[j];
         on[j] = in[j] && q[j] < live;
         w[j] = weight ? weight[p] : 1.0f;
     }
-    for (int c = lane * W; c < width; c += G * W) {
-        const int left = width - c;
-        const Chunk<T> d = load_chunk(dout + i * ld + c, left);
-        Chunk<T> y[S];
+    auto step = [&](int c0, auto checked) {
+        const int c = c0 + lane, at = P::start(min(c, chunks - 1), width);
+        const int skip = c < chunks ? c * W - at : W;      // values of this chunk that another one counts
+        P d, y[S];
+        d.load(dout + i * ld + at);
         if (dweight) {
 #pragma unroll
-            for (int j = 0; j < S; ++j) y[j] = load_chunk(sorted + (int64_t)(on[j] ? q[j] : 0) * width + c, left);
+            for (int j = 0; j < S; ++j) y[j].load(sorted + (int64_t)(on[j] ? q[j] : 0) * width + at);
         }
 #pragma unroll
         for (int j = 0; j < S; ++j) {
-            Chunk<T> o;
+            P o;
+#pragma unroll
+            for (int e = 0; e < W; ++e) o.v[e] = from_f32<T>(on[j] ? w[j] * to_f32(d.v[e]) : 0.0f);
+            if (!checked() || in[j]) o.store(dsorted + (int64_t)q[j] * width + at);
+        }
+        if (dweight) {
 #pragma unroll
             for (int e = 0; e < W; ++e) {
-                const float v = to_f32(d.v[e]);
-                if (dweight) dot[j] = fmaf(v, to_f32(y[j].v[e]), dot[j]);
-                o.v[e] = from_f32<T>(on[j] ? w[j] * v : 0.0f);
+                const float v = e < skip ? 0.0f : to_f32(d.v[e]);
+#pragma unroll
+                for (int j = 0; j < S; ++j) dot[j] = e < skip ? dot[j] : fmaf(v, to_f32(y[j].v[e]), dot[j]);
             }
-            if (in[j]) store_chunk(dsorted + (int64_t)q[j] * width + c, o, left);
         }
+    };
+    if (__all(all_in)) {
+        for (int c = 0; c < chunks; c += G) step(c, std::false_type{});
+    } else {
+        for (int c = 0; c < chunks; c += G) step(c, std::true_type{});
     }
     if (dweight) {
 #pragma unroll
@@ -269,36 +362,56 @@ __global__ __launch_bounds__(256) void k_route_combine_back(int64_t n, int k, in
 
 }  // namespace
 
+template <int ITEMS>
+static Status plan(Context &cx, int64_t pairs, int n_experts, const int32_t *expert, int32_t *offsets, int32_t *source,
+                   int32_t *position) {
+    constexpr int kChunk = kPlanThreads * ITEMS;
+    const int64_t blocks = std::max<int64_t>(1, (pairs + kChunk - 1) / kChunk);
+    const int bins = n_experts + 1;
+    int32_t *counts = nullptr, *total = nullptr;
+    if (blocks > 1) {
+        MPNN_TRY(cx.grow(cx.rows_ws, sizeof(int32_t) * (size_t)bins * (size_t)(blocks + 1)));
+        counts = cx.rows_ws.as<int32_t>();
+        k_route_count<ITEMS><<<(unsigned)blocks, kPlanThreads, 0, cx.stream>>>(expert, pairs, n_experts, counts);
+        MPNN_HIP(hipGetLastError());
+        if (blocks * bins > kSumCounts) {
+            total = counts + blocks * bins;
+            k_route_scan<<<(bins + 15) / 16, 1024, 0, cx.stream>>>(counts, (int)blocks, bins, total);
+            MPNN_HIP(hipGetLastError());
+        }
+    }
+    k_route_place<ITEMS><<<(unsigned)blocks, kPlanThreads, 0, cx.stream>>>(expert, pairs, n_experts, counts, total, offsets, source,
+                                                                           position);
+    MPNN_HIP(hipGetLastError());
+    return Status::ok();
+}
+
+// 1,024 pairs a block, so that the pairs of some 100,000 atoms already fill the GPU's CUs; 4,096 where there are enough
+// of them, for fewer counts.
 Status route_plan(Context &cx, int64_t n, int k, int n_experts, const int32_t *expert, int32_t *offsets, int32_t *source,
                   int32_t *position) {
     const int64_t pairs = n * k;
-    const int64_t blocks = (pairs + kPlanChunk - 1) / kPlanChunk;
-    if (blocks <= 1) {
-        k_route_place<<<1, kPlanThreads, 0, cx.stream>>>(expert, pairs, n_experts, nullptr, nullptr, offsets, source, position);
-        MPNN_HIP(hipGetLastError());
-        return Status::ok();
-    }
-    MPNN_TRY(cx.grow(cx.rows_ws, sizeof(int32_t) * (size_t)(n_experts + 1) * (size_t)(blocks + 1)));
-    int32_t *counts = cx.rows_ws.as<int32_t>();
-    int32_t *total = counts + (int64_t)(n_experts + 1) * blocks;
-    k_route_count<<<(unsigned)blocks, kPlanThreads, 0, cx.stream>>>(expert, pairs, n_experts, counts);
-    MPNN_HIP(hipGetLastError());
-    k_route_scan<<<n_experts + 1, kPlanThreads, 0, cx.stream>>>(counts, (int)blocks, total);
-    MPNN_HIP(hipGetLastError());
-    k_route_place<<<(unsigned)blocks, kPlanThreads, 0, cx.stream>>>(expert, pairs, n_experts, counts, total, offsets, source, position);
-    MPNN_HIP(hipGetLastError());
-    return Status::ok();
+    return pairs > (1 << 20) ? plan<16>(cx, pairs, n_experts, expert, offsets, source, position)
+                             : plan<4>(cx, pairs, n_experts, expert, offsets, source, position);
+}
+
+// Slots that a kernel takes together, as a constant.
+template <class F> Status by_slots(int k, F run) {
+    if (k == 1) return run(std::integral_constant<int, 1>{});
+    if (k == 2) return run(std::integral_constant<int, 2>{});
+    return run(std::integral_constant<int, 4>{});
 }
 
 template <class T>
 static Status scatter_t(Context &cx, int64_t n, int k, int width, const void *x, int64_t ldx, const int32_t *position,
                         const int32_t *used, void *sorted) {
-    constexpr int W = Chunk<T>::W;
-    const Items it = items_of(n, width < W ? width : (width + W - 1) / W);
-    auto *kernel = width < W ? k_route_scatter<T, true> : k_route_scatter<T, false>;
-    kernel<<<grid_of(it), 256, 0, cx.stream>>>(it, k, width, (const T *)x, ldx, position, used, (T *)sorted);
-    MPNN_HIP(hipGetLastError());
-    return Status::ok();
+    const Items it = items_of(n, chunks_of<T>(width));
+    return by_slots(k, [&](auto slots) -> Status {
+        auto *kernel = width < Chunk<T>::W ? k_route_scatter<T, true, slots()> : k_route_scatter<T, false, slots()>;
+        kernel<<<grid_of(it), 256, 0, cx.stream>>>(it, k, width, (const T *)x, ldx, position, used, (T *)sorted);
+        MPNN_HIP(hipGetLastError());
+        return Status::ok();
+    });
 }
 
 Status route_scatter(Context &cx, int dtype, int64_t n, int k, int width, const void *x, int64_t ldx, const int32_t *position,
@@ -311,12 +424,13 @@ Status route_scatter(Context &cx, int dtype, int64_t n, int k, int width, const 
 template <class T>
 static Status combine_t(Context &cx, int64_t n, int k, int width, const void *sorted, const int32_t *position, const int32_t *used,
                         const float *weight, void *out) {
-    constexpr int W = Chunk<T>::W;
-    const Items it = items_of(n, width < W ? width : (width + W - 1) / W);
-    auto *kernel = width < W ? k_route_combine<T, true> : k_route_combine<T, false>;
-    kernel<<<grid_of(it), 256, 0, cx.stream>>>(it, k, width, (const T *)sorted, position, used, weight, (T *)out);
-    MPNN_HIP(hipGetLastError());
-    return Status::ok();
+    const Items it = items_of(n, chunks_of<T>(width));
+    return by_slots(k, [&](auto slots) -> Status {
+        auto *kernel = width < Chunk<T>::W ? k_route_combine<T, true, slots()> : k_route_combine<T, false, slots()>;
+        kernel<<<grid_of(it), 256, 0, cx.stream>>>(it, k, width, (const T *)sorted, position, used, weight, (T *)out);
+        MPNN_HIP(hipGetLastError());
+        return Status::ok();
+    });
 }
 
 Status route_combine(Context &cx, int dtype, int64_t n, int k, int width, const void *sorted, const int32_t *position,
@@ -329,17 +443,22 @@ Status route_combine(Context &cx, int dtype, int64_t n, int k, int width, const 
 template <class T>
 static Status combine_back_t(Context &cx, int64_t n, int k, int width, const void *dout, int64_t ld, const void *sorted,
                              const int32_t *position, const int32_t *used, const float *weight, void *dsorted, float *dweight) {
-    const int chunks = (width + Chunk<T>::W - 1) / Chunk<T>::W, batches = (k + kBackSlots - 1) / kBackSlots;
-    auto run = [&](auto *kernel, int lanes) -> Status {
-        kernel<<<grid_for(n * batches, 256 / lanes), 256, 0, cx.stream>>>(n, k, batches, width, (const T *)dout, ld, (const T *)sorted,
-                                                                          position, used, weight, (T *)dsorted, dweight);
-        MPNN_HIP(hipGetLastError());
-        return Status::ok();
-    };
-    if (chunks <= 8) return run(k_route_combine_back<T, 8>, 8);
-    if (chunks <= 16) return run(k_route_combine_back<T, 16>, 16);
-    if (chunks <= 32) return run(k_route_combine_back<T, 32>, 32);
-    return run(k_route_combine_back<T, 64>, 64);
+    return by_slots(k, [&](auto slots) -> Status {
+        constexpr int S = slots();
+        const int chunks = chunks_of<T>(width), batches = (k + S - 1) / S;
+        auto run = [&](auto *kernel, int lanes) -> Status {
+            kernel<<<grid_xcd(n * batches, 256 / lanes), 256, 0, cx.stream>>>(n, k, batches, width, (const T *)dout, ld,
+                                                                              (const T *)sorted, position, used, weight,
+                                                                              (T *)dsorted, dweight);
+            MPNN_HIP(hipGetLastError());
+            return Status::ok();
+        };
+        if (width < Chunk<T>::W) return run(k_route_combine_back<T, true, 8, S>, 8);
+        if (chunks <= 8) return run(k_route_combine_back<T, false, 8, S>, 8);
+        if (chunks <= 16) return run(k_route_combine_back<T, false, 16, S>, 16);
+        if (chunks <= 32) return run(k_route_combine_back<T, false, 32, S>, 32);
+        return run(k_route_combine_back<T, false, 64, S>, 64);
+    });
 }
 
 Status route_combine_backward(Context &cx, int dtype, int64_t n, int k, int width, const void *dout, int64_t ld, const void *sorted,

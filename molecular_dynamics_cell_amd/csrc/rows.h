@@ -67,34 +67,40 @@ template <int G> __device__ __forceinline__ float lanes_sum(float v) {
 __device__ __forceinline__ float wave_sum(float v) { return lanes_sum<64>(v); }
 
 // Items of a row operator without sums along the rows: `per` chunks a row.  A block takes `rows` whole rows, or, of
-// rows longer than kItems chunks, one stretch (blockIdx.y); a thread takes every 256th item, kUnroll of them at a time
-// so that their loads are in flight together.
-constexpr int kItems = 1024, kUnroll = 4;
+// rows longer than its `items`, one stretch (blockIdx.y); a thread takes every 256th item, kUnroll of them (one in
+// small calls, which are spread over more blocks), whose loads are in flight together.  Consecutive stretches of rows
+// go to one XCD, so that lines shared by neighbouring rows are completed in its L2.
+constexpr int kUnroll = 4;
 struct Items {
     int64_t n;
-    int per, rows;
+    int per, rows, items;
     float inv;      // 1 / per
 };
 inline Items items_of(int64_t n, int per) {
-    const int rows = per < kItems ? kItems / per : 1;
-    return Items{n, per, rows, 1.0f / (float)per};
+    const int items = n * per > 256 * 2048 ? 256 * kUnroll : 256;
+    const int rows = per < items ? items / per : 1;
+    return Items{n, per, rows, items, 1.0f / (float)per};
 }
-inline dim3 grid_of(const Items &it) { return dim3((unsigned)((it.n + it.rows - 1) / it.rows), (unsigned)((it.per + kItems - 1) / kItems)); }
+inline dim3 grid_of(const Items &it) { return dim3(grid_xcd(it.n, it.rows), (unsigned)((it.per + it.items - 1) / it.items)); }
 
-// The block's u-th item of this thread: its row and chunk; false past the last.
-__device__ __forceinline__ bool item_at(const Items &it, int u, int64_t &row, int &c) {
-    const int l = u * 256 + threadIdx.x;
+// This thread's u-th item: its row and chunk.  Threads past the block's last item, and blocks past the last row, repeat
+// a last one (of the same place in a group of L chunks), so that no load or store has a condition: what they write is
+// what its owner writes.
+template <int L = 1> __device__ __forceinline__ void item_at(const Items &it, int64_t block, int u, int64_t &row, int &c) {
+    int l = u * 256 + threadIdx.x;
     if (it.rows == 1) {
-        row = blockIdx.x;
-        c = blockIdx.y * kItems + l;
-        return c < it.per;
+        row = min(block, it.n - 1);
+        c = blockIdx.y * it.items + (l < it.items ? l : it.items - L + l % L);
+        if (c >= it.per) c = it.per - L + l % L;
+        return;
     }
+    const int last = it.rows * it.per;
+    if (l >= last) l = last - L + l % L;
     int q = (int)((float)l * it.inv);      // off by one at most
     q -= q * it.per > l;
     q += (q + 1) * it.per <= l;
-    row = (int64_t)blockIdx.x * it.rows + q;
+    row = min(block * it.rows + q, it.n - 1);
     c = l - q * it.per;
-    return q < it.rows && row < it.n;
 }
 
 }  // namespace mpnn
