@@ -180,6 +180,7 @@ mpnn_status mpnn_checkpoint_weight_grad(mpnn_ctx *ctx, int32_t dtype, int64_t n,
         if (n_out < 1 || n_out > 1 << 16) return bad("bad output width");
         if (n_experts < 1 || n_experts > kMaxExperts) return bad("n_experts must be in 1..1024");
         MPNN_TRY(check_ld(ld_dy, n_out, "ld_dy smaller than the output width"));
+        if (ld_dy > 1 << 24) return bad("ld_dy larger than 2^24");
         if (!offsets || !dweight || (n > 0 && (!dy || !codes || !scales))) return bad("null array");
         return mpnn::weight_grad(cx, dtype, n, n_out, width, n_experts, offsets, dy, ld_dy, codes, scales, dweight, dbias);
     });

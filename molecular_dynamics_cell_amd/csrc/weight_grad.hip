@@ -104,21 +104,29 @@ __device__ __forceinline__ void clear_quad(Quad32 &q) { q.v[0] = q.v[1] = q.v[2]
 __device__ __forceinline__ void clear_quad(Quad16 &q) { q.v[0] = q.v[1] = 0u; }
 
 // Column j of eight rows as the operand words of each term.
-__device__ __forceinline__ void column(const Quad16 (&q)[8], int j, uint4 (&w)[1]) {
+__device__ __forceinline__ void column(const Quad16 (&q)[8], int j, uint4 (&w)[1], bool) {
     uint32_t p[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
         p[i] = j & 1 ? high_halves(q[2 * i].v[j >> 1], q[2 * i + 1].v[j >> 1]) : low_halves(q[2 * i].v[j >> 1], q[2 * i + 1].v[j >> 1]);
     w[0] = make_uint4(p[0], p[1], p[2], p[3]);
 }
-__device__ __forceinline__ void column(const Quad32 (&q)[8], int j, uint4 (&w)[3]) {
+__device__ __forceinline__ bool infinite(const Quad16 (&)[8]) { return false; }
+__device__ __forceinline__ bool infinite(const Quad32 (&q)[8]) {
+    float m = 0.0f;
+#pragma unroll
+    for (int r = 0; r < 8; ++r) m = fmaxf(m, fmaxf(fmaxf(fabsf(q[r].v[0]), fabsf(q[r].v[1])), fmaxf(fabsf(q[r].v[2]), fabsf(q[r].v[3]))));
+    return m == __uint_as_float(0x7f800000u);
+}
+// `inf`: an infinity may be among the values; nothing is left of one after its first term.
+__device__ __forceinline__ void column(const Quad32 (&q)[8], int j, uint4 (&w)[3], bool inf) {
     uint32_t t[3][8];
 #pragma unroll
     for (int r = 0; r < 8; ++r) {
         const float v = q[r].v[j];
         const uint32_t top = __float_as_uint(v) & 0xffff0000u;
-        // exact: what is left has 16 significant bits; nothing is left of an infinity
-        const float left = fabsf(v) < __uint_as_float(0x7f800000u) ? v - __uint_as_float(top) : 0.0f;
+        float left = v - __uint_as_float(top);                         // exact: 16 significant bits
+        if (inf) left = fabsf(v) == __uint_as_float(0x7f800000u) ? 0.0f : left;
         const uint32_t middle = __float_as_uint(left) & 0xffff0000u;
         t[0][r] = top;
         t[1][r] = middle;
@@ -167,43 +175,50 @@ __global__ __launch_bounds__(256, 2) void k_weight_grad(int out, int width, int 
     // columns past the last repeat it: their products are not written
     const int ac = min(o0 + 4 * am, out - 1), xc = min(c0 + 4 * xm, width - 1);
     const int alast = out - 1 - ac, xlast = width - 1 - xc;
-    const T *ap = dy + ac;
-    const int8_t *xp = codes + xc;
-    const uint8_t *sp = scales + xc / 32;
+    // A wave's 16 rows and four groups of columns have 64 scales: a lane loads one and hands it to the lanes that need it.
+    const int sr = (wave * 2 + (lane >> 5)) * 8 + (lane & 7);
+    const int sg = min(c0 / 32 + ((lane >> 3) & 3), groups - 1);
+    const int sfrom = (lane & 32) + (xm >> 3) * 8;
 
     // The loads of a stage: rows past the last repeat it and are cleared when they are staged, so that no load waits
     // for a condition of another.
     Quad a[8];
     uint32_t x[8];
-    uint8_t scale[8];
-    auto fetch = [&](int64_t q0) {
-        int64_t qa[8], qx[8];
+    uint8_t scale;
+    uint32_t qa[8], qx[8], qs;      // distances from the stage's first row
+    auto rows_of = [&](int last) {
 #pragma unroll
         for (int r = 0; r < 8; ++r) {
-            qa[r] = min(q0 + ak * 8 + r, to - 1);
-            qx[r] = min(q0 + xk * 8 + r, to - 1);
+            qa[r] = (uint32_t)min(ak * 8 + r, last) * (uint32_t)ld + ac;
+            qx[r] = (uint32_t)min(xk * 8 + r, last) * (uint32_t)width + xc;
         }
+        qs = (uint32_t)min(sr, last) * (uint32_t)groups + sg;
+    };
+    rows_of(kBK - 1);
+    auto fetch = [&](int64_t q0) {
+        if (q0 + kBK > to) rows_of((int)(to - 1 - q0));      // the last stage
+        const T *ap = dy + q0 * ld;
+        const int8_t *xp = codes + q0 * width;
         if (ak < kChunks) {
             if (vec_dy) {
 #pragma unroll
-                for (int r = 0; r < 8; ++r) load_quad(a[r], ap + qa[r] * ld);
+                for (int r = 0; r < 8; ++r) load_quad(a[r], ap + qa[r]);
             } else {
 #pragma unroll
-                for (int r = 0; r < 8; ++r) load_quad(a[r], ap + qa[r] * ld, alast);
+                for (int r = 0; r < 8; ++r) load_quad(a[r], ap + qa[r], alast);
             }
         }
         if (vec_x) {
 #pragma unroll
-            for (int r = 0; r < 8; ++r) x[r] = *reinterpret_cast<const uint32_t *>(xp + qx[r] * width);
+            for (int r = 0; r < 8; ++r) x[r] = *reinterpret_cast<const uint32_t *>(xp + qx[r]);
         } else {
 #pragma unroll
             for (int r = 0; r < 8; ++r) {
-                const uint8_t *p = reinterpret_cast<const uint8_t *>(xp + qx[r] * width);
+                const uint8_t *p = reinterpret_cast<const uint8_t *>(xp + qx[r]);
                 x[r] = (uint32_t)p[0] | (uint32_t)p[min(1, xlast)] << 8 | (uint32_t)p[min(2, xlast)] << 16 | (uint32_t)p[min(3, xlast)] << 24;
             }
         }
-#pragma unroll
-        for (int r = 0; r < 8; ++r) scale[r] = sp[qx[r] * groups];
+        scale = (scales + q0 * groups)[qs];
     };
 
     floatx16 acc[MT][NT];
@@ -218,19 +233,22 @@ __global__ __launch_bounds__(256, 2) void k_weight_grad(int out, int width, int 
         __syncthreads();
         if (q0 + kBK > to) {
 #pragma unroll
-            for (int r = 0; r < 8; ++r) {
+            for (int r = 0; r < 8; ++r)
                 if (q0 + ak * 8 + r >= to) clear_quad(a[r]);
-                if (q0 + xk * 8 + r >= to) scale[r] = 0;   // a step of zero
-            }
+            if (q0 + sr >= to) scale = 0;   // a step of zero
         }
         if (ak < kChunks) {
+            auto stage = [&](bool inf) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                uint4 w[TERMS];
-                column(a, j, w);
+                for (int j = 0; j < 4; ++j) {
+                    uint4 w[TERMS];
+                    column(a, j, w, inf);
 #pragma unroll
-                for (int t = 0; t < TERMS; ++t) A[t][ak][j * (BM / 4) + am] = w[t];
-            }
+                    for (int t = 0; t < TERMS; ++t) A[t][ak][j * (BM / 4) + am] = w[t];
+                }
+            };
+            if (__any(infinite(a))) stage(true);
+            else stage(false);
             if (c0 == 0) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
@@ -238,9 +256,10 @@ __global__ __launch_bounds__(256, 2) void k_weight_grad(int out, int width, int 
                     for (int r = 0; r < 8; ++r) bias[j] += a[r].at(j);
             }
         }
+        const float held = __uint_as_float(scale == 255 ? 0x7fc00000u : (uint32_t)scale << 23);
         float step[8];
 #pragma unroll
-        for (int r = 0; r < 8; ++r) step[r] = __uint_as_float(scale[r] == 255 ? 0x7fc00000u : (uint32_t)scale[r] << 23);
+        for (int r = 0; r < 8; ++r) step[r] = __shfl(held, sfrom + r);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             uint32_t v[8];
@@ -321,7 +340,8 @@ template <class T, int BM>
 Status launch(Context &cx, int64_t n, int out, int width, int n_experts, const int32_t *offsets, const T *dy, int64_t ld,
               const int8_t *codes, const uint8_t *scales, float *dweight, float *dbias) {
     const int tiles_n = (width + kBN - 1) / kBN, tiles = tiles_n * ((out + BM - 1) / BM);
-    const int64_t want = std::max<int64_t>(1, 512 / tiles);
+    // two blocks a CU, all at once: an expert's last piece may be short, so a few pieces less than fill them
+    const int64_t want = std::max<int64_t>(1, 512 / tiles - n_experts);
     const int64_t rows = std::max<int64_t>(512, ((n + want - 1) / want + kBK - 1) / kBK * kBK);
     const int64_t pieces = n / rows + n_experts;              // at most; an expert of several pieces has more than `rows` rows
     const int64_t matrix = (int64_t)out * width, slots = n > rows ? 2 * (n / rows) : 0;   // an expert of p > 1 pieces fills p / 2 whole ones
