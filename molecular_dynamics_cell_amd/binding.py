@@ -165,6 +165,7 @@ class MPNN(rows.RowOperators):
 
     def set_stream(self, stream: torch.cuda.Stream):
         self._stream = stream
+        self._at = stream.device
         self._check(lib().mpnn_set_stream(self.h, C.c_void_p(stream.cuda_stream)))
 
     def use_torch_allocator(self):

@@ -14,6 +14,7 @@ import torch
 GROUP = 32      # columns that share one scale of a checkpoint
 _DTYPE = {torch.float32: 0, torch.bfloat16: 1}
 _KIND = {"rms": 0, "layer": 1}
+_CALLS = {}     # the library's functions by name, once they have been used
 
 
 class Norm(C.Structure):
@@ -33,51 +34,54 @@ def _ptr(t):
 
 
 class RowOperators:
-    # ---- checks ----
+    # A small call is bound by what happens here, so checks are few comparisons and a dense tensor is taken as it is.
     def _rows(self, name, t, n=None, width=None, dtype=None):
         """The tensor as rows with a row stride: (tensor, stride)."""
-        if t.dim() != 2 or t.dtype not in _DTYPE or (dtype is not None and t.dtype != dtype) or \
-                (n is not None and t.shape[0] != n) or (width is not None and t.shape[1] != width):
+        shape = t.shape
+        if len(shape) != 2 or t.dtype not in _DTYPE or (dtype is not None and t.dtype != dtype) or \
+                (n is not None and shape[0] != n) or (width is not None and shape[1] != width):
             raise ValueError(f"{name}: expected rows [{'n' if n is None else n}, {'width' if width is None else width}] "
-                             f"of {dtype or 'float32 or bfloat16'}, got {tuple(t.shape)} of {t.dtype}")
-        self._here(name, t)
-        rows, columns = t.shape
+                             f"of {dtype or 'float32 or bfloat16'}, got {tuple(shape)} of {t.dtype}")
+        if t.device != self._at:
+            raise ValueError(f"{name}: on {t.device}, the context is on {self._at}")
+        rows, columns = shape
+        if t.is_contiguous():
+            return t, columns
         down, across = t.stride()
         if (across != 1 and columns > 1) or (down < columns and rows > 1):
-            t, down = t.contiguous(), columns
+            return t.contiguous(), columns
         return t, max(down, columns)
 
     def _dense(self, name, t, shape, dtype):
-        if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+        if t.shape != shape or t.dtype != dtype:
             raise ValueError(f"{name}: expected {tuple(shape)} of {dtype}, got {tuple(t.shape)} of {t.dtype}")
-        self._here(name, t)
+        if t.device != self._at:
+            raise ValueError(f"{name}: on {t.device}, the context is on {self._at}")
         return t if t.is_contiguous() else t.contiguous()
 
-    def _here(self, name, t):
-        if t.device.type != self.device.type or (self.device.index is not None and t.device.index != self.device.index):
-            raise ValueError(f"{name}: on {t.device}, the context is on {self.device}")
-
-    def _new(self, like, *shape, dtype=None):
-        return torch.empty(shape, dtype=dtype or like.dtype, device=like.device)
+    @staticmethod
+    def _new(like, *shape, dtype=None):
+        return like.new_empty(shape) if dtype is None else like.new_empty(shape, dtype=dtype)
 
     def _call(self, name, tensors, *args):
         """One library call on the context's stream, ordered with torch's current stream."""
-        current, own = torch.cuda.current_stream(self.device), self._stream
-        apart = current != own
+        call = _CALLS.get(name)
+        if call is None:
+            from . import binding
+            call = _CALLS[name] = getattr(binding.lib(), name)
+        own = self._stream
+        current = torch.cuda.current_stream(self._at)
+        apart = current.cuda_stream != own.cuda_stream
         if apart:
             own.wait_stream(current)
-        code = getattr(self._lib(), name)(self.h, *args)
+        code = call(self.h, *args)
         if apart:
             current.wait_stream(own)
             for t in tensors:
                 if t is not None:
                     t.record_stream(own)
-        self._check(code)
-
-    @staticmethod
-    def _lib():
-        from . import binding
-        return binding.lib()
+        if code:
+            self._check(code)
 
     # ---- rows by expert ----
     def route_plan(self, expert: torch.Tensor, n_experts: int):
