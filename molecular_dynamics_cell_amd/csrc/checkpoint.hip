@@ -38,6 +38,14 @@ template <class T> __device__ __forceinline__ float group_max(const float (&v)[C
     return f;
 }
 
+// sigma(z) and 1 - sigma(z) from a = exp(-|z|) <= 1, without a reciprocal of a large number (1 / (1 + exp(-z)) would pass
+// through one that the hardware's reciprocal flushes to zero): r = 1 / (1 + a) and a r.
+__device__ __forceinline__ void sigmoids(float z, float &s, float &rest) {
+    const float a = expf(-fabsf(z)), r = __builtin_amdgcn_rcpf(1.0f + a), ar = a * r;
+    s = z >= 0.0f ? r : ar;
+    rest = z >= 0.0f ? ar : r;
+}
+
 // The codes of one chunk and, by the group's first lane, the scale.
 template <class T>
 __device__ __forceinline__ void save_chunk(const float (&v)[Chunk<T>::W], int in, int8_t *codes, uint8_t *scale, bool first) {
@@ -78,7 +86,7 @@ __global__ __launch_bounds__(256) void k_checkpoint_save(Items it, int groups, i
         if (u >= units) break;
         item_at<L>(it, block, u, row[u], c[u]);
         const int left = FULL ? W : width - c[u] * W;
-        if (FULL || left > 0) v[u] = load_chunk(z + row[u] * ld + c[u] * W, left);
+        if (FULL || left > 0) v[u].load(z + row[u] * ld + c[u] * W, left);
         else __builtin_memset(&v[u], 0, sizeof v[u]);
     }
 #pragma unroll
@@ -94,10 +102,12 @@ __global__ __launch_bounds__(256) void k_checkpoint_save(Items it, int groups, i
             Chunk<T> o;
 #pragma unroll
             for (int j = 0; j < W; ++j) {
-                f[j] = f[j] / (1.0f + expf(-f[j]));
+                float s, rest;
+                sigmoids(f[j], s, rest);
+                f[j] *= s;
                 o.v[j] = from_f32<T>(f[j]);
             }
-            if (FULL || left > 0) store_chunk(y + at, o, left);
+            if (FULL || left > 0) o.store(y + at, left);
             if (ycodes) save_chunk<T>(f, left, ycodes + at, yscales + g, c[u] % L == 0);
         }
     }
@@ -136,7 +146,7 @@ __global__ __launch_bounds__(256) void k_checkpoint_use(Items it, int groups, in
         if (u >= units) break;
         item_at(it, block, u, row[u], c[u]);
         const int left = FULL ? W : width - c[u] * W;
-        if (BACK) d[u] = load_chunk(dy + row[u] * ld + c[u] * W, left);
+        if (BACK) d[u].load(dy + row[u] * ld + c[u] * W, left);
         z[u].load(codes + row[u] * width + c[u] * W, scales + row[u] * groups + c[u] / L, left);
     }
 #pragma unroll
@@ -148,12 +158,13 @@ __global__ __launch_bounds__(256) void k_checkpoint_use(Items it, int groups, in
         for (int j = 0; j < W; ++j) {
             float v = (float)z[u].code[j] * step;
             if (BACK) {
-                const float s = __builtin_amdgcn_rcpf(1.0f + expf(-v));
-                v = to_f32(d[u].v[j]) * s * fmaf(v, 1.0f - s, 1.0f);
+                float s, rest;
+                sigmoids(v, s, rest);
+                v = to_f32(d[u].v[j]) * s * fmaf(v, rest, 1.0f);
             }
             o.v[j] = from_f32<T>(v);
         }
-        store_chunk(out + row[u] * width + c[u] * W, o, FULL ? W : width - c[u] * W);
+        o.store(out + row[u] * width + c[u] * W, FULL ? W : width - c[u] * W);
     }
 }
 

@@ -31,45 +31,41 @@ struct NormArgs {
 // below half an ulp of 1 in the result; infinities and NaN come out as the formula has them.
 __device__ __forceinline__ float sigmoid(float g) { return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504f * g)); }
 
-// What a launch is compiled for.  kAny: any width up to the lanes' slots, any of the optional arrays missing.  The
-// others: rows that fill the slots exactly, every array there, and the gate of that kind.  Their row loop has no
-// condition around a load or a store, so a wait for a load is a wait for that load alone; with conditions it waits for
-// all that is under way, the stores of the row before among it (gradient of 8,192 x 4,096 bf16: 242 us, 140 us without).
+// What a launch is compiled for.  kAny: some of the optional arrays may be missing.  The others: every array there, and
+// the gate of that kind, in fewer registers, so with more waves (gradient of 8,192 x 4,096 bf16: 242 us with the
+// conditions, 140 us without).
 enum Mode { kAny = -1, kNoGate = 0, kRowGate = 1, kElementGate = 2 };
 
-// A row's place in the block's registers.
-template <class T, int G, int CH, bool EXACT>
+// A row's place in the block's registers: W values a chunk, CH chunks a lane, G lanes.  The chunk that would pass the
+// row's end is moved back to end with it, and lanes past the last chunk repeat it, so that every access is a whole chunk
+// of the row; the values that another lane has too count in no sum (`mine` is 0), and what is stored of them is what
+// their owner stores.  EXACT: there are none.
+template <class T, int W, int G, int CH, bool EXACT>
 struct Lanes {
-    static constexpr int W = Chunk<T>::W, E = CH * W;      // values of a row per lane
+    static constexpr int E = CH * W;                       // values of a row per lane
     static constexpr int kThreads = G > 64 ? G : 256, kGroups = kThreads / G;   // several waves a row: one row a block
     static constexpr int kWaves = G / 64;                  // waves of a row (0: part of one)
     int lane, group;
     int width;
-    bool whole;            // a row is whole chunks: each is all inside it or all outside (EXACT: inside)
-    __device__ __forceinline__ Lanes(int w) : lane(threadIdx.x % G), group(threadIdx.x / G), width(w), whole(w % W == 0) {}
-    __device__ __forceinline__ int column(int c) const { return (c * G + lane) * W; }
-    // A row as it is in memory; zeros past its end.
+    int column[CH];
+    float mine[EXACT ? 1 : E];
+    __device__ __forceinline__ Lanes(int w) : lane(threadIdx.x % G), group(threadIdx.x / G), width(w) {
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            const int at = (c * G + lane) * W;
+            column[c] = EXACT ? at : min(at, width - W);
+            if (!EXACT)
+#pragma unroll
+                for (int j = 0; j < W; ++j) mine[c * W + j] = column[c] + j >= at ? 1.0f : 0.0f;
+        }
+    }
+    // A row as it is in memory.
     struct Raw {
-        Chunk<T> c[CH];
+        Chunk<T, W> c[CH];
     };
     __device__ __forceinline__ void fetch(Raw &t, const T *row) const {
-        if (EXACT) {
 #pragma unroll
-            for (int c = 0; c < CH; ++c) t.c[c] = load_chunk(row + column(c));
-            return;
-        }
-        __builtin_memset(&t, 0, sizeof t);
-        if (whole) {
-#pragma unroll
-            for (int c = 0; c < CH; ++c)
-                if (column(c) < width) t.c[c] = load_chunk(row + column(c));
-        } else {
-#pragma unroll
-            for (int c = 0; c < CH; ++c) {
-                const int left = width - column(c);
-                if (left > 0) t.c[c] = load_chunk(row + column(c), left);
-            }
-        }
+        for (int c = 0; c < CH; ++c) t.c[c].load(row + column[c]);
     }
     __device__ __forceinline__ void values(float (&v)[E], const Raw &t) const {
 #pragma unroll
@@ -80,52 +76,44 @@ struct Lanes {
     __device__ __forceinline__ void store(T *row, const float (&v)[E]) const {
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
-            Chunk<T> t;
+            Chunk<T, W> t;
 #pragma unroll
             for (int j = 0; j < W; ++j) t.v[j] = from_f32<T>(v[c * W + j]);
-            const int left = width - column(c);
-            if (EXACT) {
-                store_chunk(row + column(c), t);
-            } else if (whole) {
-                if (left > 0) store_chunk(row + column(c), t);
-            } else {
-                if (left > 0) store_chunk(row + column(c), t, left);
-            }
+            t.store(row + column[c]);
         }
     }
-    // a vector's values of this lane's columns; zeros past the width
+    // a vector's values of this lane's columns
     __device__ __forceinline__ void vector(float (&v)[E], const float *p, float otherwise) const {
 #pragma unroll
-        for (int e = 0; e < E; ++e) v[e] = p ? 0.0f : column(e / W) + e % W < width ? otherwise : 0.0f;
+        for (int e = 0; e < E; ++e) v[e] = otherwise;
         if (!p) return;
-        if (whole) {
 #pragma unroll
-            for (int c = 0; c < CH; ++c)
-                if (column(c) < width) __builtin_memcpy(&v[c * W], p + column(c), W * sizeof(float));
-        } else {
-#pragma unroll
-            for (int c = 0; c < CH; ++c)
-#pragma unroll
-                for (int j = 0; j < W; ++j)
-                    if (column(c) + j < width) v[c * W + j] = p[column(c) + j];
-        }
+        for (int c = 0; c < CH; ++c) __builtin_memcpy(&v[c * W], p + column[c], W * sizeof(float));
     }
+    // one value's share of a sum
+    __device__ __forceinline__ float share(float v, int e) const { return EXACT ? v : v * mine[EXACT ? 0 : e]; }
     // The reverse pass keeps its vectors in LDS (zeros past the width), whose registers its sums need.  The offset is
     // zero, but not to the compiler, which would move the reads out of the row loop, into registers.
     static constexpr int kSlots = G * E;
     __device__ __forceinline__ void keep(float *sh, const float *p, float otherwise) const {
-        for (int c = threadIdx.x; c < kSlots; c += kThreads) sh[c] = c < width ? (p ? p[c] : otherwise) : 0.0f;
+        for (int c = threadIdx.x; c < width; c += kThreads) sh[c] = p ? p[c] : otherwise;
     }
     __device__ __forceinline__ void kept(float (&v)[E], const float *sh) const {
         int z = 0;
         asm volatile("" : "+v"(z));
 #pragma unroll
-        for (int c = 0; c < CH; ++c)
+        for (int c = 0; c < CH; ++c) {
+            if constexpr (EXACT && W % 4 == 0) {
 #pragma unroll
-            for (int j = 0; j < W; j += 4) {
-                const float4 t = *reinterpret_cast<const float4 *>(sh + column(c) + j + z);
-                v[c * W + j] = t.x; v[c * W + j + 1] = t.y; v[c * W + j + 2] = t.z; v[c * W + j + 3] = t.w;
+                for (int j = 0; j < W; j += 4) {
+                    const float4 t = *reinterpret_cast<const float4 *>(sh + column[c] + j + z);
+                    v[c * W + j] = t.x; v[c * W + j + 1] = t.y; v[c * W + j + 2] = t.z; v[c * W + j + 3] = t.w;
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < W; ++j) v[c * W + j] = sh[column[c] + j + z];
             }
+        }
     }
     // sums over the row's lanes, the same bits in each
     template <int N, int M> __device__ __forceinline__ void sums(float (&s)[N], float (&sh)[2][M], int &turn) const {
@@ -151,51 +139,43 @@ struct Lanes {
             }
         }
     }
-    // v becomes its distance from m (0 past the width)
-    __device__ __forceinline__ void centre(float (&v)[E], float m) const {
+    // v becomes its normed values; returns one over the root
+    template <int M> __device__ __forceinline__ float normalise(float (&v)[E], bool layer, float eps, float inv_width, float (&sh)[2][M],
+                                                                int &turn) const {
+        if (layer) {
+            float m[1] = {0.0f};
 #pragma unroll
-        for (int c = 0; c < CH; ++c) {
-            const float mc = EXACT || column(c) < width ? m : 0.0f;      // a chunk outside holds zeros
+            for (int e = 0; e < E; ++e) m[0] += share(v[e], e);
+            sums(m, sh, turn);
+            m[0] *= inv_width;
 #pragma unroll
-            for (int j = 0; j < W; ++j) v[c * W + j] -= mc;
+            for (int e = 0; e < E; ++e) v[e] -= m[0];
         }
-        if (!EXACT && !whole) {
+        float q[1] = {0.0f};
 #pragma unroll
-            for (int c = 0; c < CH; ++c)
+        for (int e = 0; e < E; ++e) q[0] = fmaf(share(v[e], e), v[e], q[0]);
+        sums(q, sh, turn);
+        const float inv = rsqrtf(q[0] * inv_width + eps);
 #pragma unroll
-                for (int j = 0; j < W; ++j)
-                    if (column(c) + j >= width) v[c * W + j] = 0.0f;
-        }
+        for (int e = 0; e < E; ++e) v[e] *= inv;
+        return inv;
     }
 };
 
-template <int E> __device__ __forceinline__ float sum_of(const float (&v)[E]) {
-    float s = 0.0f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) s += v[e];
-    return s;
-}
-template <int E> __device__ __forceinline__ float dot_of(const float (&v)[E], const float (&w)[E]) {
-    float s = 0.0f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) s = fmaf(v[e], w[e], s);
-    return s;
-}
-
 // In a group of several waves all waves of the block take the same row, so barriers inside the row loop are uniform.
-template <class T, int G, int CH, int MODE>
-__global__ __launch_bounds__((Lanes<T, G, CH, false>::kThreads)) void k_norm_residual(NormArgs a, const T *__restrict__ x, int64_t ldx,
+template <class T, int W, int G, int CH, int MODE, bool EXACT>
+__global__ __launch_bounds__((Lanes<T, W, G, CH, false>::kThreads)) void k_norm_residual(NormArgs a, const T *__restrict__ x, int64_t ldx,
                                                                              const T *__restrict__ block, int64_t ldb,
                                                                              const T *__restrict__ gate, int64_t ldg, T *r,
                                                                              T *__restrict__ h) {
-    constexpr bool EXACT = MODE != kAny;
-    using L = Lanes<T, G, CH, EXACT>;
+    constexpr bool FULL = MODE != kAny;
+    using L = Lanes<T, W, G, CH, EXACT>;
     constexpr int E = L::E;
     __shared__ float sh[2][L::kWaves > 1 ? L::kWaves : 1];
     int turn = 0;
     const L at(a.width);
-    const int gate_kind = EXACT ? (int)MODE : a.gate_width > 1 ? (int)kElementGate : a.gate_width;   // widths of 1 count as one gate a row
-    const bool has_block = EXACT || block, has_r = EXACT || r, has_h = EXACT || h;
+    const int gate_kind = FULL ? (int)MODE : a.gate_width > 1 ? (int)kElementGate : a.gate_width;   // widths of 1 count as one gate a row
+    const bool has_block = FULL || block, has_r = FULL || r, has_h = FULL || h;
     float pw[E], pb[E], qw[E], qb[E];
     if (has_block) {
         float sc[E];
@@ -212,18 +192,7 @@ __global__ __launch_bounds__((Lanes<T, G, CH, false>::kThreads)) void k_norm_res
         at.vector(qw, a.pre_weight, 1.0f);
         at.vector(qb, a.pre_bias, 0.0f);
     }
-    auto normalise = [&](float (&v)[E]) {
-        if (a.layer) {
-            float m[1] = {sum_of(v)};
-            at.sums(m, sh, turn);
-            at.centre(v, m[0] * a.inv_width);
-        }
-        float q[1] = {dot_of(v, v)};
-        at.sums(q, sh, turn);
-        const float inv = rsqrtf(q[0] * a.inv_width + a.eps);
-#pragma unroll
-        for (int e = 0; e < E; ++e) v[e] *= inv;
-    };
+    auto normalise = [&](float (&v)[E]) { at.normalise(v, a.layer, a.eps, a.inv_width, sh, turn); };
     // the next row's loads are under way while a row is worked on
     typename L::Raw rx, rb, rg;
     T row_gate{};
@@ -275,23 +244,23 @@ __global__ __launch_bounds__((Lanes<T, G, CH, false>::kThreads)) void k_norm_res
 //   post weight: du hat_b, post bias: du, scale: total sigma(gate) u, pre weight: dh hat_r, pre bias: dh
 // The first three are combinations of two sums, of total sigma hat_b (P) and of total sigma (Q), by the column's own
 // values: scale P, scale Q and weight P + bias Q.
-template <class T, int G, int CH, int MODE>
-__global__ __launch_bounds__((Lanes<T, G, CH, false>::kThreads)) void k_norm_residual_back(NormArgs a, const T *dr, const T *__restrict__ dh,
+template <class T, int W, int G, int CH, int MODE, bool EXACT>
+__global__ __launch_bounds__((Lanes<T, W, G, CH, false>::kThreads)) void k_norm_residual_back(NormArgs a, const T *dr, const T *__restrict__ dh,
                                                                                   const T *__restrict__ r, int64_t ldr,
                                                                                   const T *__restrict__ block, int64_t ldb,
                                                                                   const T *__restrict__ gate, int64_t ldg, T *dx,
                                                                                   T *__restrict__ dblock, T *__restrict__ dgate,
                                                                                   float *__restrict__ part) {
-    constexpr bool EXACT = MODE != kAny;
-    using L = Lanes<T, G, CH, EXACT>;
+    constexpr bool FULL = MODE != kAny;
+    using L = Lanes<T, W, G, CH, EXACT>;
     constexpr int E = L::E;
     constexpr int kShared = L::kWaves > 1 ? 3 * L::kWaves : 1;
     __shared__ float sh1[2][L::kWaves > 1 ? L::kWaves : 1], sh2[2][L::kWaves > 1 ? 2 * L::kWaves : 1], sh3[2][kShared];
     __shared__ float columns[L::kGroups > 1 ? L::kGroups * G * E : 1];
     int turn1 = 0, turn2 = 0, turn3 = 0;
     const L at(a.width);
-    const int gate_kind = EXACT ? (int)MODE : a.gate_width > 1 ? (int)kElementGate : a.gate_width;   // widths of 1 count as one gate a row
-    const bool has_dr = EXACT || dr, has_dh = EXACT || dh, has_block = EXACT || block;
+    const int gate_kind = FULL ? (int)MODE : a.gate_width > 1 ? (int)kElementGate : a.gate_width;   // widths of 1 count as one gate a row
+    const bool has_dr = FULL || dr, has_dh = FULL || dh, has_block = FULL || block;
     __shared__ __attribute__((aligned(16))) float vectors[4][L::kSlots];
     at.keep(vectors[0], a.post_weight, 1.0f);
     at.keep(vectors[1], a.post_bias, 0.0f);
@@ -300,21 +269,7 @@ __global__ __launch_bounds__((Lanes<T, G, CH, false>::kThreads)) void k_norm_res
     __syncthreads();
     // sums over the group's rows: total sigma hat_b, total sigma, dh hat_r, dh
     float s0[E] = {}, s1[E] = {}, s3[E] = {}, s4[E] = {};
-    // v becomes its normed values; returns one over the root
-    auto normalise = [&](float (&v)[E]) {
-        if (a.layer) {
-            float m[1] = {sum_of(v)};
-            at.sums(m, sh1, turn1);
-            at.centre(v, m[0] * a.inv_width);
-        }
-        float q[1] = {dot_of(v, v)};
-        at.sums(q, sh1, turn1);
-        const float inv = rsqrtf(q[0] * a.inv_width + a.eps);
-#pragma unroll
-        for (int e = 0; e < E; ++e) v[e] *= inv;
-        return inv;
-    };
-    // the next row's loads are under way while a row is worked on
+    auto normalise = [&](float (&v)[E]) { return at.normalise(v, a.layer, a.eps, a.inv_width, sh1, turn1); };
     typename L::Raw rdr, rdh, rr, rb, rg;
     T row_gate{};
     auto fetch_pre = [&](int64_t i) {
@@ -330,16 +285,10 @@ __global__ __launch_bounds__((Lanes<T, G, CH, false>::kThreads)) void k_norm_res
         if (gate_kind == kElementGate) at.fetch(rg, gate + i * ldg);
         else if (gate_kind == kRowGate) row_gate = gate[i * ldg];
     };
-    constexpr bool kAhead = !EXACT;      // without conditions the block's other waves hide the loads, in fewer registers
     const int64_t stride = (int64_t)gridDim.x * L::kGroups;
     int64_t i = (int64_t)blockIdx.x * L::kGroups + at.group;
-    if (kAhead && i < a.n) {
-        fetch_pre(i);
-        fetch_post(i);
-    }
     for (; i < a.n; i += stride) {
-        const int64_t next = i + stride;
-        if (!kAhead) fetch_pre(i);
+        fetch_pre(i);
         float t[E];
         if (has_dr) at.values(t, rdr);
         else
@@ -349,7 +298,6 @@ __global__ __launch_bounds__((Lanes<T, G, CH, false>::kThreads)) void k_norm_res
             float hat[E], d[E];
             at.values(hat, rr);
             at.values(d, rdh);
-            if (kAhead && next < a.n) fetch_pre(next);
             const float inv = normalise(hat);
             float qw[E];
             at.kept(qw, vectors[3]);
@@ -359,23 +307,22 @@ __global__ __launch_bounds__((Lanes<T, G, CH, false>::kThreads)) void k_norm_res
                 s3[e] = fmaf(d[e], hat[e], s3[e]);
                 s4[e] += d[e];
                 d[e] *= qw[e];
-                m[0] += d[e];
-                m[1] = fmaf(d[e], hat[e], m[1]);
+                const float mine = at.share(d[e], e);
+                m[0] += mine;
+                m[1] = fmaf(mine, hat[e], m[1]);
             }
             at.sums(m, sh2, turn2);
             const float m1 = a.layer ? m[0] * a.inv_width : 0.0f, m2 = m[1] * a.inv_width;
 #pragma unroll
             for (int e = 0; e < E; ++e) t[e] = fmaf(inv, d[e] - m1 - hat[e] * m2, t[e]);
         }
-        if (!has_dh && kAhead && next < a.n) fetch_pre(next);
-        if (EXACT || dx) at.store(dx + i * a.width, t);
+        if (FULL || dx) at.store(dx + i * a.width, t);
         if (has_block) {
-            if (!kAhead) fetch_post(i);
+            fetch_post(i);
             float b[E], g[E];
             at.values(b, rb);
             if (gate_kind == kElementGate) at.values(g, rg);
             else g[0] = to_f32(row_gate);
-            if (kAhead && next < a.n) fetch_post(next);
             const float inv = normalise(b);
             float pw[E], pb[E], sc[E];
             at.kept(pw, vectors[0]);
@@ -393,9 +340,10 @@ __global__ __launch_bounds__((Lanes<T, G, CH, false>::kThreads)) void k_norm_res
                 du[e] = ts * sc[e];
                 dg[e] = du[e] * fmaf(b[e], pw[e], pb[e]) * (1.0f - s);
                 du[e] *= pw[e];
-                m[0] += du[e];
-                m[1] = fmaf(du[e], b[e], m[1]);
-                m[2] += dg[e];
+                const float mine = at.share(du[e], e);
+                m[0] += mine;
+                m[1] = fmaf(mine, b[e], m[1]);
+                m[2] += at.share(dg[e], e);
             }
             if (gate_kind == kElementGate) at.store(dgate + i * a.width, dg);
             at.sums(m, sh3, turn3);
@@ -410,23 +358,22 @@ __global__ __launch_bounds__((Lanes<T, G, CH, false>::kThreads)) void k_norm_res
     // the block's sums of each column, its groups in order: part[block][4][width]
     auto write = [&](int q, const float (&s)[E]) {
         float *to = part + ((int64_t)blockIdx.x * 4 + q) * a.width;
+        // columns that several lanes have hold the same sum in each
         if constexpr (L::kGroups == 1) {
 #pragma unroll
             for (int c = 0; c < CH; ++c)
 #pragma unroll
-                for (int j = 0; j < L::W; ++j)
-                    if (at.column(c) + j < a.width) to[at.column(c) + j] = s[c * L::W + j];
+                for (int j = 0; j < W; ++j) to[at.column[c] + j] = s[c * W + j];
         } else {
-            constexpr int kRow = G * E;
 #pragma unroll
             for (int c = 0; c < CH; ++c)
 #pragma unroll
-                for (int j = 0; j < L::W; ++j) columns[at.group * kRow + at.column(c) + j] = s[c * L::W + j];
+                for (int j = 0; j < W; ++j) columns[at.group * L::kSlots + at.column[c] + j] = s[c * W + j];
             __syncthreads();
             for (int c = threadIdx.x; c < a.width; c += L::kThreads) {
                 float v = 0.0f;
 #pragma unroll
-                for (int g = 0; g < L::kGroups; ++g) v += columns[g * kRow + c];
+                for (int g = 0; g < L::kGroups; ++g) v += columns[g * L::kSlots + c];
                 to[c] = v;
             }
             __syncthreads();
@@ -480,37 +427,50 @@ NormArgs args_of(const mpnn_norm &p, int64_t n, bool gate) {
                     p.post_weight, p.post_bias, p.scale, p.pre_weight, p.pre_bias};
 }
 
-// Lanes of a row and chunks of a lane: the fewest slots that hold the row's chunks (312 fp32 values are 78 chunks: 32
-// lanes of 3 waste 18 of 96 slots, 64 lanes of 2 would waste 50 of 128), up to 12 values a lane, which leaves room for
-// the reverse pass's five sums a column in registers; 16 values for the widest rows, whose 1,024 lanes would leave only
-// 128 registers each.
+// Values a chunk, lanes and chunks of a lane: the fewest slots that hold the row, in steps of a half (312 values: 32
+// lanes of 3 chunks of 4 have 384 slots, 64 lanes of 2 would have 512), up to 12 values a lane, which leaves room for the
+// reverse pass's four sums a column in registers; 16 where another wave a row would cost more than it brings.  Rows
+// shorter than a chunk go value by value.
 template <class F>
 Status by_width(int dtype, int width, F run) {
-#define MPNN_ROW(type, limit, lanes, chunks) \
-    if (width <= limit) return run(type{}, std::integral_constant<int, lanes>{}, std::integral_constant<int, chunks>{});
+#define MPNN_ROW(type, limit, wide, lanes, chunks)                                                                      \
+    if (width <= limit)                                                                                                 \
+        return run(type{}, std::integral_constant<int, wide>{}, std::integral_constant<int, lanes>{}, std::integral_constant<int, chunks>{});
     if (dtype == MPNN_BF16) {
-        MPNN_ROW(bf16, 64, 8, 1)
-        MPNN_ROW(bf16, 128, 16, 1)
-        MPNN_ROW(bf16, 256, 32, 1)
-        MPNN_ROW(bf16, 512, 64, 1)
-        MPNN_ROW(bf16, 1024, 128, 1)
-        MPNN_ROW(bf16, 2048, 256, 1)
-        MPNN_ROW(bf16, 4096, 512, 1)
-        MPNN_ROW(bf16, 8192, 512, 2)
+        MPNN_ROW(bf16, 7, 1, 8, 1)
+        MPNN_ROW(bf16, 64, 8, 8, 1)
+        MPNN_ROW(bf16, 96, 4, 8, 3)
+        MPNN_ROW(bf16, 128, 8, 16, 1)
+        MPNN_ROW(bf16, 192, 4, 16, 3)
+        MPNN_ROW(bf16, 256, 8, 32, 1)
+        MPNN_ROW(bf16, 384, 4, 32, 3)
+        MPNN_ROW(bf16, 512, 8, 64, 1)
+        MPNN_ROW(bf16, 768, 4, 64, 3)
+        MPNN_ROW(bf16, 1024, 8, 64, 2)
+        MPNN_ROW(bf16, 1536, 4, 128, 3)
+        MPNN_ROW(bf16, 2048, 8, 256, 1)
+        MPNN_ROW(bf16, 256 * 12, 4, 256, 3)
+        MPNN_ROW(bf16, 4096, 8, 512, 1)
+        MPNN_ROW(bf16, 6144, 4, 512, 3)
+        MPNN_ROW(bf16, 8192, 8, 512, 2)
     } else {
-        MPNN_ROW(float, 32, 8, 1)
-        MPNN_ROW(float, 64, 8, 2)
-        MPNN_ROW(float, 96, 8, 3)
-        MPNN_ROW(float, 128, 16, 2)
-        MPNN_ROW(float, 192, 16, 3)
-        MPNN_ROW(float, 256, 32, 2)
-        MPNN_ROW(float, 384, 32, 3)
-        MPNN_ROW(float, 512, 64, 2)
-        MPNN_ROW(float, 768, 64, 3)
-        MPNN_ROW(float, 1024, 128, 2)
-        MPNN_ROW(float, 2048, 256, 2)
-        MPNN_ROW(float, 4096, 512, 2)
-        MPNN_ROW(float, 8192, 512, 4)
+        MPNN_ROW(float, 3, 1, 8, 1)
+        MPNN_ROW(float, 32, 4, 8, 1)
+        MPNN_ROW(float, 64, 4, 8, 2)
+        MPNN_ROW(float, 96, 4, 8, 3)
+        MPNN_ROW(float, 128, 4, 16, 2)
+        MPNN_ROW(float, 192, 4, 16, 3)
+        MPNN_ROW(float, 256, 4, 32, 2)
+        MPNN_ROW(float, 384, 4, 32, 3)
+        MPNN_ROW(float, 512, 4, 64, 2)
+        MPNN_ROW(float, 768, 4, 64, 3)
+        MPNN_ROW(float, 1024, 4, 128, 2)
+        MPNN_ROW(float, 1536, 4, 128, 3)
+        MPNN_ROW(float, 2048, 4, 256, 2)
+        MPNN_ROW(float, 256 * 12, 4, 256, 3)
+        MPNN_ROW(float, 4096, 4, 512, 2)
+        MPNN_ROW(float, 6144, 4, 512, 3)
+        MPNN_ROW(float, 8192, 4, 512, 4)
     }
 #undef MPNN_ROW
     return Status::err(MPNN_E_INVALID_ARG, "bad width");
@@ -518,13 +478,14 @@ Status by_width(int dtype, int width, F run) {
 
 constexpr int64_t kForwardBlocks = 2048, kBackBlocks = 1024;
 
-// The kernel for a call: run gets the mode as a constant.
+// The kernel for a call: run gets the mode, and whether the rows fill their slots, as constants.
 template <class F>
-Status by_mode(bool exact, int gate_width, F run) {
-    if (!exact) return run(std::integral_constant<int, kAny>{});
-    if (gate_width == 0) return run(std::integral_constant<int, kNoGate>{});
-    if (gate_width == 1) return run(std::integral_constant<int, kRowGate>{});
-    return run(std::integral_constant<int, kElementGate>{});
+Status by_mode(bool full, bool exact, int gate_width, F run) {
+    const auto with = [&](auto mode) -> Status { return exact ? run(mode, std::true_type{}) : run(mode, std::false_type{}); };
+    if (!full) return run(std::integral_constant<int, kAny>{}, std::false_type{});
+    if (gate_width == 0) return with(std::integral_constant<int, kNoGate>{});
+    if (gate_width == 1) return with(std::integral_constant<int, kRowGate>{});
+    return with(std::integral_constant<int, kElementGate>{});
 }
 
 }  // namespace
@@ -533,12 +494,12 @@ Status norm_residual(Context &cx, const mpnn_norm &p, int64_t n, const void *x, 
                      const void *gate, int64_t ldg, void *r, void *h) {
     if (n == 0) return Status::ok();
     const NormArgs a = args_of(p, n, gate);
-    return by_width(p.dtype, p.width, [&](auto type, auto lanes, auto chunks) -> Status {
+    return by_width(p.dtype, p.width, [&](auto type, auto wide, auto lanes, auto chunks) -> Status {
         using T = decltype(type);
-        using L = Lanes<T, lanes(), chunks(), false>;
+        using L = Lanes<T, wide(), lanes(), chunks(), false>;
         const int64_t blocks = std::min<int64_t>((n + L::kGroups - 1) / L::kGroups, kForwardBlocks);
-        return by_mode(p.width == L::kSlots && block && r && h, a.gate_width, [&](auto mode) -> Status {
-            k_norm_residual<T, lanes(), chunks(), mode()><<<(unsigned)blocks, L::kThreads, 0, cx.stream>>>(
+        return by_mode(block && r && h, p.width == L::kSlots, a.gate_width, [&](auto mode, auto exact) -> Status {
+            k_norm_residual<T, wide(), lanes(), chunks(), mode(), exact()><<<(unsigned)blocks, L::kThreads, 0, cx.stream>>>(
                 a, (const T *)x, ldx, (const T *)block, ldb, (const T *)gate, ldg, (T *)r, (T *)h);
             MPNN_HIP(hipGetLastError());
             return Status::ok();
@@ -550,16 +511,16 @@ Status norm_residual_backward(Context &cx, const mpnn_norm &p, int64_t n, const 
                               const void *block, int64_t ldb, const void *gate, int64_t ldg, void *dx, void *dblock, void *dgate,
                               float *const dvec[5]) {
     const NormArgs a = args_of(p, n, gate);
-    return by_width(p.dtype, p.width, [&](auto type, auto lanes, auto chunks) -> Status {
+    return by_width(p.dtype, p.width, [&](auto type, auto wide, auto lanes, auto chunks) -> Status {
         using T = decltype(type);
-        using L = Lanes<T, lanes(), chunks(), false>;
+        using L = Lanes<T, wide(), lanes(), chunks(), false>;
         const int64_t blocks = std::min<int64_t>((n + L::kGroups - 1) / L::kGroups, kBackBlocks * 256 / L::kThreads);
         const bool columns = dvec[0] || dvec[1] || dvec[2] || dvec[3] || dvec[4];
         if (columns) MPNN_TRY(cx.grow(cx.rows_ws, sizeof(float) * (size_t)(blocks * 4 * p.width)));
         float *part = columns ? cx.rows_ws.as<float>() : nullptr;
         if (n > 0)
-            MPNN_TRY(by_mode(p.width == L::kSlots && dr && dh && block && dx, a.gate_width, [&](auto mode) -> Status {
-                k_norm_residual_back<T, lanes(), chunks(), mode()><<<(unsigned)blocks, L::kThreads, 0, cx.stream>>>(
+            MPNN_TRY(by_mode(dr && dh && block && dx, p.width == L::kSlots, a.gate_width, [&](auto mode, auto exact) -> Status {
+                k_norm_residual_back<T, wide(), lanes(), chunks(), mode(), exact()><<<(unsigned)blocks, L::kThreads, 0, cx.stream>>>(
                     a, (const T *)dr, (const T *)dh, (const T *)r, ldr, (const T *)block, ldb, (const T *)gate, ldg, (T *)dx,
                     (T *)dblock, (T *)dgate, part);
                 MPNN_HIP(hipGetLastError());

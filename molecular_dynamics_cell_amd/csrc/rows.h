@@ -11,37 +11,28 @@ using bf16 = __bf16;
 template <class T> __device__ __forceinline__ float to_f32(T v) { return (float)v; }
 template <class T> __device__ __forceinline__ T from_f32(float v) { return (T)v; }
 
-// 16 bytes of a row.  Rows may start on any value's boundary (odd widths, column blocks of wider rows): the access is
-// declared with the value's alignment, and gfx950's global loads and stores take it in one instruction all the same.
-template <class T>
+// W values of a row, 16 bytes of it unless said otherwise.  Rows may start on any value's boundary (odd widths, column
+// blocks of wider rows): the access is declared with the value's alignment, and gfx950's global loads and stores take it
+// in one instruction all the same.
+template <class T, int WIDE = 16 / sizeof(T)>
 struct Chunk {
-    static constexpr int W = 16 / sizeof(T);
+    static constexpr int W = WIDE;
     T v[W];
-};
-template <class T> __device__ __forceinline__ Chunk<T> load_chunk(const T *p) {
-    Chunk<T> c;
-    __builtin_memcpy(&c, p, sizeof c);
-    return c;
-}
-template <class T> __device__ __forceinline__ void store_chunk(T *p, const Chunk<T> &c) { __builtin_memcpy(p, &c, sizeof c); }
-
-// The first `in` values of a chunk (all of them from W on), zeros after them.
-template <class T> __device__ __forceinline__ Chunk<T> load_chunk(const T *p, int in) {
-    if (in >= Chunk<T>::W) return load_chunk(p);
-    Chunk<T> c;
+    __device__ __forceinline__ void load(const T *p) { __builtin_memcpy(this, p, sizeof *this); }
+    __device__ __forceinline__ void store(T *p) const { __builtin_memcpy(p, this, sizeof *this); }
+    // the first `in` values (all of them from W on), zeros after them
+    __device__ __forceinline__ void load(const T *p, int in) {
+        if (in >= W) return load(p);
 #pragma unroll
-    for (int j = 0; j < Chunk<T>::W; ++j) c.v[j] = j < in ? p[j] : from_f32<T>(0.0f);
-    return c;
-}
-template <class T> __device__ __forceinline__ void store_chunk(T *p, const Chunk<T> &c, int in) {
-    if (in >= Chunk<T>::W) {
-        store_chunk(p, c);
-        return;
+        for (int j = 0; j < W; ++j) v[j] = j < in ? p[j] : from_f32<T>(0.0f);
     }
+    __device__ __forceinline__ void store(T *p, int in) const {
+        if (in >= W) return store(p);
 #pragma unroll
-    for (int j = 0; j < Chunk<T>::W; ++j)
-        if (j < in) p[j] = c.v[j];
-}
+        for (int j = 0; j < W; ++j)
+            if (j < in) p[j] = v[j];
+    }
+};
 
 // Sum over G = 4 .. 64 neighbouring lanes, the same bits in each of them: exchanges inside 16 lanes by data-parallel
 // primitives (neighbours, pairs, mirrored halves), across them by the lane swaps.
