@@ -16,6 +16,10 @@ _DTYPE = {torch.float32: 0, torch.bfloat16: 1}
 _KIND = {"rms": 0, "layer": 1}
 _CALLS = {}     # the library's functions by name, once they have been used
 
+# the handle of torch's current stream on a device (a stream object for each call costs 2 us)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
 
 class Norm(C.Structure):
     _fields_ = [("dtype", C.c_int32), ("width", C.c_int32), ("kind", C.c_int32), ("gate_width", C.c_int32),
@@ -53,11 +57,11 @@ class RowOperators:
         return t, max(down, columns)
 
     def _dense(self, name, t, shape, dtype):
+        if t.dtype is dtype and t.shape == shape and t.device == self._at:
+            return t if t.is_contiguous() else t.contiguous()
         if t.shape != shape or t.dtype != dtype:
             raise ValueError(f"{name}: expected {tuple(shape)} of {dtype}, got {tuple(t.shape)} of {t.dtype}")
-        if t.device != self._at:
-            raise ValueError(f"{name}: on {t.device}, the context is on {self._at}")
-        return t if t.is_contiguous() else t.contiguous()
+        raise ValueError(f"{name}: on {t.device}, the context is on {self._at}")
 
     @staticmethod
     def _new(like, *shape, dtype=None):
@@ -70,9 +74,9 @@ class RowOperators:
             from . import binding
             call = _CALLS[name] = getattr(binding.lib(), name)
         own = self._stream
-        current = torch.cuda.current_stream(self._at)
-        apart = current.cuda_stream != own.cuda_stream
+        apart = _current_stream(self._at.index) != own.cuda_stream
         if apart:
+            current = torch.cuda.current_stream(self._at)
             own.wait_stream(current)
         code = call(self.h, *args)
         if apart:
