@@ -1,0 +1,159 @@
+"""Fits a routed readout to the atomic energies of a message-passing model, with the library's row operators.
+
+Teacher: the three-layer water model of the benchmark (4,608 atoms, E_i of its last layer).  Student: one layer of
+orbital sums (the teacher's own O^0, through their density features) under a small network that the caller owns:
+
+    r = x W_in^T,  h = N(r),  then for each block
+        two of `EXPERTS` experts a row by a router on h, rows sorted by expert, W2_e silu(W1_e . + b1_e) + b2_e for each
+        expert's rows, back to their rows with the router's weights, and  r += scale sigma(h W_g^T) N(.),  h = N(r)
+    E_i = h . w_out + b_out[species]
+
+The forward pass keeps the layers' inputs as 8-bit checkpoints; the backward pass takes the weight gradients and silu'
+from them.  Plain products with the weights are torch's; everything between them is the library's.
+
+    python examples/routed_readout.py [steps]        (needs the GPU)
+"""
+import os
+import sys
+
+import torch
+
+sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+from molecular_dynamics_cell_amd import binding, inputs  # noqa: E402
+
+HIDDEN, EXPERTS, SLOTS, BLOCKS = 64, 4, 2, 2
+
+
+def density_features(O, K, L):
+    """rho of orbital sums O [n, K M]: for each l the weighted products over the monomials of degree l, a <= b."""
+    n = O.shape[0]
+    O = O.reshape(n, K, -1)
+    a, b = torch.triu_indices(K, K)
+    out, first = [], 0
+    factorial = (1, 1, 2, 6)
+    for l in range(L + 1):
+        w = torch.tensor([factorial[l] / (factorial[x] * factorial[y] * factorial[l - x - y])
+                          for x in range(l, -1, -1) for y in range(l - x, -1, -1)], dtype=O.dtype, device=O.device)
+        part = O[:, :, first:first + len(w)]
+        out.append(((part[:, a] * part[:, b]) * w).sum(-1))
+        first += len(w)
+    return torch.cat(out, 1)
+
+
+class Readout:
+    def __init__(self, m, width, species, seed=0):
+        self.m = m
+        g = torch.Generator(device="cuda")
+        g.manual_seed(seed)
+
+        def normal(*shape, size):
+            return torch.randn(*shape, generator=g, device="cuda") * size
+
+        H = HIDDEN
+        self.p = {"in": normal(H, width, size=width ** -0.5), "out": normal(H, size=0.1 * H ** -0.5),
+                  "shift": torch.zeros(species, device="cuda"), "norm0": torch.ones(H, device="cuda")}
+        for i in range(BLOCKS):
+            self.p |= {f"router{i}": normal(EXPERTS, H, size=H ** -0.5), f"gate{i}": normal(H, H, size=H ** -0.5),
+                       f"w1_{i}": normal(EXPERTS, 2 * H, H, size=H ** -0.5), f"b1_{i}": torch.zeros(EXPERTS, 2 * H, device="cuda"),
+                       f"w2_{i}": normal(EXPERTS, H, 2 * H, size=(2 * H) ** -0.5), f"b2_{i}": torch.zeros(EXPERTS, H, device="cuda"),
+                       f"post{i}": torch.ones(H, device="cuda"), f"scale{i}": torch.full((H,), 0.5, device="cuda"),
+                       f"pre{i}": torch.ones(H, device="cuda")}
+
+    def _segments(self, x, ends, weight, bias=None):
+        """Each expert's rows times its weight^T (rows past the last segment are not used: zeros)."""
+        out = x.new_zeros(x.shape[0], weight.shape[1])
+        for e in range(EXPERTS):
+            rows = slice(ends[e], ends[e + 1])
+            out[rows] = x[rows] @ weight[e].T if bias is None else torch.addmm(bias[e], x[rows], weight[e].T)
+        return out
+
+    def forward(self, x, types, chosen=None):
+        """Energies; chosen: the experts of each block's rows ([n, SLOTS] each), else the router's best."""
+        m, p = self.m, self.p
+        self.one = torch.tensor([0, x.shape[0]], dtype=torch.int32, device="cuda")
+        self.types = types
+        self.x = m.checkpoint_save(x)
+        r = x @ p["in"].T
+        _, h = m.norm_residual(r, pre_weight=p["norm0"], kind="rms")
+        self.kept = [(r, h)]
+        for i in range(BLOCKS):
+            score = h @ p[f"router{i}"].T
+            expert = torch.topk(score, SLOTS, dim=1)[1] if chosen is None else chosen[i]
+            weight = torch.softmax(score.gather(1, expert), 1)
+            offsets, source, position = m.route_plan(expert.to(torch.int32), EXPERTS)
+            ends = offsets.tolist()
+            rows = m.route_scatter(h, position, offsets)
+            rows_held = m.checkpoint_save(rows)
+            z = self._segments(rows, ends, p[f"w1_{i}"], p[f"b1_{i}"])
+            y, z_held, y_held = m.checkpoint_silu(z, save_output=True)
+            o = self._segments(y, ends, p[f"w2_{i}"], p[f"b2_{i}"])
+            block = m.route_combine(o, position, offsets, weight)
+            gate = h @ p[f"gate{i}"].T
+            r, h = m.norm_residual(r, block, gate, **self._vectors(i))
+            self.kept.append((r, h, expert, weight, position, offsets, ends, rows_held, z_held, y_held, o, block, gate))
+        return h @ p["out"] + p["shift"][types]
+
+    def _vectors(self, i):
+        return {"post_weight": self.p[f"post{i}"], "scale": self.p[f"scale{i}"], "pre_weight": self.p[f"pre{i}"], "kind": "rms"}
+
+    def backward(self, de):
+        """Gradients of every parameter for the gradient de of the energies."""
+        m, p, g = self.m, self.p, {}
+        g["out"] = de @ self.kept[-1][1]
+        g["shift"] = torch.zeros_like(p["shift"]).index_add_(0, self.types, de)
+        dh, dr = de.unsqueeze(1) * p["out"], None
+        for i in reversed(range(BLOCKS)):
+            r, h, expert, weight, position, offsets, ends, rows_held, z_held, y_held, o, block, gate = self.kept[i + 1]
+            before = self.kept[i][1]
+            dr, dblock, dgate, g[f"post{i}"], _, g[f"scale{i}"], g[f"pre{i}"], _ = m.norm_residual_backward(
+                dr, dh, r, block, gate, **self._vectors(i))
+            do, dweight = m.route_combine_backward(dblock, o, position, offsets, weight)
+            g[f"w2_{i}"], g[f"b2_{i}"] = m.checkpoint_weight_grad(do, y_held, offsets)
+            dz = m.checkpoint_silu_backward(self._segments(do, ends, p[f"w2_{i}"].transpose(1, 2)), z_held)
+            g[f"w1_{i}"], g[f"b1_{i}"] = m.checkpoint_weight_grad(dz, rows_held, offsets)
+            drows = self._segments(dz, ends, p[f"w1_{i}"].transpose(1, 2))
+            dlogit = weight * (dweight - (weight * dweight).sum(1, keepdim=True))
+            dscore = torch.zeros(h.shape[0], EXPERTS, device="cuda").scatter_(1, expert.long(), dlogit)
+            g[f"router{i}"] = dscore.T @ before
+            g[f"gate{i}"] = dgate.T @ before
+            dh = m.route_combine(drows, position, offsets) + dgate @ p[f"gate{i}"] + dscore @ p[f"router{i}"]
+        r, h = self.kept[0]
+        dr, _, _, _, _, _, g["norm0"], _ = m.norm_residual_backward(dr, dh, r, pre_weight=p["norm0"], kind="rms")
+        g["in"] = m.checkpoint_weight_grad(dr, self.x, self.one)[0][0]
+        return g
+
+
+def teacher():
+    """(features, species, atomic energies) of the water model, features and energies scaled to unit size."""
+    s, params = inputs.make_system(2), inputs.make_params(2)
+    m = binding.MPNN(params, "cuda")
+    m.build_neighbors(torch.tensor(s.pos, device="cuda"), torch.tensor(s.types, device="cuda"), s.box)
+    _, _, energy = m.energy_forces(atom_energy=True)
+    x = density_features(m.get_intermediate(1, 0), params.spec.K, params.spec.L)
+    types = torch.tensor(s.types, device="cuda").long()
+    x = (x / x.pow(2).mean(0).sqrt().clamp(min=1e-12)).float()
+    energy = ((energy - energy.mean()) / energy.std()).float()
+    return m, x, types, energy
+
+
+def fit(steps=200, rate=3e-3, report=None):
+    """Losses (mean square error of the atomic energies, in their variance) of `steps` Adam steps."""
+    m, x, types, target = teacher()
+    net = Readout(m, x.shape[1], int(types.max()) + 1)
+    state = {k: (torch.zeros_like(v), torch.zeros_like(v)) for k, v in net.p.items()}
+    losses = []
+    for t in range(1, steps + 1):
+        off = net.forward(x, types) - target
+        losses.append(float((off * off).mean()))
+        for k, g in net.backward(2 * off / len(off)).items():
+            a, b = state[k]
+            a.lerp_(g, 0.1)
+            b.lerp_(g * g, 0.001)
+            net.p[k] -= rate * (a / (1 - 0.9 ** t)) / ((b / (1 - 0.999 ** t)).sqrt() + 1e-8)
+        if report and (t % 20 == 0 or t == 1):
+            report(f"step {t:4d}: mean square error {losses[-1]:.4f} of the variance")
+    return losses
+
+
+if __name__ == "__main__":
+    fit(int(sys.argv[1]) if len(sys.argv) > 1 else 200, report=lambda line: print(line, flush=True))
