@@ -9,6 +9,9 @@
 // Operands on the bf16 matrix cores: x is exact in bf16 (7 bits and a power of two).  A bf16 dy is one as it stands;
 // an fp32 dy is cut into three bf16 terms of 8 bits each, top, middle and last, which add up to it exactly, so that
 // every product is exact and the sums are fp32 as with fp32 products.
+#include <algorithm>
+#include <type_traits>
+
 #include "impl.h"
 #include "rows.h"
 
@@ -19,7 +22,6 @@ namespace {
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float floatx16 __attribute__((ext_vector_type(16)));
 
-constexpr int kBN = 128;         // columns of x per block
 constexpr int kBK = 64;          // rows per stage: 8 chunks of 8, one matrix-core operand word each
 constexpr int kChunks = kBK / 8;
 
@@ -83,18 +85,12 @@ template <> struct QuadOf<float> { using type = Quad32; };
 template <> struct QuadOf<bf16> { using type = Quad16; };
 
 // `last`: the last of the four columns that is there; those past it repeat it (their results are not written).
-__device__ __forceinline__ void load_quad(Quad32 &q, const float *p) {
-    const float4 t = *reinterpret_cast<const float4 *>(p);
-    q.v[0] = t.x; q.v[1] = t.y; q.v[2] = t.z; q.v[3] = t.w;
-}
+__device__ __forceinline__ void load_quad(Quad32 &q, const float *p) { __builtin_memcpy(&q, p, sizeof q); }
 __device__ __forceinline__ void load_quad(Quad32 &q, const float *p, int last) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) q.v[j] = p[min(j, last)];
 }
-__device__ __forceinline__ void load_quad(Quad16 &q, const bf16 *p) {
-    const uint2 t = *reinterpret_cast<const uint2 *>(p);
-    q.v[0] = t.x; q.v[1] = t.y;
-}
+__device__ __forceinline__ void load_quad(Quad16 &q, const bf16 *p) { __builtin_memcpy(&q, p, sizeof q); }
 __device__ __forceinline__ void load_quad(Quad16 &q, const bf16 *p, int last) {
     const uint16_t *u = reinterpret_cast<const uint16_t *>(p);
     q.v[0] = (uint32_t)u[0] | (uint32_t)u[min(1, last)] << 16;
@@ -143,19 +139,24 @@ __device__ __forceinline__ void column(const Quad32 (&q)[8], int j, uint4 (&w)[3
 // LDS holds [chunk][position][8 rows]; column m of a tile of B columns sits at position (m % 4) (B / 4) + m / 4, so
 // that neighbouring threads write neighbouring words (no bank conflict), and the operand reads are neighbouring words
 // too.  The permutation only reorders the tile's results.
-// A wave owns 32 MT x 32 NT positions: BM = 128: 2 x 2 waves of 64 x 64; 64: 2 x 2 of 32 x 64; 32: 1 x 4 of 32 x 32.
-template <class T, int BM>
+// WM x WN waves own 32 MT x 32 NT positions each.
+// VEC: quads are loaded whole, at any alignment; the last one of a row is moved back to end with it, and the window of the
+// last stage to end with the array (what it holds of other rows is cleared when it is staged).  Otherwise (fewer than kBK
+// rows or 4 columns, or a moved quad of two groups) values are loaded one by one, rows and columns past the last repeat it.
+template <class T, int MT, int NT, int WM, int WN, bool VEC>
 __global__ __launch_bounds__(256, 2) void k_weight_grad(int out, int width, int groups, int n_experts, int64_t n, int64_t rows, int tiles_n,
                                                         int tiles, const int32_t *__restrict__ offsets, const T *__restrict__ dy, int64_t ld,
-                                                        const int8_t *__restrict__ codes, const uint8_t *__restrict__ scales, int vec_dy,
-                                                        int vec_x, int64_t slots, float *__restrict__ part, float *__restrict__ dweight,
+                                                        const int8_t *__restrict__ codes, const uint8_t *__restrict__ scales, int64_t slots, float *__restrict__ part, float *__restrict__ dweight,
                                                         float *__restrict__ dbias) {
     constexpr int TERMS = sizeof(T) == 4 ? 3 : 1;
-    constexpr int WN = BM == 32 ? 4 : 2, WM = 4 / WN;
-    constexpr int MT = BM / 32 / WM, NT = kBN / 32 / WN;
+    constexpr int BM = 32 * MT * WM, BN = 32 * NT * WN;
+    constexpr int QA = BM / 4, QX = BN / 4, GX = BN / 32;               // quads and groups of columns
+    constexpr int XT = (QX * kChunks + 255) / 256, ST = (GX * kBK + 255) / 256;   // x quads and scales per thread
+    static_assert(WM * WN == 4 && QA * kChunks <= 256, "four waves, one quad of dy a thread");
     using Quad = typename QuadOf<T>::type;
     __shared__ uint4 A[TERMS][kChunks][BM];
-    __shared__ uint4 B[kChunks][kBN];
+    __shared__ uint4 B[kChunks][BN];
+    __shared__ __attribute__((aligned(16))) float steps[2][GX][kBK];
     __shared__ float sums[kChunks][BM];
 
     // blocks are dealt to the XCDs in turn: give the tiles of one piece (the same rows) to one XCD
@@ -167,58 +168,77 @@ __global__ __launch_bounds__(256, 2) void k_weight_grad(int out, int width, int 
     pieces_of(offsets, pc.expert, n, rows, from, to);
     from += pc.piece * rows;
     to = min(to, from + rows);
-    const int o0 = tile / tiles_n * BM, c0 = tile % tiles_n * kBN;
+    const int o0 = tile / tiles_n * BM, c0 = tile % tiles_n * BN;
 
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int am = tid % (BM / 4), ak = tid / (BM / 4);       // dy: column quad, chunk (threads with ak < 8)
-    const int xm = tid % (kBN / 4), xk = tid / (kBN / 4);     // x
-    // columns past the last repeat it: their products are not written
-    const int ac = min(o0 + 4 * am, out - 1), xc = min(c0 + 4 * xm, width - 1);
-    const int alast = out - 1 - ac, xlast = width - 1 - xc;
-    // A wave's 16 rows and four groups of columns have 64 scales: a lane loads one and hands it to the lanes that need it.
-    const int sr = (wave * 2 + (lane >> 5)) * 8 + (lane & 7);
-    const int sg = min(c0 / 32 + ((lane >> 3) & 3), groups - 1);
-    const int sfrom = (lane & 32) + (xm >> 3) * 8;
-
-    // The loads of a stage: rows past the last repeat it and are cleared when they are staged, so that no load waits
-    // for a condition of another.
-    Quad a[8];
-    uint32_t x[8];
-    uint8_t scale;
-    uint32_t qa[8], qx[8], qs;      // distances from the stage's first row
-    auto rows_of = [&](int last) {
+    const int am = tid % QA, ak = tid / QA;                   // dy: column quad, chunk (threads with ak < 8)
+    // quads past the last (VEC) or columns past the last repeat it
+    const int ac = min(o0 + 4 * am, out - (VEC ? 4 : 1)), alast = out - 1 - ac;
+    const uint32_t abase = (uint32_t)ak * 8 * (uint32_t)ld + ac;
+    int xm[XT], xk[XT];
+    uint32_t xbase[XT];
+    bool x_in[XT];
 #pragma unroll
-        for (int r = 0; r < 8; ++r) {
-            qa[r] = (uint32_t)min(ak * 8 + r, last) * (uint32_t)ld + ac;
-            qx[r] = (uint32_t)min(xk * 8 + r, last) * (uint32_t)width + xc;
-        }
-        qs = (uint32_t)min(sr, last) * (uint32_t)groups + sg;
-    };
-    rows_of(kBK - 1);
+    for (int i = 0; i < XT; ++i) {
+        const int t = tid + i * 256;
+        xm[i] = t % QX;
+        xk[i] = t / QX;
+        x_in[i] = xk[i] < kChunks;
+        if (!x_in[i]) xk[i] = kChunks - 1;                    // loads what another thread does, stores nothing
+        xbase[i] = (uint32_t)xk[i] * 8 * (uint32_t)width + min(c0 + 4 * xm[i], width - (VEC ? 4 : 1));
+    }
+
+    Quad a[8];
+    uint32_t x[XT][8];
+    uint8_t scale[ST];
+    const auto window = [&](int64_t q0) { return VEC ? min(q0, n - kBK) : q0; };
+    // The loads of a stage: its rows from a uniform row address and this thread's distance from it.
     auto fetch = [&](int64_t q0) {
-        if (q0 + kBK > to) rows_of((int)(to - 1 - q0));      // the last stage
+        q0 = window(q0);
         const T *ap = dy + q0 * ld;
         const int8_t *xp = codes + q0 * width;
-        if (ak < kChunks) {
-            if (vec_dy) {
+        if constexpr (VEC) {
+            if (ak < kChunks) {
 #pragma unroll
-                for (int r = 0; r < 8; ++r) load_quad(a[r], ap + qa[r]);
-            } else {
-#pragma unroll
-                for (int r = 0; r < 8; ++r) load_quad(a[r], ap + qa[r], alast);
+                for (int r = 0; r < 8; ++r) load_quad(a[r], ap + r * ld + abase);
             }
-        }
-        if (vec_x) {
 #pragma unroll
-            for (int r = 0; r < 8; ++r) x[r] = *reinterpret_cast<const uint32_t *>(xp + qx[r]);
+            for (int i = 0; i < XT; ++i)
+#pragma unroll
+                for (int r = 0; r < 8; ++r) __builtin_memcpy(&x[i][r], xp + r * (int64_t)width + xbase[i], 4);
         } else {
+            const int last = (int)min(to - 1 - q0, (int64_t)(kBK - 1));
+            if (ak < kChunks) {
 #pragma unroll
-            for (int r = 0; r < 8; ++r) {
-                const uint8_t *p = reinterpret_cast<const uint8_t *>(xp + qx[r]);
-                x[r] = (uint32_t)p[0] | (uint32_t)p[min(1, xlast)] << 8 | (uint32_t)p[min(2, xlast)] << 16 | (uint32_t)p[min(3, xlast)] << 24;
+                for (int r = 0; r < 8; ++r) load_quad(a[r], ap + (uint32_t)min(ak * 8 + r, last) * (uint32_t)ld + ac, alast);
+            }
+#pragma unroll
+            for (int i = 0; i < XT; ++i) {
+                const int xc = min(c0 + 4 * xm[i], width - 1), xlast = width - 1 - xc;
+#pragma unroll
+                for (int r = 0; r < 8; ++r) {
+                    const uint8_t *u = reinterpret_cast<const uint8_t *>(xp) + (uint32_t)min(xk[i] * 8 + r, last) * (uint32_t)width + xc;
+                    x[i][r] = (uint32_t)u[0] | (uint32_t)u[min(1, xlast)] << 8 | (uint32_t)u[min(2, xlast)] << 16 | (uint32_t)u[min(3, xlast)] << 24;
+                }
             }
         }
-        scale = (scales + q0 * groups)[qs];
+    };
+    // The scales go through LDS a stage ahead: [group][row], as steps, 0 for rows that are not this stage's.
+    auto fetch_scales = [&](int64_t q0) {
+#pragma unroll
+        for (int i = 0; i < ST; ++i) {
+            const int t = min(tid + i * 256, GX * kBK - 1), g = min(c0 / 32 + t % GX, groups - 1);
+            scale[i] = scales[min(window(q0) + t / GX, to - 1) * groups + g];
+        }
+    };
+    auto store_scales = [&](int64_t q0, int buffer) {
+#pragma unroll
+        for (int i = 0; i < ST; ++i) {
+            const int t = min(tid + i * 256, GX * kBK - 1), r = t / GX;
+            const uint32_t bits = scale[i] == 255 ? 0x7fc00000u : (uint32_t)scale[i] << 23;
+            const int64_t q = window(q0) + r;
+            steps[buffer][t % GX][r] = q >= q0 && q < to ? __uint_as_float(bits) : 0.0f;
+        }
     };
 
     floatx16 acc[MT][NT];
@@ -228,14 +248,21 @@ __global__ __launch_bounds__(256, 2) void k_weight_grad(int out, int width, int 
         for (int j = 0; j < NT; ++j) acc[i][j] = (floatx16)(0.0f);
     float bias[4] = {};
     const int wm = wave / WN, wn = wave % WN;
-    if (from < to) fetch(from);
+    if (from < to) {
+        fetch_scales(from);
+        fetch(from);
+        store_scales(from, 0);
+        fetch_scales(min(from + kBK, to - 1));
+    }
+    int buffer = 0;
     for (int64_t q0 = from; q0 < to; q0 += kBK) {
         __syncthreads();
         if (q0 + kBK > to) {
 #pragma unroll
-            for (int r = 0; r < 8; ++r)
-                if (q0 + ak * 8 + r >= to) clear_quad(a[r]);
-            if (q0 + sr >= to) scale = 0;   // a step of zero
+            for (int r = 0; r < 8; ++r) {
+                const int64_t q = window(q0) + ak * 8 + r;
+                if (q < q0 || q >= to) clear_quad(a[r]);
+            }
         }
         if (ak < kChunks) {
             auto stage = [&](bool inf) {
@@ -244,7 +271,7 @@ __global__ __launch_bounds__(256, 2) void k_weight_grad(int out, int width, int 
                     uint4 w[TERMS];
                     column(a, j, w, inf);
 #pragma unroll
-                    for (int t = 0; t < TERMS; ++t) A[t][ak][j * (BM / 4) + am] = w[t];
+                    for (int t = 0; t < TERMS; ++t) A[t][ak][j * QA + am] = w[t];
                 }
             };
             if (__any(infinite(a))) stage(true);
@@ -256,21 +283,29 @@ __global__ __launch_bounds__(256, 2) void k_weight_grad(int out, int width, int 
                     for (int r = 0; r < 8; ++r) bias[j] += a[r].at(j);
             }
         }
-        const float held = __uint_as_float(scale == 255 ? 0x7fc00000u : (uint32_t)scale << 23);
-        float step[8];
 #pragma unroll
-        for (int r = 0; r < 8; ++r) step[r] = __shfl(held, sfrom + r);
+        for (int i = 0; i < XT; ++i) {
+            const float4 lo = *reinterpret_cast<const float4 *>(&steps[buffer][xm[i] / 8][xk[i] * 8]);
+            const float4 hi = *reinterpret_cast<const float4 *>(&steps[buffer][xm[i] / 8][xk[i] * 8 + 4]);
+            const float step[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            uint32_t v[8];
+            for (int j = 0; j < 4; ++j) {
+                uint32_t v[8];
 #pragma unroll
-            for (int r = 0; r < 8; ++r)   // (code + 128) step - 128 step: exact, and NaN where the step is
-                v[r] = __float_as_uint(fmaf((float)((x[r] ^ 0x80808080u) >> 8 * j & 255u), step[r], -128.0f * step[r]));
-            B[xk][j * (kBN / 4) + xm] = make_uint4(high_halves(v[0], v[1]), high_halves(v[2], v[3]), high_halves(v[4], v[5]),
-                                                   high_halves(v[6], v[7]));
+                for (int r = 0; r < 8; ++r)   // (code + 128) step - 128 step: exact, and NaN where the step is
+                    v[r] = __float_as_uint(fmaf((float)((x[i][r] ^ 0x80808080u) >> 8 * j & 255u), step[r], -128.0f * step[r]));
+                if (x_in[i])
+                    B[xk[i]][j * QX + xm[i]] = make_uint4(high_halves(v[0], v[1]), high_halves(v[2], v[3]), high_halves(v[4], v[5]),
+                                                          high_halves(v[6], v[7]));
+            }
         }
+        store_scales(q0 + kBK, buffer ^ 1);
+        buffer ^= 1;
         __syncthreads();
-        if (q0 + kBK < to) fetch(q0 + kBK);
+        if (q0 + kBK < to) {
+            fetch(q0 + kBK);
+            fetch_scales(min(q0 + 2 * kBK, to - 1));
+        }
 #pragma unroll
         for (int s = 0; s < kChunks / 2; ++s) {
             const int c = 2 * s + (lane >> 5);
@@ -298,19 +333,20 @@ __global__ __launch_bounds__(256, 2) void k_weight_grad(int out, int width, int 
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
             const int pm = (wm * MT + i) * 32 + 8 * (r / 4) + 4 * (lane >> 5) + r % 4;
-            const int o = o0 + 4 * (pm % (BM / 4)) + pm / (BM / 4);
-            if (o >= out) continue;
+            const int oq = o0 + 4 * (pm % QA), o = (VEC ? min(oq, out - 4) : oq) + pm / QA;
+            if (oq >= out || o >= out) continue;
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
                 const int pn = (wn * NT + j) * 32 + (lane & 31);
-                const int c = c0 + 4 * (pn % (kBN / 4)) + pn / (kBN / 4);
-                if (c < width) to_w[(int64_t)o * width + c] = acc[i][j][r];
+                const int cq = c0 + 4 * (pn % QX), c = (VEC ? min(cq, width - 4) : cq) + pn / QX;
+                if (cq < width && c < width) to_w[(int64_t)o * width + c] = acc[i][j][r];
             }
         }
     if (c0 == 0 && to_b) {
         if (ak < kChunks)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) sums[ak][4 * am + j] = bias[j];
+            for (int j = 0; j < 4; ++j)
+                if (o0 + 4 * am < out && ac + j >= o0) sums[ak][ac - o0 + j] = bias[j];   // a moved quad begins in the tile before
         __syncthreads();
         if (tid < BM && o0 + tid < out) {
             float s = 0.0f;
@@ -336,21 +372,21 @@ __global__ void k_weight_grad_sum(int n_experts, int64_t n, int64_t rows, int64_
     else if (dbias) dbias[(int64_t)e * out + (v - matrix)] = s;
 }
 
-template <class T, int BM>
+template <class T, int MT, int NT, int WM, int WN>
 Status launch(Context &cx, int64_t n, int out, int width, int n_experts, const int32_t *offsets, const T *dy, int64_t ld,
               const int8_t *codes, const uint8_t *scales, float *dweight, float *dbias) {
-    const int tiles_n = (width + kBN - 1) / kBN, tiles = tiles_n * ((out + BM - 1) / BM);
+    constexpr int BM = 32 * MT * WM, BN = 32 * NT * WN;
+    const int tiles_n = (width + BN - 1) / BN, tiles = tiles_n * ((out + BM - 1) / BM);
     // two blocks a CU, all at once: an expert's last piece may be short, so a few pieces less than fill them
     const int64_t want = std::max<int64_t>(1, 512 / tiles - n_experts);
     const int64_t rows = std::max<int64_t>(512, ((n + want - 1) / want + kBK - 1) / kBK * kBK);
     const int64_t pieces = n / rows + n_experts;              // at most; an expert of several pieces has more than `rows` rows
     const int64_t matrix = (int64_t)out * width, slots = n > rows ? 2 * (n / rows) : 0;   // an expert of p > 1 pieces fills p / 2 whole ones
     MPNN_TRY(cx.grow(cx.rows_ws, sizeof(float) * (size_t)(slots * (matrix + out))));
-    const int vec_dy = out % 4 == 0 && ld % 4 == 0 && (uintptr_t)dy % (4 * sizeof(T)) == 0;
-    const int vec_x = width % 4 == 0 && (uintptr_t)codes % 4 == 0;
-    k_weight_grad<T, BM><<<grid_xcd(pieces * tiles, 1), 256, 0, cx.stream>>>(out, width, (width + 31) / 32, n_experts, n, rows, tiles_n,
-                                                                             tiles, offsets, dy, ld, codes, scales, vec_dy, vec_x, slots,
-                                                                             cx.rows_ws.as<float>(), dweight, dbias);
+    const bool vec = n >= kBK && out >= 4 && width >= 4 && (width % 32 == 0 || width % 32 > 3);
+    auto *kernel = vec ? k_weight_grad<T, MT, NT, WM, WN, true> : k_weight_grad<T, MT, NT, WM, WN, false>;
+    kernel<<<grid_xcd(pieces * tiles, 1), 256, 0, cx.stream>>>(out, width, (width + 31) / 32, n_experts, n, rows, tiles_n, tiles, offsets,
+                                                               dy, ld, codes, scales, slots, cx.rows_ws.as<float>(), dweight, dbias);
     MPNN_HIP(hipGetLastError());
     if (slots) {
         k_weight_grad_sum<<<dim3(grid_for(matrix + out), n_experts), kBlock, 0, cx.stream>>>(n_experts, n, rows, slots, matrix, out, offsets,
@@ -363,9 +399,17 @@ Status launch(Context &cx, int64_t n, int out, int width, int n_experts, const i
 template <class T>
 Status weight_grad_t(Context &cx, int64_t n, int out, int width, int n_experts, const int32_t *offsets, const void *dy, int64_t ld,
                      const int8_t *codes, const uint8_t *scales, float *dweight, float *dbias) {
-    if (out <= 32) return launch<T, 32>(cx, n, out, width, n_experts, offsets, (const T *)dy, ld, codes, scales, dweight, dbias);
-    if (out <= 64) return launch<T, 64>(cx, n, out, width, n_experts, offsets, (const T *)dy, ld, codes, scales, dweight, dbias);
-    return launch<T, 128>(cx, n, out, width, n_experts, offsets, (const T *)dy, ld, codes, scales, dweight, dbias);
+    // tiles of 32, 64 or 128 x 128: of the wider ones tried, 64 x 192, 64 x 320 and 64 x 128 were slower at 128,000 rows
+    // 312 -> 128 (81, 78, 86 us, 70 us with 128 x 128; bf16 52, 49, 49 and 44 us)
+    constexpr std::integral_constant<int, 1> one{};
+    constexpr std::integral_constant<int, 2> two{};
+    constexpr std::integral_constant<int, 4> four{};
+    auto tile = [&](auto mt, auto nt, auto wm, auto wn) -> Status {
+        return launch<T, mt(), nt(), wm(), wn()>(cx, n, out, width, n_experts, offsets, (const T *)dy, ld, codes, scales, dweight, dbias);
+    };
+    if (out <= 32) return tile(one, one, one, four);
+    if (out <= 64) return tile(one, two, two, two);
+    return tile(two, two, two, two);
 }
 
 }  // namespace
