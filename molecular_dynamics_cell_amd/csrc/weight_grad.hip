@@ -159,8 +159,10 @@ __global__ __launch_bounds__(256, 2) void k_weight_grad(int out, int width, int 
     __shared__ __attribute__((aligned(16))) float steps[2][GX][kBK];
     __shared__ float sums[kChunks][BM];
 
-    // blocks are dealt to the XCDs in turn: give the tiles of one piece (the same rows) to one XCD
-    const int64_t number = xcd_block();
+    // Blocks are dealt to the XCDs in turn: where experts are cut into pieces, give the tiles of one piece (the same rows)
+    // to one XCD; with an expert a piece deal each expert's tiles to all of them, since experts differ in length
+    // (16,384 rows 1024 -> 1024 x 8 with shares from 4 to 20 %: bf16 111 -> 92 us, fp32 254 -> 177 us).
+    const int64_t number = n > rows ? xcd_block() : (int64_t)blockIdx.x;
     const int tile = (int)(number % tiles);
     const Piece pc = find_piece(offsets, n_experts, n, rows, (int)(number / tiles), -1);
     if (pc.expert < 0) return;
