@@ -37,6 +37,9 @@ struct Piece {
     int slot;                    // partial sums of the expert's first piece (pieces > 1)
 };
 
+// Floats of a piece's partial sums, dW then db, in whole 16 bytes.
+__host__ __device__ __forceinline__ int64_t slot_size(int64_t values) { return (values + 3) / 4 * 4; }
+
 // The piece with the given number, by one wave: a prefix sum over the experts, 64 at a time.  want_expert >= 0 looks
 // that expert up instead.
 __device__ __forceinline__ Piece find_piece(const int32_t *offsets, int n_experts, int64_t n, int64_t rows, int number, int want_expert) {
@@ -136,9 +139,10 @@ __device__ __forceinline__ void column(const Quad32 (&q)[8], int j, uint4 (&w)[3
 
 // Layout.  Both operands have the rows as their slow axis, while a matrix-core operand word holds eight of them for
 // one column: a thread loads 4 neighbouring columns of 8 rows, turns them in registers and writes four 16-byte words.
-// LDS holds [chunk][position][8 rows]; column m of a tile of B columns sits at position (m % 4) (B / 4) + m / 4, so
+// LDS holds [chunk][position][8 rows].  Column m of dy's tile of B columns sits at position (m % 4) (B / 4) + m / 4, so
 // that neighbouring threads write neighbouring words (no bank conflict), and the operand reads are neighbouring words
-// too.  The permutation only reorders the tile's results.
+// too; the permutation only reorders the tile's results.  x's columns are placed so that a lane ends up with NT
+// neighbouring ones, which it stores together.
 // WM x WN waves own 32 MT x 32 NT positions each.
 // VEC: quads are loaded whole, at any alignment; the last one of a row is moved back to end with it, and the window of the
 // last stage to end with the array (what it holds of other rows is cleared when it is staged).  Otherwise (fewer than kBK
@@ -162,9 +166,9 @@ __global__ __launch_bounds__(256, 2) void k_weight_grad(int out, int width, int 
     // Blocks are dealt to the XCDs in turn: where experts are cut into pieces, give the tiles of one piece (the same rows)
     // to one XCD; with an expert a piece deal each expert's tiles to all of them, since experts differ in length
     // (16,384 rows 1024 -> 1024 x 8 with shares from 4 to 20 %: bf16 111 -> 92 us, fp32 254 -> 177 us).
-    const int64_t number = n > rows ? xcd_block() : (int64_t)blockIdx.x;
-    const int tile = (int)(number % tiles);
-    const Piece pc = find_piece(offsets, n_experts, n, rows, (int)(number / tiles), -1);
+    const uint32_t number = n > rows ? (uint32_t)xcd_block() : blockIdx.x;
+    const int tile = (int)(number % (uint32_t)tiles);
+    const Piece pc = find_piece(offsets, n_experts, n, rows, (int)(number / (uint32_t)tiles), -1);
     if (pc.expert < 0) return;
     int64_t from, to;
     pieces_of(offsets, pc.expert, n, rows, from, to);
@@ -189,6 +193,9 @@ __global__ __launch_bounds__(256, 2) void k_weight_grad(int out, int width, int 
         if (!x_in[i]) xk[i] = kChunks - 1;                    // loads what another thread does, stores nothing
         xbase[i] = (uint32_t)xk[i] * 8 * (uint32_t)width + min(c0 + 4 * xm[i], width - (VEC ? 4 : 1));
     }
+
+    // column c of the tile: wave c / (32 NT), there lane c / NT of tile c % NT
+    const auto x_place = [](int c) { return (c / (32 * NT) * NT + c % NT) * 32 + c / NT % 32; };
 
     Quad a[8];
     uint32_t x[XT][8];
@@ -297,7 +304,7 @@ __global__ __launch_bounds__(256, 2) void k_weight_grad(int out, int width, int 
                 for (int r = 0; r < 8; ++r)   // (code + 128) step - 128 step: exact, and NaN where the step is
                     v[r] = __float_as_uint(fmaf((float)((x[i][r] ^ 0x80808080u) >> 8 * j & 255u), step[r], -128.0f * step[r]));
                 if (x_in[i])
-                    B[xk[i]][j * QX + xm[i]] = make_uint4(high_halves(v[0], v[1]), high_halves(v[2], v[3]), high_halves(v[4], v[5]),
+                    B[xk[i]][x_place(4 * xm[i] + j)] = make_uint4(high_halves(v[0], v[1]), high_halves(v[2], v[3]), high_halves(v[4], v[5]),
                                                           high_halves(v[6], v[7]));
             }
         }
@@ -328,7 +335,7 @@ __global__ __launch_bounds__(256, 2) void k_weight_grad(int out, int width, int 
     const int64_t matrix = (int64_t)out * width;
     const bool whole = pc.pieces == 1;
     if (!whole && pc.slot + pc.piece >= slots) return;   // offsets that do not ascend name more pieces than there are
-    float *to_w = whole ? dweight + pc.expert * matrix : part + (int64_t)(pc.slot + pc.piece) * (matrix + out);
+    float *to_w = whole ? dweight + pc.expert * matrix : part + (int64_t)(pc.slot + pc.piece) * slot_size(matrix + out);
     float *to_b = whole ? (dbias ? dbias + (int64_t)pc.expert * out : nullptr) : to_w + matrix;
 #pragma unroll
     for (int i = 0; i < MT; ++i)
@@ -337,11 +344,20 @@ __global__ __launch_bounds__(256, 2) void k_weight_grad(int out, int width, int 
             const int pm = (wm * MT + i) * 32 + 8 * (r / 4) + 4 * (lane >> 5) + r % 4;
             const int oq = o0 + 4 * (pm % QA), o = (VEC ? min(oq, out - 4) : oq) + pm / QA;
             if (oq >= out || o >= out) continue;
+            const int cl = c0 + wn * 32 * NT + NT * (lane & 31);          // this lane's NT columns
+            float *row = to_w + (int64_t)o * width;
+            if (!VEC || cl + NT > width || (cl + NT > width - 4 && width % 4)) {
+                // at the row's end: the last quad was moved back to end with it
 #pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                const int pn = (wn * NT + j) * 32 + (lane & 31);
-                const int cq = c0 + 4 * (pn % QX), c = (VEC ? min(cq, width - 4) : cq) + pn / QX;
-                if (cq < width && c < width) to_w[(int64_t)o * width + c] = acc[i][j][r];
+                for (int j = 0; j < NT; ++j) {
+                    const int cq = (cl + j) / 4 * 4, c = (VEC ? min(cq, width - 4) : cq) + (cl + j) % 4;
+                    if (cq < width && c < width) row[c] = acc[i][j][r];
+                }
+            } else {
+                float v[NT];
+#pragma unroll
+                for (int j = 0; j < NT; ++j) v[j] = acc[i][j][r];
+                __builtin_memcpy(row + cl, v, sizeof v);
             }
         }
     if (c0 == 0 && to_b) {
@@ -359,19 +375,37 @@ __global__ __launch_bounds__(256, 2) void k_weight_grad(int out, int width, int 
     }
 }
 
-// The pieces of each expert that has several, added in their order.
-__global__ void k_weight_grad_sum(int n_experts, int64_t n, int64_t rows, int64_t slots, int64_t matrix, int out, const int32_t *__restrict__ offsets,
-                                  const float *__restrict__ part, float *__restrict__ dweight, float *__restrict__ dbias) {
-    const int e = blockIdx.y;
+// The pieces of each expert that has several, added in a fixed order: a thread takes four values of every fourth piece,
+// then the four sums of a value are added.
+__global__ __launch_bounds__(256) void k_weight_grad_sum(int n_experts, int64_t n, int64_t rows, int64_t slots, int64_t matrix, int out,
+                                                         const int32_t *__restrict__ offsets, const float *__restrict__ part,
+                                                         float *__restrict__ dweight, float *__restrict__ dbias) {
+    __shared__ float4 sums[4][64];
+    const int e = blockIdx.y, lane = threadIdx.x & 63, slice = threadIdx.x >> 6;
     const Piece pc = find_piece(offsets, n_experts, n, rows, 0, e);
-    const int64_t v = (int64_t)blockIdx.x * kBlock + threadIdx.x, values = matrix + out;
-    if (pc.pieces <= 1 || v >= values || pc.slot + (int64_t)pc.pieces > slots) return;
-    float s = 0.0f;
-    const float *p = part + (int64_t)pc.slot * values + v;
+    if (pc.pieces <= 1 || pc.slot + (int64_t)pc.pieces > slots) return;
+    const int64_t stride = slot_size(matrix + out), v = ((int64_t)blockIdx.x * 64 + lane) * 4;
+    const float *p = part + (int64_t)pc.slot * stride + min(v, stride - 4);
+    float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 8
-    for (int i = 0; i < pc.pieces; ++i) s += p[i * values];
-    if (v < matrix) dweight[e * matrix + v] = s;
-    else if (dbias) dbias[(int64_t)e * out + (v - matrix)] = s;
+    for (int i = slice; i < pc.pieces; i += 4) {
+        const float4 t = *reinterpret_cast<const float4 *>(p + i * stride);
+        s.x += t.x; s.y += t.y; s.z += t.z; s.w += t.w;
+    }
+    sums[slice][lane] = s;
+    __syncthreads();
+    if (slice != 0) return;
+#pragma unroll
+    for (int k = 1; k < 4; ++k) {
+        const float4 t = sums[k][lane];
+        s.x += t.x; s.y += t.y; s.z += t.z; s.w += t.w;
+    }
+    const float o[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        if (v + j < matrix) dweight[e * matrix + v + j] = o[j];
+        else if (v + j < matrix + out && dbias) dbias[(int64_t)e * out + (v + j - matrix)] = o[j];
+    }
 }
 
 template <class T, int MT, int NT, int WM, int WN>
@@ -384,14 +418,14 @@ Status launch(Context &cx, int64_t n, int out, int width, int n_experts, const i
     const int64_t rows = std::max<int64_t>(512, ((n + want - 1) / want + kBK - 1) / kBK * kBK);
     const int64_t pieces = n / rows + n_experts;              // at most; an expert of several pieces has more than `rows` rows
     const int64_t matrix = (int64_t)out * width, slots = n > rows ? 2 * (n / rows) : 0;   // an expert of p > 1 pieces fills p / 2 whole ones
-    MPNN_TRY(cx.grow(cx.rows_ws, sizeof(float) * (size_t)(slots * (matrix + out))));
+    MPNN_TRY(cx.grow(cx.rows_ws, sizeof(float) * (size_t)(slots * slot_size(matrix + out))));
     const bool vec = n >= kBK && out >= 4 && width >= 4 && (width % 32 == 0 || width % 32 > 3);
     auto *kernel = vec ? k_weight_grad<T, MT, NT, WM, WN, true> : k_weight_grad<T, MT, NT, WM, WN, false>;
     kernel<<<grid_xcd(pieces * tiles, 1), 256, 0, cx.stream>>>(out, width, (width + 31) / 32, n_experts, n, rows, tiles_n, tiles, offsets,
                                                                dy, ld, codes, scales, slots, cx.rows_ws.as<float>(), dweight, dbias);
     MPNN_HIP(hipGetLastError());
     if (slots) {
-        k_weight_grad_sum<<<dim3(grid_for(matrix + out), n_experts), kBlock, 0, cx.stream>>>(n_experts, n, rows, slots, matrix, out, offsets,
+        k_weight_grad_sum<<<dim3(grid_for(slot_size(matrix + out) / 4, 64), n_experts), 256, 0, cx.stream>>>(n_experts, n, rows, slots, matrix, out, offsets,
                                                                                              cx.rows_ws.as<float>(), dweight, dbias);
         MPNN_HIP(hipGetLastError());
     }
