@@ -61,12 +61,14 @@ __device__ __forceinline__ Piece find_piece(const int32_t *offsets, int n_expert
         }
         const uint64_t hit = __ballot(want_expert >= 0 ? e == want_expert : e < n_experts && number < before + s);
         if (hit) {
-            const int l = __ffsll((unsigned long long)hit) - 1;
-            const int pc = __shfl(c, l);
-            return Piece{base + l, number - (before + __shfl(s, l) - pc), pc, slots + __shfl(t, l) - __shfl(m, l)};
+            // the same in all lanes, and known to be: what follows from it is computed once a wave
+            const int l = __builtin_amdgcn_readfirstlane(__ffsll((unsigned long long)hit) - 1);
+            const auto of = [&](int v) { return __builtin_amdgcn_readlane(v, l); };
+            const int pc = of(c);
+            return Piece{base + l, number - (before + of(s) - pc), pc, slots + of(t) - of(m)};
         }
-        before += __shfl(s, 63);
-        slots += __shfl(t, 63);
+        before += __builtin_amdgcn_readlane(s, 63);
+        slots += __builtin_amdgcn_readlane(t, 63);
     }
     return Piece{-1, 0, 0, 0};
 }
@@ -103,7 +105,7 @@ __device__ __forceinline__ void clear_quad(Quad32 &q) { q.v[0] = q.v[1] = q.v[2]
 __device__ __forceinline__ void clear_quad(Quad16 &q) { q.v[0] = q.v[1] = 0u; }
 
 // Column j of eight rows as the operand words of each term.
-__device__ __forceinline__ void column(const Quad16 (&q)[8], int j, uint4 (&w)[1], bool) {
+__device__ __forceinline__ void column(const Quad16 (&q)[8], int j, uint4 (&w)[1]) {
     uint32_t p[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -114,18 +116,19 @@ __device__ __forceinline__ bool infinite(const Quad16 (&)[8]) { return false; }
 __device__ __forceinline__ bool infinite(const Quad32 (&q)[8]) {
     float m = 0.0f;
 #pragma unroll
-    for (int r = 0; r < 8; ++r) m = fmaxf(m, fmaxf(fmaxf(fabsf(q[r].v[0]), fabsf(q[r].v[1])), fmaxf(fabsf(q[r].v[2]), fabsf(q[r].v[3]))));
+    for (int r = 0; r < 8; ++r) {
+        m = fmaxf(fmaxf(m, fabsf(q[r].v[0])), fabsf(q[r].v[1]));
+        m = fmaxf(fmaxf(m, fabsf(q[r].v[2])), fabsf(q[r].v[3]));
+    }
     return m == __uint_as_float(0x7f800000u);
 }
-// `inf`: an infinity may be among the values; nothing is left of one after its first term.
-__device__ __forceinline__ void column(const Quad32 (&q)[8], int j, uint4 (&w)[3], bool inf) {
+__device__ __forceinline__ void column(const Quad32 (&q)[8], int j, uint4 (&w)[3]) {
     uint32_t t[3][8];
 #pragma unroll
     for (int r = 0; r < 8; ++r) {
         const float v = q[r].v[j];
         const uint32_t top = __float_as_uint(v) & 0xffff0000u;
-        float left = v - __uint_as_float(top);                         // exact: 16 significant bits
-        if (inf) left = fabsf(v) == __uint_as_float(0x7f800000u) ? 0.0f : left;
+        const float left = v - __uint_as_float(top);                   // exact: 16 significant bits
         const uint32_t middle = __float_as_uint(left) & 0xffff0000u;
         t[0][r] = top;
         t[1][r] = middle;
@@ -179,8 +182,9 @@ __global__ __launch_bounds__(256, 2) void k_weight_grad(int out, int width, int 
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int am = tid % QA, ak = tid / QA;                   // dy: column quad, chunk (threads with ak < 8)
     // quads past the last (VEC) or columns past the last repeat it
-    const int ac = min(o0 + 4 * am, out - (VEC ? 4 : 1)), alast = out - 1 - ac;
-    const uint32_t abase = (uint32_t)ak * 8 * (uint32_t)ld + ac;
+    const int ac = min(o0 + 4 * am, out - (VEC ? 4 : 1));
+    [[maybe_unused]] const int alast = out - 1 - ac;
+    const uint32_t abase = ((uint32_t)ak * 8 * (uint32_t)ld + ac) * sizeof(T);      // bytes; ld is at most 2^24
     int xm[XT], xk[XT];
     uint32_t xbase[XT];
     bool x_in[XT];
@@ -200,7 +204,13 @@ __global__ __launch_bounds__(256, 2) void k_weight_grad(int out, int width, int 
     Quad a[8];
     uint32_t x[XT][8];
     uint8_t scale[ST];
-    const auto window = [&](int64_t q0) { return VEC ? min(q0, n - kBK) : q0; };
+    uint32_t sbase[ST];
+#pragma unroll
+    for (int i = 0; i < ST; ++i) {
+        const int t = min(tid + i * 256, GX * kBK - 1);
+        sbase[i] = (uint32_t)(t / GX) * (uint32_t)groups + min(c0 / 32 + t % GX, groups - 1);
+    }
+    const auto window = [&](int64_t q0) { return VEC ? min(q0, n - kBK) : min(q0, to - 1); };
     // The loads of a stage: its rows from a uniform row address and this thread's distance from it.
     auto fetch = [&](int64_t q0) {
         q0 = window(q0);
@@ -209,7 +219,7 @@ __global__ __launch_bounds__(256, 2) void k_weight_grad(int out, int width, int 
         if constexpr (VEC) {
             if (ak < kChunks) {
 #pragma unroll
-                for (int r = 0; r < 8; ++r) load_quad(a[r], ap + r * ld + abase);
+                for (int r = 0; r < 8; ++r) load_quad(a[r], reinterpret_cast<const T *>(reinterpret_cast<const char *>(ap + r * ld) + abase));
             }
 #pragma unroll
             for (int i = 0; i < XT; ++i)
@@ -234,19 +244,21 @@ __global__ __launch_bounds__(256, 2) void k_weight_grad(int out, int width, int 
     };
     // The scales go through LDS a stage ahead: [group][row], as steps, 0 for rows that are not this stage's.
     auto fetch_scales = [&](int64_t q0) {
+        const int64_t w = window(q0);
+        const uint8_t *sp = scales + w * groups;
 #pragma unroll
-        for (int i = 0; i < ST; ++i) {
-            const int t = min(tid + i * 256, GX * kBK - 1), g = min(c0 / 32 + t % GX, groups - 1);
-            scale[i] = scales[min(window(q0) + t / GX, to - 1) * groups + g];
-        }
+        for (int i = 0; i < ST; ++i) scale[i] = VEC ? sp[sbase[i]] : sp[min((int64_t)sbase[i], (to - w) * groups - 1)];
     };
     auto store_scales = [&](int64_t q0, int buffer) {
 #pragma unroll
         for (int i = 0; i < ST; ++i) {
             const int t = min(tid + i * 256, GX * kBK - 1), r = t / GX;
-            const uint32_t bits = scale[i] == 255 ? 0x7fc00000u : (uint32_t)scale[i] << 23;
-            const int64_t q = window(q0) + r;
-            steps[buffer][t % GX][r] = q >= q0 && q < to ? __uint_as_float(bits) : 0.0f;
+            float step = __uint_as_float(scale[i] == 255 ? 0x7fc00000u : (uint32_t)scale[i] << 23);
+            if (q0 + kBK > to) {
+                const int64_t q = window(q0) + r;
+                if (q < q0 || q >= to) step = 0.0f;
+            }
+            steps[buffer][t % GX][r] = step;
         }
     };
 
@@ -261,7 +273,7 @@ __global__ __launch_bounds__(256, 2) void k_weight_grad(int out, int width, int 
         fetch_scales(from);
         fetch(from);
         store_scales(from, 0);
-        fetch_scales(min(from + kBK, to - 1));
+        fetch_scales(from + kBK);
     }
     int buffer = 0;
     for (int64_t q0 = from; q0 < to; q0 += kBK) {
@@ -274,17 +286,24 @@ __global__ __launch_bounds__(256, 2) void k_weight_grad(int out, int width, int 
             }
         }
         if (ak < kChunks) {
-            auto stage = [&](bool inf) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    uint4 w[TERMS];
-                    column(a, j, w, inf);
+            for (int j = 0; j < 4; ++j) {
+                uint4 w[TERMS];
+                column(a, j, w);
 #pragma unroll
-                    for (int t = 0; t < TERMS; ++t) A[t][ak][j * QA + am] = w[t];
+                for (int t = 0; t < TERMS; ++t) A[t][ak][j * QA + am] = w[t];
+            }
+            if (TERMS > 1 && __any(infinite(a))) {
+                // the terms of an infinity after the first are nothing, not the difference of two infinities
+                for (int e = 0; e < 32; ++e) {
+                    float v = 0.0f;
+#pragma unroll
+                    for (int f = 0; f < 32; ++f) v = e == f ? a[f >> 2].at(f & 3) : v;
+                    if (fabsf(v) == __uint_as_float(0x7f800000u))
+#pragma unroll
+                        for (int t = 1; t < TERMS; ++t) reinterpret_cast<uint16_t *>(&A[t][ak][(e & 3) * QA + am])[e >> 2] = 0;
                 }
-            };
-            if (__any(infinite(a))) stage(true);
-            else stage(false);
+            }
             if (c0 == 0) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
@@ -301,8 +320,7 @@ __global__ __launch_bounds__(256, 2) void k_weight_grad(int out, int width, int 
             for (int j = 0; j < 4; ++j) {
                 uint32_t v[8];
 #pragma unroll
-                for (int r = 0; r < 8; ++r)   // (code + 128) step - 128 step: exact, and NaN where the step is
-                    v[r] = __float_as_uint(fmaf((float)((x[i][r] ^ 0x80808080u) >> 8 * j & 255u), step[r], -128.0f * step[r]));
+                for (int r = 0; r < 8; ++r) v[r] = __float_as_uint((float)(int8_t)(x[i][r] >> 8 * j) * step[r]);   // exact
                 if (x_in[i])
                     B[xk[i]][x_place(4 * xm[i] + j)] = make_uint4(high_halves(v[0], v[1]), high_halves(v[2], v[3]), high_halves(v[4], v[5]),
                                                           high_halves(v[6], v[7]));
@@ -313,7 +331,7 @@ __global__ __launch_bounds__(256, 2) void k_weight_grad(int out, int width, int 
         __syncthreads();
         if (q0 + kBK < to) {
             fetch(q0 + kBK);
-            fetch_scales(min(q0 + 2 * kBK, to - 1));
+            fetch_scales(q0 + 2 * kBK);
         }
 #pragma unroll
         for (int s = 0; s < kChunks / 2; ++s) {
