@@ -100,7 +100,8 @@ class Readout:
         """Gradients of every parameter for the gradient de of the energies."""
         m, p, g = self.m, self.p, {}
         g["out"] = de @ self.kept[-1][1]
-        g["shift"] = torch.zeros_like(p["shift"]).index_add_(0, self.types, de)
+        # (a sum per species without atomics, so that a fit gives the same bits again)
+        g["shift"] = (self.types == torch.arange(len(p["shift"]), device="cuda").unsqueeze(1)).float() @ de
         dh, dr = de.unsqueeze(1) * p["out"], None
         for i in reversed(range(BLOCKS)):
             r, h, expert, weight, position, offsets, ends, rows_held, z_held, y_held, o, block, gate = self.kept[i + 1]
