@@ -431,8 +431,11 @@ Status launch(Context &cx, int64_t n, int out, int width, int n_experts, const i
               const int8_t *codes, const uint8_t *scales, float *dweight, float *dbias) {
     constexpr int BM = 32 * MT * WM, BN = 32 * NT * WN;
     const int tiles_n = (width + BN - 1) / BN, tiles = tiles_n * ((out + BM - 1) / BM);
-    // two blocks a CU, all at once: an expert's last piece may be short, so a few pieces less than fill them
-    const int64_t want = std::max<int64_t>(1, 512 / tiles - n_experts);
+    // The blocks that run at once, two a CU of the widest tile, three of the narrower ones; an expert's last piece may be
+    // short, so a few pieces less than fill them.  (128,000 rows 312 -> 128 x 5 fp32 with one, two and three blocks a CU:
+    // 86, 65 and 79 us; 2,000,000 rows 108 -> 64 bf16: 179, 119 and 109 us.)
+    constexpr int kResident = BM > 64 ? 512 : 768;
+    const int64_t want = std::max<int64_t>(1, kResident / tiles - n_experts);
     const int64_t rows = std::max<int64_t>(512, ((n + want - 1) / want + kBK - 1) / kBK * kBK);
     const int64_t pieces = n / rows + n_experts;              // at most; an expert of several pieces has more than `rows` rows
     const int64_t matrix = (int64_t)out * width, slots = n > rows ? 2 * (n / rows) : 0;   // an expert of p > 1 pieces fills p / 2 whole ones
