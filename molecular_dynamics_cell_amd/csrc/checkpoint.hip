@@ -39,9 +39,11 @@ template <class T> __device__ __forceinline__ float group_max(const float (&v)[C
 }
 
 // sigma(z) and 1 - sigma(z) from a = exp(-|z|) <= 1, without a reciprocal of a large number (1 / (1 + exp(-z)) would pass
-// through one that the hardware's reciprocal flushes to zero): r = 1 / (1 + a) and a r.
+// through one that the hardware's reciprocal flushes to zero): r = 1 / (1 + a) and a r. The reciprocal of 1 .. 2 gets one
+// Newton step, r + r (1 - (1 + a) r): its own error of an ulp moves more codes across a rounding edge than exp's does.
 __device__ __forceinline__ void sigmoids(float z, float &s, float &rest) {
-    const float a = expf(-fabsf(z)), r = __builtin_amdgcn_rcpf(1.0f + a), ar = a * r;
+    const float a = expf(-fabsf(z)), r0 = __builtin_amdgcn_rcpf(1.0f + a);
+    const float r = fmaf(r0, fmaf(-(1.0f + a), r0, 1.0f), r0), ar = a * r;
     s = z >= 0.0f ? r : ar;
     rest = z >= 0.0f ? ar : r;
 }
