@@ -73,6 +73,23 @@ __device__ __forceinline__ Piece find_piece(const int32_t *offsets, int n_expert
     return Piece{-1, 0, 0, 0};
 }
 
+// With an expert a piece (and at most 64 experts, one a lane): the expert whose tiles are the number-th to start.  The
+// longest experts start first, `row` of them on all CUs, and the next ones in turn from the shortest and the longest, so that
+// a CU that holds two blocks holds a long and a short one (16,384 rows 1024 -> 1024 x 8, shares from 4 to 20 %: bf16 85 -> 79 us,
+// fp32 163 -> 156 us).
+__device__ __forceinline__ int expert_in_turn(const int32_t *offsets, int n_experts, int64_t n, int row, int number) {
+    const int lane = threadIdx.x & 63, e = min(lane, n_experts - 1);
+    const int from = (int)min(max((int64_t)offsets[e], (int64_t)0), n), to = (int)min(max((int64_t)offsets[e + 1], (int64_t)from), n);
+    const int length = to - from;
+    int rank = 0;
+    for (int f = 0; f < n_experts; ++f) {
+        const int other = __builtin_amdgcn_readlane(length, f);
+        rank += other > length || (other == length && f < lane);
+    }
+    const int in = number % row, want = (number / row & 1) && number - in + row <= n_experts ? number - in + row - 1 - in : number;
+    return __ffsll((unsigned long long)__ballot(lane < n_experts && rank == want)) - 1;
+}
+
 __device__ __forceinline__ uint32_t low_halves(uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x05040100u); }
 __device__ __forceinline__ uint32_t high_halves(uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x07060302u); }
 
@@ -142,10 +159,10 @@ __device__ __forceinline__ void column(const Quad32 (&q)[8], int j, uint4 (&w)[3
 
 // Layout.  Both operands have the rows as their slow axis, while a matrix-core operand word holds eight of them for
 // one column: a thread loads 4 neighbouring columns of 8 rows, turns them in registers and writes four 16-byte words.
-// LDS holds [chunk][position][8 rows].  Column m of dy's tile of B columns sits at position (m % 4) (B / 4) + m / 4, so
+// LDS holds [chunk][position][8 rows].  Column m of a tile of B columns sits at position (m % 4) (B / 4) + m / 4, so
 // that neighbouring threads write neighbouring words (no bank conflict), and the operand reads are neighbouring words
-// too; the permutation only reorders the tile's results.  x's columns are placed so that a lane ends up with NT
-// neighbouring ones, which it stores together.
+// too; the permutation only reorders the tile's results (of 128 columns of x a lane ends up with NT neighbouring ones,
+// which it stores together).
 // WM x WN waves own 32 MT x 32 NT positions each.
 // VEC: quads are loaded whole, at any alignment; the last one of a row is moved back to end with it, and the window of the
 // last stage to end with the array (what it holds of other rows is cleared when it is staged).  Otherwise (fewer than kBK
@@ -159,7 +176,8 @@ __global__ __launch_bounds__(256, 2) void k_weight_grad(int out, int width, int 
     constexpr int BM = 32 * MT * WM, BN = 32 * NT * WN;
     constexpr int QA = BM / 4, QX = BN / 4, GX = BN / 32;               // quads and groups of columns
     constexpr int XT = (QX * kChunks + 255) / 256, ST = (GX * kBK + 255) / 256;   // x quads and scales per thread
-    static_assert(WM * WN == 4 && QA * kChunks <= 256, "four waves, one quad of dy a thread");
+    constexpr bool kAllA = QA * kChunks == 256, kAllX = QX * kChunks % 256 == 0;   // every thread has a quad to stage
+    static_assert(BN == 128 && WM * WN == 4 && QA * kChunks <= 256, "four waves, one quad of dy a thread");
     using Quad = typename QuadOf<T>::type;
     __shared__ uint4 A[TERMS][kChunks][BM];
     __shared__ uint4 B[kChunks][BN];
@@ -171,7 +189,9 @@ __global__ __launch_bounds__(256, 2) void k_weight_grad(int out, int width, int 
     // (16,384 rows 1024 -> 1024 x 8 with shares from 4 to 20 %: bf16 111 -> 92 us, fp32 254 -> 177 us).
     const uint32_t number = n > rows ? (uint32_t)xcd_block() : blockIdx.x;
     const int tile = (int)(number % (uint32_t)tiles);
-    const Piece pc = find_piece(offsets, n_experts, n, rows, (int)(number / (uint32_t)tiles), -1);
+    int turn = (int)(number / (uint32_t)tiles);
+    if (n <= rows && n_experts <= 64 && turn < n_experts) turn = expert_in_turn(offsets, n_experts, n, max(1, 256 / tiles), turn);
+    const Piece pc = find_piece(offsets, n_experts, n, rows, turn, -1);
     if (pc.expert < 0) return;
     int64_t from, to;
     pieces_of(offsets, pc.expert, n, rows, from, to);
@@ -193,13 +213,10 @@ __global__ __launch_bounds__(256, 2) void k_weight_grad(int out, int width, int 
         const int t = tid + i * 256;
         xm[i] = t % QX;
         xk[i] = t / QX;
-        x_in[i] = xk[i] < kChunks;
+        x_in[i] = kAllX || xk[i] < kChunks;
         if (!x_in[i]) xk[i] = kChunks - 1;                    // loads what another thread does, stores nothing
         xbase[i] = (uint32_t)xk[i] * 8 * (uint32_t)width + min(c0 + 4 * xm[i], width - (VEC ? 4 : 1));
     }
-
-    // column c of the tile: wave c / (32 NT), there lane c / NT of tile c % NT
-    const auto x_place = [](int c) { return (c / (32 * NT) * NT + c % NT) * 32 + c / NT % 32; };
 
     Quad a[8];
     uint32_t x[XT][8];
@@ -217,17 +234,28 @@ __global__ __launch_bounds__(256, 2) void k_weight_grad(int out, int width, int 
         const T *ap = dy + q0 * ld;
         const int8_t *xp = codes + q0 * width;
         if constexpr (VEC) {
-            if (ak < kChunks) {
+            // Each load is a scalar row address and a 32-bit distance, which the empty asm keeps apart: otherwise the additions
+            // become one of 64 bits a load and thread (16,384 rows 1024 -> 1024 x 8 bf16 79 -> 74 us).
+            uint32_t adist = abase, xdist[XT];
 #pragma unroll
-                for (int r = 0; r < 8; ++r) load_quad(a[r], reinterpret_cast<const T *>(reinterpret_cast<const char *>(ap + r * ld) + abase));
+            for (int i = 0; i < XT; ++i) xdist[i] = xbase[i];
+            if (kAllA || ak < kChunks) {
+#pragma unroll
+                for (int r = 0; r < 8; ++r) {
+                    asm volatile("" : "+v"(adist));
+                    load_quad(a[r], reinterpret_cast<const T *>(reinterpret_cast<const char *>(ap + r * ld) + adist));
+                }
             }
 #pragma unroll
             for (int i = 0; i < XT; ++i)
 #pragma unroll
-                for (int r = 0; r < 8; ++r) __builtin_memcpy(&x[i][r], xp + r * (int64_t)width + xbase[i], 4);
+                for (int r = 0; r < 8; ++r) {
+                    asm volatile("" : "+v"(xdist[i]));
+                    __builtin_memcpy(&x[i][r], xp + r * (int64_t)width + xdist[i], 4);
+                }
         } else {
             const int last = (int)min(to - 1 - q0, (int64_t)(kBK - 1));
-            if (ak < kChunks) {
+            if (kAllA || ak < kChunks) {
 #pragma unroll
                 for (int r = 0; r < 8; ++r) load_quad(a[r], ap + (uint32_t)min(ak * 8 + r, last) * (uint32_t)ld + ac, alast);
             }
@@ -285,7 +313,7 @@ __global__ __launch_bounds__(256, 2) void k_weight_grad(int out, int width, int 
                 if (q < q0 || q >= to) clear_quad(a[r]);
             }
         }
-        if (ak < kChunks) {
+        if (kAllA || ak < kChunks) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 uint4 w[TERMS];
@@ -322,7 +350,7 @@ __global__ __launch_bounds__(256, 2) void k_weight_grad(int out, int width, int 
 #pragma unroll
                 for (int r = 0; r < 8; ++r) v[r] = __float_as_uint((float)(int8_t)(x[i][r] >> 8 * j) * step[r]);   // exact
                 if (x_in[i])
-                    B[xk[i]][x_place(4 * xm[i] + j)] = make_uint4(high_halves(v[0], v[1]), high_halves(v[2], v[3]), high_halves(v[4], v[5]),
+                    B[xk[i]][j * QX + xm[i]] = make_uint4(high_halves(v[0], v[1]), high_halves(v[2], v[3]), high_halves(v[4], v[5]),
                                                           high_halves(v[6], v[7]));
             }
         }
@@ -333,21 +361,32 @@ __global__ __launch_bounds__(256, 2) void k_weight_grad(int out, int width, int 
             fetch(q0 + kBK);
             fetch_scales(q0 + 2 * kBK);
         }
-#pragma unroll
-        for (int s = 0; s < kChunks / 2; ++s) {
+        bf16x8 af[2][TERMS][MT], bf[2][NT];
+        auto operands = [&](int s) {
             const int c = 2 * s + (lane >> 5);
-            bf16x8 bf[NT];
 #pragma unroll
-            for (int j = 0; j < NT; ++j) bf[j] = __builtin_bit_cast(bf16x8, B[c][(wn * NT + j) * 32 + (lane & 31)]);
+            for (int j = 0; j < NT; ++j) bf[s & 1][j] = __builtin_bit_cast(bf16x8, B[c][(wn * NT + j) * 32 + (lane & 31)]);
 #pragma unroll
             for (int t = TERMS - 1; t >= 0; --t)
 #pragma unroll
-                for (int i = 0; i < MT; ++i) {
-                    const bf16x8 af = __builtin_bit_cast(bf16x8, A[t][c][(wm * MT + i) * 32 + (lane & 31)]);
+                for (int i = 0; i < MT; ++i) af[s & 1][t][i] = __builtin_bit_cast(bf16x8, A[t][c][(wm * MT + i) * 32 + (lane & 31)]);
+        };
+        // operands are read a step ahead, and a wave that multiplies goes before one that stages (128,000 rows 312 -> 128 x 5
+        // fp32 66 -> 63 us; 16,384 rows 1024 -> 1024 x 8 fp32 153 -> 147 us, bf16 74 and 75 us)
+        operands(0);
+        __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-                    for (int j = 0; j < NT; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(af, bf[j], acc[i][j], 0, 0, 0);
-                }
+        for (int s = 0; s < kChunks / 2; ++s) {
+            if (s + 1 < kChunks / 2) operands(s + 1);
+#pragma unroll
+            for (int t = TERMS - 1; t >= 0; --t)
+#pragma unroll
+                for (int i = 0; i < MT; ++i)
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(af[s & 1][t][i], bf[s & 1][j], acc[i][j], 0, 0, 0);
+            __builtin_amdgcn_sched_barrier(0);
         }
+        __builtin_amdgcn_s_setprio(0);
     }
 
     const int64_t matrix = (int64_t)out * width;
@@ -362,7 +401,7 @@ __global__ __launch_bounds__(256, 2) void k_weight_grad(int out, int width, int 
             const int pm = (wm * MT + i) * 32 + 8 * (r / 4) + 4 * (lane >> 5) + r % 4;
             const int oq = o0 + 4 * (pm % QA), o = (VEC ? min(oq, out - 4) : oq) + pm / QA;
             if (oq >= out || o >= out) continue;
-            const int cl = c0 + wn * 32 * NT + NT * (lane & 31);          // this lane's NT columns
+            const int cl = c0 + 4 * (lane & 31) + wn * NT;          // this lane's NT columns
             float *row = to_w + (int64_t)o * width;
             if (!VEC || cl + NT > width || (cl + NT > width - 4 && width % 4)) {
                 // at the row's end: the last quad was moved back to end with it
@@ -379,7 +418,7 @@ __global__ __launch_bounds__(256, 2) void k_weight_grad(int out, int width, int 
             }
         }
     if (c0 == 0 && to_b) {
-        if (ak < kChunks)
+        if (kAllA || ak < kChunks)
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 if (o0 + 4 * am < out && ac + j >= o0) sums[ak][ac - o0 + j] = bias[j];   // a moved quad begins in the tile before
