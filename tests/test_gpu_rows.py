@@ -390,6 +390,24 @@ def test_weight_grad(m, n, out, width, counts, dtype):
     assert torch.equal(again[0], dweight) and torch.equal(again[1], dbias)
 
 
+@pytest.mark.parametrize("n,out,width,experts_", [(600, 1030, 1030, 7), (1100, 1024, 1024, 8), (500, 130, 1000, 64), (400, 40, 200, 66),
+                                                  (300, 300, 140, 1)])
+def test_weight_grad_experts_of_unlike_length(m, n, out, width, experts_):
+    """One piece an expert: the order in which experts start changes no result, empty ones and equal lengths included."""
+    g = rng(n + experts_)
+    share = torch.rand(experts_, generator=g, dtype=torch.float64).pow(3)
+    share[experts_ // 2] = 0.0 if experts_ > 1 else 1.0
+    ends = torch.round(torch.cumsum(share, 0) / share.sum() * n).long()
+    offsets = torch.cat([torch.zeros(1, dtype=torch.long), ends]).to(DEV, torch.int32)
+    dy, held = normal(g, n, out, dtype=torch.bfloat16), m.checkpoint_save(normal(g, n, width))
+    dweight, dbias = m.checkpoint_weight_grad(dy, held, offsets)
+    x64, dy64 = R.load(held.codes.cpu(), held.scales.cpu()), f64(dy)
+    for e in range(experts_):
+        a, b = dy64[offsets[e]:offsets[e + 1]], x64[offsets[e]:offsets[e + 1]]
+        check("dweight", dweight[e], a.T @ b, (len(a) + 8) * U * (a.abs().T @ b.abs()))
+        check("dbias", dbias[e], a.sum(0), (len(a) + 8) * U * a.abs().sum(0))
+
+
 def test_weight_grad_special_values(m):
     """A held NaN reaches its column only, a row outside every segment nothing; differences of a loss."""
     g = rng(9)
