@@ -95,8 +95,8 @@ struct Lanes {
     // The reverse pass keeps its vectors in LDS (zeros past the width), whose registers its sums need.  The offset is
     // zero, but not to the compiler, which would move the reads out of the row loop, into registers.
     static constexpr int kSlots = G * E;
-    __device__ __forceinline__ void keep(float *sh, const float *p, float otherwise) const {
-        for (int c = threadIdx.x; c < width; c += kThreads) sh[c] = p ? p[c] : otherwise;
+    __device__ __forceinline__ void keep(float *sh, const float *p, float otherwise, const float *factor) const {
+        for (int c = threadIdx.x; c < width; c += kThreads) sh[c] = (p ? p[c] : otherwise) * (factor ? factor[c] : 1.0f);
     }
     __device__ __forceinline__ void kept(float (&v)[E], const float *sh) const {
         int z = 0;
@@ -257,15 +257,18 @@ __global__ __launch_bounds__((Lanes<T, W, G, CH, false>::kThreads)) void k_norm_
     constexpr int kShared = L::kWaves > 1 ? 3 * L::kWaves : 1;
     __shared__ float sh1[2][L::kWaves > 1 ? L::kWaves : 1], sh2[2][L::kWaves > 1 ? 2 * L::kWaves : 1], sh3[2][kShared];
     __shared__ float columns[L::kGroups > 1 ? L::kGroups * G * E : 1];
+    // Rows of several waves that do not fill their slots take more registers, and run in fewer waves: there the block's and
+    // the gate's loads go out with the first ones, if they are short (bf16: 8,192 x 5,000 217 -> 202 us; where rows fill
+    // their slots 237 -> 242 us at 32,768 x 2,048).
+    constexpr bool kEarly = sizeof(T) == 2 && !EXACT && L::kWaves > 1;
     int turn1 = 0, turn2 = 0, turn3 = 0;
     const L at(a.width);
     const int gate_kind = FULL ? (int)MODE : a.gate_width > 1 ? (int)kElementGate : a.gate_width;   // widths of 1 count as one gate a row
     const bool has_dr = FULL || dr, has_dh = FULL || dh, has_block = FULL || block;
-    __shared__ __attribute__((aligned(16))) float vectors[4][L::kSlots];
-    at.keep(vectors[0], a.post_weight, 1.0f);
-    at.keep(vectors[1], a.post_bias, 0.0f);
-    at.keep(vectors[2], a.scale, 1.0f);
-    at.keep(vectors[3], a.pre_weight, 1.0f);
+    __shared__ __attribute__((aligned(16))) float vectors[3][L::kSlots];
+    at.keep(vectors[0], a.post_weight, 1.0f, a.scale);
+    at.keep(vectors[1], a.post_bias, 0.0f, a.scale);
+    at.keep(vectors[2], a.pre_weight, 1.0f, nullptr);
     __syncthreads();
     // sums over the group's rows: total sigma hat_b, total sigma, dh hat_r, dh
     float s0[E] = {}, s1[E] = {}, s3[E] = {}, s4[E] = {};
@@ -289,6 +292,7 @@ __global__ __launch_bounds__((Lanes<T, W, G, CH, false>::kThreads)) void k_norm_
     int64_t i = (int64_t)blockIdx.x * L::kGroups + at.group;
     for (; i < a.n; i += stride) {
         fetch_pre(i);
+        if (kEarly) fetch_post(i);
         float t[E];
         if (has_dr) at.values(t, rdr);
         else
@@ -300,7 +304,7 @@ __global__ __launch_bounds__((Lanes<T, W, G, CH, false>::kThreads)) void k_norm_
             at.values(d, rdh);
             const float inv = normalise(hat);
             float qw[E];
-            at.kept(qw, vectors[3]);
+            at.kept(qw, vectors[2]);
             float m[2] = {0.0f, 0.0f};
 #pragma unroll
             for (int e = 0; e < E; ++e) {
@@ -318,16 +322,15 @@ __global__ __launch_bounds__((Lanes<T, W, G, CH, false>::kThreads)) void k_norm_
         }
         if (FULL || dx) at.store(dx + i * a.width, t);
         if (has_block) {
-            fetch_post(i);
+            if (!kEarly) fetch_post(i);
             float b[E], g[E];
             at.values(b, rb);
             if (gate_kind == kElementGate) at.values(g, rg);
             else g[0] = to_f32(row_gate);
             const float inv = normalise(b);
-            float pw[E], pb[E], sc[E];
+            float pw[E], pb[E];   // times the scale
             at.kept(pw, vectors[0]);
             at.kept(pb, vectors[1]);
-            at.kept(sc, vectors[2]);
             float m[3] = {0.0f, 0.0f, 0.0f};
             if (gate_kind == kRowGate) g[0] = sigmoid(g[0]);
             float du[E], dg[E];
@@ -337,9 +340,8 @@ __global__ __launch_bounds__((Lanes<T, W, G, CH, false>::kThreads)) void k_norm_
                 const float ts = t[e] * s;
                 s0[e] = fmaf(ts, b[e], s0[e]);
                 s1[e] += ts;
-                du[e] = ts * sc[e];
-                dg[e] = du[e] * fmaf(b[e], pw[e], pb[e]) * (1.0f - s);
-                du[e] *= pw[e];
+                dg[e] = ts * fmaf(b[e], pw[e], pb[e]) * (1.0f - s);
+                du[e] = ts * pw[e];
                 const float mine = at.share(du[e], e);
                 m[0] += mine;
                 m[1] = fmaf(mine, b[e], m[1]);
@@ -430,8 +432,11 @@ NormArgs args_of(const mpnn_norm &p, int64_t n, bool gate) {
 // Values a chunk, lanes and chunks of a lane: the fewest slots that hold the row, in steps of a half (312 values: 32
 // lanes of 3 chunks of 4 have 384 slots, 64 lanes of 2 would have 512), up to 12 values a lane, which leaves room for the
 // reverse pass's four sums a column in registers; 16 where another wave a row would cost more than it brings.  Rows
-// shorter than a chunk go value by value.
-template <class F>
+// shorter than a chunk go value by value.  BACK: of the widest rows, whose vectors leave LDS for one block a CU, the
+// reverse pass takes more waves (bf16 8,192 x 8,192 512 lanes of 16 and 1024 of 8: 289 and 231 us, forward 137 and 150 us;
+// 8,192 x 6,144 512 of 12 and 768 of 8: 233 and 186 us, forward 100 and 116 us; fp32 8,192 x 8,192 512
+// of 16 and 1024 of 8: reverse 449 and 418 us, forward 251 and 249 us).
+template <bool BACK, class F>
 Status by_width(int dtype, int width, F run) {
 #define MPNN_ROW(type, limit, wide, lanes, chunks)                                                                      \
     if (width <= limit)                                                                                                 \
@@ -447,12 +452,17 @@ Status by_width(int dtype, int width, F run) {
         MPNN_ROW(bf16, 512, 8, 64, 1)
         MPNN_ROW(bf16, 768, 4, 64, 3)
         MPNN_ROW(bf16, 1024, 8, 64, 2)
-        MPNN_ROW(bf16, 1536, 4, 128, 3)
+        MPNN_ROW(bf16, 1536, 8, 192, 1)
         MPNN_ROW(bf16, 2048, 8, 256, 1)
         MPNN_ROW(bf16, 256 * 12, 4, 256, 3)
         MPNN_ROW(bf16, 4096, 8, 512, 1)
-        MPNN_ROW(bf16, 6144, 4, 512, 3)
-        MPNN_ROW(bf16, 8192, 8, 512, 2)
+        if constexpr (BACK) {
+            MPNN_ROW(bf16, 6144, 8, 768, 1)
+            MPNN_ROW(bf16, 8192, 8, 1024, 1)
+        } else {
+            MPNN_ROW(bf16, 6144, 4, 512, 3)
+            MPNN_ROW(bf16, 8192, 8, 512, 2)
+        }
     } else {
         MPNN_ROW(float, 3, 1, 8, 1)
         MPNN_ROW(float, 32, 4, 8, 1)
@@ -470,7 +480,7 @@ Status by_width(int dtype, int width, F run) {
         MPNN_ROW(float, 256 * 12, 4, 256, 3)
         MPNN_ROW(float, 4096, 4, 512, 2)
         MPNN_ROW(float, 6144, 4, 512, 3)
-        MPNN_ROW(float, 8192, 4, 512, 4)
+        MPNN_ROW(float, 8192, 4, 1024, 2)
     }
 #undef MPNN_ROW
     return Status::err(MPNN_E_INVALID_ARG, "bad width");
@@ -494,7 +504,7 @@ Status norm_residual(Context &cx, const mpnn_norm &p, int64_t n, const void *x, 
                      const void *gate, int64_t ldg, void *r, void *h) {
     if (n == 0) return Status::ok();
     const NormArgs a = args_of(p, n, gate);
-    return by_width(p.dtype, p.width, [&](auto type, auto wide, auto lanes, auto chunks) -> Status {
+    return by_width<false>(p.dtype, p.width, [&](auto type, auto wide, auto lanes, auto chunks) -> Status {
         using T = decltype(type);
         using L = Lanes<T, wide(), lanes(), chunks(), false>;
         const int64_t blocks = std::min<int64_t>((n + L::kGroups - 1) / L::kGroups, kForwardBlocks);
@@ -511,10 +521,12 @@ Status norm_residual_backward(Context &cx, const mpnn_norm &p, int64_t n, const 
                               const void *block, int64_t ldb, const void *gate, int64_t ldg, void *dx, void *dblock, void *dgate,
                               float *const dvec[5]) {
     const NormArgs a = args_of(p, n, gate);
-    return by_width(p.dtype, p.width, [&](auto type, auto wide, auto lanes, auto chunks) -> Status {
+    return by_width<true>(p.dtype, p.width, [&](auto type, auto wide, auto lanes, auto chunks) -> Status {
         using T = decltype(type);
         using L = Lanes<T, wide(), lanes(), chunks(), false>;
-        const int64_t blocks = std::min<int64_t>((n + L::kGroups - 1) / L::kGroups, kBackBlocks * 256 / L::kThreads);
+        // a whole number of blocks a CU
+        constexpr int64_t most = std::max<int64_t>(1, kBackBlocks / L::kThreads) * 256;
+        const int64_t blocks = std::min<int64_t>((n + L::kGroups - 1) / L::kGroups, most);
         const bool columns = dvec[0] || dvec[1] || dvec[2] || dvec[3] || dvec[4];
         if (columns) MPNN_TRY(cx.grow(cx.rows_ws, sizeof(float) * (size_t)(blocks * 4 * p.width)));
         float *part = columns ? cx.rows_ws.as<float>() : nullptr;
