@@ -486,7 +486,20 @@ Status by_width(int dtype, int width, F run) {
     return Status::err(MPNN_E_INVALID_ARG, "bad width");
 }
 
-constexpr int64_t kForwardBlocks = 2048, kBackBlocks = 1024;
+// Blocks for n rows: enough that the rows which a CU's blocks ask for at a time come to `bytes`, no more than run at once.
+// More of them bring no bandwidth, and each writes partial sums (gradient of 128,000 x 312 fp32 with one and two blocks of
+// four rows a CU: 237 and 255 us, bf16 185 and 138 us; forward of 400,002 x 128 fp32 with 32 KB a CU, with all that fit and
+// with eight blocks a CU: 186, 201 and 198 us; of 8,192 x 8,192 bf16 with one block and eight: 122 and 137 us).
+constexpr int kForwardBytes = 32 * 1024, kBackBytes = 52 * 1024;
+template <auto *Kernel, class L, class T>
+int64_t blocks_for(int64_t n, int arrays, int bytes) {
+    static const int resident = [] {
+        int per = 0;
+        return hipOccupancyMaxActiveBlocksPerMultiprocessor(&per, Kernel, L::kThreads, 0) == hipSuccess && per > 0 ? per : 1;
+    }();
+    const int span = L::kThreads * L::E * (int)sizeof(T) * arrays;
+    return std::min<int64_t>((n + L::kGroups - 1) / L::kGroups, 256 * (int64_t)std::min(resident, (bytes + span - 1) / span));
+}
 
 // The kernel for a call: run gets the mode, and whether the rows fill their slots, as constants.
 template <class F>
@@ -507,10 +520,11 @@ Status norm_residual(Context &cx, const mpnn_norm &p, int64_t n, const void *x, 
     return by_width<false>(p.dtype, p.width, [&](auto type, auto wide, auto lanes, auto chunks) -> Status {
         using T = decltype(type);
         using L = Lanes<T, wide(), lanes(), chunks(), false>;
-        const int64_t blocks = std::min<int64_t>((n + L::kGroups - 1) / L::kGroups, kForwardBlocks);
         return by_mode(block && r && h, p.width == L::kSlots, a.gate_width, [&](auto mode, auto exact) -> Status {
-            k_norm_residual<T, wide(), lanes(), chunks(), mode(), exact()><<<(unsigned)blocks, L::kThreads, 0, cx.stream>>>(
-                a, (const T *)x, ldx, (const T *)block, ldb, (const T *)gate, ldg, (T *)r, (T *)h);
+            constexpr auto *kernel = k_norm_residual<T, wide(), lanes(), chunks(), mode(), exact()>;
+            const int64_t blocks = blocks_for<kernel, L, T>(n, mode() == kElementGate ? 3 : 2, kForwardBytes);
+            kernel<<<(unsigned)blocks, L::kThreads, 0, cx.stream>>>(a, (const T *)x, ldx, (const T *)block, ldb, (const T *)gate, ldg,
+                                                                    (T *)r, (T *)h);
             MPNN_HIP(hipGetLastError());
             return Status::ok();
         });
@@ -524,20 +538,20 @@ Status norm_residual_backward(Context &cx, const mpnn_norm &p, int64_t n, const 
     return by_width<true>(p.dtype, p.width, [&](auto type, auto wide, auto lanes, auto chunks) -> Status {
         using T = decltype(type);
         using L = Lanes<T, wide(), lanes(), chunks(), false>;
-        // a whole number of blocks a CU
-        constexpr int64_t most = std::max<int64_t>(1, kBackBlocks / L::kThreads) * 256;
-        const int64_t blocks = std::min<int64_t>((n + L::kGroups - 1) / L::kGroups, most);
         const bool columns = dvec[0] || dvec[1] || dvec[2] || dvec[3] || dvec[4];
-        if (columns) MPNN_TRY(cx.grow(cx.rows_ws, sizeof(float) * (size_t)(blocks * 4 * p.width)));
-        float *part = columns ? cx.rows_ws.as<float>() : nullptr;
-        if (n > 0)
-            MPNN_TRY(by_mode(dr && dh && block && dx, p.width == L::kSlots, a.gate_width, [&](auto mode, auto exact) -> Status {
-                k_norm_residual_back<T, wide(), lanes(), chunks(), mode(), exact()><<<(unsigned)blocks, L::kThreads, 0, cx.stream>>>(
-                    a, (const T *)dr, (const T *)dh, (const T *)r, ldr, (const T *)block, ldb, (const T *)gate, ldg, (T *)dx,
-                    (T *)dblock, (T *)dgate, part);
-                MPNN_HIP(hipGetLastError());
-                return Status::ok();
-            }));
+        int64_t blocks = 0;
+        float *part = nullptr;
+        MPNN_TRY(by_mode(dr && dh && block && dx, p.width == L::kSlots, a.gate_width, [&](auto mode, auto exact) -> Status {
+            constexpr auto *kernel = k_norm_residual_back<T, wide(), lanes(), chunks(), mode(), exact()>;
+            blocks = blocks_for<kernel, L, T>(n, mode() == kElementGate ? 5 : 4, kBackBytes);
+            if (columns) MPNN_TRY(cx.grow(cx.rows_ws, sizeof(float) * (size_t)(blocks * 4 * p.width)));
+            part = columns ? cx.rows_ws.as<float>() : nullptr;
+            if (n == 0) return Status::ok();
+            kernel<<<(unsigned)blocks, L::kThreads, 0, cx.stream>>>(a, (const T *)dr, (const T *)dh, (const T *)r, ldr, (const T *)block, ldb,
+                                                                   (const T *)gate, ldg, (T *)dx, (T *)dblock, (T *)dgate, part);
+            MPNN_HIP(hipGetLastError());
+            return Status::ok();
+        }));
         if (columns) {
             k_norm_columns<<<dim3((p.width + 15) / 16, 2), 1024, 0, cx.stream>>>(a, (int)blocks, part,
                                                                                  Vectors{{dvec[0], dvec[1], dvec[2], dvec[3], dvec[4]}});
