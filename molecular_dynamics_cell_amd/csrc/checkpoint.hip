@@ -72,8 +72,11 @@ __device__ __forceinline__ void save_chunk(const float (&v)[Chunk<T>::W], int in
 }
 
 // A lane per chunk of a whole number of groups (chunks past the row's end hold zeros), kUnroll chunks in flight.
-// FULL: the rows are whole groups.
-template <class T, bool SILU, bool FULL>
+// MOVED: the last group holds at least a chunk.  A chunk that would pass the row's end, or begins after it, is moved back
+// to end with the row: it stays in its group, so the group's largest value and the codes are the same, and what two lanes
+// store they store alike.  No load or store has a condition then (128,000 x 312 fp32 with SiLU 83 us, 107 with them; x 311 bf16
+// read back 20 us, 41 with them).
+template <class T, bool SILU, bool MOVED>
 __global__ __launch_bounds__(256) void k_checkpoint_save(Items it, int groups, int width, const T *__restrict__ z, int64_t ld,
                                                          T *__restrict__ y, int8_t *__restrict__ codes, uint8_t *__restrict__ scales,
                                                          int8_t *__restrict__ ycodes, uint8_t *__restrict__ yscales) {
@@ -83,19 +86,20 @@ __global__ __launch_bounds__(256) void k_checkpoint_save(Items it, int groups, i
     int64_t row[kUnroll];
     int c[kUnroll];
     Chunk<T> v[kUnroll];
+    const auto column = [&](int u) { return MOVED ? min(c[u] * W, width - W) : c[u] * W; };
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
         if (u >= units) break;
         item_at<L>(it, block, u, row[u], c[u]);
-        const int left = FULL ? W : width - c[u] * W;
-        if (FULL || left > 0) v[u].load(z + row[u] * ld + c[u] * W, left);
+        const int left = MOVED ? W : width - c[u] * W;
+        if (MOVED || left > 0) v[u].load(z + row[u] * ld + column(u), left);
         else __builtin_memset(&v[u], 0, sizeof v[u]);
     }
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
         if (u >= units) break;
-        const int left = FULL ? W : width - c[u] * W;
-        const int64_t at = row[u] * width + c[u] * W, g = row[u] * groups + c[u] / L;
+        const int left = MOVED ? W : width - c[u] * W;
+        const int64_t at = row[u] * width + column(u), g = row[u] * groups + c[u] / L;
         float f[W];
 #pragma unroll
         for (int j = 0; j < W; ++j) f[j] = to_f32(v[u].v[j]);
@@ -109,7 +113,7 @@ __global__ __launch_bounds__(256) void k_checkpoint_save(Items it, int groups, i
                 f[j] *= s;
                 o.v[j] = from_f32<T>(f[j]);
             }
-            if (FULL || left > 0) o.store(y + at, left);
+            if (MOVED || left > 0) o.store(y + at, left);
             if (ycodes) save_chunk<T>(f, left, ycodes + at, yscales + g, c[u] % L == 0);
         }
     }
@@ -132,7 +136,7 @@ struct Held {
 };
 
 // out = the held values, or with dy the gradient dz = dy s (1 + z (1 - s)), s = sigma(z), at the held z
-template <class T, bool BACK, bool FULL>
+template <class T, bool BACK, bool MOVED>
 __global__ __launch_bounds__(256) void k_checkpoint_use(Items it, int groups, int width, const T *__restrict__ dy, int64_t ld,
                                                         const int8_t *__restrict__ codes, const uint8_t *__restrict__ scales,
                                                         T *__restrict__ out) {
@@ -143,13 +147,14 @@ __global__ __launch_bounds__(256) void k_checkpoint_use(Items it, int groups, in
     int c[kUnroll];
     Chunk<T> d[kUnroll];
     Held<W> z[kUnroll];
+    const auto column = [&](int u) { return MOVED ? min(c[u] * W, width - W) : c[u] * W; };
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
         if (u >= units) break;
         item_at(it, block, u, row[u], c[u]);
-        const int left = FULL ? W : width - c[u] * W;
-        if (BACK) d[u].load(dy + row[u] * ld + c[u] * W, left);
-        z[u].load(codes + row[u] * width + c[u] * W, scales + row[u] * groups + c[u] / L, left);
+        const int left = MOVED ? W : width - c[u] * W;
+        if (BACK) d[u].load(dy + row[u] * ld + column(u), left);
+        z[u].load(codes + row[u] * width + column(u), scales + row[u] * groups + c[u] / L, left);
     }
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
@@ -166,20 +171,23 @@ __global__ __launch_bounds__(256) void k_checkpoint_use(Items it, int groups, in
             }
             o.v[j] = from_f32<T>(v);
         }
-        o.store(out + row[u] * width + c[u] * W, FULL ? W : width - c[u] * W);
+        o.store(out + row[u] * width + column(u), MOVED ? W : width - c[u] * W);
     }
 }
 
 }  // namespace
+
+// A row's last chunk may be moved back inside its group.
+template <class T> static bool can_move(int width) { return width % kGroup == 0 || width % kGroup >= Chunk<T>::W; }
 
 template <class T>
 static Status save_t(Context &cx, bool silu, int64_t n, int width, const void *z, int64_t ld, void *y, int8_t *codes, uint8_t *scales,
                      int8_t *ycodes, uint8_t *yscales) {
     const int groups = (width + kGroup - 1) / kGroup;
     const Items it = items_of(n, groups * kGroupLanes<T>);
-    const bool full = width % kGroup == 0;
-    auto *kernel = silu ? (full ? k_checkpoint_save<T, true, true> : k_checkpoint_save<T, true, false>)
-                        : (full ? k_checkpoint_save<T, false, true> : k_checkpoint_save<T, false, false>);
+    const bool moved = can_move<T>(width);
+    auto *kernel = silu ? (moved ? k_checkpoint_save<T, true, true> : k_checkpoint_save<T, true, false>)
+                        : (moved ? k_checkpoint_save<T, false, true> : k_checkpoint_save<T, false, false>);
     kernel<<<grid_of(it), 256, 0, cx.stream>>>(it, groups, width, (const T *)z, ld, (T *)y, codes, scales, ycodes, yscales);
     MPNN_HIP(hipGetLastError());
     return Status::ok();
@@ -196,7 +204,7 @@ template <class T, bool BACK>
 static Status use_t(Context &cx, int64_t n, int width, const void *dy, int64_t ld, const int8_t *codes, const uint8_t *scales,
                     void *out) {
     const Items it = items_of(n, (width + Chunk<T>::W - 1) / Chunk<T>::W);
-    auto *kernel = width % Chunk<T>::W == 0 ? k_checkpoint_use<T, BACK, true> : k_checkpoint_use<T, BACK, false>;
+    auto *kernel = can_move<T>(width) ? k_checkpoint_use<T, BACK, true> : k_checkpoint_use<T, BACK, false>;
     kernel<<<grid_of(it), 256, 0, cx.stream>>>(it, (width + kGroup - 1) / kGroup, width, (const T *)dy, ld, codes,
                                                                   scales, (T *)out);
     MPNN_HIP(hipGetLastError());
