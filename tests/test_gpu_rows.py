@@ -253,6 +253,15 @@ def test_norm_residual_backward(m, n, width, kind, gate, vectors, given, dtype):
             check(name, v, want[name][0], (4 * width + 64 + n) * U * want[name][1])
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("n,width", [(3, 1400), (5, 2600), (2, 6144), (1300, 1400), (700, 5000), (600, 8192), (9000, 96)])
+def test_norms_of_wide_and_many_rows(m, n, width, dtype):
+    """Rows of every number of waves, and more rows than groups run at once."""
+    test_norm_residual(m, n, width, "layer", "element", True, dtype)
+    test_norm_residual_backward(m, n, width, "rms", "element", True, "both", dtype)
+    test_norm_residual_backward(m, n, width, "layer", "row", True, "both", dtype)
+
+
 @pytest.mark.parametrize("kind,gate", [("rms", "element"), ("layer", "row"), ("layer", "none")])
 def test_norm_gradient_against_differences(m, kind, gate):
     """Central differences of the 64-bit forward pass along random directions, for each input in turn."""
