@@ -387,29 +387,30 @@ __global__ __launch_bounds__((Lanes<T, W, G, CH, false>::kThreads)) void k_norm_
     write(3, s4);
 }
 
-// The blocks' sums of 16 columns (blockIdx.y 0: P and Q, 1: the pre norm's two): 64 threads a column take every 64th
-// block, then their sums in order.
+// The blocks' sums of 32 columns (blockIdx.y 0: P and Q, 1: the pre norm's two): 32 threads a column take every 32nd
+// block, then their sums in order (8,192 x 4,096 bf16, 512 blocks' 33 MB: the gradient 126 us, with 16 columns 129 us).
+constexpr int kColumns = 32, kSlices = 1024 / kColumns;
 struct Vectors {
     float *v[5];
 };
 __global__ __launch_bounds__(1024) void k_norm_columns(NormArgs a, int parts, const float *__restrict__ part, Vectors out) {
-    __shared__ float sh[2][64][17];
-    const int c = blockIdx.x * 16 + (threadIdx.x & 15), slice = threadIdx.x >> 4;
+    __shared__ float sh[2][kSlices][kColumns + 1];
+    const int c = blockIdx.x * kColumns + threadIdx.x % kColumns, slice = threadIdx.x / kColumns;
     float s[2] = {};
     if (c < a.width)
 #pragma unroll 8
-        for (int b = slice; b < parts; b += 64) {
+        for (int b = slice; b < parts; b += kSlices) {
             const float *p = part + ((int64_t)b * 4 + blockIdx.y * 2) * a.width + c;
             s[0] += p[0];
             s[1] += p[a.width];
         }
-    sh[0][slice][threadIdx.x & 15] = s[0];
-    sh[1][slice][threadIdx.x & 15] = s[1];
+    sh[0][slice][threadIdx.x % kColumns] = s[0];
+    sh[1][slice][threadIdx.x % kColumns] = s[1];
     __syncthreads();
     if (slice != 0 || c >= a.width) return;
     float p = 0.0f, q = 0.0f;
 #pragma unroll
-    for (int b = 0; b < 64; ++b) {
+    for (int b = 0; b < kSlices; ++b) {
         p += sh[0][b][threadIdx.x];
         q += sh[1][b][threadIdx.x];
     }
@@ -432,7 +433,9 @@ NormArgs args_of(const mpnn_norm &p, int64_t n, bool gate) {
 // Values a chunk, lanes and chunks of a lane: the fewest slots that hold the row, in steps of a half (312 values: 32
 // lanes of 3 chunks of 4 have 384 slots, 64 lanes of 2 would have 512), up to 12 values a lane, which leaves room for the
 // reverse pass's four sums a column in registers; 16 where another wave a row would cost more than it brings.  Rows
-// shorter than a chunk go value by value.  BACK: of the widest rows, whose vectors leave LDS for one block a CU, the
+// shorter than a chunk go value by value.  Three waves a row (8 values of 192 lanes, for 1,536) are not used: four such
+// blocks fill a CU's registers only if their waves fall evenly on its SIMDs (24,000 x 1,400 bf16 133 us or 177 us, 137 us
+// with 128 lanes of 12).  BACK: of the widest rows, whose vectors leave LDS for one block a CU, the
 // reverse pass takes more waves (bf16 8,192 x 8,192 512 lanes of 16 and 1024 of 8: 289 and 231 us, forward 137 and 150 us;
 // 8,192 x 6,144 512 of 12 and 768 of 8: 233 and 186 us, forward 100 and 116 us; fp32 8,192 x 8,192 512
 // of 16 and 1024 of 8: reverse 449 and 418 us, forward 251 and 249 us).
@@ -452,7 +455,7 @@ Status by_width(int dtype, int width, F run) {
         MPNN_ROW(bf16, 512, 8, 64, 1)
         MPNN_ROW(bf16, 768, 4, 64, 3)
         MPNN_ROW(bf16, 1024, 8, 64, 2)
-        MPNN_ROW(bf16, 1536, 8, 192, 1)
+        MPNN_ROW(bf16, 1536, 4, 128, 3)
         MPNN_ROW(bf16, 2048, 8, 256, 1)
         MPNN_ROW(bf16, 256 * 12, 4, 256, 3)
         MPNN_ROW(bf16, 4096, 8, 512, 1)
@@ -553,7 +556,7 @@ Status norm_residual_backward(Context &cx, const mpnn_norm &p, int64_t n, const 
             return Status::ok();
         }));
         if (columns) {
-            k_norm_columns<<<dim3((p.width + 15) / 16, 2), 1024, 0, cx.stream>>>(a, (int)blocks, part,
+            k_norm_columns<<<dim3((p.width + kColumns - 1) / kColumns, 2), 1024, 0, cx.stream>>>(a, (int)blocks, part,
                                                                                  Vectors{{dvec[0], dvec[1], dvec[2], dvec[3], dvec[4]}});
             MPNN_HIP(hipGetLastError());
         }
