@@ -5,7 +5,7 @@
 //
 // All of it is bound by HBM, the plan by its launches.  Rows sent to their places: 128,000 x 312 fp32 to one place 65 us
 // (320 MB, 4.9 TB/s), 16,384 x 2,048 bf16 to eight 130 us (604 MB, 4.6 TB/s); added up again 57 us (5.6 TB/s) and, with
-// dropped pairs, 129 .. 165 us; the gradient with the weights' dot products, 65,536 x 1,024 bf16 from four: 224 us (1.21 GB,
+// dropped pairs, 157 us; the gradient with the weights' dot products, 65,536 x 1,024 bf16 from four: 224 us (1.21 GB,
 // 5.4 TB/s).  The plan of 128,000 pairs: 11 us in two launches, one launch up to 1,024 pairs (4 us).
 #include <algorithm>
 #include <type_traits>
@@ -205,7 +205,8 @@ struct Piece : Chunk<T, SHORT ? 1 : 16 / sizeof(T)> {
 template <class T> int chunks_of(int width) { return width < Chunk<T>::W ? width : (width + Chunk<T>::W - 1) / Chunk<T>::W; }
 
 // out[i] = sum over s of weight[i, s] sorted[position[i, s]], in the order of the slots, in fp32.  S slots of kUnroll / S
-// items are loaded together.
+// items are loaded together, a thread's only ones (with four items a thread at any S 165 us at 16,384 x 2,048 bf16 from
+// eight, 157 us with one).
 template <class T, bool SHORT, int S>
 __global__ __launch_bounds__(256) void k_route_combine(Items it, int k, int width, const T *__restrict__ sorted,
                                                        const int32_t *__restrict__ position, const int32_t *__restrict__ used,
@@ -214,46 +215,43 @@ __global__ __launch_bounds__(256) void k_route_combine(Items it, int k, int widt
     constexpr int W = P::W, U = kUnroll / S;
     const int64_t block = xcd_block();
     const int live = *used, units = it.items / 256;
-#pragma unroll 1
-    for (int u0 = 0; u0 < units; u0 += U) {
-        int64_t row[U];
-        int at[U];
-        float sum[U][W] = {};
+    int64_t row[U];
+    int at[U];
+    float sum[U][W] = {};
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            item_at(it, block, min(u0 + u, units - 1), row[u], at[u]);
-            at[u] = P::start(at[u], width);
-        }
-        for (int s0 = 0; s0 < k; s0 += S) {
-            P y[U][S];
-            bool on[U][S];
-            float w[U][S];
+    for (int u = 0; u < U; ++u) {
+        item_at(it, block, min(u, units - 1), row[u], at[u]);
+        at[u] = P::start(at[u], width);
+    }
+    for (int s0 = 0; s0 < k; s0 += S) {
+        P y[U][S];
+        bool on[U][S];
+        float w[U][S];
 #pragma unroll
-            for (int u = 0; u < U; ++u)
+        for (int u = 0; u < U; ++u)
 #pragma unroll
-                for (int j = 0; j < S; ++j) {
-                    const int64_t p = row[u] * k + min(s0 + j, k - 1);
-                    const int q = position[p];
-                    on[u][j] = s0 + j < k && (unsigned)q < (unsigned)live;
-                    w[u][j] = weight ? weight[p] : 1.0f;
-                    // a place without an expert reads another row, whose values are not used
-                    y[u][j].load(sorted + (int64_t)(on[u][j] ? q : 0) * width + at[u]);
-                }
+            for (int j = 0; j < S; ++j) {
+                const int64_t p = row[u] * k + min(s0 + j, k - 1);
+                const int q = position[p];
+                on[u][j] = s0 + j < k && (unsigned)q < (unsigned)live;
+                w[u][j] = weight ? weight[p] : 1.0f;
+                // a place without an expert reads another row, whose values are not used
+                y[u][j].load(sorted + (int64_t)(on[u][j] ? q : 0) * width + at[u]);
+            }
 #pragma unroll
-            for (int u = 0; u < U; ++u)
+        for (int u = 0; u < U; ++u)
 #pragma unroll
-                for (int j = 0; j < S; ++j)
+            for (int j = 0; j < S; ++j)
 #pragma unroll
-                    for (int e = 0; e < W; ++e)
-                        sum[u][e] = on[u][j] ? fmaf(w[u][j], to_f32(y[u][j].v[e]), sum[u][e]) : sum[u][e];
-        }
+                for (int e = 0; e < W; ++e)
+                    sum[u][e] = on[u][j] ? fmaf(w[u][j], to_f32(y[u][j].v[e]), sum[u][e]) : sum[u][e];
+    }
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            P o;
+    for (int u = 0; u < U; ++u) {
+        P o;
 #pragma unroll
-            for (int e = 0; e < W; ++e) o.v[e] = from_f32<T>(sum[u][e]);
-            o.store(out + row[u] * width + at[u]);
-        }
+        for (int e = 0; e < W; ++e) o.v[e] = from_f32<T>(sum[u][e]);
+        o.store(out + row[u] * width + at[u]);
     }
 }
 
@@ -372,8 +370,8 @@ template <class F> Status by_slots(int k, F run) {
 template <class T>
 static Status combine_t(Context &cx, int64_t n, int k, int width, const void *sorted, const int32_t *position, const int32_t *used,
                         const float *weight, void *out) {
-    const Items it = items_of(n, chunks_of<T>(width));
     return by_slots(k, [&](auto slots) -> Status {
+        const Items it = items_of(n, chunks_of<T>(width), kUnroll / slots());
         auto *kernel = width < Chunk<T>::W ? k_route_combine<T, true, slots()> : k_route_combine<T, false, slots()>;
         kernel<<<grid_of(it), 256, 0, cx.stream>>>(it, k, width, (const T *)sorted, position, used, weight, (T *)out);
         MPNN_HIP(hipGetLastError());

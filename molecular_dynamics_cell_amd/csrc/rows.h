@@ -58,7 +58,7 @@ template <int G> __device__ __forceinline__ float lanes_sum(float v) {
 __device__ __forceinline__ float wave_sum(float v) { return lanes_sum<64>(v); }
 
 // Items of a row operator without sums along the rows: `per` chunks a row.  A block takes `rows` whole rows, or, of
-// rows longer than its `items`, one stretch (blockIdx.y); a thread takes every 256th item, kUnroll of them (one in
+// rows longer than its `items`, one stretch (blockIdx.y); a thread takes every 256th item, `unroll` of them (one in
 // small calls, which are spread over more blocks), whose loads are in flight together.  Consecutive stretches of rows
 // go to one XCD, so that lines shared by neighbouring rows are completed in its L2.
 constexpr int kUnroll = 4;
@@ -67,8 +67,8 @@ struct Items {
     int per, rows, items;
     float inv;      // 1 / per
 };
-inline Items items_of(int64_t n, int per) {
-    const int items = n * per > 256 * 2048 ? 256 * kUnroll : 256;
+inline Items items_of(int64_t n, int per, int unroll = kUnroll) {
+    const int items = n * per > 256 * 2048 ? 256 * unroll : 256;
     const int rows = per < items ? items / per : 1;
     return Items{n, per, rows, items, 1.0f / (float)per};
 }
