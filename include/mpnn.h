@@ -296,8 +296,9 @@ mpnn_status mpnn_route_plan(mpnn_ctx *ctx, int64_t n, int32_t k, int32_t n_exper
                             int32_t *offsets, int32_t *source, int32_t *position);
 
 /* sorted[position[i][s]] = x[i]; the rows of dropped pairs are zeros.  The gradient of x is
- * mpnn_route_combine of the gradient of sorted without weights.  Places outside 0 .. n k - 1 are
- * ignored here and below. */
+ * mpnn_route_combine of the gradient of sorted without weights.  Here and below places outside
+ * 0 .. n k - 1 are ignored, and a count offsets[n_experts] outside 0 .. n k counts as the nearer of the
+ * two, so that offsets and places of another plan read and write nothing outside the n k rows. */
 mpnn_status mpnn_route_scatter(mpnn_ctx *ctx, int32_t dtype, int64_t n, int32_t k, int32_t width, const void *x,
                                int64_t ldx, const int32_t *position, const int32_t *offsets, int32_t n_experts,
                                void *sorted);

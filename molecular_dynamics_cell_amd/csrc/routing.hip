@@ -204,6 +204,10 @@ struct Piece : Chunk<T, SHORT ? 1 : 16 / sizeof(T)> {
 };
 template <class T> int chunks_of(int width) { return width < Chunk<T>::W ? width : (width + Chunk<T>::W - 1) / Chunk<T>::W; }
 
+// Places below this one have an expert.  The count is the caller's memory, and may be that of a longer plan: no place past
+// the sorted rows is one, whatever it says.
+__device__ __forceinline__ int live_places(const int32_t *used, int64_t pairs) { return (int)min(max((int64_t)*used, (int64_t)0), pairs); }
+
 // out[i] = sum over s of weight[i, s] sorted[position[i, s]], in the order of the slots, in fp32.  S slots of kUnroll / S
 // items are loaded together, a thread's only ones (with four items a thread at any S 165 us at 16,384 x 2,048 bf16 from
 // eight, 157 us with one).
@@ -214,7 +218,7 @@ __global__ __launch_bounds__(256) void k_route_combine(Items it, int k, int widt
     using P = Piece<T, SHORT>;
     constexpr int W = P::W, U = kUnroll / S;
     const int64_t block = xcd_block();
-    const int live = *used, units = it.items / 256;
+    const int live = live_places(used, it.n * k), units = it.items / 256;
     int64_t row[U];
     int at[U];
     float sum[U][W] = {};
@@ -273,7 +277,7 @@ __global__ __launch_bounds__(256) void k_route_combine_back(int64_t n, int k, in
     const int64_t i = batches == 1 ? job : job / batches;
     if (i >= n) return;                                   // a whole group of lanes
     const int s0 = batches == 1 ? 0 : (int)(job - i * batches) * S;
-    const int lane = threadIdx.x % G, live = *used, chunks = (width + W - 1) / W;
+    const int lane = threadIdx.x % G, live = live_places(used, pairs), chunks = (width + W - 1) / W;
     int q[S];
     bool in[S], on[S], all_in = true;
     float w[S], dot[S] = {};
@@ -283,7 +287,7 @@ __global__ __launch_bounds__(256) void k_route_combine_back(int64_t n, int k, in
         q[j] = position[p];
         in[j] = (unsigned)q[j] < (uint64_t)pairs;
         all_in = all_in && in[j];
-        on[j] = in[j] && q[j] < live;
+        on[j] = (unsigned)q[j] < (unsigned)live;
         w[j] = weight ? weight[p] : 1.0f;
     }
     auto step = [&](int c0, auto checked) {
