@@ -188,13 +188,17 @@ template <class T>
 static Status save_t(Context &cx, bool silu, int64_t n, int width, const void *z, int64_t ld, void *y, int8_t *codes, uint8_t *scales,
                      int8_t *ycodes, uint8_t *yscales) {
     const int groups = (width + kGroup - 1) / kGroup;
-    const Items it = items_of(n, groups * kGroupLanes<T>);
     const bool moved = can_move<T>(width);
     auto *kernel = silu ? (moved ? k_checkpoint_save<T, true, true> : k_checkpoint_save<T, true, false>)
                         : (moved ? k_checkpoint_save<T, false, true> : k_checkpoint_save<T, false, false>);
-    kernel<<<grid_of(it), 256, 0, cx.stream>>>(it, groups, width, (const T *)z, ld, (T *)y, codes, scales, ycodes, yscales);
-    MPNN_HIP(hipGetLastError());
-    return Status::ok();
+    return by_launches(n, kLaunchBlocks * items_of(n, groups * kGroupLanes<T>).rows, [&](int64_t from, int64_t rows) -> Status {
+        const Items it = items_of(rows, groups * kGroupLanes<T>);
+        kernel<<<grid_of(it), 256, 0, cx.stream>>>(it, groups, width, (const T *)z + from * ld, ld, y ? (T *)y + from * width : nullptr,
+                                                   codes + from * width, scales + from * groups,
+                                                   ycodes ? ycodes + from * width : nullptr, yscales ? yscales + from * groups : nullptr);
+        MPNN_HIP(hipGetLastError());
+        return Status::ok();
+    });
 }
 
 Status checkpoint_save(Context &cx, int dtype, bool silu, int64_t n, int width, const void *z, int64_t ld, void *y, int8_t *codes,
@@ -207,12 +211,15 @@ Status checkpoint_save(Context &cx, int dtype, bool silu, int64_t n, int width, 
 template <class T, bool BACK>
 static Status use_t(Context &cx, int64_t n, int width, const void *dy, int64_t ld, const int8_t *codes, const uint8_t *scales,
                     void *out) {
-    const Items it = items_of(n, (width + Chunk<T>::W - 1) / Chunk<T>::W);
+    const int groups = (width + kGroup - 1) / kGroup, chunks = (width + Chunk<T>::W - 1) / Chunk<T>::W;
     auto *kernel = can_move<T>(width) ? k_checkpoint_use<T, BACK, true> : k_checkpoint_use<T, BACK, false>;
-    kernel<<<grid_of(it), 256, 0, cx.stream>>>(it, (width + kGroup - 1) / kGroup, width, (const T *)dy, ld, codes,
-                                                                  scales, (T *)out);
-    MPNN_HIP(hipGetLastError());
-    return Status::ok();
+    return by_launches(n, kLaunchBlocks * items_of(n, chunks).rows, [&](int64_t from, int64_t rows) -> Status {
+        const Items it = items_of(rows, chunks);
+        kernel<<<grid_of(it), 256, 0, cx.stream>>>(it, groups, width, dy ? (const T *)dy + from * ld : nullptr, ld, codes + from * width,
+                                                   scales + from * groups, (T *)out + from * width);
+        MPNN_HIP(hipGetLastError());
+        return Status::ok();
+    });
 }
 
 Status checkpoint_load(Context &cx, int dtype, int64_t n, int width, const int8_t *codes, const uint8_t *scales, void *out) {

@@ -212,13 +212,13 @@ __device__ __forceinline__ int live_places(const int32_t *used, int64_t pairs) {
 // items are loaded together, a thread's only ones (with four items a thread at any S 165 us at 16,384 x 2,048 bf16 from
 // eight, 157 us with one).
 template <class T, bool SHORT, int S>
-__global__ __launch_bounds__(256) void k_route_combine(Items it, int k, int width, const T *__restrict__ sorted,
+__global__ __launch_bounds__(256) void k_route_combine(Items it, int64_t pairs, int k, int width, const T *__restrict__ sorted,
                                                        const int32_t *__restrict__ position, const int32_t *__restrict__ used,
                                                        const float *__restrict__ weight, T *__restrict__ out) {
     using P = Piece<T, SHORT>;
     constexpr int W = P::W, U = kUnroll / S;
     const int64_t block = xcd_block();
-    const int live = live_places(used, it.n * k), units = it.items / 256;
+    const int live = live_places(used, pairs), units = it.items / 256;
     int64_t row[U];
     int at[U];
     float sum[U][W] = {};
@@ -266,13 +266,12 @@ __global__ __launch_bounds__(256) void k_route_combine(Items it, int k, int widt
 // took 107 us at 128,000 x 312 fp32 to one place and 181 us at 16,384 x 2,048 bf16 to eight; by groups of lanes 67 and
 // 139 us.)
 template <class T, bool SHORT, int G, int S>
-__global__ __launch_bounds__(256) void k_route_combine_back(int64_t n, int k, int batches, int width, const T *__restrict__ dout, int64_t ld,
+__global__ __launch_bounds__(256) void k_route_combine_back(int64_t n, int64_t pairs, int k, int batches, int width, const T *__restrict__ dout, int64_t ld,
                                                             const T *__restrict__ sorted, const int32_t *__restrict__ position,
                                                             const int32_t *__restrict__ used, const float *__restrict__ weight,
                                                             T *__restrict__ dsorted, float *__restrict__ dweight) {
     using P = Piece<T, SHORT>;
     constexpr int W = P::W;
-    const int64_t pairs = n * k;
     const int64_t job = xcd_block() * (256 / G) + threadIdx.x / G;
     const int64_t i = batches == 1 ? job : job / batches;
     if (i >= n) return;                                   // a whole group of lanes
@@ -375,11 +374,15 @@ template <class T>
 static Status combine_t(Context &cx, int64_t n, int k, int width, const void *sorted, const int32_t *position, const int32_t *used,
                         const float *weight, void *out) {
     return by_slots(k, [&](auto slots) -> Status {
-        const Items it = items_of(n, chunks_of<T>(width), kUnroll / slots());
+        const int per = chunks_of<T>(width);
         auto *kernel = width < Chunk<T>::W ? k_route_combine<T, true, slots()> : k_route_combine<T, false, slots()>;
-        kernel<<<grid_of(it), 256, 0, cx.stream>>>(it, k, width, (const T *)sorted, position, used, weight, (T *)out);
-        MPNN_HIP(hipGetLastError());
-        return Status::ok();
+        return by_launches(n, kLaunchBlocks * items_of(n, per, kUnroll / slots()).rows, [&](int64_t from, int64_t rows) -> Status {
+            const Items it = items_of(rows, per, kUnroll / slots());
+            kernel<<<grid_of(it), 256, 0, cx.stream>>>(it, n * k, k, width, (const T *)sorted, position + from * k, used,
+                                                       weight ? weight + from * k : nullptr, (T *)out + from * width);
+            MPNN_HIP(hipGetLastError());
+            return Status::ok();
+        });
     });
 }
 
@@ -397,11 +400,13 @@ static Status combine_back_t(Context &cx, int64_t n, int k, int width, const voi
         constexpr int S = slots();
         const int chunks = chunks_of<T>(width), batches = (k + S - 1) / S;
         auto run = [&](auto *kernel, int lanes) -> Status {
-            kernel<<<grid_xcd(n * batches, 256 / lanes), 256, 0, cx.stream>>>(n, k, batches, width, (const T *)dout, ld,
-                                                                              (const T *)sorted, position, used, weight,
-                                                                              (T *)dsorted, dweight);
-            MPNN_HIP(hipGetLastError());
-            return Status::ok();
+            return by_launches(n, kLaunchBlocks * (256 / lanes) / batches, [&](int64_t from, int64_t rows) -> Status {
+                kernel<<<grid_xcd(rows * batches, 256 / lanes), 256, 0, cx.stream>>>(
+                    rows, n * k, k, batches, width, (const T *)dout + from * ld, ld, (const T *)sorted, position + from * k, used,
+                    weight ? weight + from * k : nullptr, (T *)dsorted, dweight ? dweight + from * k : nullptr);
+                MPNN_HIP(hipGetLastError());
+                return Status::ok();
+            });
         };
         if (width < Chunk<T>::W) return run(k_route_combine_back<T, true, 8, S>, 8);
         if (chunks <= 8) return run(k_route_combine_back<T, false, 8, S>, 8);

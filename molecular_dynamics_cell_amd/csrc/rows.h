@@ -1,7 +1,9 @@
 // Device helpers of the row operators (routing.hip, residual.hip, checkpoint.hip, weight_grad.hip).
 #pragma once
 
-#include "common.h"
+#include <algorithm>
+
+#include "impl.h"
 
 namespace mpnn {
 
@@ -71,6 +73,13 @@ inline Items items_of(int64_t n, int per, int unroll = kUnroll) {
     const int items = n * per > 256 * 2048 ? 256 * unroll : 256;
     const int rows = per < items ? items / per : 1;
     return Items{n, per, rows, items, 1.0f / (float)per};
+}
+// A launch counts its threads in 32 bits, and one of more leaves rows out without an error: rows past `most`, those of
+// the most blocks of 256 threads that a launch holds, go into further launches.
+constexpr int64_t kLaunchBlocks = (int64_t(1) << 24) - kXcds;
+template <class F> Status by_launches(int64_t n, int64_t most, F run) {
+    for (int64_t from = 0; from < n; from += most) MPNN_TRY(run(from, std::min(n - from, most)));
+    return Status::ok();
 }
 inline dim3 grid_of(const Items &it) { return dim3(grid_xcd(it.n, it.rows), (unsigned)((it.per + it.items - 1) / it.items)); }
 

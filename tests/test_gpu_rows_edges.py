@@ -64,3 +64,43 @@ def test_counts_that_are_not_the_rows(m, n, k, width, routed, dtype):
     _, dweight = m.route_combine_backward(dout, rows, position, offsets, weight)
     products = f64(dout).unsqueeze(1) * taken
     check("dweight", dweight, products.sum(-1), (width + 1) * U * products.abs().sum(-1))
+
+
+def test_rows_sent_out_by_more_threads_than_a_launch_holds(m):
+    """268,500,007 rows of one value to five places: 2^32 threads and more."""
+    n, k = 268500007, 5
+    x = (torch.arange(n, dtype=torch.int32, device=DEV) % 251).to(torch.bfloat16).unsqueeze(1)
+    position = torch.arange(n * k, dtype=torch.int32, device=DEV).reshape(n, k)
+    offsets = torch.tensor([0, n * k], dtype=torch.int32, device=DEV)
+    rows = m.route_scatter(x, position, offsets)
+    assert torch.equal(rows.reshape(n, k), x.expand(n, k))
+    del rows
+    # the weights' gradient <dout, row> and the rows' own, against the same call on the last rows alone
+    dout, weight = x, torch.full((n, k), 0.5, device=DEV)
+    rows = x.expand(n, k).reshape(n * k, 1)
+    dy, dweight = m.route_combine_backward(dout, rows, position, offsets, weight)
+    assert torch.equal(dy.reshape(n, k), (x * 0.5).expand(n, k))
+    assert torch.equal(dweight, (x.float() * x.float()).expand(n, k))
+
+
+def test_rows_added_up_by_more_threads_than_a_launch_holds(m):
+    """16,780,000 rows of 1,032 columns, a block each, from three slots; a few rows have places, the others are zeros.  (The
+    sorted rows are only those below the routed count, which is all that may be read.)"""
+    n, k, width = 16780000, 3, 1032
+    g = rng(7)
+    rows = normal(g, 16, width, dtype=torch.bfloat16)
+    position = torch.full((n, k), -1, dtype=torch.int32, device=DEV)
+    some = torch.tensor([0, 1, 8388607, 8388608, 16777206, 16777207, 16777208, 16777209, 16777215, 16777216, n - 1])
+    places = torch.randint(0, 16, (len(some), k), generator=g, dtype=torch.int32)
+    position[some.to(DEV)] = places.to(DEV)
+    offsets = torch.tensor([0, 16], dtype=torch.int32, device=DEV)
+    weight = torch.ones(n, k, device=DEV)
+    out = torch.full((n, width), float("nan"), dtype=torch.bfloat16, device=DEV)
+    L = binding.lib()
+    assert L.mpnn_route_combine(m.h, 1, n, k, width, rows.data_ptr(), position.data_ptr(), offsets.data_ptr(), 1,
+                                weight.data_ptr(), out.data_ptr()) == 0, L.mpnn_last_error(m.h)
+    torch.cuda.synchronize()
+    taken = f64(rows)[places.long()]
+    check("out", out[some.to(DEV)], taken.sum(1), 4 * U * taken.abs().sum(1), torch.bfloat16)
+    out[some.to(DEV)] = 0
+    assert int(out.view(torch.int32).count_nonzero()) == 0
