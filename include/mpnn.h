@@ -270,9 +270,12 @@ mpnn_status mpnn_set_subdomains(mpnn_ctx *ctx, int32_t px, int32_t py, int32_t p
  * Row operators: the atom-wise parts of networks that a caller builds, trains and differentiates
  * outside the model above (for example a deeper, routed readout on the orbital sums of
  * mpnn_get_intermediate).  They need no neighbour list, only a context: its stream, its device
- * scratch (one buffer, grown by the first call of a size, so a call that is to be captured into a
- * graph runs once before) and its error text.  They enqueue work and return; nothing is copied to
- * the host.
+ * scratch and its error text.  They enqueue work and return; nothing is copied to the host.
+ *   - Scratch is one block for each stream that calls have run on, grown by the first call of a
+ *     size.  Captured calls take theirs, while the stream is being captured, from blocks of their own
+ *     that stay in place until mpnn_destroy: a graph may be replayed until then, on any stream and
+ *     beside eager calls.  The graphs captured from one context share that scratch, so replay them one
+ *     after another, not at the same time.
  *   - Rows are row-major [n][width] of fp32 or bf16 values (mpnn_dtype); an argument ld is the
  *     distance between rows in values (>= width), arrays without one are dense.  Arithmetic, sums
  *     and statistics are fp32; a result is rounded once, to nearest even, to the rows' type.

@@ -50,6 +50,40 @@ Status Context::grow_keep(Buf &b, size_t bytes, size_t keep) {
     return Status::ok();
 }
 
+Status Context::rows_scratch(size_t bytes, void **p) {
+    *p = nullptr;
+    if (bytes == 0) return Status::ok();
+    hipStreamCaptureStatus capture = hipStreamCaptureStatusNone;
+    if (const hipError_t e = hipStreamIsCapturing(stream, &capture); e != hipSuccess) {
+        (void)hipGetLastError();
+        return Status::err(MPNN_E_HIP, std::string("hipStreamIsCapturing: ") + hipGetErrorString(e));
+    }
+    if (capture != hipStreamCaptureStatusNone) {
+        if (rows_captured.empty() || rows_captured.back().bytes < bytes) {
+            rows_captured.reserve(rows_captured.size() + 1);
+            Buf b;
+            hipStreamCaptureMode mode = hipStreamCaptureModeRelaxed;   // an allocation is no part of the graph
+            MPNN_HIP(hipThreadExchangeStreamCaptureMode(&mode));
+            const Status s = grow(b, bytes);
+            MPNN_HIP(hipThreadExchangeStreamCaptureMode(&mode));
+            MPNN_TRY(s);
+            rows_captured.push_back(b);
+        }
+        *p = rows_captured.back().p;
+        return Status::ok();
+    }
+    for (Scratch &w : rows_ws)
+        if (w.stream == stream) {
+            MPNN_TRY(grow(w.buf, bytes));
+            *p = w.buf.p;
+            return Status::ok();
+        }
+    rows_ws.push_back({stream, Buf{}});
+    MPNN_TRY(grow(rows_ws.back().buf, bytes));
+    *p = rows_ws.back().buf.p;
+    return Status::ok();
+}
+
 const char *const kProfNames[kProfCount] = {
     "build_sort", "build_ghosts", "build_rows", "build_transpose", "build_species", "ghost_positions",
     "compact", "aggregate", "net_forward", "net_energy", "net_backward", "ghost_messages",
@@ -114,7 +148,7 @@ Context::~Context() {
                   &ghost_off, &row_off, &row_len, &slab_off, &nbr, &cellpos, &t_off, &t_eid, &sp_list, &sp_off, &c, &O, &feat, &grho, &Gc,
                   &gedge, &w, &amask, &act_n, &t_act, &dact, &nact, &Frecv, &F, &Ei, &red, &flag, &tmp_a, &tmp_b, &tmp_c,
                   &tmp_d, &tmp_scan,
-                  &types_caller, &stage_pos, &stage_vel, &bak_pos, &bak_vel, &bak_F, &rows_ws};
+                  &types_caller, &stage_pos, &stage_vel, &bak_pos, &bak_vel, &bak_F};
     for (const Chunk &c : graphs) (void)hipGraphExecDestroy(c.exec);
     if (cap_stream) (void)hipStreamSynchronize(cap_stream);
     for (hipEvent_t e : cap_ev)
@@ -125,6 +159,9 @@ Context::~Context() {
         if (e) (void)hipEventDestroy(e);
     if (side_stream) (void)hipStreamDestroy(side_stream);
     for (Buf *b : all) release(*b);
+    if (rows_ws.size() > 1 || !rows_captured.empty()) (void)hipDeviceSynchronize();   // work on other streams than the last
+    for (Scratch &w : rows_ws) release(w.buf);
+    for (Buf &b : rows_captured) release(b);
     prof_harvest();
     for (hipEvent_t e : prof_pool) (void)hipEventDestroy(e);
 }

@@ -177,7 +177,16 @@ struct Context {
     void prof_end(int id);
     void prof_harvest();                // after a stream synchronisation
 
-    Buf rows_ws;                  // scratch of one row operator call (routing counts, partial sums)
+    // Scratch of the row operators (routing counts, partial sums), all of it for one call at a time: a block for each
+    // stream that calls have run on, so that calls on two streams share none, and one for captured calls, whose address
+    // recorded graphs keep: a larger one is taken beside it (the last is the one in use), and all stay to the end.
+    struct Scratch {
+        hipStream_t stream;
+        Buf buf;
+    };
+    std::vector<Scratch> rows_ws;
+    std::vector<Buf> rows_captured;
+    Status rows_scratch(size_t bytes, void **p);   // bytes 0: none
 
     Buf types_caller;             // int32 [n] species in caller order (for rebuilds)
     Buf stage_pos, stage_vel;     // double [n][3] caller-order staging

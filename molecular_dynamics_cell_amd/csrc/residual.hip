@@ -551,8 +551,9 @@ Status norm_residual_backward(Context &cx, const mpnn_norm &p, int64_t n, const 
         MPNN_TRY(by_mode(dr && dh && block && dx, p.width == L::kSlots, a.gate_width, [&](auto mode, auto exact) -> Status {
             constexpr auto *kernel = k_norm_residual_back<T, wide(), lanes(), chunks(), mode(), exact()>;
             blocks = blocks_for<kernel, L, T>(n, mode() == kElementGate ? 5 : 4, kBackBytes);
-            if (columns) MPNN_TRY(cx.grow(cx.rows_ws, sizeof(float) * (size_t)(blocks * 4 * p.width)));
-            part = columns ? cx.rows_ws.as<float>() : nullptr;
+            void *ws = nullptr;
+            if (columns) MPNN_TRY(cx.rows_scratch(sizeof(float) * (size_t)(blocks * 4 * p.width), &ws));
+            part = static_cast<float *>(ws);
             if (n == 0) return Status::ok();
             kernel<<<(unsigned)blocks, L::kThreads, 0, cx.stream>>>(a, (const T *)dr, (const T *)dh, (const T *)r, ldr, (const T *)block, ldb,
                                                                    (const T *)gate, ldg, (T *)dx, (T *)dblock, (T *)dgate, part);

@@ -338,8 +338,9 @@ static Status plan(Context &cx, int64_t pairs, int n_experts, const int32_t *exp
     const int bins = n_experts + 1;
     int32_t *counts = nullptr, *total = nullptr;
     if (blocks > 1) {
-        MPNN_TRY(cx.grow(cx.rows_ws, sizeof(int32_t) * (size_t)bins * (size_t)(blocks + 1)));
-        counts = cx.rows_ws.as<int32_t>();
+        void *ws = nullptr;
+        MPNN_TRY(cx.rows_scratch(sizeof(int32_t) * (size_t)bins * (size_t)(blocks + 1), &ws));
+        counts = static_cast<int32_t *>(ws);
         k_route_count<ITEMS><<<(unsigned)blocks, kPlanThreads, 0, cx.stream>>>(expert, pairs, n_experts, counts);
         MPNN_HIP(hipGetLastError());
         if (blocks * bins > kSumCounts) {

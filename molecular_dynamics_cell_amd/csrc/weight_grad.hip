@@ -485,15 +485,17 @@ Status launch(Context &cx, int64_t n, int out, int width, int n_experts, const i
     const int64_t rows = std::max<int64_t>(512, ((n + want - 1) / want + kBK - 1) / kBK * kBK);
     const int64_t pieces = n / rows + n_experts;              // at most; an expert of several pieces has more than `rows` rows
     const int64_t matrix = (int64_t)out * width, slots = n > rows ? 2 * (n / rows) : 0;   // an expert of p > 1 pieces fills p / 2 whole ones
-    MPNN_TRY(cx.grow(cx.rows_ws, sizeof(float) * (size_t)(slots * slot_size(matrix + out))));
+    void *ws = nullptr;
+    MPNN_TRY(cx.rows_scratch(sizeof(float) * (size_t)(slots * slot_size(matrix + out)), &ws));
+    float *const part = static_cast<float *>(ws);
     const bool vec = n >= kBK && out >= 4 && width >= 4 && (width % 32 == 0 || width % 32 > 3);
     auto *kernel = vec ? k_weight_grad<T, MT, NT, WM, WN, true> : k_weight_grad<T, MT, NT, WM, WN, false>;
     kernel<<<grid_xcd(pieces * tiles, 1), 256, 0, cx.stream>>>(out, width, (width + 31) / 32, n_experts, n, rows, tiles_n, tiles, offsets,
-                                                               dy, ld, codes, scales, slots, cx.rows_ws.as<float>(), dweight, dbias);
+                                                               dy, ld, codes, scales, slots, part, dweight, dbias);
     MPNN_HIP(hipGetLastError());
     if (slots) {
         k_weight_grad_sum<<<dim3(grid_for(slot_size(matrix + out) / 4, 64), n_experts), 256, 0, cx.stream>>>(n_experts, n, rows, slots, matrix, out, offsets,
-                                                                                             cx.rows_ws.as<float>(), dweight, dbias);
+                                                                                             part, dweight, dbias);
         MPNN_HIP(hipGetLastError());
     }
     return Status::ok();

@@ -3,7 +3,9 @@ and the calls.  Rows are 2-D tensors [n, width] of float32 or bfloat16 on the co
 row tensor may have any row stride (a column block of a wider tensor), other layouts are copied.
 
 Work runs on the context's stream.  When torch's current stream is another one, the call waits for
-it, and it waits for the call, so tensors may be made and used there."""
+it, and it waits for the call, so tensors may be made and used there.  Calls may be captured into a
+graph, which may be replayed as long as the context lives; replay the graphs captured from one context
+one after another (they share its scratch for captured calls)."""
 from __future__ import annotations
 
 import ctypes as C

@@ -104,3 +104,98 @@ def test_rows_added_up_by_more_threads_than_a_launch_holds(m):
     check("out", out[some.to(DEV)], taken.sum(1), 4 * U * taken.abs().sum(1), torch.bfloat16)
     out[some.to(DEV)] = 0
     assert int(out.view(torch.int32).count_nonzero()) == 0
+
+
+class Pieces:
+    """Allocator hooks that hand out pieces of one tensor and note what is taken and given back; nothing is used twice."""
+
+    def __init__(self, m, megabytes=256):
+        self.base = torch.empty(megabytes << 20, dtype=torch.uint8, device=DEV)
+        self.at, self.taken, self.back = 0, [], []
+
+        def alloc(nbytes, user):
+            p = self.base.data_ptr() + self.at
+            self.at += (int(nbytes) + 255) // 256 * 256
+            assert self.at <= self.base.numel()
+            self.taken.append(p)
+            return p
+
+        self.hooks = (binding._ALLOC_FN(alloc), binding._FREE_FN(lambda p, user: self.back.append(p)))
+        assert binding.lib().mpnn_set_allocator(m.h, *self.hooks, None) == 0
+
+
+def uneven(g, n, E):
+    return torch.randint(-1, E, (n, 1), generator=g, dtype=torch.int32).to(DEV)
+
+
+def test_scratch_of_a_captured_call_stays():
+    """A graph keeps its scratch's address: later eager calls, larger ones too, neither give that memory back nor use it."""
+    m = binding.MPNN(I.make_params(1), DEV)
+    pieces = Pieces(m)
+    g = rng(1)
+    e, big = uneven(g, 9000, 300), uneven(g, 200000, 1000)
+    x, dy = normal(g, 3000, 100), normal(g, 3000, 40)
+    held, seg = m.checkpoint_save(x), torch.tensor([0, 3000], dtype=torch.int32, device=DEV)
+
+    def step():
+        return [*m.route_plan(e, 300), *m.norm_residual_backward(x, x, x, x)[3:], *m.checkpoint_weight_grad(dy, held, seg)]
+
+    step()
+    home, graph = m._stream, torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    try:
+        with torch.cuda.graph(graph):
+            m.set_stream(torch.cuda.current_stream())
+            kept = step()
+    finally:
+        m.set_stream(home)
+    step()
+    eager = len(pieces.taken)
+    m.route_plan(big, 1000)
+    torch.cuda.synchronize()
+    assert len(pieces.taken) > eager                     # the larger plan took a larger block,
+    recorded = [p for p in pieces.taken if p not in pieces.back]
+    assert len(recorded) >= 2                            # beside the graph's, which was not given back
+    offsets, source, position = m.route_plan(big, 1000)
+    side = torch.cuda.Stream()
+    for seed in range(4):
+        e.copy_(uneven(rng(seed), 9000, 300))
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):                    # replays beside eager calls on the context's stream
+            for _ in range(5):
+                graph.replay()
+        for _ in range(5):
+            again = m.route_plan(big, 1000)
+        torch.cuda.synchronize()
+        assert torch.equal(again[0], offsets) and torch.equal(again[1], source) and torch.equal(again[2], position)
+        for a, b in zip([t.clone() for t in kept], step()):
+            assert torch.equal(a, b)
+    torch.cuda.synchronize()
+    del graph
+    m.close()
+    assert sorted(pieces.taken) == sorted(pieces.back)
+
+
+def test_scratch_of_each_stream():
+    """Calls on two streams, neither waiting for the other, do not share scratch; every block goes back in the end."""
+    m = binding.MPNN(I.make_params(1), DEV)
+    pieces = Pieces(m)
+    g = rng(2)
+    plans = [uneven(g, 200000 + 5000 * i, 700) for i in range(2)]
+    want = [R.plan(e, 700) for e in plans]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = []
+    for turn in range(6):
+        for e, s in zip(plans, streams):
+            with torch.cuda.stream(s):
+                m.set_stream(s)
+                got.append(m.route_plan(e, 700))
+    assert len(pieces.taken) == 2 and not pieces.back
+    torch.cuda.synchronize()
+    for i, (offsets, source, position) in enumerate(got):
+        for a, b in zip((offsets, source, position), want[i % 2]):
+            assert (a.cpu().numpy() == b).all()
+    del got
+    m.close()
+    assert sorted(pieces.taken) == sorted(pieces.back)
