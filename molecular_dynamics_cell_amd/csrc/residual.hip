@@ -42,8 +42,8 @@ enum Mode { kAny = -1, kNoGate = 0, kRowGate = 1, kElementGate = 2 };
 
 // A row's place in the block's registers: W values a chunk, CH chunks a lane, G lanes.  The chunk that would pass the
 // row's end is moved back to end with it, and lanes past the last chunk repeat it, so that every access is a whole chunk
-// of the row; the values that another lane has too count in no sum (`mine` is 0), and what is stored of them is what
-// their owner stores.  EXACT: there are none.
+// of the row; the values that another lane has too (the first `skip` of a lane's last chunk: every chunk before it lies
+// inside the row) count in no sum, and what is stored of them is what their owner stores.  EXACT: there are none.
 template <class T, int W, int G, int CH, bool EXACT>
 struct Lanes {
     static constexpr int E = CH * W;                       // values of a row per lane
@@ -52,15 +52,13 @@ struct Lanes {
     int lane, group;
     int width;
     int column[CH];
-    float mine[EXACT ? 1 : E];
+    int skip;
     __device__ __forceinline__ Lanes(int w) : lane(threadIdx.x % G), group(threadIdx.x / G), width(w) {
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
             const int at = (c * G + lane) * W;
             column[c] = EXACT ? at : min(at, width - W);
-            if (!EXACT)
-#pragma unroll
-                for (int j = 0; j < W; ++j) mine[c * W + j] = column[c] + j >= at ? 1.0f : 0.0f;
+            skip = at - column[c];
         }
     }
     // A row as it is in memory.
@@ -94,8 +92,8 @@ struct Lanes {
 #pragma unroll
         for (int c = 0; c < CH; ++c) __builtin_memcpy(&v[c * W], p + column[c], W * sizeof(float));
     }
-    // one value's share of a sum
-    __device__ __forceinline__ float share(float v, int e) const { return EXACT ? v : v * mine[EXACT ? 0 : e]; }
+    // one value's share of a sum: the value or nothing, not a product with 0, which of an infinity is NaN
+    __device__ __forceinline__ float share(float v, int e) const { return EXACT || e < E - W || e - (E - W) >= skip ? v : 0.0f; }
     // The reverse pass keeps its vectors in LDS (zeros past the width), whose registers its sums need.  The offset is
     // zero, but not to the compiler, which would move the reads out of the row loop, into registers.
     static constexpr int kSlots = G * E;
@@ -157,7 +155,10 @@ struct Lanes {
         }
         float q[1] = {0.0f};
 #pragma unroll
-        for (int e = 0; e < E; ++e) q[0] = fmaf(share(v[e], e), v[e], q[0]);
+        for (int e = 0; e < E; ++e) {
+            const float mine = share(v[e], e);
+            q[0] = fmaf(mine, mine, q[0]);
+        }
         sums(q, sh, turn);
         const float inv = rsqrtf(q[0] * inv_width + eps);
 #pragma unroll
@@ -446,7 +447,7 @@ NormArgs args_of(const mpnn_norm &p, int64_t n, bool gate) {
 template <bool BACK, class F>
 Status by_width(int dtype, int width, F run) {
 #define MPNN_ROW(type, limit, wide, lanes, chunks)                                                                      \
-    if (width <= limit)                                                                                                 \
+    if (width <= limit && width > wide * lanes * (chunks - 1))                                                          \
         return run(type{}, std::integral_constant<int, wide>{}, std::integral_constant<int, lanes>{}, std::integral_constant<int, chunks>{});
     if (dtype == MPNN_BF16) {
         MPNN_ROW(bf16, 7, 1, 8, 1)

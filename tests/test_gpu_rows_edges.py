@@ -199,3 +199,56 @@ def test_scratch_of_each_stream():
     del got
     m.close()
     assert sorted(pieces.taken) == sorted(pieces.back)
+
+
+def same_kind(got, want):
+    """Not-a-numbers and infinities in the same places, of the same sign."""
+    got = f64(got)
+    assert torch.equal(got.isnan(), want.isnan()), (got.isnan().sum(), want.isnan().sum())
+    assert torch.equal(got.isinf(), want.isinf()) and torch.equal(got[got.isinf()] > 0, want[want.isinf()] > 0)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("kind", ["rms", "layer"])
+@pytest.mark.parametrize("width", [6, 30, 108, 312, 1000, 1400, 5000])
+def test_one_infinity_in_a_row(m, width, kind, dtype):
+    """An rms row with an infinity is the bias elsewhere (1 over an infinite root is 0), whichever column holds it: rows that
+    do not fill their lanes hold some columns twice.  A layer row is NaN throughout."""
+    g = rng(width)
+    columns = sorted({0, 1, width // 2, *range(max(0, width - 12), width)})
+    n = len(columns) + 1                                    # the last row is finite
+    at = (torch.arange(n - 1, device=DEV), torch.tensor(columns, device=DEV))
+    w = {k: normal(g, width, size=0.3, at=0.0 if "bias" in k else 1.0)
+         for k in ("post_weight", "post_bias", "scale", "pre_weight", "pre_bias")}
+    w64 = {k: f64(v) for k, v in w.items()}
+    x, block = normal(g, n, width, dtype=dtype), normal(g, n, width, dtype=dtype)
+    size = (width + 64) * U * 16      # of a finite row: sums of `width` terms and the rest of the formula, values of size < 16
+    block[at] = float("inf")
+    block[0, columns[0]] = float("-inf")
+    for gate in (None, normal(g, n, 1, dtype=dtype), normal(g, n, width, dtype=dtype)):
+        r, h = m.norm_residual(x, block, gate, **w, kind=kind, eps=EPS)
+        r64, h64 = R.residual(f64(x), f64(block), f64(gate), w64, kind == "layer", EPS)
+        check("r", r, r64, size, dtype)
+        check("h", h, h64, size * 4, dtype)
+    x[at] = float("inf")
+    _, h = m.norm_residual(x, pre_weight=w["pre_weight"], pre_bias=w["pre_bias"], kind=kind, eps=EPS)
+    check("h of x", h, R.normed(f64(x), kind == "layer", EPS)[0] * w64["pre_weight"] + w64["pre_bias"], size, dtype)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("width", [6, 30, 108, 312, 1000, 1400, 5000])
+def test_one_infinity_in_a_gradient(m, width, dtype):
+    """An infinity in dr: where the formula has infinities and where NaN, in any column."""
+    g = rng(width)
+    columns = sorted({0, width // 2, *range(max(0, width - 9), width)})
+    n = len(columns)
+    dr, block = normal(g, n, width, dtype=dtype), normal(g, n, width, dtype=dtype)
+    block[block == 0] = 1.0
+    dr[torch.arange(n, device=DEV), torch.tensor(columns, device=DEV)] = float("inf")
+    gate = normal(g, n, 1, dtype=dtype)
+    dx, dblock, dgate, *_ = m.norm_residual_backward(dr, None, None, block, gate, kind="rms", eps=EPS)
+    hat, inv = R.normed(f64(block), False, EPS)
+    sig = torch.sigmoid(f64(gate))
+    same_kind(dx, f64(dr))
+    same_kind(dblock, R.normed_back(f64(dr) * sig, hat, inv, False))
+    same_kind(dgate, (f64(dr) * hat * sig * (1 - sig)).sum(-1, keepdim=True))
