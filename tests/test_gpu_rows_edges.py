@@ -252,3 +252,28 @@ def test_one_infinity_in_a_gradient(m, width, dtype):
     same_kind(dx, f64(dr))
     same_kind(dblock, R.normed_back(f64(dr) * sig, hat, inv, False))
     same_kind(dgate, (f64(dr) * hat * sig * (1 - sig)).sum(-1, keepdim=True))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("form", ["row", "element"])
+@pytest.mark.parametrize("n,width", [(13, 108), (13, 312), (9, 1024), (7, 1400)])
+def test_gate_gradient_far_from_zero(m, n, width, form, dtype):
+    """sigma'(g) = sigma(g) sigma(-g) to fp32 accuracy at both signs: |g| 2^-24 from the exponent's argument and a few
+    units from the rest, relative to total scale u sigma (1 - sigma) term by term."""
+    g = rng(width)
+    far = torch.tensor([8.0, 12.0, 15.0, 17.5, 20.0, 30.0, 80.0])
+    far = torch.cat([far, -far])
+    gate = far[torch.randint(0, len(far), (n, 1 if form == "row" else width), generator=g)].to(dtype).to(DEV)
+    dr, dh, r, block = (normal(g, n, width, dtype=dtype) for _ in range(4))
+    _, _, dgate, *_ = m.norm_residual_backward(dr, dh, r, block, gate, kind="rms", eps=EPS)
+    rhat, rinv = R.normed(f64(r), False, EPS)
+    hat, inv = R.normed(f64(block), False, EPS)
+    total = f64(dr) + R.normed_back(f64(dh), rhat, rinv, False)
+    size = f64(dr).abs() + R.normed_back_size(f64(dh).abs(), rhat, rinv) * (1 + rinv * f64(r).abs().mean(-1, keepdim=True))
+    g64 = f64(gate)
+    slope = 1 / (1 + torch.exp(-g64)) / (1 + torch.exp(g64))
+    us = hat.abs() + inv * f64(block).abs().mean(-1, keepdim=True)
+    want, bound = total * hat * slope, (4 * width + 64 + 4 * g64.abs()) * U * size * us * slope
+    if form == "row":
+        want, bound = want.sum(-1, keepdim=True), bound.sum(-1, keepdim=True)
+    check("dgate", dgate, want, bound, dtype)
