@@ -178,8 +178,11 @@ struct Lanes {
 };
 
 // In a group of several waves all waves of the block take the same row, so barriers inside the row loop are uniform.
+// r may be x, so neither is __restrict__: where a row does not fill its lanes, another wave stores columns that this one
+// loads too, and the loads have to stay before the barriers of the block's norm, which that store comes after.  (Rows without
+// a block are stored as they were loaded.)
 template <class T, int W, int G, int CH, int MODE, bool EXACT>
-__global__ __launch_bounds__((Lanes<T, W, G, CH, false>::kThreads)) void k_norm_residual(NormArgs a, const T *__restrict__ x, int64_t ldx,
+__global__ __launch_bounds__((Lanes<T, W, G, CH, false>::kThreads)) void k_norm_residual(NormArgs a, const T *x, int64_t ldx,
                                                                              const T *__restrict__ block, int64_t ldb,
                                                                              const T *__restrict__ gate, int64_t ldg, T *r,
                                                                              T *__restrict__ h) {

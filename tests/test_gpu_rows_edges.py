@@ -277,3 +277,29 @@ def test_gate_gradient_far_from_zero(m, n, width, form, dtype):
     if form == "row":
         want, bound = want.sum(-1, keepdim=True), bound.sum(-1, keepdim=True)
     check("dgate", dgate, want, bound, dtype)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("gate_kind", ["none", "row", "element"])
+@pytest.mark.parametrize("width", [30, 108, 312, 1000, 1400, 2600, 5000, 8192])
+def test_in_place_rows_of_several_waves(m, width, gate_kind, dtype):
+    """r = x and dx = dr give the bits of separate arrays, also where lanes of another wave hold the same columns."""
+    g = rng(width)
+    n = 700
+    x, block, dr, dh = (normal(g, n, width, dtype=dtype) for _ in range(4))
+    gate = {"none": None, "row": normal(g, n, 1, dtype=dtype), "element": normal(g, n, width, dtype=dtype)}[gate_kind]
+    p, _ = m._norm(x, width, gate, "layer", EPS, [])
+    ptr, wide = None if gate is None else gate.data_ptr(), 0 if gate is None else gate.shape[1]
+    r, h = m.norm_residual(x, block, gate, kind="layer", eps=EPS)
+    dx, dblock, dgate, *_ = m.norm_residual_backward(dr, dh, r, block, gate, kind="layer", eps=EPS)
+    h2, db = torch.empty_like(x), torch.empty_like(x)
+    dg = None if gate is None else torch.empty_like(gate)
+    L = binding.lib()
+    assert L.mpnn_norm_residual(m.h, C.byref(p), n, x.data_ptr(), width, block.data_ptr(), width, ptr, wide, x.data_ptr(),
+                                h2.data_ptr()) == 0
+    assert L.mpnn_norm_residual_backward(m.h, C.byref(p), n, dr.data_ptr(), dh.data_ptr(), r.data_ptr(), width, block.data_ptr(),
+                                         width, ptr, wide, dr.data_ptr(), db.data_ptr(), None if dg is None else dg.data_ptr(),
+                                         *[None] * 5) == 0
+    torch.cuda.synchronize()
+    assert torch.equal(x, r) and torch.equal(h2, h) and torch.equal(dr, dx) and torch.equal(db, dblock)
+    assert dg is None or torch.equal(dg, dgate)
