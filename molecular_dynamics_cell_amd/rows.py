@@ -3,7 +3,9 @@ and the calls.  Rows are 2-D tensors [n, width] of float32 or bfloat16 on the co
 row tensor may have any row stride (a column block of a wider tensor), other layouts are copied.
 
 Work runs on the context's stream.  When torch's current stream is another one, the call waits for
-it, and it waits for the call, so tensors may be made and used there.  Calls may be captured into a
+it, and it waits for the call, so tensors may be made and used there.  The methods are no autograd
+functions (each gradient is a method of its own): with gradients enabled a tensor that requires one is
+refused, rather than its gradient dropped; call them under torch.no_grad().  Calls may be captured into a
 graph, which may be replayed as long as the context lives; replay the graphs captured from one context
 one after another (they share its scratch for captured calls)."""
 from __future__ import annotations
@@ -71,6 +73,11 @@ class RowOperators:
 
     def _call(self, name, tensors, *args):
         """One library call on the context's stream, ordered with torch's current stream."""
+        if torch.is_grad_enabled():
+            for t in tensors:
+                if t is not None and t.requires_grad:
+                    raise ValueError(f"{name[5:]}: a tensor requires a gradient, which the result would not carry; call it "
+                                     "under torch.no_grad() and take gradients from the methods for them")
         call = _CALLS.get(name)
         if call is None:
             from . import binding

@@ -68,3 +68,37 @@ def test_plain_silu_slope():
     z = torch.linspace(-20, 20, 81, dtype=torch.float64)
     assert torch.allclose(R.silu_slope(z), (R.silu(z + 1e-5) - R.silu(z - 1e-5)) / 2e-5, atol=1e-9)
     assert np.isfinite(R.silu(z).numpy()).all()
+
+
+class Unlaunched:
+    """The methods of a context without a library behind them: what they refuse by themselves."""
+
+    def __new__(cls):
+        from molecular_dynamics_cell_amd import rows
+        m = rows.RowOperators()
+        m.h, m._at, m._stream = None, torch.device("cpu"), None
+        return m
+
+
+def test_tensors_that_require_a_gradient_are_refused():
+    """A result without a gradient in place of one that a caller would train through; without gradients nothing is refused."""
+    m, x, w = Unlaunched(), torch.zeros(6, 8), torch.ones(8)
+    position, offsets = torch.zeros(3, 2, dtype=torch.int32), torch.zeros(4, dtype=torch.int32)
+    weight, rows = torch.zeros(3, 2), torch.zeros(3, 8)
+    held = (torch.zeros(6, 8, dtype=torch.int8), torch.zeros(6, 1, dtype=torch.uint8))
+    seg = torch.tensor([0, 6], dtype=torch.int32)
+    calls = [lambda g: m.route_scatter(g(rows), position, offsets), lambda g: m.route_combine(g(x), position, offsets),
+             lambda g: m.route_combine(x, position, offsets, g(weight)),
+             lambda g: m.route_combine_backward(g(rows), None, position, offsets),
+             lambda g: m.norm_residual(g(x)), lambda g: m.norm_residual(x, g(x)), lambda g: m.norm_residual(x, x, g(x)),
+             lambda g: m.norm_residual(x, pre_weight=g(w)), lambda g: m.norm_residual(x, x, scale=g(w)),
+             lambda g: m.norm_residual(g(x[:, ::2])),
+             lambda g: m.norm_residual_backward(g(x), x, x), lambda g: m.checkpoint_save(g(x)), lambda g: m.checkpoint_silu(g(x)),
+             lambda g: m.checkpoint_silu_backward(g(x), held), lambda g: m.checkpoint_weight_grad(g(x), held, seg)]
+    for call in calls:
+        with pytest.raises(ValueError, match="requires a gradient"):
+            call(lambda t: t.clone().requires_grad_())
+        for enabled in (True, False):         # past the refusal: there is no library to reach, which is another error
+            with torch.set_grad_enabled(enabled), pytest.raises(Exception) as e:
+                call(lambda t: t if enabled else t.clone().requires_grad_())
+            assert "requires a gradient" not in str(e.value)
