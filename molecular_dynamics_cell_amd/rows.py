@@ -170,6 +170,8 @@ class RowOperators:
         n, width = like.shape
         block, ldb = (None, 0) if block is None else self._rows("block", block, n, width, like.dtype)
         gate, ldg = (None, 0) if gate is None else self._rows("gate", gate, n, None, like.dtype)
+        if gate is not None and gate.shape[1] == 0:     # its null pointer would stand for no gate
+            raise ValueError(f"gate: expected [{n}, {width}] or [{n}, 1], got {tuple(gate.shape)}")
         return block, ldb, gate, ldg
 
     def norm_residual(self, x: torch.Tensor, block: torch.Tensor = None, gate: torch.Tensor = None, *,

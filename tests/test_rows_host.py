@@ -102,3 +102,11 @@ def test_tensors_that_require_a_gradient_are_refused():
             with torch.set_grad_enabled(enabled), pytest.raises(Exception) as e:
                 call(lambda t: t if enabled else t.clone().requires_grad_())
             assert "requires a gradient" not in str(e.value)
+
+
+def test_gate_without_columns_is_refused():
+    m, x = Unlaunched(), torch.zeros(6, 8)
+    with pytest.raises(ValueError, match="gate"):
+        m.norm_residual(x, x, x[:, :0])
+    with pytest.raises(ValueError, match="gate"):
+        m.norm_residual_backward(x, x, x, x, x[:, :0])
