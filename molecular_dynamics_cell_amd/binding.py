@@ -6,6 +6,7 @@ from __future__ import annotations
 import ctypes as C
 import os
 import re
+import weakref
 
 import numpy as np
 import torch
@@ -169,13 +170,13 @@ class MPNN(rows.RowOperators):
         self._check(lib().mpnn_set_stream(self.h, C.c_void_p(stream.cuda_stream)))
 
     def use_torch_allocator(self):
-        """Take the context's later device buffers from torch's caching allocator, on the
-        context's stream (existing buffers stay where they are)."""
-        dev, stream = self.device, self._stream
+        """Take the context's later device buffers from torch's caching allocator, on the stream that
+        the context then has (existing buffers stay where they are)."""
+        dev, me = self.device, weakref.proxy(self)
 
         def alloc(nbytes, user):
             try:
-                return torch.cuda.caching_allocator_alloc(int(nbytes), dev, stream)
+                return torch.cuda.caching_allocator_alloc(int(nbytes), dev, me._stream)
             except RuntimeError:
                 return None   # NULL: the library reports out of memory
 

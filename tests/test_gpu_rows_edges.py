@@ -303,3 +303,47 @@ def test_in_place_rows_of_several_waves(m, width, gate_kind, dtype):
     torch.cuda.synchronize()
     assert torch.equal(x, r) and torch.equal(h2, h) and torch.equal(dr, dx) and torch.equal(db, dblock)
     assert dg is None or torch.equal(dg, dgate)
+
+
+def test_torch_allocator_follows_the_stream(monkeypatch):
+    """Scratch taken from torch's allocator is memory of the stream that the call runs on, captured calls' included, and all
+    of it goes back."""
+    g = rng(3)
+    e, n, E = uneven(g, 50000, 400), 50000, 400
+    want = R.plan(e, E)
+    streams, side = [], torch.cuda.Stream()
+    real = torch.cuda.caching_allocator_alloc
+
+    def noted(size, device=None, stream=None):
+        streams.append(stream.cuda_stream)
+        return real(size, device, stream)
+
+    monkeypatch.setattr(torch.cuda, "caching_allocator_alloc", noted)
+    torch.cuda.synchronize()
+    m = binding.MPNN(I.make_params(1), DEV)
+    m.use_torch_allocator()
+    home = m._stream
+    first = m.route_plan(e, E)
+    m.set_stream(side)
+    with torch.cuda.stream(side):
+        second = m.route_plan(e, E)
+    torch.cuda.synchronize()
+    assert streams == [home.cuda_stream, side.cuda_stream]
+    graph = torch.cuda.CUDAGraph()
+    try:
+        with torch.cuda.graph(graph):
+            recording = torch.cuda.current_stream()
+            m.set_stream(recording)
+            third = m.route_plan(e, E)
+    finally:
+        m.set_stream(home)
+    assert streams[2:] == [recording.cuda_stream]
+    for _ in range(3):
+        graph.replay()
+        torch.cuda.synchronize()
+        for got in (first, second, third, m.route_plan(e, E)):
+            for a, b in zip(got, want):
+                assert (a.cpu().numpy() == b).all()
+    assert len(streams) == 3
+    del graph, got, third
+    m.close()
