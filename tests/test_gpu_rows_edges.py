@@ -347,3 +347,31 @@ def test_torch_allocator_follows_the_stream(monkeypatch):
     assert len(streams) == 3
     del graph, got, third
     m.close()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("width,pad,shift", [(64, 64, 0), (108, 20, 4), (64, 1, 1), (312, 9, 3), (33, 7, 2), (1024, 1024, 0),
+                                             (1400, 3, 1), (5000, 8, 8)])
+@pytest.mark.parametrize("kind,gate", [("rms", "element"), ("layer", "row"), ("layer", "none")])
+def test_strided_rows_bit_for_bit(m, width, pad, shift, kind, gate, dtype):
+    """The layout in memory changes no lane's work and no order of a sum: column blocks give the dense rows' bits."""
+    g = rng(width)
+    n, k = 50, 2
+
+    def pair(w=width):
+        part = normal(g, n, w + pad + shift, dtype=dtype)[:, shift:shift + w]
+        return part, part.contiguous()
+
+    (x, xd), (b, bd), (dy, dyd) = pair(), pair(), pair()
+    t, td = {"none": (None, None), "row": pair(1), "element": pair()}[gate]
+    for p, q in zip(m.norm_residual(x, b, t, kind=kind), m.norm_residual(xd, bd, td, kind=kind)):
+        assert torch.equal(p, q)
+    for p, q in zip(m.norm_residual_backward(dyd, xd, x, b, t, kind=kind), m.norm_residual_backward(dyd, xd, xd, bd, td, kind=kind)):
+        assert (p is None and q is None) or torch.equal(p, q)
+    offsets, source, position = m.route_plan(torch.randint(-1, 3, (n, k), generator=g, dtype=torch.int32).to(DEV), 3)
+    y = normal(g, n * k, width, dtype=dtype)
+    for p, q in zip(m.route_combine_backward(dy, y, position, offsets), m.route_combine_backward(dyd, y, position, offsets)):
+        assert torch.equal(p, q)
+    held, seg = m.checkpoint_save(x), torch.tensor([0, 20, 50], dtype=torch.int32, device=DEV)
+    for p, q in zip(m.checkpoint_weight_grad(dy, held, seg), m.checkpoint_weight_grad(dyd, held, seg)):
+        assert torch.equal(p, q)
