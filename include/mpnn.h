@@ -377,6 +377,7 @@ mpnn_status mpnn_checkpoint_silu_backward(mpnn_ctx *ctx, int32_t dtype, int64_t 
  * dweight[e][o][c] = sum of dy[q][o] x[q][c] over the rows offsets[e] <= q < offsets[e + 1] (offsets device
  * [n_experts + 1], as mpnn_route_plan writes them; clamped to 0 .. n), dbias[e][o] = sum of dy[q][o] (may be
  * NULL).  fp32, as accurate as fp32 products and sums for both types; an expert without rows gets zeros.
+ * Rows are split among blocks as for experts of alike lengths: one expert that holds most of the rows of many takes longer.
  * width and n_out at most 65,536, ld_dy at most 2^24. */
 mpnn_status mpnn_checkpoint_weight_grad(mpnn_ctx *ctx, int32_t dtype, int64_t n, int32_t n_out, int32_t width,
                                         int32_t n_experts, const int32_t *offsets, const void *dy, int64_t ld_dy,

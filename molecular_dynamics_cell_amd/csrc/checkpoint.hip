@@ -6,8 +6,9 @@
 // and reading one back rounds nothing.
 //
 // Bound by HBM: a lane takes 16 bytes of the rows, and a group's largest value comes from its 4 or 8 neighbouring lanes
-// without LDS.  400,002 x 128: fp32 saved in 42 us (258 MB, 6.1 TB/s), with SiLU and both checkpoints 106 us (515 MB,
-// 4.9 TB/s), its gradient 88 us (5.2 TB/s), read back 38 us; bf16 31, 70, 55 and 24 us.
+// without LDS.  400,002 x 128: fp32 saved in 42 us (258 MB, 6.1 TB/s), with SiLU and both checkpoints 102 us (515 MB,
+// 5.0 TB/s), its gradient 88 us (5.2 TB/s), read back 38 us; bf16 29, 69, 52 and 24 us in a loop of one of them, 73, 55 and
+// 30 us for the last three one after another.
 #include "impl.h"
 #include "rows.h"
 

@@ -11,7 +11,7 @@
 // in a fixed order.
 //
 // Bound by HBM: forward of 400,002 x 128 fp32 187 us (1.02 GB, 5.5 TB/s), reverse of 128,000 x 312 fp32 with a gate a row
-// 187 us (959 MB, 5.1 TB/s), of 8,192 x 4,096 bf16 126 us (537 MB, 4.3 TB/s: 114 us and 10 us for 33 MB of blocks' sums,
+// 184 us (959 MB, 5.2 TB/s), of 8,192 x 4,096 bf16 125 us (537 MB, 4.3 TB/s: 115 us and 8 us for 33 MB of blocks' sums,
 // which rows this wide cost).  One row alone takes 3 us.
 #include <algorithm>
 #include <type_traits>
@@ -276,8 +276,8 @@ __global__ __launch_bounds__((Lanes<T, W, G, CH, false>::kThreads)) void k_norm_
     __shared__ float sh1[2][L::kWaves > 1 ? L::kWaves : 1], sh2[2][L::kWaves > 1 ? 2 * L::kWaves : 1], sh3[2][kShared];
     __shared__ float columns[L::kGroups > 1 ? L::kGroups * G * E : 1];
     // Rows of several waves that do not fill their slots take more registers, and run in fewer waves: there the block's and
-    // the gate's loads go out with the first ones, if they are short (bf16: 8,192 x 5,000 217 -> 202 us; where rows fill
-    // their slots 237 -> 242 us at 32,768 x 2,048).
+    // the gate's loads go out with the first ones, if they are short (bf16: 24,000 x 2,600 257 -> 225 us, x 1,400 121 -> 124 us,
+    // 8,192 x 5,000 194 us either way; where rows fill their slots 214 -> 220 us at 32,768 x 2,048, so not there).
     constexpr bool kEarly = sizeof(T) == 2 && !EXACT && L::kWaves > 1;
     int turn1 = 0, turn2 = 0, turn3 = 0;
     const L at(a.width);

@@ -4,9 +4,10 @@
 // a kernel reads from them is one it can check against n k.
 //
 // All of it is bound by HBM, the plan by its launches.  Rows sent to their places: 128,000 x 312 fp32 to one place 65 us
-// (320 MB, 4.9 TB/s), 16,384 x 2,048 bf16 to eight 130 us (604 MB, 4.6 TB/s); added up again 57 us (5.6 TB/s) and, with
-// dropped pairs, 157 us; the gradient with the weights' dot products, 65,536 x 1,024 bf16 from four: 224 us (1.21 GB,
-// 5.4 TB/s).  The plan of 128,000 pairs: 11 us in two launches, one launch up to 1,024 pairs (4 us).
+// (320 MB, 4.9 TB/s), 16,384 x 2,048 bf16 to eight 130 us (604 MB, 4.6 TB/s); added up again 57 us (5.6 TB/s) and 122 us
+// (5.0 TB/s; 156 us right after the rows were sent out, whose lines are still on their way to memory); the gradient with the
+// weights' dot products, 65,536 x 1,024 bf16 from four: 224 us (1.21 GB, 5.4 TB/s).  The plan of 128,000 pairs: 11 us in two
+// launches, one launch up to 1,024 pairs (4 us).
 #include <algorithm>
 #include <type_traits>
 
@@ -210,7 +211,7 @@ __device__ __forceinline__ int live_places(const int32_t *used, int64_t pairs) {
 
 // out[i] = sum over s of weight[i, s] sorted[position[i, s]], in the order of the slots, in fp32.  S slots of kUnroll / S
 // items are loaded together, a thread's only ones (with four items a thread at any S 165 us at 16,384 x 2,048 bf16 from
-// eight, 157 us with one).
+// eight right after they were sent out, 156 us with one).
 template <class T, bool SHORT, int S>
 __global__ __launch_bounds__(256) void k_route_combine(Items it, int64_t pairs, int k, int width, const T *__restrict__ sorted,
                                                        const int32_t *__restrict__ position, const int32_t *__restrict__ used,

@@ -2,8 +2,10 @@
 //   dW_e[o][c] = sum over the rows q of expert e of dy[q][o] x[q][c],  db_e[o] = sum of dy[q][o],
 // with x the values that the checkpoint holds: a product whose long axis is the rows.
 //
-// The rows of an expert are cut into pieces of at most `rows`; a block takes one piece and one BM x 128 tile of dW.
-// An expert of one piece is written at once, the pieces of the others are added afterwards in their order, so results
+// The rows of an expert are cut into pieces of at most `rows`; a block takes one piece and one BM x 128 tile of dW.  How
+// long a piece is follows from the experts being alike: where they and their tiles fill the GPU already none is cut, and
+// one that holds most of the rows takes its few blocks' time (65,536 rows 256 -> 512 x 64 bf16: 43 us with equal shares,
+// 1,164 us with 95 % in one).  An expert of one piece is written at once, the pieces of the others are added afterwards in their order, so results
 // do not depend on the launch.
 //
 // Operands on the bf16 matrix cores: x is exact in bf16 (7 bits and a power of two).  A bf16 dy is one as it stands;
@@ -11,9 +13,9 @@
 // every product is exact and the sums are fp32 as with fp32 products.
 //
 // 128,000 rows 312 -> 128 x 5 fp32: 51 us and 7 us for the pieces' sums (10 GFLOP, three products each: 0.6 PFLOP/s on the
-// matrix cores in the first; the operands are 107 MB, 22 us); bf16 38 us together; 16,384 rows 1024 -> 1024 x 8 bf16: 74 us
-// (0.46 PFLOP/s).  A stage of 64 rows costs a wave, with two waves a SIMD: 600 .. 700 cycles to cut and store dy in bf16 (1,900
-// in fp32), 600 for x, 800 for the products (512 are the instructions; fp32 2,100 and 1,536) and 1,000 to get its 17 loads
+// matrix cores in the first; the operands are 107 MB, 22 us); bf16 38 us together; 16,384 rows 1024 -> 1024 x 8 bf16: 65 .. 75 us
+// by the run (0.46 .. 0.53 PFLOP/s).  A stage of 64 rows costs a wave, with two waves a SIMD: 600 .. 700 cycles to cut and
+// store dy in bf16 (1,900 in fp32), 600 for x, 800 for the products (512 are the instructions; fp32 2,100 and 1,536) and 1,000 to get its 17 loads
 // issued.  Without the loads the time is the same: it is the issue of vector, LDS and matrix instructions by few waves.
 // What is read of memory is 5 TB/s at most, mostly from the L2s.
 #include <algorithm>

@@ -5,9 +5,11 @@ row tensor may have any row stride (a column block of a wider tensor), other lay
 Work runs on the context's stream.  When torch's current stream is another one, the call waits for
 it, and it waits for the call, so tensors may be made and used there.  The methods are no autograd
 functions (each gradient is a method of its own): with gradients enabled a tensor that requires one is
-refused, rather than its gradient dropped; call them under torch.no_grad().  Calls may be captured into a
-graph, which may be replayed as long as the context lives; replay the graphs captured from one context
-one after another (they share its scratch for captured calls)."""
+refused, rather than its gradient dropped; call them under torch.no_grad().
+
+Calls may be captured into a graph (with the captured stream as the context's: set_stream), which may
+be replayed as long as the context lives; replay the graphs captured from one context one after another
+(they share its scratch for captured calls)."""
 from __future__ import annotations
 
 import ctypes as C
