@@ -383,6 +383,61 @@ mpnn_status mpnn_checkpoint_weight_grad(mpnn_ctx *ctx, int32_t dtype, int64_t n,
                                         int32_t n_experts, const int32_t *offsets, const void *dy, int64_t ld_dy,
                                         const int8_t *codes, const uint8_t *scales, float *dweight, float *dbias);
 
+/* Products of sorted rows with their experts' weights: for offsets[e] <= q < offsets[e + 1] (offsets device
+ * [n_experts + 1], as mpnn_route_plan writes them; clamped to 0 .. n, e in 0 .. n_experts - 1, at most 1024),
+ *   y[q][o] = act(sum over c of weight[e][o][c] x[s(q)][c] + bias[e][o]),   act(z) = z or z / (1 + exp(-z)).
+ * Rows of no expert (before offsets[0], from offsets[n_experts] on) are zeros, whatever x holds there.  source NULL:
+ * x has the n rows, s(q) = q.  With source (device [n], as mpnn_route_plan writes it) x has n_x rows before they are
+ * sorted, n = n_x k with 1 <= k <= 64, and s(q) = source[q] / k, kept in 0 .. n_x - 1: sorted rows are not written.
+ * weight [n_experts][n_out][width] has the rows' type, bias (fp32, [n_experts][n_out]) may be NULL.  Sums are fp32, and
+ * as accurate as fp32 products and sums for both types; they are rounded once, after the activation.  width, n_out <= 65,536. */
+typedef enum { MPNN_ACT_NONE = 0, MPNN_ACT_SILU = 1 } mpnn_act;
+mpnn_status mpnn_expert_product(mpnn_ctx *ctx, int32_t dtype, int64_t n, int32_t width, int32_t n_out, int32_t n_experts,
+                                const int32_t *offsets, const void *x, int64_t ldx, const int32_t *source, int64_t n_x,
+                                const void *weight, const float *bias, int32_t act, void *y);
+
+/* Its gradients at act = MPNN_ACT_NONE: towards the sorted rows, dx[q][c] = sum over o of dy[q][o] weight[e][o][c] (zeros
+ * for rows of no expert; mpnn_route_combine adds a row's slots up), and towards weights and biases,
+ * dweight[e][o][c] = sum over the rows q of e of dy[q][o] x[s(q)][c], dbias[e][o] = sum of dy[q][o] (may be NULL), fp32 and
+ * zeros for an expert without rows.  Rows are split among blocks as for experts of alike lengths. */
+mpnn_status mpnn_expert_input_grad(mpnn_ctx *ctx, int32_t dtype, int64_t n, int32_t width, int32_t n_out, int32_t n_experts,
+                                   const int32_t *offsets, const void *dy, int64_t ld_dy, const void *weight, void *dx);
+mpnn_status mpnn_expert_weight_grad(mpnn_ctx *ctx, int32_t dtype, int64_t n, int32_t width, int32_t n_out, int32_t n_experts,
+                                    const int32_t *offsets, const void *dy, int64_t ld_dy, const void *x, int64_t ldx,
+                                    const int32_t *source, int64_t n_x, float *dweight, float *dbias);
+
+/* Rows in microscaled 4-bit floating point: with g = ceil(width / 32) groups of 32 columns a row, codes [n][16 g] (two
+ * columns a byte, the lower one in the low bits; zeros past the last column) and scales [n][g].  With `largest` the group's
+ * largest magnitude, m 2^E (1 <= m < 2), the step is 2^e, e = E - 2 but at least -100, and the scale byte e + 127; a code is the
+ * sign (8) and the number of the nearest of 0, 0.5, 1, 1.5, 2, 3, 4, 6 steps, ties to the even one, 6 beyond it.  A group with a
+ * value that is not finite gets the byte 255 and reads back as NaN.  Other scale bytes are 27 .. 252.  Held values are exact in
+ * fp32 and bf16. */
+mpnn_status mpnn_micro_save(mpnn_ctx *ctx, int32_t dtype, int64_t n, int32_t width, const void *x, int64_t ldx, uint8_t *codes,
+                            uint8_t *scales);
+mpnn_status mpnn_micro_load(mpnn_ctx *ctx, int32_t dtype, int64_t n, int32_t width, const uint8_t *codes, const uint8_t *scales,
+                            void *out);
+
+/* mpnn_expert_product with weights held in 4 bits (the n_experts n_out rows of [n_experts][n_out][width], from mpnn_micro_save).
+ * x_dtype: the type of x, or MPNN_MICRO for rows that are held too (x their codes, x_scales their scales, ldx ignored; x_scales
+ * is ignored otherwise).  y has y_dtype.  Products of held values are exact, sums fp32. */
+enum { MPNN_MICRO = 2 };
+mpnn_status mpnn_micro_product(mpnn_ctx *ctx, int32_t x_dtype, int32_t y_dtype, int64_t n, int32_t width, int32_t n_out,
+                               int32_t n_experts, const int32_t *offsets, const void *x, int64_t ldx, const uint8_t *x_scales,
+                               const int32_t *source, int64_t n_x, const uint8_t *codes, const uint8_t *scales, const float *bias,
+                               int32_t act, void *y);
+
+/* Rows of a table by index (an atom's species, a token): out[i] = scale table[index[i]], zeros where index[i] is outside
+ * 0 .. n_entries - 1 (at most 2^20 entries); table dense [n_entries][width].
+ * mpnn_embed_plan orders the rows by index, those of one entry ascending, those of none last: offsets[n_entries + 1] and
+ * source[n], the row at each place.  mpnn_embed_backward adds the rows of each entry up in that order:
+ * dtable[v] = scale * sum of dout[source[q]] over offsets[v] <= q < offsets[v + 1], fp32, zeros for an entry without rows;
+ * offsets are clamped to 0 .. n, places in source to 0 .. n - 1. */
+mpnn_status mpnn_embed(mpnn_ctx *ctx, int32_t dtype, int64_t n, int32_t width, int32_t n_entries, const int32_t *index,
+                       const void *table, double scale, void *out);
+mpnn_status mpnn_embed_plan(mpnn_ctx *ctx, int64_t n, int32_t n_entries, const int32_t *index, int32_t *offsets, int32_t *source);
+mpnn_status mpnn_embed_backward(mpnn_ctx *ctx, int32_t dtype, int64_t n, int32_t width, int32_t n_entries, const void *dout,
+                                int64_t ld_dout, const int32_t *offsets, const int32_t *source, double scale, float *dtable);
+
 /* Text of the last error on this context ("" if none); valid until the next call. */
 const char *mpnn_last_error(const mpnn_ctx *ctx);
 

@@ -99,6 +99,15 @@ def lib():
             "mpnn_checkpoint_silu": ([p, i32, i64, i32, p, i64, p, p, p, p, p], st),
             "mpnn_checkpoint_silu_backward": ([p, i32, i64, i32, p, i64, p, p, p], st),
             "mpnn_checkpoint_weight_grad": ([p, i32, i64, i32, i32, i32, p, p, i64, p, p, p, p], st),
+            "mpnn_expert_product": ([p, i32, i64, i32, i32, i32, p, p, i64, p, i64, p, p, i32, p], st),
+            "mpnn_expert_input_grad": ([p, i32, i64, i32, i32, i32, p, p, i64, p, p], st),
+            "mpnn_expert_weight_grad": ([p, i32, i64, i32, i32, i32, p, p, i64, p, i64, p, i64, p, p], st),
+            "mpnn_micro_save": ([p, i32, i64, i32, p, i64, p, p], st),
+            "mpnn_micro_load": ([p, i32, i64, i32, p, p, p], st),
+            "mpnn_micro_product": ([p, i32, i32, i64, i32, i32, i32, p, p, i64, p, p, i64, p, p, p, i32, p], st),
+            "mpnn_embed": ([p, i32, i64, i32, i32, p, p, d, p], st),
+            "mpnn_embed_plan": ([p, i64, i32, p, p, p], st),
+            "mpnn_embed_backward": ([p, i32, i64, i32, i32, p, i64, p, p, d, p], st),
             "mpnn_last_error": ([p], C.c_char_p),
         }
         for name, (args, res) in sig.items():

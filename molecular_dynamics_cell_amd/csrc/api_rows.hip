@@ -186,4 +186,126 @@ mpnn_status mpnn_checkpoint_weight_grad(mpnn_ctx *ctx, int32_t dtype, int64_t n,
     });
 }
 
+static Status check_product(int32_t dtype, int64_t n, int32_t width, int32_t n_out, int32_t n_experts, const int32_t *offsets) {
+    MPNN_TRY(check_rows(dtype, n, width, 1 << 16));
+    if (n_out < 1 || n_out > 1 << 16) return bad("bad output width");
+    if (n_experts < 1 || n_experts > kMaxExperts) return bad("n_experts must be in 1..1024");
+    if (!offsets) return bad("null array");
+    return Status::ok();
+}
+
+static Status check_source(int64_t n, const int32_t *source, int64_t n_x) {
+    if (!source || n == 0) return Status::ok();
+    if (n_x < 1 || n % n_x || n / n_x > kMaxSlots) return bad("with a source n must be n_x times 1..64 slots");
+    return Status::ok();
+}
+
+static Status check_act(int32_t act) { return act == MPNN_ACT_NONE || act == MPNN_ACT_SILU ? Status::ok() : bad("bad activation"); }
+
+mpnn_status mpnn_expert_product(mpnn_ctx *ctx, int32_t dtype, int64_t n, int32_t width, int32_t n_out, int32_t n_experts,
+                                const int32_t *offsets, const void *x, int64_t ldx, const int32_t *source, int64_t n_x,
+                                const void *weight, const float *bias, int32_t act, void *y) {
+    return guarded(ctx, [&](mpnn::Context &cx) -> Status {
+        MPNN_TRY(check_product(dtype, n, width, n_out, n_experts, offsets));
+        MPNN_TRY(check_ld(ldx, width, "ldx smaller than the width"));
+        MPNN_TRY(check_source(n, source, n_x));
+        MPNN_TRY(check_act(act));
+        if (n > 0 && (!x || !weight || !y)) return bad("null array");
+        return mpnn::expert_product(cx, dtype, n, width, n_out, n_experts, offsets, x, ldx, source, n_x, weight, bias, act, y);
+    });
+}
+
+mpnn_status mpnn_expert_input_grad(mpnn_ctx *ctx, int32_t dtype, int64_t n, int32_t width, int32_t n_out, int32_t n_experts,
+                                   const int32_t *offsets, const void *dy, int64_t ld_dy, const void *weight, void *dx) {
+    return guarded(ctx, [&](mpnn::Context &cx) -> Status {
+        MPNN_TRY(check_product(dtype, n, width, n_out, n_experts, offsets));
+        MPNN_TRY(check_ld(ld_dy, n_out, "ld_dy smaller than the output width"));
+        if (n > 0 && (!dy || !weight || !dx)) return bad("null array");
+        return mpnn::expert_input_grad(cx, dtype, n, width, n_out, n_experts, offsets, dy, ld_dy, weight, dx);
+    });
+}
+
+mpnn_status mpnn_expert_weight_grad(mpnn_ctx *ctx, int32_t dtype, int64_t n, int32_t width, int32_t n_out, int32_t n_experts,
+                                    const int32_t *offsets, const void *dy, int64_t ld_dy, const void *x, int64_t ldx,
+                                    const int32_t *source, int64_t n_x, float *dweight, float *dbias) {
+    return guarded(ctx, [&](mpnn::Context &cx) -> Status {
+        MPNN_TRY(check_product(dtype, n, width, n_out, n_experts, offsets));
+        MPNN_TRY(check_ld(ld_dy, n_out, "ld_dy smaller than the output width"));
+        MPNN_TRY(check_ld(ldx, width, "ldx smaller than the width"));
+        MPNN_TRY(check_source(n, source, n_x));
+        if (!dweight || (n > 0 && (!dy || !x))) return bad("null array");
+        return mpnn::expert_weight_grad(cx, dtype, n, width, n_out, n_experts, offsets, dy, ld_dy, x, ldx, source, n_x, dweight, dbias);
+    });
+}
+
+mpnn_status mpnn_micro_save(mpnn_ctx *ctx, int32_t dtype, int64_t n, int32_t width, const void *x, int64_t ldx, uint8_t *codes,
+                            uint8_t *scales) {
+    return guarded(ctx, [&](mpnn::Context &cx) -> Status {
+        MPNN_TRY(check_rows(dtype, n, width, kMaxWidth));
+        MPNN_TRY(check_ld(ldx, width, "ldx smaller than the width"));
+        if (n > 0 && (!x || !codes || !scales)) return bad("null array");
+        return mpnn::micro_save(cx, dtype, n, width, x, ldx, codes, scales);
+    });
+}
+
+mpnn_status mpnn_micro_load(mpnn_ctx *ctx, int32_t dtype, int64_t n, int32_t width, const uint8_t *codes, const uint8_t *scales,
+                            void *out) {
+    return guarded(ctx, [&](mpnn::Context &cx) -> Status {
+        MPNN_TRY(check_rows(dtype, n, width, kMaxWidth));
+        if (n > 0 && (!codes || !scales || !out)) return bad("null array");
+        return mpnn::micro_load(cx, dtype, n, width, codes, scales, out);
+    });
+}
+
+mpnn_status mpnn_micro_product(mpnn_ctx *ctx, int32_t x_dtype, int32_t y_dtype, int64_t n, int32_t width, int32_t n_out,
+                               int32_t n_experts, const int32_t *offsets, const void *x, int64_t ldx, const uint8_t *x_scales,
+                               const int32_t *source, int64_t n_x, const uint8_t *codes, const uint8_t *scales, const float *bias,
+                               int32_t act, void *y) {
+    return guarded(ctx, [&](mpnn::Context &cx) -> Status {
+        MPNN_TRY(check_product(x_dtype == MPNN_MICRO ? MPNN_F32 : x_dtype, n, width, n_out, n_experts, offsets));
+        if (y_dtype != MPNN_F32 && y_dtype != MPNN_BF16) return bad("y_dtype must be MPNN_F32 or MPNN_BF16");
+        if (x_dtype != MPNN_MICRO) MPNN_TRY(check_ld(ldx, width, "ldx smaller than the width"));
+        MPNN_TRY(check_source(n, source, n_x));
+        MPNN_TRY(check_act(act));
+        if (n > 0 && (!x || !codes || !scales || !y || (x_dtype == MPNN_MICRO && !x_scales))) return bad("null array");
+        return mpnn::micro_product(cx, x_dtype, y_dtype, n, width, n_out, n_experts, offsets, x, ldx, x_scales, source, n_x, codes, scales, bias, act, y);
+    });
+}
+
+static Status check_entries(int64_t n, int32_t n_entries, double scale) {
+    if (n < 0 || n > INT32_MAX) return bad("bad row count");
+    if (n_entries < 1 || n_entries > 1 << 20) return bad("n_entries must be in 1..2^20");
+    if (!std::isfinite(scale) || !std::isfinite((float)scale)) return bad("scale must be finite");
+    return Status::ok();
+}
+
+mpnn_status mpnn_embed(mpnn_ctx *ctx, int32_t dtype, int64_t n, int32_t width, int32_t n_entries, const int32_t *index,
+                       const void *table, double scale, void *out) {
+    return guarded(ctx, [&](mpnn::Context &cx) -> Status {
+        MPNN_TRY(check_rows(dtype, n, width, kMaxWidth));
+        MPNN_TRY(check_entries(n, n_entries, scale));
+        if (n > 0 && (!index || !table || !out)) return bad("null array");
+        return mpnn::embed(cx, dtype, n, width, n_entries, index, table, (float)scale, out);
+    });
+}
+
+mpnn_status mpnn_embed_plan(mpnn_ctx *ctx, int64_t n, int32_t n_entries, const int32_t *index, int32_t *offsets, int32_t *source) {
+    return guarded(ctx, [&](mpnn::Context &cx) -> Status {
+        MPNN_TRY(check_entries(n, n_entries, 1.0));
+        if (!offsets || (n > 0 && (!index || !source))) return bad("null array");
+        return mpnn::embed_plan(cx, n, n_entries, index, offsets, source);
+    });
+}
+
+mpnn_status mpnn_embed_backward(mpnn_ctx *ctx, int32_t dtype, int64_t n, int32_t width, int32_t n_entries, const void *dout,
+                                int64_t ld_dout, const int32_t *offsets, const int32_t *source, double scale, float *dtable) {
+    return guarded(ctx, [&](mpnn::Context &cx) -> Status {
+        MPNN_TRY(check_rows(dtype, n, width, kMaxWidth));
+        MPNN_TRY(check_entries(n, n_entries, scale));
+        MPNN_TRY(check_ld(ld_dout, width, "ld_dout smaller than the width"));
+        if (!offsets || !dtable || (n > 0 && (!dout || !source))) return bad("null array");
+        return mpnn::embed_backward(cx, dtype, n, width, n_entries, dout, ld_dout, offsets, source, (float)scale, dtable);
+    });
+}
+
 }  // extern "C"

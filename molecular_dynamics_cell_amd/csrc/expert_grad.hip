@@ -1,0 +1,177 @@
+// Weight gradients of the experts' products (mpnn_expert_weight_grad):
+//   dW_e[o][c] = sum over the rows q of expert e of dy[q][o] x[q][c],  db_e[o] = sum of dy[q][o].
+// Rows are cut into pieces as for the gradient from checkpoints; both operands have the rows as their slow axis and are
+// turned by the transposing reads of LDS.
+#include <algorithm>
+#include <type_traits>
+
+#include "impl.h"
+#include "pieces.h"
+#include "rows.h"
+#include "tiles.h"
+
+namespace mpnn {
+
+namespace {
+
+struct Args {
+    int64_t n, rows;                // rows; of a piece
+    int out, width, n_experts, tiles_c, tiles;
+    const int32_t *offsets, *source;
+    int64_t n_x;
+    int slots;
+    int64_t part_slots;
+    float *part, *dweight, *dbias;
+};
+
+template <class T, int MT, int NT, int WM, int WN>
+__global__ __launch_bounds__(256, 2) void k_expert_weight_grad(const Args a, const RowsOf<T> dy, const RowsOf<T> x) {
+    constexpr int TERMS = kTerms<T>, WORDS = TERMS > 1 ? 4 : 8, STEPS = 8 * WORDS;
+    constexpr int BC = 32 * MT * WM, BO = 32 * NT * WN;
+    using P = Across<TERMS, BC, WORDS>;
+    using Q = Across<TERMS, BO, WORDS>;
+    __shared__ uint4 lds[P::kWords + Q::kWords];
+    __shared__ float sums[256][8];
+    uint4 *const lp = lds, *const lq = lds + P::kWords;
+
+    const uint32_t number = (uint32_t)xcd_block();
+    const int tile = (int)(number % (uint32_t)a.tiles);
+    const Piece pc = find_piece(a.offsets, a.n_experts, a.n, a.rows, (int)(number / (uint32_t)a.tiles), -1);
+    if (pc.expert < 0) return;
+    int64_t from, to;
+    pieces_of(a.offsets, pc.expert, a.n, a.rows, from, to);
+    from += pc.piece * a.rows;
+    to = min(to, from + a.rows);
+    const int o0 = tile / a.tiles_c * BO, c0 = tile % a.tiles_c * BC;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, wm = wave / WN, wn = wave % WN;
+
+    constexpr int WP = BC / 8, WQ = BO / 8, XP = STEPS * WP / 256, XQ = STEPS * WQ / 256;     // words a row; words a thread
+    static_assert(STEPS * WP % 256 == 0 && STEPS * WQ % 256 == 0, "whole words a thread");
+    Word<T> pv[XP], qv[XQ];
+    int32_t at[XP];
+    const auto places = [&](int64_t q0) {
+#pragma unroll
+        for (int i = 0; i < XP; ++i) {
+            const int64_t q = min(q0 + tid / WP + i * (256 / WP), a.n - 1);
+            at[i] = a.source ? (int32_t)min((int64_t)((uint32_t)max(a.source[q], 0) / (uint32_t)a.slots), a.n_x - 1) : (int32_t)q;
+        }
+    };
+    const auto fetch = [&](int64_t q0) {
+#pragma unroll
+        for (int i = 0; i < XP; ++i) {
+            if (q0 + tid / WP + i * (256 / WP) < to) RowsOf<T>::load(pv[i], x.row(at[i]), c0 + tid % WP * 8, a.width);
+            else pv[i].clear();
+        }
+#pragma unroll
+        for (int i = 0; i < XQ; ++i) {
+            const int64_t q = q0 + tid / WQ + i * (256 / WQ);
+            if (q < to) RowsOf<T>::load(qv[i], dy.row(q), o0 + tid % WQ * 8, a.out);
+            else qv[i].clear();
+        }
+    };
+    floatx16 acc[MT][NT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) acc[i][j] = (floatx16)(0.0f);
+    float bias[8] = {}, largest = 0.0f;
+    if (from < to) {
+        places(from);
+        fetch(from);
+    }
+    for (int64_t q0 = from; q0 < to; q0 += STEPS) {
+        places(q0 + STEPS);
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < XP; ++i) {
+            uint4 t[TERMS];
+            pv[i].terms(t, largest);
+            P::store(lp, tid / WP + i * (256 / WP), tid % WP, t);
+        }
+#pragma unroll
+        for (int i = 0; i < XQ; ++i) {
+            uint4 t[TERMS];
+            qv[i].terms(t, largest);
+            Q::store(lq, tid / WQ + i * (256 / WQ), tid % WQ, t);
+            if (c0 == 0)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) bias[j] += qv[i].at(j);
+        }
+        __syncthreads();
+        if (q0 + STEPS < to) fetch(q0 + STEPS);
+        multiply<P, Q, TERMS, TERMS, MT, NT, WORDS>(lp, lq, wm * MT * 32, wn * NT * 32, lane, acc);
+    }
+    const bool huge = TERMS > 1 && __syncthreads_or(largest >= kHuge);
+
+    const int64_t matrix = (int64_t)a.out * a.width;
+    const bool whole = pc.pieces == 1;
+    if (!whole && pc.slot + pc.piece >= a.part_slots) return;     // offsets that do not ascend name more pieces than there are
+    float *to_w = whole ? a.dweight + pc.expert * matrix : a.part + (int64_t)(pc.slot + pc.piece) * slot_size(matrix + a.out);
+    float *to_b = whole ? (a.dbias ? a.dbias + (int64_t)pc.expert * a.out : nullptr) : to_w + matrix;
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+        const int o = o0 + (wn * NT + j) * 32 + (lane & 31);
+        if (o >= a.out) continue;
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const int c = c0 + (wm * MT + i) * 32 + 8 * g + 4 * (lane >> 5), in = a.width - c;
+                if (in <= 0) continue;
+                Chunk<float, 4> v;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) v.v[r] = acc[i][j][4 * g + r];
+                if (huge)
+                    for (int r = 0; r < 4; ++r)
+                        if (v.v[r] != v.v[r] && r < in) {
+                            float s = 0.0f;
+                            for (int64_t q = from; q < to; ++q) {
+                                const int64_t at = a.source ? min((int64_t)((uint32_t)max(a.source[q], 0) / (uint32_t)a.slots), a.n_x - 1) : q;
+                                s = fmaf(dy.at(q, o), x.at(at, c + r), s);
+                            }
+                            v.v[r] = s;
+                        }
+                v.store(to_w + (int64_t)o * a.width + c, in);
+            }
+    }
+    if (c0 == 0 && to_b) {
+        // the threads of a word's columns, in their order
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sums[tid][j] = bias[j];
+        __syncthreads();
+        if (tid < BO && o0 + tid < a.out) {
+            float s = 0.0f;
+            for (int k = tid / 8; k < 256; k += WQ) s += sums[k][tid % 8];
+            to_b[o0 + tid] = s;
+        }
+    }
+}
+
+template <class T>
+Status weight_grad_t(Context &cx, Args a, const RowsOf<T> &dy, const RowsOf<T> &x) {
+    constexpr int BC = 128, BO = 128;
+    a.tiles_c = (a.width + BC - 1) / BC;
+    a.tiles = a.tiles_c * ((a.out + BO - 1) / BO);
+    const int64_t want = std::max<int64_t>(1, 512 / a.tiles - a.n_experts);
+    a.rows = std::max<int64_t>(512, ((a.n + want - 1) / want + 63) / 64 * 64);
+    const int64_t pieces = a.n / a.rows + a.n_experts;
+    const int64_t matrix = (int64_t)a.out * a.width;
+    a.part_slots = a.n > a.rows ? 2 * (a.n / a.rows) : 0;
+    void *ws = nullptr;
+    MPNN_TRY(cx.rows_scratch(sizeof(float) * (size_t)(a.part_slots * slot_size(matrix + a.out)), &ws));
+    a.part = static_cast<float *>(ws);
+    k_expert_weight_grad<T, 2, 2, 2, 2><<<grid_xcd(pieces * a.tiles, 1), 256, 0, cx.stream>>>(a, dy, x);
+    MPNN_HIP(hipGetLastError());
+    return a.part_slots ? join_pieces(cx, a.n_experts, a.n, a.rows, a.part_slots, matrix, a.out, a.offsets, a.part, a.dweight, a.dbias) : Status::ok();
+}
+
+}  // namespace
+
+Status expert_weight_grad(Context &cx, int dtype, int64_t n, int width, int n_out, int n_experts, const int32_t *offsets, const void *dy,
+                          int64_t ld_dy, const void *x, int64_t ldx, const int32_t *source, int64_t n_x, float *dweight, float *dbias) {
+    const Args a{n, 0, n_out, width, n_experts, 0, 0, offsets, source, source ? n_x : n, source ? (int)(n / n_x) : 1, 0, nullptr, dweight, dbias};
+    if (dtype == MPNN_BF16) return weight_grad_t<bf16>(cx, a, {(const bf16 *)dy, ld_dy}, {(const bf16 *)x, ldx});
+    return weight_grad_t<float>(cx, a, {(const float *)dy, ld_dy}, {(const float *)x, ldx});
+}
+
+}  // namespace mpnn

@@ -265,6 +265,10 @@ Status unpermute_rows(Context &cx, const float *sorted, int width, int stride, d
 // ---- routing.hip ----
 Status route_plan(Context &cx, int64_t n, int k, int n_experts, const int32_t *expert, int32_t *offsets, int32_t *source,
                   int32_t *position);
+// the same in scratch that the caller has taken, of so many bytes; position may be null
+size_t route_plan_scratch(int64_t pairs, int n_experts);
+Status route_plan_at(Context &cx, int64_t pairs, int n_experts, const int32_t *expert, int32_t *offsets, int32_t *source,
+                     int32_t *position, void *ws);
 Status route_scatter(Context &cx, int dtype, int64_t n, int k, int width, const void *x, int64_t ldx, const int32_t *position,
                      const int32_t *used, void *sorted);
 Status route_combine(Context &cx, int dtype, int64_t n, int k, int width, const void *sorted, const int32_t *position,
@@ -287,6 +291,25 @@ Status checkpoint_silu_backward(Context &cx, int dtype, int64_t n, int width, co
 // ---- weight_grad.hip ----
 Status weight_grad(Context &cx, int dtype, int64_t n, int out, int width, int n_experts, const int32_t *offsets, const void *dy,
                    int64_t ld, const int8_t *codes, const uint8_t *scales, float *dweight, float *dbias);
+// ---- expert.hip; source null: x has the n sorted rows, else n_x rows ----
+Status expert_product(Context &cx, int dtype, int64_t n, int width, int n_out, int n_experts, const int32_t *offsets, const void *x,
+                      int64_t ldx, const int32_t *source, int64_t n_x, const void *weight, const float *bias, int act, void *y);
+Status expert_input_grad(Context &cx, int dtype, int64_t n, int width, int n_out, int n_experts, const int32_t *offsets, const void *dy,
+                         int64_t ld, const void *weight, void *dx);
+Status micro_product(Context &cx, int x_dtype, int y_dtype, int64_t n, int width, int n_out, int n_experts, const int32_t *offsets,
+                     const void *x, int64_t ldx, const uint8_t *x_scales, const int32_t *source, int64_t n_x, const uint8_t *codes,
+                     const uint8_t *scales, const float *bias, int act, void *y);
+// ---- expert_grad.hip ----
+Status expert_weight_grad(Context &cx, int dtype, int64_t n, int width, int n_out, int n_experts, const int32_t *offsets, const void *dy,
+                          int64_t ld_dy, const void *x, int64_t ldx, const int32_t *source, int64_t n_x, float *dweight, float *dbias);
+// ---- micro.hip ----
+Status micro_save(Context &cx, int dtype, int64_t n, int width, const void *x, int64_t ld, uint8_t *codes, uint8_t *scales);
+Status micro_load(Context &cx, int dtype, int64_t n, int width, const uint8_t *codes, const uint8_t *scales, void *out);
+// ---- embed.hip ----
+Status embed(Context &cx, int dtype, int64_t n, int width, int entries, const int32_t *index, const void *table, float scale, void *out);
+Status embed_plan(Context &cx, int64_t n, int entries, const int32_t *index, int32_t *offsets, int32_t *source);
+Status embed_backward(Context &cx, int dtype, int64_t n, int width, int entries, const void *dout, int64_t ld, const int32_t *offsets,
+                      const int32_t *source, float scale, float *dtable);
 
 }  // namespace mpnn
 

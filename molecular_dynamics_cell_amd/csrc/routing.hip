@@ -189,7 +189,7 @@ __global__ __launch_bounds__(kPlanThreads) void k_route_place(const int32_t *__r
         if (bin[j] >= 0) {
             const int q = h[wave][bin[j]] + __popcll(same & ((1ull << lane) - 1));
             source[q] = (int32_t)p;
-            position[p] = q;
+            if (position) position[p] = q;
             // the highest lane of the bin moves its start past this iteration's pairs
             if ((same >> lane) == 1) h[wave][bin[j]] = q + 1;
         }
@@ -331,16 +331,18 @@ __global__ __launch_bounds__(256) void k_route_combine_back(int64_t n, int64_t p
 
 }  // namespace
 
+template <int ITEMS> static int64_t plan_blocks(int64_t pairs) {
+    constexpr int kChunk = kPlanThreads * ITEMS;
+    return std::max<int64_t>(1, (pairs + kChunk - 1) / kChunk);
+}
+
 template <int ITEMS>
 static Status plan(Context &cx, int64_t pairs, int n_experts, const int32_t *expert, int32_t *offsets, int32_t *source,
-                   int32_t *position) {
-    constexpr int kChunk = kPlanThreads * ITEMS;
-    const int64_t blocks = std::max<int64_t>(1, (pairs + kChunk - 1) / kChunk);
+                   int32_t *position, void *ws) {
+    const int64_t blocks = plan_blocks<ITEMS>(pairs);
     const int bins = n_experts + 1;
     int32_t *counts = nullptr, *total = nullptr;
     if (blocks > 1) {
-        void *ws = nullptr;
-        MPNN_TRY(cx.rows_scratch(sizeof(int32_t) * (size_t)bins * (size_t)(blocks + 1), &ws));
         counts = static_cast<int32_t *>(ws);
         k_route_count<ITEMS><<<(unsigned)blocks, kPlanThreads, 0, cx.stream>>>(expert, pairs, n_experts, counts);
         MPNN_HIP(hipGetLastError());
@@ -358,11 +360,24 @@ static Status plan(Context &cx, int64_t pairs, int n_experts, const int32_t *exp
 
 // 1,024 pairs a block, so that the pairs of some 100,000 atoms already fill the GPU's CUs; 4,096 where there are enough
 // of them, for fewer counts.
+static bool many_pairs(int64_t pairs) { return pairs > (1 << 20); }
+
+size_t route_plan_scratch(int64_t pairs, int n_experts) {
+    const int64_t blocks = many_pairs(pairs) ? plan_blocks<16>(pairs) : plan_blocks<4>(pairs);
+    return blocks > 1 ? sizeof(int32_t) * (size_t)(n_experts + 1) * (size_t)(blocks + 1) : 0;
+}
+
+Status route_plan_at(Context &cx, int64_t pairs, int n_experts, const int32_t *expert, int32_t *offsets, int32_t *source,
+                     int32_t *position, void *ws) {
+    return many_pairs(pairs) ? plan<16>(cx, pairs, n_experts, expert, offsets, source, position, ws)
+                             : plan<4>(cx, pairs, n_experts, expert, offsets, source, position, ws);
+}
+
 Status route_plan(Context &cx, int64_t n, int k, int n_experts, const int32_t *expert, int32_t *offsets, int32_t *source,
                   int32_t *position) {
-    const int64_t pairs = n * k;
-    return pairs > (1 << 20) ? plan<16>(cx, pairs, n_experts, expert, offsets, source, position)
-                             : plan<4>(cx, pairs, n_experts, expert, offsets, source, position);
+    void *ws = nullptr;
+    MPNN_TRY(cx.rows_scratch(route_plan_scratch(n * k, n_experts), &ws));
+    return route_plan_at(cx, n * k, n_experts, expert, offsets, source, position, ws);
 }
 
 // Slots that a kernel takes together, as a constant.

@@ -1,0 +1,251 @@
+// Tiles of matrix products on the bf16 matrix cores (expert.hip, expert_grad.hip): words of eight values are loaded to
+// registers, turned into matrix-core operands and held in LDS.
+//
+// Operands.  A bf16 value is one as it stands, and so is a 4-bit value times its power-of-two step.  An fp32 value is cut
+// into three bf16 terms by rounding, each to nearest: the second is at most 2^-9 of the value, the third 2^-18, and the three add
+// up to it exactly.  Of the nine products of two such values the six largest are taken; what is left out is below
+// 2 * 2^-9 * 2^-18 = 2^-26 of the product, less than fp32's own rounding of it.  A value of 0x1.ffp127 and more rounds to an
+// infinity, whose other terms are not numbers: kernels keep the largest magnitude they have met and compute the results
+// that are not numbers again, one by one, where it is that large.
+//
+// Layouts in LDS (a word is 16 bytes: eight bf16 values).  For rows along the reduced axis [row][word], for a reduced
+// axis across the rows [step along it][word of eight columns], which the transposing reads turn.  Words are permuted inside
+// a row by exclusive-or, so that neither the stores nor the reads of a wave meet in a bank.
+#pragma once
+
+#include <type_traits>
+
+#include "impl.h"
+#include "rows.h"
+
+namespace mpnn {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef float floatx2 __attribute__((ext_vector_type(2)));
+typedef float floatx16 __attribute__((ext_vector_type(16)));
+typedef short shortx4 __attribute__((ext_vector_type(4)));
+
+struct Micro {};                             // values in 4 bits: 16 bytes of codes and a scale byte for 32 columns
+constexpr int kMicroGroup = 32;
+
+constexpr float kHuge = 0x1.ffp127f;         // rounds to an infinity in bf16
+
+template <class T> constexpr int kTerms = std::is_same<T, float>::value ? 3 : 1;
+
+__device__ __forceinline__ float micro_step(uint32_t byte) { return __uint_as_float(byte == 255 ? 0x7fc00000u : byte << 23); }
+
+// Eight neighbouring values of a row as they are loaded.
+template <class T> struct Word;
+template <> struct Word<float> {
+    float v[8];
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+    }
+    __device__ __forceinline__ void load(const float *p) { __builtin_memcpy(v, p, 32); }
+    __device__ __forceinline__ void load(const float *p, int in) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = j < in ? p[j] : 0.0f;
+    }
+    __device__ __forceinline__ float at(int j) const { return v[j]; }
+    __device__ __forceinline__ void terms(uint4 (&w)[3], float &largest) const {
+        float a[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            a[j] = v[j];
+            largest = fmaxf(largest, fabsf(a[j]));
+        }
+#pragma unroll
+        for (int t = 0; t < 3; ++t) {
+            uint32_t h[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                h[j] = __builtin_bit_cast(uint32_t, __builtin_convertvector(floatx2{a[2 * j], a[2 * j + 1]}, bf16x2));
+                if (t < 2) {
+                    a[2 * j] -= __uint_as_float(h[j] << 16);
+                    a[2 * j + 1] -= __uint_as_float(h[j] & 0xffff0000u);
+                }
+            }
+            w[t] = make_uint4(h[0], h[1], h[2], h[3]);
+        }
+    }
+};
+template <> struct Word<bf16> {
+    uint32_t v[4];
+    __device__ __forceinline__ void clear() { v[0] = v[1] = v[2] = v[3] = 0; }
+    __device__ __forceinline__ void load(const bf16 *p) { __builtin_memcpy(v, p, 16); }
+    __device__ __forceinline__ void load(const bf16 *p, int in) {
+        const uint16_t *u = reinterpret_cast<const uint16_t *>(p);
+        uint16_t s[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s[j] = j < in ? u[j] : (uint16_t)0;
+        __builtin_memcpy(v, s, 16);
+    }
+    __device__ __forceinline__ float at(int j) const { return __uint_as_float(j & 1 ? v[j >> 1] & 0xffff0000u : v[j >> 1] << 16); }
+    __device__ __forceinline__ void terms(uint4 (&w)[1], float &) const { w[0] = make_uint4(v[0], v[1], v[2], v[3]); }
+};
+template <> struct Word<Micro> {
+    uint32_t v;         // eight codes, the first in the low bits
+    uint8_t scale;
+    __device__ __forceinline__ void clear() {
+        v = 0;
+        scale = 127;
+    }
+    __device__ __forceinline__ void terms(uint4 (&w)[1], float &) const {
+        const float s = micro_step(scale);
+        const auto two = [&](auto k) { return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(v, s, k())); };
+        w[0] = make_uint4(two(std::integral_constant<int, 0>{}), two(std::integral_constant<int, 1>{}),
+                          two(std::integral_constant<int, 2>{}), two(std::integral_constant<int, 3>{}));
+    }
+};
+
+// Rows of values, `ld` apart; of 4-bit codes, `groups` groups a row.
+template <class T> struct RowsOf {
+    const T *p;
+    int64_t ld;
+    struct Row {
+        const T *p;
+    };
+    __device__ __forceinline__ Row row(int64_t i) const { return {p + i * ld}; }
+    // the word at column c of a row that has `width` of them (zeros past the end)
+    __device__ __forceinline__ static void load(Word<T> &w, const Row &r, int c, int width) {
+        const int in = width - c;
+        if (in >= 8) w.load(r.p + c);
+        else w.load(r.p + c, in);
+    }
+    __device__ __forceinline__ float at(int64_t i, int c) const { return to_f32(p[i * ld + c]); }
+};
+template <> struct RowsOf<Micro> {
+    const uint8_t *codes, *scales;
+    int64_t groups;
+    struct Row {
+        const uint8_t *codes, *scales;
+    };
+    __device__ __forceinline__ Row row(int64_t i) const { return {codes + i * groups * (kMicroGroup / 2), scales + i * groups}; }
+    __device__ __forceinline__ static void load(Word<Micro> &w, const Row &r, int c, int width) {
+        if (c >= width) return w.clear();
+        __builtin_memcpy(&w.v, r.codes + c / 2, 4);
+        w.scale = r.scales[c / kMicroGroup];
+    }
+    __device__ __forceinline__ float at(int64_t i, int c) const {
+        const Row r = row(i);
+        const uint32_t code = r.codes[c / 2] >> 4 * (c & 1) & 15, m = code & 7;
+        const float v = m < 2 ? 0.5f * m : __uint_as_float(((m >> 1) + 126) << 23 | (m & 1) << 22);
+        return (code & 8 ? -v : v) * micro_step(r.scales[c / kMicroGroup]);
+    }
+};
+
+// A tile in LDS of `ROWS` rows with WORDS words of the reduced axis each (4 or 8).
+template <int TERMS, int ROWS, int WORDS> struct Along {
+    static constexpr int kWords = TERMS * ROWS * WORDS;
+    // a row's words are permuted by the bits of the row that its 16 neighbours in a read do not share a bank by
+    __device__ __forceinline__ static int slot(int row, int word) {
+        return row * WORDS + (WORDS == 8 ? word ^ (row >> 1 & 7) : word ^ (row >> 2 & 3));
+    }
+    __device__ __forceinline__ static void store(uint4 *lds, int row, int word, const uint4 (&w)[TERMS]) {
+#pragma unroll
+        for (int t = 0; t < TERMS; ++t) lds[t * ROWS * WORDS + slot(row, word)] = w[t];
+    }
+    // the operand of 32 rows from `first` at step s (16 values of the reduced axis)
+    __device__ __forceinline__ static bf16x8 read(const uint4 *lds, int t, int first, int s, int lane) {
+        return __builtin_bit_cast(bf16x8, lds[t * ROWS * WORDS + slot(first + (lane & 31), 2 * s + (lane >> 5))]);
+    }
+};
+
+// The same with the reduced axis across the rows: 8 WORDS of its steps, COLUMNS columns each.
+template <int TERMS, int COLUMNS, int WORDS> struct Across {
+    static constexpr int kWords = TERMS * COLUMNS * WORDS;
+    static constexpr int kWide = COLUMNS / 8;      // words of a step
+    // pairs of words (32 bytes, what the lanes of a transposing read take together) are permuted by the step
+    __device__ __forceinline__ static int slot(int step, int word) { return step * kWide + (word ^ (step & (kWide / 2 - 1) & 7) * 2); }
+    __device__ __forceinline__ static void store(uint4 *lds, int step, int word, const uint4 (&w)[TERMS]) {
+#pragma unroll
+        for (int t = 0; t < TERMS; ++t) lds[t * COLUMNS * WORDS + slot(step, word)] = w[t];
+    }
+    // Lane i of 16 names four columns of step i / 4 and gets column i of four steps.
+    __device__ __forceinline__ static bf16x8 read(const uint4 *lds, int t, int first, int s, int lane) {
+        const int i = lane & 15, step = 16 * s + 8 * (lane >> 5) + i / 4, word = (first + (lane & 16)) / 8 + (i >> 1 & 1);
+        typedef __attribute__((address_space(3))) shortx4 *Ptr;
+        const auto four = [&](int k) {
+            const char *p = reinterpret_cast<const char *>(lds + t * COLUMNS * WORDS + slot(k, word)) + (i & 1) * 8;
+            return __builtin_amdgcn_ds_read_tr16_b64_v4i16((Ptr)(p));
+        };
+        const shortx4 a = four(step), b = four(step + 4);
+        return __builtin_bit_cast(bf16x8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+    }
+};
+
+// acc[i][j] += P_i^T Q_j over the WORDS / 2 steps of a stage, P columns of the result and Q its rows: smallest terms first.
+template <class P, class Q, int TP, int TQ, int MT, int NT, int WORDS>
+__device__ __forceinline__ void multiply(const uint4 *p, const uint4 *q, int pfirst, int qfirst, int lane, floatx16 (&acc)[MT][NT]) {
+#pragma unroll
+    for (int s = 0; s < WORDS / 2; ++s) {
+        bf16x8 a[TP][MT], b[TQ][NT];
+#pragma unroll
+        for (int t = 0; t < TP; ++t)
+#pragma unroll
+            for (int i = 0; i < MT; ++i) a[t][i] = P::read(p, t, pfirst + 32 * i, s, lane);
+#pragma unroll
+        for (int t = 0; t < TQ; ++t)
+#pragma unroll
+            for (int j = 0; j < NT; ++j) b[t][j] = Q::read(q, t, qfirst + 32 * j, s, lane);
+#pragma unroll
+        for (int sum = 2; sum >= 0; --sum)
+#pragma unroll
+            for (int u = 0; u < TP; ++u) {
+                const int v = sum - u;
+                if (v < 0 || v >= TQ) continue;
+#pragma unroll
+                for (int i = 0; i < MT; ++i)
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[u][i], b[v][j], acc[i][j], 0, 0, 0);
+            }
+    }
+}
+
+// Row tiles of the experts' segments, and of the rows that no expert has (before the first segment and after the last;
+// expert < 0), which get zeros.
+struct Tile {
+    int expert;
+    int64_t from, to;       // its rows; from >= to: past the last tile
+};
+__device__ __forceinline__ int64_t clamped(int32_t v, int64_t low, int64_t n) { return min(max((int64_t)v, low), n); }
+__device__ __forceinline__ Tile find_tile(const int32_t *offsets, int n_experts, int64_t n, int rows, int64_t number) {
+    const int lane = threadIdx.x & 63;
+    int64_t before = 0;
+    for (int base = 0; base < n_experts + 2; base += 64) {
+        const int e = base + lane;
+        int64_t from = 0, to = 0;
+        if (e < n_experts) {
+            from = clamped(offsets[e], 0, n);
+            to = clamped(offsets[e + 1], from, n);
+        } else if (e == n_experts) {
+            from = clamped(offsets[n_experts], 0, n);
+            to = n;
+        } else if (e == n_experts + 1) {
+            to = clamped(offsets[0], 0, n);
+        }
+        const int c = (int)((to - from + rows - 1) / rows);
+        int s = c;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int a = __shfl_up(s, d);
+            if (lane >= d) s += a;
+        }
+        const uint64_t hit = __ballot(number < before + s);
+        if (hit) {
+            const int l = __builtin_amdgcn_readfirstlane(__ffsll((unsigned long long)hit) - 1);
+            const auto of = [&](int v) { return __builtin_amdgcn_readlane(v, l); };
+            const int64_t first = (int64_t)of((int)from) + (number - (before + of(s) - of(c))) * rows;     // n is below 2^31
+            const int64_t last = of((int)to);
+            return Tile{base + l < n_experts ? base + l : -1, first, min(last, first + rows)};
+        }
+        before += __builtin_amdgcn_readlane(s, 63);
+    }
+    return Tile{-1, 0, 0};
+}
+// At most so many row tiles: one short one for each expert that has rows, and for the two outer segments.
+inline int64_t row_tiles(int64_t n, int n_experts, int rows) { return n / rows + std::min<int64_t>(n, n_experts) + 2; }
+
+}  // namespace mpnn

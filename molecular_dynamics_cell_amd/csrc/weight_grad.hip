@@ -22,6 +22,7 @@
 #include <type_traits>
 
 #include "impl.h"
+#include "pieces.h"
 #include "rows.h"
 
 namespace mpnn {
@@ -33,71 +34,6 @@ typedef float floatx16 __attribute__((ext_vector_type(16)));
 
 constexpr int kBK = 64;          // rows per stage: 8 chunks of 8, one matrix-core operand word each
 constexpr int kChunks = kBK / 8;
-
-// Pieces of each expert: at least one (an expert without rows writes its zeros).
-__device__ __forceinline__ int pieces_of(const int32_t *offsets, int e, int64_t n, int64_t rows, int64_t &from, int64_t &to) {
-    from = min(max((int64_t)offsets[e], (int64_t)0), n);
-    to = min(max((int64_t)offsets[e + 1], from), n);
-    return (int)max((int64_t)1, (to - from + rows - 1) / rows);
-}
-
-struct Piece {
-    int expert, piece, pieces;   // piece of its expert's pieces; expert < 0: past the last
-    int slot;                    // partial sums of the expert's first piece (pieces > 1)
-};
-
-// Floats of a piece's partial sums, dW then db, in whole 16 bytes.
-__host__ __device__ __forceinline__ int64_t slot_size(int64_t values) { return (values + 3) / 4 * 4; }
-
-// The piece with the given number, by one wave: a prefix sum over the experts, 64 at a time.  want_expert >= 0 looks
-// that expert up instead.
-__device__ __forceinline__ Piece find_piece(const int32_t *offsets, int n_experts, int64_t n, int64_t rows, int number, int want_expert) {
-    const int lane = threadIdx.x & 63;
-    int before = 0, slots = 0;
-    for (int base = 0; base < n_experts; base += 64) {
-        const int e = base + lane;
-        int64_t from, to;
-        const int c = e < n_experts ? pieces_of(offsets, e, n, rows, from, to) : 0;
-        const int m = c > 1 ? c : 0;
-        int s = c, t = m;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const int a = __shfl_up(s, d), b = __shfl_up(t, d);
-            if (lane >= d) {
-                s += a;
-                t += b;
-            }
-        }
-        const uint64_t hit = __ballot(want_expert >= 0 ? e == want_expert : e < n_experts && number < before + s);
-        if (hit) {
-            // the same in all lanes, and known to be: what follows from it is computed once a wave
-            const int l = __builtin_amdgcn_readfirstlane(__ffsll((unsigned long long)hit) - 1);
-            const auto of = [&](int v) { return __builtin_amdgcn_readlane(v, l); };
-            const int pc = of(c);
-            return Piece{base + l, number - (before + of(s) - pc), pc, slots + of(t) - of(m)};
-        }
-        before += __builtin_amdgcn_readlane(s, 63);
-        slots += __builtin_amdgcn_readlane(t, 63);
-    }
-    return Piece{-1, 0, 0, 0};
-}
-
-// With an expert a piece (and at most 64 experts, one a lane): the expert whose tiles are the number-th to start.  The
-// longest experts start first, `row` of them on all CUs, and the next ones in turn from the shortest and the longest, so that
-// a CU that holds two blocks holds a long and a short one (16,384 rows 1024 -> 1024 x 8, shares from 4 to 20 %: bf16 85 -> 79 us,
-// fp32 163 -> 156 us).
-__device__ __forceinline__ int expert_in_turn(const int32_t *offsets, int n_experts, int64_t n, int row, int number) {
-    const int lane = threadIdx.x & 63, e = min(lane, n_experts - 1);
-    const int from = (int)min(max((int64_t)offsets[e], (int64_t)0), n), to = (int)min(max((int64_t)offsets[e + 1], (int64_t)from), n);
-    const int length = to - from;
-    int rank = 0;
-    for (int f = 0; f < n_experts; ++f) {
-        const int other = __builtin_amdgcn_readlane(length, f);
-        rank += other > length || (other == length && f < lane);
-    }
-    const int in = number % row, want = (number / row & 1) && number - in + row <= n_experts ? number - in + row - 1 - in : number;
-    return __ffsll((unsigned long long)__ballot(lane < n_experts && rank == want)) - 1;
-}
 
 __device__ __forceinline__ uint32_t low_halves(uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x05040100u); }
 __device__ __forceinline__ uint32_t high_halves(uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x07060302u); }
@@ -495,12 +431,7 @@ Status launch(Context &cx, int64_t n, int out, int width, int n_experts, const i
     kernel<<<grid_xcd(pieces * tiles, 1), 256, 0, cx.stream>>>(out, width, (width + 31) / 32, n_experts, n, rows, tiles_n, tiles, offsets,
                                                                dy, ld, codes, scales, slots, part, dweight, dbias);
     MPNN_HIP(hipGetLastError());
-    if (slots) {
-        k_weight_grad_sum<<<dim3(grid_for(slot_size(matrix + out) / 4, 64), n_experts), 256, 0, cx.stream>>>(n_experts, n, rows, slots, matrix, out, offsets,
-                                                                                             part, dweight, dbias);
-        MPNN_HIP(hipGetLastError());
-    }
-    return Status::ok();
+    return slots ? join_pieces(cx, n_experts, n, rows, slots, matrix, out, offsets, part, dweight, dbias) : Status::ok();
 }
 
 template <class T>
@@ -520,6 +451,14 @@ Status weight_grad_t(Context &cx, int64_t n, int out, int width, int n_experts, 
 }
 
 }  // namespace
+
+Status join_pieces(Context &cx, int n_experts, int64_t n, int64_t rows, int64_t slots, int64_t matrix, int out, const int32_t *offsets,
+                   const float *part, float *dweight, float *dbias) {
+    k_weight_grad_sum<<<dim3(grid_for(slot_size(matrix + out) / 4, 64), n_experts), 256, 0, cx.stream>>>(n_experts, n, rows, slots, matrix,
+                                                                                                         out, offsets, part, dweight, dbias);
+    MPNN_HIP(hipGetLastError());
+    return Status::ok();
+}
 
 Status weight_grad(Context &cx, int dtype, int64_t n, int out, int width, int n_experts, const int32_t *offsets, const void *dy,
                    int64_t ld, const int8_t *codes, const uint8_t *scales, float *dweight, float *dbias) {

@@ -20,6 +20,7 @@ import torch
 GROUP = 32      # columns that share one scale of a checkpoint
 _DTYPE = {torch.float32: 0, torch.bfloat16: 1}
 _KIND = {"rms": 0, "layer": 1}
+_ACT = {"none": 0, "silu": 1}
 _CALLS = {}     # the library's functions by name, once they have been used
 
 # the handle of torch's current stream on a device (a stream object for each call costs 2 us)
@@ -37,6 +38,14 @@ class Checkpoint(NamedTuple):
     """Rows held in 8 bits: codes int8 [n, width], scales uint8 [n, ceil(width / 32)]."""
     codes: torch.Tensor
     scales: torch.Tensor
+
+
+class Micro(NamedTuple):
+    """Rows in microscaled 4-bit floating point: codes uint8 [n, 16 ceil(width / 32)], scales uint8
+    [n, ceil(width / 32)], and the rows' width."""
+    codes: torch.Tensor
+    scales: torch.Tensor
+    width: int
 
 
 def _ptr(t):
@@ -298,3 +307,176 @@ class RowOperators:
         self._call("mpnn_checkpoint_weight_grad", (dy, codes, scales, offsets, dweight, dbias), _DTYPE[dy.dtype], n, n_out,
                    width, experts, _ptr(offsets), _ptr(dy), ld, _ptr(codes), _ptr(scales), _ptr(dweight), _ptr(dbias))
         return dweight, dbias
+
+    # ---- products by expert ----
+    def _offsets(self, offsets):
+        if offsets.dim() != 1 or offsets.shape[0] < 2:
+            raise ValueError(f"offsets: expected [n_experts + 1], got {tuple(offsets.shape)}")
+        return self._dense("offsets", offsets, offsets.shape, torch.int32)
+
+    def _sorted(self, n_x, source):
+        """(rows after sorting, source) for rows [n_x] and the plan's source [n_x k], or None."""
+        if source is None:
+            return n_x, None
+        if source.dim() != 1 or (n_x == 0 and source.shape[0]) or (n_x and (source.shape[0] % n_x or not source.shape[0])):
+            raise ValueError(f"source: expected [n k] for {n_x} rows, got {tuple(source.shape)}")
+        return source.shape[0], self._dense("source", source, source.shape, torch.int32)
+
+    def _weight(self, weight, like, experts, n_out=None, width=None):
+        shape = weight.shape
+        if len(shape) != 3 or shape[0] != experts or (n_out is not None and shape[1] != n_out) or \
+                (width is not None and shape[2] != width):
+            raise ValueError(f"weight: expected [{experts}, {'n_out' if n_out is None else n_out}, {'width' if width is None else width}], "
+                             f"got {tuple(shape)}")
+        return self._dense("weight", weight, shape, like.dtype)
+
+    @staticmethod
+    def _act(act):
+        if act not in _ACT:
+            raise ValueError(f"act: expected 'none' or 'silu', got {act!r}")
+        return _ACT[act]
+
+    def expert_product(self, x: torch.Tensor, weight: torch.Tensor, offsets: torch.Tensor, bias: torch.Tensor = None, *,
+                       act="none", source: torch.Tensor = None):
+        """act(x W_e^T + b_e) for the rows offsets[e] .. offsets[e + 1] - 1 of expert e, weight [E, n_out, width] of x's
+        type, bias float32 [E, n_out]: [n, n_out], zeros in rows of no expert.  With the plan's source x is taken as
+        it was before it was sorted ([n / k, width])."""
+        x, ld = self._rows("x", x)
+        n_x, width = x.shape
+        n, source = self._sorted(n_x, source)
+        offsets = self._offsets(offsets)
+        experts = offsets.shape[0] - 1
+        weight = self._weight(weight, x, experts, None, width)
+        n_out = weight.shape[1]
+        bias = None if bias is None else self._dense("bias", bias, (experts, n_out), torch.float32)
+        y = self._new(x, n, n_out)
+        self._call("mpnn_expert_product", (x, weight, offsets, bias, source, y), _DTYPE[x.dtype], n, width, n_out, experts,
+                   _ptr(offsets), _ptr(x), ld, _ptr(source), n_x, _ptr(weight), _ptr(bias), self._act(act), _ptr(y))
+        return y
+
+    def expert_product_backward(self, dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, offsets: torch.Tensor, *,
+                                source: torch.Tensor = None):
+        """Gradient of expert_product without an activation: (dx [n, width] of the sorted rows, dweight [E, n_out, width],
+        dbias [E, n_out], float32).  x None: no dweight and dbias; weight None: no dx.  With source x is taken as it was
+        before it was sorted; route_combine brings dx back to it."""
+        dy, ld = self._rows("dy", dy)
+        n, n_out = dy.shape
+        offsets = self._offsets(offsets)
+        experts = offsets.shape[0] - 1
+        if x is None and weight is None:
+            raise ValueError("x and weight are both None")
+        width = None if x is None else x.shape[1] if x.dim() == 2 else -1
+        dx = dweight = dbias = None
+        if x is not None:
+            x, ldx = self._rows("x", x, None, width, dy.dtype)
+            rows, source = self._sorted(x.shape[0], source)
+            if rows != n:
+                raise ValueError(f"dy: expected {rows} rows, got {n}")
+        if weight is not None:
+            weight = self._weight(weight, dy, experts, n_out, width)
+            width = weight.shape[2]
+            dx = self._new(dy, n, width)
+            self._call("mpnn_expert_input_grad", (dy, weight, offsets, dx), _DTYPE[dy.dtype], n, width, n_out, experts,
+                       _ptr(offsets), _ptr(dy), ld, _ptr(weight), _ptr(dx))
+        if x is not None:
+            dweight = self._new(dy, experts, n_out, width, dtype=torch.float32)
+            dbias = self._new(dy, experts, n_out, dtype=torch.float32)
+            self._call("mpnn_expert_weight_grad", (dy, x, offsets, source, dweight, dbias), _DTYPE[dy.dtype], n, width, n_out,
+                       experts, _ptr(offsets), _ptr(dy), ld, _ptr(x), ldx, _ptr(source), x.shape[0], _ptr(dweight), _ptr(dbias))
+        return dx, dweight, dbias
+
+    # ---- rows in 4 bits ----
+    def _micro(self, name, held):
+        codes, scales, width = held
+        groups = -(-int(width) // GROUP)
+        if codes.dim() != 2:
+            raise ValueError(f"{name}: expected codes [n, {16 * groups}], got {tuple(codes.shape)}")
+        n = codes.shape[0]
+        return (self._dense(name, codes, (n, 16 * groups), torch.uint8), self._dense(name, scales, (n, groups), torch.uint8),
+                int(width))
+
+    def micro_save(self, x: torch.Tensor) -> Micro:
+        """x [n, width] in 4 bits, one power-of-two step per 32 columns of a row."""
+        x, ld = self._rows("x", x)
+        n, width = x.shape
+        groups = -(-width // GROUP)
+        held = Micro(self._new(x, n, 16 * groups, dtype=torch.uint8), self._new(x, n, groups, dtype=torch.uint8), width)
+        self._call("mpnn_micro_save", (x, held.codes, held.scales), _DTYPE[x.dtype], n, width, _ptr(x), ld, _ptr(held.codes),
+                   _ptr(held.scales))
+        return held
+
+    def micro_load(self, held, dtype=torch.float32) -> torch.Tensor:
+        """The values that 4-bit rows hold (exact in either type)."""
+        if dtype not in _DTYPE:
+            raise ValueError(f"dtype: expected float32 or bfloat16, got {dtype}")
+        codes, scales, width = self._micro("held", held)
+        out = self._new(codes, codes.shape[0], width, dtype=dtype)
+        self._call("mpnn_micro_load", (codes, scales, out), _DTYPE[dtype], codes.shape[0], width, _ptr(codes), _ptr(scales),
+                   _ptr(out))
+        return out
+
+    def micro_product(self, x, held, offsets: torch.Tensor, bias: torch.Tensor = None, *, act="none",
+                      source: torch.Tensor = None, dtype=None):
+        """expert_product with weights held in 4 bits (micro_save of the weights as [E n_out, width]); x: rows, or rows
+        held in 4 bits themselves.  The result has `dtype`, or x's type (bfloat16 for held rows)."""
+        codes, scales, width = self._micro("held", held)
+        offsets = self._offsets(offsets)
+        experts = offsets.shape[0] - 1
+        if codes.shape[0] % experts:
+            raise ValueError(f"held: {codes.shape[0]} rows are not {experts} experts' alike")
+        n_out = codes.shape[0] // experts
+        if isinstance(x, torch.Tensor):
+            x, ld = self._rows("x", x, None, width)
+            kind, x_scales, like = _DTYPE[x.dtype], None, x.dtype
+        else:
+            x, x_scales, wide = self._micro("x", x)
+            if wide != width:
+                raise ValueError(f"x: expected rows of {width} columns, got {wide}")
+            kind, ld, like = 2, width, torch.bfloat16
+        dtype = like if dtype is None else dtype
+        if dtype not in _DTYPE:
+            raise ValueError(f"dtype: expected float32 or bfloat16, got {dtype}")
+        n, source = self._sorted(x.shape[0], source)
+        bias = None if bias is None else self._dense("bias", bias, (experts, n_out), torch.float32)
+        y = self._new(x, n, n_out, dtype=dtype)
+        self._call("mpnn_micro_product", (x, x_scales, codes, scales, offsets, bias, source, y), kind, _DTYPE[dtype], n, width,
+                   n_out, experts, _ptr(offsets), _ptr(x), ld, _ptr(x_scales), _ptr(source), x.shape[0], _ptr(codes),
+                   _ptr(scales), _ptr(bias), self._act(act), _ptr(y))
+        return y
+
+    # ---- embedding rows ----
+    def embed(self, index: torch.Tensor, table: torch.Tensor, scale: float = 1.0):
+        """scale * table[index] for index int32 [n] (rows of zeros where it names no entry): [n, width]."""
+        if index.dim() != 1:
+            raise ValueError(f"index: expected [n], got {tuple(index.shape)}")
+        if table.dim() != 2 or table.dtype not in _DTYPE:
+            raise ValueError(f"table: expected [entries, width] of float32 or bfloat16, got {tuple(table.shape)} of {table.dtype}")
+        index = self._dense("index", index, index.shape, torch.int32)
+        table = self._dense("table", table, table.shape, table.dtype)
+        n, (entries, width) = index.shape[0], table.shape
+        out = self._new(table, n, width)
+        self._call("mpnn_embed", (index, table, out), _DTYPE[table.dtype], n, width, entries, _ptr(index), _ptr(table),
+                   float(scale), _ptr(out))
+        return out
+
+    def embed_plan(self, index: torch.Tensor, n_entries: int):
+        """Stable order of the rows by index int32 [n] (rows of no entry last): offsets [n_entries + 1], source [n], int32."""
+        if index.dim() != 1:
+            raise ValueError(f"index: expected [n], got {tuple(index.shape)}")
+        index = self._dense("index", index, index.shape, torch.int32)
+        offsets, source = self._new(index, max(int(n_entries), 0) + 1), self._new(index, index.shape[0])
+        self._call("mpnn_embed_plan", (index, offsets, source), index.shape[0], int(n_entries), _ptr(index), _ptr(offsets),
+                   _ptr(source))
+        return offsets, source
+
+    def embed_backward(self, dout: torch.Tensor, offsets: torch.Tensor, source: torch.Tensor, scale: float = 1.0):
+        """Gradient of embed towards the table, by embed_plan's order: float32 [n_entries, width]."""
+        dout, ld = self._rows("dout", dout)
+        n, width = dout.shape
+        offsets = self._offsets(offsets)
+        source = self._dense("source", source, (n,), torch.int32)
+        entries = offsets.shape[0] - 1
+        dtable = self._new(dout, entries, width, dtype=torch.float32)
+        self._call("mpnn_embed_backward", (dout, offsets, source, dtable), _DTYPE[dout.dtype], n, width, entries, _ptr(dout), ld,
+                   _ptr(offsets), _ptr(source), float(scale), _ptr(dtable))
+        return dtable

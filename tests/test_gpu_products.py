@@ -1,0 +1,658 @@
+"""Products by expert and their gradients, rows and weights in 4 bits, and embedding rows, against plain 64-bit
+implementations, on the GPU.
+
+Bounds.  U = 2^-24.  A matrix instruction adds 16 products four at a time to an fp32 sum, each addition off by at most 2 U of
+the sum of the magnitudes `size` (if it cuts instead of rounding): K / 2 U size for sums of K products of bf16 values, which are
+exact.  fp32 values are cut into three terms each and take six instructions a step (3 K U size), what is left out is below
+U / 4 of each product; with operands of one and three terms three instructions (3 K / 2).  Eight U size are added for the short
+sums' other roundings.  The activation z / (1 + exp(-z)) has a slope of at most 1.1 and three operations of a few U of its
+value; below z = -87 exp overflows and the value is less than 1e-35."""
+import numpy as np
+import pytest
+import torch
+
+from molecular_dynamics_cell_amd import binding
+from molecular_dynamics_cell_amd import inputs as I
+from tests import products_util as P
+from tests import rows_util as R
+from tests.rows_util import U, check, f64
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda:0"
+TYPES = [torch.float32, torch.bfloat16]
+
+
+@pytest.fixture(scope="module")
+def m():
+    ctx = binding.MPNN(I.make_params(1), DEV)
+    yield ctx
+    torch.cuda.synchronize()
+    ctx.close()
+
+
+@pytest.fixture(autouse=True)
+def say_name(request):
+    print(f"[products] {request.node.name}", flush=True)
+    yield
+    torch.cuda.synchronize()
+
+
+def rng(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def normal(g, *shape, dtype=torch.float32, size=1.0):
+    return (torch.randn(*shape, generator=g) * size).to(dtype).to(DEV)
+
+
+def rows(g, n, width, dtype=torch.float32):
+    """Rows of unlike sizes."""
+    return (torch.randn(n, width, generator=g) * torch.exp(torch.randn(n, 1, generator=g))).to(dtype).to(DEV)
+
+
+def ends(counts, first=0):
+    return torch.tensor([first] + list(first + np.cumsum(counts)), dtype=torch.int32, device=DEV)
+
+
+def bound(K, size, *types):
+    terms = [3 if t == torch.float32 else 1 for t in types]
+    return (terms[0] * terms[1] / (3 if terms == [3, 3] else 2) + 0.5) * K * U * size + 8 * U * size
+
+
+def act_bound(b, y, act):
+    return b if act == "none" else 1.1 * b + 8 * U * y.abs() + 1e-35
+
+
+# n, width, n_out, counts, first place of the first expert
+SHAPES = [(0, 8, 8, [0, 0], 0), (1, 1, 1, [1], 0), (1, 4096, 130, [0, 1, 0], 0), (3, 7, 5, [1, 0, 2], 0), (5, 30, 33, [2, 0, 2], 1), (8, 2048, 64, [1] * 8, 0),
+          (17, 8, 16, [16, 1], 0), (64, 64, 64, [64], 0), (108, 64, 128, [50, 0, 58], 0), (300, 33, 65, [290], 3), (400, 312, 128, [1, 0, 130, 200], 40),
+          (777, 127, 17, [100, 0, 0, 600], 0), (640, 96, 256, [640], 0), (260, 520, 260, [3] * 70, 0), (1025, 64, 1, [1025], 0), (1500, 3, 1000, [700, 700], 100),
+          (2000, 136, 392, [0, 1990, 5], 2), (1300, 256, 512, [640, 1, 659], 0), (600, 1, 40, [600], 0), (3000, 40, 8, [40] * 75, 0)]
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("act,with_bias", [("none", False), ("silu", True)])
+@pytest.mark.parametrize("n,width,out,counts,first", SHAPES)
+def test_product(m, n, width, out, counts, first, act, with_bias, dtype):
+    g = rng(n + width + out)
+    x, w = rows(g, n, width, dtype), normal(g, len(counts), out, width, dtype=dtype, size=width ** -0.5)
+    offsets, bias = ends(counts, first), normal(g, len(counts), out) if with_bias else None
+    outside = torch.ones(n, dtype=torch.bool)
+    outside[first:first + sum(counts)] = False
+    x[outside.to(DEV)] = float("nan")                    # rows of no expert reach nothing
+    y = m.expert_product(x, w, offsets, bias, act=act)
+    want, size = P.product(torch.nan_to_num(x), w, offsets, bias, act, n)
+    assert y.dtype == dtype
+    check("y", y, want, act_bound(bound(width, size, dtype, dtype), want, act), dtype)
+    assert int(y[outside.to(DEV)].float().count_nonzero()) == 0
+    assert torch.equal(m.expert_product(x, w, offsets, bias, act=act), y)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("n,width,out,counts,first", SHAPES)
+def test_product_backward(m, n, width, out, counts, first, dtype):
+    g = rng(n + 3 * width + out)
+    x, w = rows(g, n, width, dtype), normal(g, len(counts), out, width, dtype=dtype, size=width ** -0.5)
+    dy, offsets = rows(g, n, out, dtype), ends(counts, first)
+    outside = torch.ones(n, dtype=torch.bool)
+    outside[first:first + sum(counts)] = False
+    x[outside.to(DEV)], dy[outside.to(DEV)] = float("inf"), float("nan")
+    dx, dw, db = m.expert_product_backward(dy, x, w, offsets)
+    dy0, x0 = dy.clone(), x.clone()
+    dy0[outside.to(DEV)], x0[outside.to(DEV)] = 0, 0
+    want, size = P.input_grad(dy0, w, offsets)
+    assert dx.dtype == dtype and dw.dtype == db.dtype == torch.float32
+    check("dx", dx, want, bound(out, size, dtype, dtype), dtype)
+    assert int(dx[outside.to(DEV)].float().count_nonzero()) == 0
+    dw64, dws, db64, dbs, count = P.weight_grad(dy0, x0, offsets)
+    for e, c in enumerate(count):
+        check("dweight", dw[e], dw64[e], bound(c, dws[e], dtype, dtype))
+        check("dbias", db[e], db64[e], (c + 2) * U * dbs[e])
+    only, none, nothing = m.expert_product_backward(dy, None, w, offsets)
+    assert none is None and nothing is None and torch.equal(only, dx)
+    none, dw2, db2 = m.expert_product_backward(dy, x, None, offsets)
+    assert none is None and torch.equal(dw2, dw) and torch.equal(db2, db)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("n,out,width,counts", [(40000, 64, 108, [30000, 10000]), (20000, 130, 40, [19000, 1, 0, 999]), (9000, 1, 1000, [9000]),
+                                                (12000, 1000, 3, [6000, 6000]), (30000, 260, 24, [300] * 100)])
+def test_weight_gradient_of_many_rows(m, n, out, width, counts, dtype):
+    g = rng(n + out)
+    dy, x, offsets = rows(g, n, out, dtype), rows(g, n, width, dtype), ends(counts)
+    _, dw, db = m.expert_product_backward(dy, x, None, offsets)
+    dw64, dws, db64, dbs, count = P.weight_grad(dy, x, offsets)
+    for e, c in enumerate(count):
+        check("dweight", dw[e], dw64[e], bound(c, dws[e], dtype, dtype))
+        check("dbias", db[e], db64[e], (c + 2) * U * dbs[e])
+    again = m.expert_product_backward(dy, x, None, offsets)
+    assert torch.equal(again[1], dw) and torch.equal(again[2], db)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("n,k,E,width,out", [(1, 8, 64, 512, 128), (1, 1, 1, 8, 8), (108, 2, 4, 64, 128), (257, 3, 5, 30, 17), (40, 64, 70, 33, 20), (700, 6, 9, 136, 72)])
+def test_rows_taken_by_source(m, n, k, E, width, out, dtype):
+    """The plan's source in place of sorted rows: the same bits; and the whole way there and back with its gradient."""
+    g = rng(n + k)
+    expert = torch.randint(-1, E, (n, k), generator=g, dtype=torch.int32).to(DEV)
+    x, w, weight = rows(g, n, width, dtype), normal(g, E, out, width, dtype=dtype), normal(g, n, k)
+    offsets, source, position = m.route_plan(expert, E)
+    y = m.expert_product(x, w, offsets, source=source)
+    sorted_x = m.route_scatter(x, position, offsets)
+    assert torch.equal(y, m.expert_product(sorted_x, w, offsets))
+    want, size = P.product(x, w, offsets, None, "none", n * k, source)
+    check("y", y, want, bound(width, size, dtype, dtype), dtype)
+    dy, _ = m.route_combine_backward(rows(g, n, out, dtype), None, position, offsets, weight)
+    got = m.expert_product_backward(dy, x, w, offsets, source=source)
+    for a, b in zip(got, m.expert_product_backward(dy, sorted_x, w, offsets)):
+        assert torch.equal(a, b)
+    # <dy, product(x + t v, w + t u)> has the gradients' slope
+    v, u = torch.randn(n, width, generator=g, dtype=torch.float64), torch.randn(E, out, width, generator=g, dtype=torch.float64)
+    dy64 = f64(dy)
+    slope = float((dy64 * (P.product(v, w, offsets, None, "none", n * k, source)[0] + P.product(x, u, offsets, None, "none", n * k, source)[0])).sum())
+    dx = torch.zeros(n, width, dtype=torch.float64).index_add_(0, source.cpu().long() // k, f64(got[0]))
+    mine = float((dx * v).sum() + (f64(got[1]) * u).sum())
+    size = float((dy64.abs() * (P.product(v.abs(), w.abs(), offsets, None, "none", n * k, source)[0]
+                                + P.product(x.abs(), u.abs(), offsets, None, "none", n * k, source)[0])).sum())
+    assert abs(mine - slope) <= (2.0 ** -8 if dtype == torch.bfloat16 else 4 * (width + n * k) * U) * size + 1e-12
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("width,pad,shift", [(64, 64, 0), (108, 20, 4), (64, 1, 1), (312, 9, 3), (33, 7, 2), (256, 256, 0), (192, 8, 8)])
+def test_strided_rows(m, width, pad, shift, dtype):
+    """Column blocks of a wider tensor, aligned or not, give the dense rows' results bit for bit."""
+    g = rng(width)
+    n, E = 300, 3
+
+    def pair(width):
+        wide = normal(g, n, width + pad + shift, dtype=dtype)
+        part = wide[:, shift:shift + width]
+        return part, part.contiguous()
+
+    (x, xd), (dy, dyd) = pair(width), pair(40)
+    w, offsets = normal(g, E, 40, width, dtype=dtype), ends([100, 0, 180])
+    assert torch.equal(m.expert_product(x, w, offsets), m.expert_product(xd, w, offsets))
+    for a, b in zip(m.expert_product_backward(dy, x, w, offsets), m.expert_product_backward(dyd, xd, w, offsets)):
+        assert torch.equal(a, b)
+    held = m.micro_save(x)
+    for a, b in zip(held[:2], m.micro_save(xd)[:2]):
+        assert torch.equal(a, b)
+    wh = m.micro_save(w.reshape(-1, width))
+    assert torch.equal(m.micro_product(x, wh, offsets), m.micro_product(xd, wh, offsets))
+    index = torch.randint(-1, 20, (n,), generator=g, dtype=torch.int32).to(DEV)
+    order = m.embed_plan(index, 20)
+    assert torch.equal(m.embed_backward(x, *order), m.embed_backward(xd, *order))
+    # tensors that start off a 16-byte boundary
+    flat = torch.cat([torch.zeros(1, dtype=dtype, device=DEV), w.reshape(-1)])[1:].reshape(w.shape)
+    assert flat.data_ptr() % 16 and torch.equal(m.expert_product(x, flat, offsets), m.expert_product(xd, w, offsets))
+    assert torch.equal(m.expert_product_backward(dy, None, flat, offsets)[0], m.expert_product_backward(dyd, None, w, offsets)[0])
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("n", [5, 40, 300])
+def test_values_that_are_not_finite(m, n, dtype):
+    """They go where the formula has them, infinities with their signs; neighbours keep their values."""
+    g = rng(11 + n)
+    width, out = 70, 40
+    x, w, dy = rows(g, n, width, dtype), normal(g, 2, out, width, dtype=dtype), rows(g, n, out, dtype)
+    offsets = ends([n - 4, 2], 1)
+    clean, cleanw, cleandy = x.clone(), w.clone(), dy.clone()
+    x[2, 5], x[1, 69] = float("inf"), float("nan")
+    w[0, 3, 7], w[1, 39, 0] = float("-inf"), float("nan")
+    if dtype == torch.float32:
+        x[3, 9], w[0, 3, 9] = 3.395e38, 0.5              # rounds to an infinity in bf16
+    dy[1, 4] = float("-inf")
+
+    def alike(got, want):
+        got = f64(got)
+        assert torch.equal(got.isnan(), want.isnan()) and torch.equal(got.isinf(), want.isinf())
+        assert torch.equal(got[got.isinf()] > 0, want[want.isinf()] > 0)
+
+    def by_the_formula(a, b):
+        """a [n, K] times b [K, o], with the sums' terms as they are: 0 times an infinity is not a number"""
+        s = (a.double().unsqueeze(2) * b.double().unsqueeze(0)).sum(1)
+        return torch.where(s.abs() > torch.finfo(dtype).max, torch.sign(s) * float("inf"), s)
+
+    y = m.expert_product(x, w, offsets)
+    want = torch.zeros(n, out, dtype=torch.float64)
+    for e, r in P.segments(offsets, n):
+        want[r] = by_the_formula(f64(x)[r], f64(w)[e].T)
+    alike(y, want)
+    usual, size = P.product(clean, cleanw, offsets, None, "none", n)
+    fine = want.isfinite() & (torch.arange(n) != 3).unsqueeze(1) & (torch.arange(out) != 3)
+    assert ((f64(y) - usual).abs() <= bound(width, size, dtype, dtype) + 2.0 ** -8 * usual.abs())[fine].all()
+    if dtype == torch.float32:
+        assert abs(float(y[3, 3]) - 3.395e38 * 0.5) < 1e33 or n < 8 or not torch.isfinite(y[3, 3])
+    dx, dw, db = m.expert_product_backward(dy, x, w, offsets)
+    want = torch.zeros(n, width, dtype=torch.float64)
+    for e, r in P.segments(offsets, n):
+        want[r] = by_the_formula(f64(dy)[r], f64(w)[e])
+        alike(dw[e], by_the_formula(f64(dy)[r].T, f64(x)[r]) if dtype == torch.float32 else f64(dw[e]))
+    alike(dx, want)
+    assert torch.isinf(db[0, 4]) and int(db.isinf().sum()) == 1
+
+
+def test_offsets_of_something_else(m):
+    """Offsets outside the rows or not ascending, a source of another plan: nothing outside the rows is read or written."""
+    g = rng(5)
+    n, width, out = 200, 48, 24
+    wide = torch.full((3 * n, width), float("nan"), device=DEV)
+    x = wide[n:2 * n]
+    x.copy_(normal(g, n, width))
+    w = normal(g, 2, out, width)
+    L = binding.lib()
+    for offsets in ([-50, 100, 500], [0, 1 << 30, -(1 << 30)], [150, 20, 180], [300, 400, 500], [0, -5, 2000000000]):
+        o = torch.tensor(offsets, dtype=torch.int32, device=DEV)
+        y = torch.full((3 * n, out), 7.0, device=DEV)
+        assert L.mpnn_expert_product(m.h, 0, n, width, out, 2, o.data_ptr(), x.data_ptr(), width, None, 0, w.data_ptr(), None, 0,
+                                     y[n:].data_ptr()) == 0
+        dw = torch.full((4, out, width), 7.0, device=DEV)
+        dy = torch.ones(n, out, device=DEV)
+        assert L.mpnn_expert_weight_grad(m.h, 0, n, width, out, 2, o.data_ptr(), dy.data_ptr(), out, x.data_ptr(), width, None, 0,
+                                         dw[1:].data_ptr(), None) == 0
+        torch.cuda.synchronize()
+        assert (y[:n] == 7).all() and (y[2 * n:] == 7).all() and (dw[0] == 7).all() and (dw[3] == 7).all()
+    source = torch.tensor([-1, 5, 2000000000, -2147483648] * 50, dtype=torch.int32, device=DEV)
+    o = ends([120, 80])
+    few = x[:50].contiguous()
+    y = m.expert_product(few, w, o, source=source)
+    kept = (source.cpu().long().clamp(min=0) // 4).clamp(max=49)
+    assert torch.equal(y, m.expert_product(few[kept.to(DEV)], w, o))
+    got = m.expert_product_backward(y, few, None, o, source=source)[1]
+    assert torch.equal(got, m.expert_product_backward(y, few[kept.to(DEV)], None, o)[1])
+    index_offsets = torch.tensor([-3, 10, 70, 900], dtype=torch.int32, device=DEV)
+    dt = m.embed_backward(x, index_offsets, source)
+    at = source.cpu().long()
+    at = torch.where((at < 0) | (at >= n), n - 1, at)
+    want = torch.stack([f64(x)[at[a:b]].sum(0) for a, b in ((0, 10), (10, 70), (70, 200))])
+    size = torch.stack([f64(x)[at[a:b]].abs().sum(0) for a, b in ((0, 10), (10, 70), (70, 200))])
+    check("dtable", dt, want, 200 * U * size)
+
+
+# ---------------------------------------------------------------------------------------------------------------
+# rows in 4 bits
+# ---------------------------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("n,width", [(0, 40), (1, 1), (1, 4096), (3, 31), (5, 32), (7, 33), (108, 64), (65, 108), (33, 312), (17, 127), (9, 1000), (2000, 40), (300, 8200)])
+def test_micro_rows(m, n, width, dtype):
+    g = rng(n + width)
+    x = rows(g, n, width, dtype)
+    if n > 2:
+        x[1], x[2] = 0, -0.0
+        x[0, ::2] *= 2.0 ** -70
+    held = m.micro_save(x)
+    codes, scales = P.micro_save(x)
+    assert held.width == width and torch.equal(held.scales.cpu(), scales)
+    back = P.micro_load(codes, scales, width)
+    assert torch.equal(P.micro_load(held.codes, held.scales, width), back)
+    pad = torch.stack((held.codes & 15, held.codes >> 4), -1).flatten(1)[:, width:]
+    assert int(pad.count_nonzero()) == 0
+    for t in TYPES:
+        assert torch.equal(f64(m.micro_load(held, t)), back)
+
+
+def test_micro_extremes(m):
+    """Ties, saturation, tiny and large values, groups that are not finite, every code."""
+    top = torch.finfo(torch.float32).max
+    x = torch.zeros(12, 40, device=DEV)
+    x[0, :10] = torch.tensor([4.0, 0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, -0.26, 7.0])
+    x[1, :4] = torch.tensor([7.99, 7.0, 6.5, -7.5])
+    x[2, :3] = torch.tensor([top, -top, top / 3])
+    x[3, :4] = torch.tensor([2.0 ** -126, 2.0 ** -149, -(2.0 ** -101), 2.0 ** -102])
+    x[4, :2] = torch.tensor([2.0 ** -98, 2.0 ** -101])
+    x[5, 3], x[6, 35], x[7, 39] = float("inf"), float("nan"), float("-inf")
+    x[8, :8] = torch.tensor([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0])
+    x[9, :8] = -x[8, :8] * 2.0 ** 100
+    x[10] = 2.0 ** -149
+    held = m.micro_save(x)
+    codes, scales = P.micro_save(x)
+    assert torch.equal(held.scales.cpu(), scales)
+    want = P.micro_load(codes, scales, 40)
+    for t in TYPES:
+        got = f64(m.micro_load(held, t))
+        assert torch.equal(got.isnan(), want.isnan()) and torch.equal(torch.nan_to_num(got), torch.nan_to_num(want))
+    every = torch.arange(256, dtype=torch.uint8, device=DEV).reshape(16, 16)
+    for byte in (27, 100, 127, 200, 252, 255):
+        scale = torch.full((16, 1), byte, dtype=torch.uint8, device=DEV)
+        for t in TYPES:
+            got, want = f64(m.micro_load((every, scale, 32), t)), P.micro_load(every, scale, 32)
+            assert torch.equal(got.isnan(), want.isnan()) and torch.equal(torch.nan_to_num(got), torch.nan_to_num(want))
+
+
+@pytest.mark.parametrize("kind", ["float32", "bfloat16", "micro"])
+@pytest.mark.parametrize("act,with_bias", [("none", False), ("silu", True)])
+@pytest.mark.parametrize("n,width,out,counts,first", SHAPES)
+def test_micro_product(m, n, width, out, counts, first, act, with_bias, kind):
+    g = rng(n + 5 * width + out)
+    dtype = torch.float32 if kind == "float32" else torch.bfloat16
+    x, offsets = rows(g, n, width, dtype), ends(counts, first)
+    held = m.micro_save(normal(g, len(counts) * out, width, size=width ** -0.5))
+    w = P.micro_load(held.codes, held.scales, width).reshape(len(counts), out, width)
+    bias = normal(g, len(counts), out) if with_bias else None
+    outside = torch.ones(n, dtype=torch.bool)
+    outside[first:first + sum(counts)] = False
+    x[outside.to(DEV)] = float("nan")
+    taken = m.micro_save(x) if kind == "micro" else x
+    x64 = torch.nan_to_num(P.micro_load(taken.codes, taken.scales, width) if kind == "micro" else f64(x))
+    want, size = P.product(x64, w, offsets, bias, act, n)
+    b = act_bound(bound(width, size, dtype, torch.bfloat16), want, act)
+    y = m.micro_product(taken, held, offsets, bias, act=act)
+    assert y.dtype == dtype
+    check("y", y, want, b, dtype)
+    assert int(y[outside.to(DEV)].float().count_nonzero()) == 0
+    other = torch.bfloat16 if dtype == torch.float32 else torch.float32
+    check("other type", m.micro_product(taken, held, offsets, bias, act=act, dtype=other), want, b, other)
+
+
+@pytest.mark.parametrize("kind", ["float32", "bfloat16", "micro"])
+@pytest.mark.parametrize("n,k,E", [(1, 8, 64), (90, 3, 7), (300, 4, 2)])
+def test_micro_product_by_source_and_not_finite(m, n, k, E, kind):
+    g = rng(n)
+    width, out = 100, 72
+    dtype = torch.float32 if kind == "float32" else torch.bfloat16
+    expert = torch.randint(-1, E, (n, k), generator=g, dtype=torch.int32).to(DEV)
+    offsets, source, position = m.route_plan(expert, E)
+    x = rows(g, n, width, dtype)
+    x[0, 50] = float("inf")
+    held = m.micro_save(normal(g, E * out, width))
+    taken = m.micro_save(x) if kind == "micro" else x
+    sorted_x = m.route_scatter(x, position, offsets)
+    y = m.micro_product(taken, held, offsets, source=source)
+    again = m.micro_product(m.micro_save(sorted_x) if kind == "micro" else sorted_x, held, offsets)
+    assert torch.equal(torch.nan_to_num(y, 7.0), torch.nan_to_num(again, 7.0))
+    w = P.micro_load(held.codes, held.scales, width).reshape(E, out, width)
+    x64 = P.micro_load(taken.codes, taken.scales, width) if kind == "micro" else f64(x)
+    whose = torch.full((n * k,), -1)
+    for e, r in P.segments(offsets, n * k):
+        whose[r] = e
+    of = source.cpu().long() // k
+    mine = (of == 0) & (whose >= 0)
+    for q in mine.nonzero().reshape(-1).tolist():
+        want = (x64[0] * w[whose[q]]).sum(1)
+        got = f64(y[q])
+        assert torch.equal(got.isnan(), want.isnan()) and torch.equal(got[got.isinf()], want[want.isinf()])
+    rest = (~mine).to(DEV)
+    assert torch.isfinite(y[rest]).all()
+
+
+def test_micro_weights_not_finite(m):
+    """A group of a weight that is not a number reaches its output column only."""
+    g = rng(8)
+    w = normal(g, 2 * 40, 70)
+    w[45, 33] = float("nan")
+    held, offsets = m.micro_save(w), ends([50, 70])
+    for x in (rows(g, 120, 70), rows(g, 120, 70, torch.bfloat16), m.micro_save(rows(g, 120, 70))):
+        bad = m.micro_product(x, held, offsets).isnan().cpu()
+        assert bad[50:, 5].all() and int(bad.sum()) == 70
+
+
+# ---------------------------------------------------------------------------------------------------------------
+# embedding rows
+# ---------------------------------------------------------------------------------------------------------------
+def indexes(g, n, entries, how):
+    if how == "even":
+        i = torch.randint(0, entries, (n,), generator=g)
+    elif how == "rare":
+        i = (torch.exp(torch.rand(n, generator=g) * np.log(entries + 1)) - 1).long().clamp(0, entries - 1)
+    elif how == "one":
+        i = torch.full((n,), entries - 1)
+    else:
+        i = torch.full((n,), -1)
+    i = i.to(torch.int32)
+    if how in ("even", "rare"):
+        i[torch.rand(n, generator=g) < 0.05] = -1
+        i[torch.rand(n, generator=g) < 0.02] = entries
+    return i.to(DEV)
+
+
+EMBEDS = [(0, 8, 3, "even"), (1, 1, 1, "one"), (1, 4096, 1000, "even"), (5, 30, 7, "even"), (108, 64, 3, "even"), (300, 33, 5000, "rare"), (65, 8, 4, "none"),
+          (1000, 312, 2, "rare"), (4097, 127, 1025, "rare"), (5000, 16, 1024, "even"), (3000, 100, 1, "one"), (70000, 8, 5, "rare"), (20000, 136, 40000, "rare"),
+          (129, 2100, 3, "even"), (40000, 3, 1 << 20, "even"), (66000, 40, 300, "one"), (64, 1030, 200, "even")]
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("n,width,entries,how", EMBEDS)
+def test_embed(m, n, width, entries, how, dtype):
+    g = rng(n + width)
+    index = indexes(g, n, entries, how)
+    table = normal(g, min(entries, 4000), width, dtype=dtype) if entries * width > 1 << 24 else normal(g, entries, width, dtype=dtype)
+    scale = float(np.sqrt(width))
+    out = m.embed(index, table, scale)
+    want = P.embed(index, table, float(np.float32(scale)))
+    assert out.dtype == dtype
+    check("out", out, want, 0.0, dtype)
+    offsets, source = m.embed_plan(index, entries)
+    for a, b in zip((offsets, source), P.embed_plan(index, entries)):
+        assert a.dtype == torch.int32 and torch.equal(a.cpu().long(), b)
+    dout = rows(g, n, width, dtype)
+    dout[((index < 0) | (index >= entries))] = float("nan")        # rows of no entry reach nothing
+    got = m.embed_backward(dout, offsets, source, scale)
+    want, size, count = P.embed_grad(index, torch.nan_to_num(dout), entries, float(np.float32(scale)))
+    check("dtable", got, want, (count.unsqueeze(1) + 2) * U * size)
+    assert torch.equal(m.embed_backward(dout, offsets, source, scale), got)
+    assert torch.equal(m.embed_backward(dout, offsets, source), m.embed_backward(dout, offsets, source, 1.0))
+
+
+def test_embed_rows_not_finite(m):
+    g = rng(3)
+    index = indexes(g, 500, 9, "even")
+    table = normal(g, 9, 20)
+    table[4, 3], table[5, 19] = float("inf"), float("nan")
+    out = m.embed(index, table, -2.0).cpu()
+    assert (out[index.cpu() == 4][:, 3] == float("-inf")).all() and out[index.cpu() == 5][:, 19].isnan().all()
+    assert int((~out.isfinite()).sum()) == int(((index == 4) | (index == 5)).sum())
+    dout = normal(g, 500, 20)
+    which = int((index == 7).nonzero()[0])
+    dout[which, 2] = float("-inf")
+    dt = m.embed_backward(dout, *m.embed_plan(index, 9)).cpu()
+    assert dt[7, 2] == float("-inf") and int((~dt.isfinite()).sum()) == 1
+
+
+# ---------------------------------------------------------------------------------------------------------------
+# together, streams, graphs, long arrays, refusals
+# ---------------------------------------------------------------------------------------------------------------
+def layer(m, t):
+    """A readout's step with the operators together: embedded species, routed rows through two products of the experts and
+    back, the gradients of all of it, and the answer with weights held in 4 bits."""
+    offsets, source, position = m.route_plan(t["expert"], len(t["w1"]))
+    h = t["x"] + m.embed(t["index"], t["table"], 2.0)
+    z = m.expert_product(h, t["w1"], offsets, t["b1"], source=source)
+    y, zh, yh = m.checkpoint_silu(z, save_output=True)
+    o = m.expert_product(y, t["w2"], offsets, t["b2"])
+    out = m.route_combine(o, position, offsets, t["gate"])
+    do, dgate = m.route_combine_backward(t["dout"], o, position, offsets, t["gate"])
+    dy, dw2, db2 = m.expert_product_backward(do, y, t["w2"], offsets)
+    dz = m.checkpoint_silu_backward(dy, zh)
+    dsorted, dw1, db1 = m.expert_product_backward(dz, h, t["w1"], offsets, source=source)
+    dh = m.route_combine(dsorted, position, offsets)
+    order = m.embed_plan(t["index"], len(t["table"]))
+    dtable = m.embed_backward(dh, *order, 2.0)
+    held = [m.micro_save(w.reshape(-1, w.shape[2])) for w in (t["w1"], t["w2"])]
+    a = m.micro_product(h, held[0], offsets, t["b1"], act="silu", source=source)
+    b = m.micro_product(m.micro_save(a), held[1], offsets, t["b2"], dtype=t["x"].dtype)
+    return {"out": out, "dgate": dgate, "dw2": dw2, "db2": db2, "dw1": dw1, "db1": db1, "dh": dh, "dtable": dtable,
+            "answer": m.route_combine(b, position, offsets, t["gate"]), "source": source, "order": order[1]}
+
+
+def layer_inputs(seed, n, width, hidden, E, k, species, dtype=torch.float32):
+    g = rng(seed)
+    return {"x": normal(g, n, width, dtype=dtype), "index": torch.randint(-1, species, (n,), generator=g, dtype=torch.int32).to(DEV),
+            "table": normal(g, species, width, dtype=dtype), "w1": normal(g, E, hidden, width, dtype=dtype, size=width ** -0.5), "b1": normal(g, E, hidden),
+            "w2": normal(g, E, width, hidden, dtype=dtype, size=hidden ** -0.5), "b2": normal(g, E, width), "gate": normal(g, n, k),
+            "dout": normal(g, n, width, dtype=dtype), "expert": torch.randint(-1, E, (n, k), generator=g, dtype=torch.int32).to(DEV)}
+
+
+def test_together(m):
+    """Against torch's differentiation of the same layer in 64 bits, with silu's slope at the z that its checkpoint holds (a z
+    that fp32 sums move over the border of two codes is a step off there: a handful of the 108,000)."""
+    n, width, hidden, E, k = 500, 40, 72, 5, 3
+    t = layer_inputs(1, n, width, hidden, E, k, 6)
+    got = layer(m, t)
+    names = ["x", "table", "w1", "b1", "w2", "b2", "gate"]
+    leaf = {v: f64(t[v]).requires_grad_() for v in names}
+    index, expert = t["index"].cpu().long(), t["expert"].cpu().long()
+    h = leaf["x"] + torch.where((index >= 0).unsqueeze(1), 2.0 * leaf["table"][index.clamp(min=0)], 0.0)
+    out, held = torch.zeros(n, width, dtype=torch.float64), torch.zeros(n, width, dtype=torch.float64)
+    w1h, w2h = (P.micro_load(*P.micro_save(t[w].reshape(E * t[w].shape[1], -1)), t[w].shape[2]).reshape(t[w].shape) for w in ("w1", "w2"))
+    for s in range(k):
+        e = expert[:, s].clamp(min=0)
+        z = torch.einsum("nhw,nw->nh", leaf["w1"][e], h) + leaf["b1"][e]
+        z0 = z.detach()
+        y = R.silu(z0) + R.silu_slope(R.load(*R.save(z0.float()))) * (z - z0)
+        o = torch.einsum("nwh,nh->nw", leaf["w2"][e], y) + leaf["b2"][e]
+        there = (expert[:, s] >= 0).double().unsqueeze(1)
+        out = out + there * leaf["gate"][:, s:s + 1] * o
+        a = torch.einsum("nhw,nw->nh", w1h[e], h) + leaf["b1"][e]
+        a = P.micro_load(*P.micro_save((a * torch.sigmoid(a)).float()), hidden)
+        held = held + there * leaf["gate"][:, s:s + 1] * (torch.einsum("nwh,nh->nw", w2h[e], a) + leaf["b2"][e])
+    check("out", got["out"], out.detach(), 1e-4)
+    (out * f64(t["dout"])).sum().backward()
+    for name, mine in (("x", "dh"), ("table", "dtable"), ("w1", "dw1"), ("b1", "db1"), ("w2", "dw2"), ("b2", "db2"), ("gate", "dgate")):
+        want = leaf[name].grad
+        off = float((f64(got[mine]) - want).norm() / want.norm())
+        print(f"[products] {mine}: off by {off:.2e}", flush=True)
+        assert off <= (2.0 ** -8 if name in ("x", "table", "w1", "b1") else 1e-5), name
+    # a value near the border of two codes may fall on the other side: one step of a few of the 72 terms
+    held = held.detach()
+    off = float((f64(got["answer"]) - held).norm() / held.norm())
+    print(f"[products] answer: off by {off:.2e}", flush=True)
+    assert off <= 2.0 ** -8
+
+
+def test_other_stream(m):
+    """Tensors made on a side stream behind a long-running producer, used there right after."""
+    t = layer_inputs(2, 3000, 96, 128, 4, 2, 5)
+    want = layer(m, t)
+    side = torch.cuda.Stream()
+    for _ in range(3):
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            big = torch.randn(4096, 4096, device=DEV)
+            for _ in range(20):
+                big = big @ big * 1e-2
+            u = {k: v + 0 for k, v in t.items()}
+            got = layer(m, u)
+            del u
+            got = {k: v + 0 for k, v in got.items()}
+        side.synchronize()
+        for k in want:
+            assert torch.equal(got[k], want[k]), k
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_graph_replays(dtype):
+    """Captured once and replayed with new inputs, between eager calls of other sizes on the same context."""
+    m = binding.MPNN(I.make_params(1), DEV)
+    n, shape = 6000, (6000, 64, 96, 4, 2, 3000, dtype)
+    t = layer_inputs(3, *shape)
+    layer(m, t)
+    home, graph = m._stream, torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    try:
+        with torch.cuda.graph(graph):
+            m.set_stream(torch.cuda.current_stream())
+            kept = layer(m, t)
+    finally:
+        m.set_stream(home)
+    for seed in range(4):
+        for k, v in layer_inputs(10 + seed, *shape).items():
+            t[k].copy_(v)
+        layer(m, layer_inputs(20, 9000, 72, 40, 7, 1, 5000))          # larger scratch than the graph's
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        got = {k: v.clone() for k, v in kept.items()}
+        want = layer(m, t)
+        for k in want:
+            assert torch.equal(got[k], want[k]), k
+    torch.cuda.synchronize()
+    del graph
+    m.close()
+
+
+def test_long_arrays(m):
+    """More than 2^31 values and 2^32 bytes of rows, results and table: the last rows are right."""
+    n, width = 280011, 8192
+    x = torch.empty(n, width, dtype=torch.bfloat16, device=DEV)
+    x.copy_((torch.arange(n, device=DEV) % 251).unsqueeze(1) + (torch.arange(width, device=DEV) % 3).unsqueeze(0))
+    g = rng(1)
+    w, tail = normal(g, 2, 8, width, dtype=torch.bfloat16), x[-300:].contiguous()
+    offsets, some = ends([n - 100, 100]), ends([200, 100])
+    assert torch.equal(m.expert_product(x, w, offsets)[-300:], m.expert_product(tail, w, some))
+    source = torch.arange(n - 1, -1, -1, dtype=torch.int32, device=DEV)
+    assert torch.equal(m.expert_product(x, w, offsets, source=source)[:64], m.expert_product(tail[-64:].flip(0), w, ends([64, 0])))
+    held = m.micro_save(x)
+    for a, b in zip(held[:2], m.micro_save(tail)[:2]):
+        assert torch.equal(a[-300:], b)
+    wh = m.micro_save(w.reshape(16, width))
+    assert torch.equal(m.micro_product(held, wh, offsets)[-300:], m.micro_product(m.micro_save(tail), wh, some))
+    back = m.micro_load(held, torch.bfloat16)
+    assert torch.equal(back[-300:], m.micro_load(m.micro_save(tail), torch.bfloat16))
+    del back, held
+    narrow = normal(g, n, 8, dtype=torch.bfloat16)
+    wide = normal(g, 2, 8, width, dtype=torch.bfloat16)
+    dx = m.expert_product_backward(narrow, None, wide, offsets)[0]
+    assert torch.equal(dx[-300:], m.expert_product_backward(narrow[-300:], None, wide, some)[0])
+    del dx
+    only = ends([0, 64], n - 64)
+    dw = m.expert_product_backward(narrow, x, None, only)[1]
+    want = m.expert_product_backward(narrow[-64:].contiguous(), tail[-64:].contiguous(), None, ends([0, 64]))[1]
+    assert torch.equal(dw, want)
+    index = torch.full((n,), -1, dtype=torch.int32, device=DEV)
+    index[-100:] = 3
+    order = m.embed_plan(index, 5)
+    check("dtable", m.embed_backward(x, *order)[3], f64(tail[-100:]).sum(0), 102 * U * f64(tail[-100:]).sum(0))
+    entry = torch.arange(n, device=DEV, dtype=torch.int32)
+    got = m.embed(entry, x, 2.0)
+    assert torch.equal(got[-100:], x[-100:] * 2) and torch.equal(got[:100], x[:100] * 2)
+
+
+def refused(code, call, *args, **kw):
+    with pytest.raises(binding.MPNNError) as e:
+        call(*args, **kw)
+    assert e.value.code == code and str(e.value)
+
+
+def test_refusals(m):
+    x, w, seg = torch.zeros(4, 16, device=DEV), torch.zeros(2, 8, 16, device=DEV), ends([2, 2])
+    L, p, o = binding.lib(), x.data_ptr(), seg.data_ptr()
+    refused(-1, m.expert_product, torch.zeros(4, 0, device=DEV), torch.zeros(2, 8, 0, device=DEV), seg)
+    refused(-1, m.expert_product, x, torch.zeros(2, 0, 16, device=DEV), seg)
+    refused(-1, m.expert_product, torch.zeros(1, 65537, device=DEV), torch.zeros(1, 1, 65537, device=DEV), ends([1]))
+    refused(-1, m.expert_product, x, torch.zeros(1025, 1, 16, device=DEV), torch.zeros(1026, dtype=torch.int32, device=DEV))
+    refused(-1, m.expert_product, x, w, seg, source=torch.zeros(4 * 65, dtype=torch.int32, device=DEV))
+    refused(-1, m.embed, torch.zeros(3, dtype=torch.int32, device=DEV), x, float("nan"))
+    refused(-1, m.embed, torch.zeros(3, dtype=torch.int32, device=DEV), x, 1e39)
+    refused(-1, m.embed_plan, torch.zeros(3, dtype=torch.int32, device=DEV), 0)
+    refused(-1, m.embed_plan, torch.zeros(3, dtype=torch.int32, device=DEV), (1 << 20) + 1)
+    refused(-1, m.embed, torch.zeros(3, dtype=torch.int32, device=DEV), torch.zeros(0, 16, device=DEV))
+    with pytest.raises(ValueError):
+        m.expert_product(x, w.cpu(), seg)
+    with pytest.raises(ValueError):
+        m.micro_product(x, m.micro_save(w.reshape(16, 16)), seg.cpu())
+    assert L.mpnn_expert_product(m.h, 2, 4, 16, 8, 2, o, p, 16, None, 0, p, None, 0, p) == -1
+    assert L.mpnn_expert_product(m.h, 0, 4, 16, 8, 2, o, p, 15, None, 0, p, None, 0, p) == -1
+    assert L.mpnn_expert_product(m.h, 0, 4, 16, 8, 2, o, p, 16, None, 0, p, None, 2, p) == -1
+    assert L.mpnn_expert_product(m.h, 0, 4, 16, 8, 2, o, p, 16, o, 3, p, None, 0, p) == -1
+    assert L.mpnn_expert_product(m.h, 0, 4, 16, 8, 2, o, None, 16, None, 0, p, None, 0, p) == -1
+    assert b"null" in L.mpnn_last_error(m.h)
+    assert L.mpnn_expert_product(m.h, 0, 4, 16, 8, 2, None, p, 16, None, 0, p, None, 0, p) == -1
+    assert L.mpnn_expert_product(m.h, 0, 1 << 31, 16, 8, 2, o, p, 16, None, 0, p, None, 0, p) == -1
+    assert L.mpnn_expert_input_grad(m.h, 0, 4, 16, 8, 2, o, p, 7, p, p) == -1
+    assert L.mpnn_expert_weight_grad(m.h, 0, 4, 16, 8, 2, o, p, 8, p, 16, None, 0, None, None) == -1
+    assert L.mpnn_expert_weight_grad(m.h, 0, 4, 16, 8, 2, o, p, 8, p, 15, None, 0, p, None) == -1
+    assert L.mpnn_micro_save(m.h, 2, 4, 16, p, 16, p, p) == -1
+    assert L.mpnn_micro_product(m.h, 3, 0, 4, 16, 8, 2, o, p, 16, None, None, 0, p, p, None, 0, p) == -1
+    assert L.mpnn_micro_product(m.h, 2, 2, 4, 16, 8, 2, o, p, 16, p, None, 0, p, p, None, 0, p) == -1
+    assert L.mpnn_micro_product(m.h, 2, 0, 4, 16, 8, 2, o, p, 16, None, None, 0, p, p, None, 0, p) == -1
+    assert L.mpnn_embed_backward(m.h, 0, 4, 16, 3, p, 15, o, o, 1.0, p) == -1
+    assert L.mpnn_embed_backward(m.h, 0, 4, 16, 3, p, 16, o, None, 1.0, p) == -1
+    # the context is usable afterwards, empty calls too
+    none = torch.zeros(0, 16, device=DEV)
+    assert m.expert_product(none, w, ends([0, 0])).shape == (0, 8)
+    dx, dw, db = m.expert_product_backward(torch.zeros(0, 8, device=DEV), none, w, ends([0, 0]))
+    assert dx.shape == (0, 16) and (dw == 0).all() and (db == 0).all()
+    assert m.micro_product(m.micro_save(none), m.micro_save(w.reshape(16, 16)), ends([0, 0])).shape == (0, 8)
+    assert (m.embed_backward(none, *m.embed_plan(torch.zeros(0, dtype=torch.int32, device=DEV), 4)) == 0).all()
+    assert m.expert_product(x, w, seg).shape == (4, 8)
