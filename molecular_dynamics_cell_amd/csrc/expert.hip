@@ -26,13 +26,41 @@ struct Args {
     int y_bf16;
 };
 
-__device__ __forceinline__ float silu(float z) { return z / (1.0f + expf(-z)); }
+// z / (1 + exp(-z)) = z r for z >= 0, z a r below, a = exp(-|z|) <= 1, r = 1 / (1 + a): exp by the hardware's power of two with
+// the rounding of its argument put back, the reciprocal of 1 .. 2 with one Newton step.  Beyond |z| = 128 a is zero.
+__device__ __forceinline__ float silu(float z) {
+    constexpr float kLog2e = 1.44269504f, kRest = 1.92596299e-8f, kLn2 = 0.693147181f;      // log2 e in two parts
+    const float m = fminf(fabsf(z), 128.0f), t = -m * kLog2e, rest = fmaf(-m, kLog2e, -t) - m * kRest;
+    const float e = __builtin_amdgcn_exp2f(t), a = fmaf(e, rest * kLn2, e);
+    const float b = 1.0f + a, r0 = __builtin_amdgcn_rcpf(b), r = fmaf(r0, fmaf(-b, r0, 1.0f), r0);
+    return z >= 0.0f ? z * r : z * a * r;
+}
+
+// 16 bytes that are not read again soon.
+template <class T> __device__ __forceinline__ void store_past(T *p, const Chunk<T> &v) {
+    typedef uint32_t Words __attribute__((ext_vector_type(4), aligned(2)));
+    __builtin_nontemporal_store(__builtin_bit_cast(Words, v), reinterpret_cast<Words *>(p));
+}
 
 template <class T> __device__ __forceinline__ void store_four(T *p, const float (&v)[4], int in) {
     Chunk<T, 4> o;
 #pragma unroll
     for (int j = 0; j < 4; ++j) o.v[j] = from_f32<T>(v[j]);
     o.store(p, in);
+}
+
+// Bias, activation and the store of four neighbouring results (`in` of them are the row's) of row q; expert < 0: none.
+__device__ __forceinline__ void finish(const Args &a, int expert, int64_t q, int c, int in, float (&v)[4]) {
+    if (expert >= 0) {
+        if (a.bias)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) v[r] += r < in ? a.bias[(int64_t)expert * a.columns + c + r] : 0.0f;
+        if (a.act == MPNN_ACT_SILU)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) v[r] = silu(v[r]);
+    }
+    if (a.y_bf16) store_four(static_cast<bf16 *>(a.y) + q * a.columns + c, v, in);
+    else store_four(static_cast<float *>(a.y) + q * a.columns + c, v, in);
 }
 
 // Tiles of 32 MT WM columns by 32 NT WN rows.  ACROSS: the weights' rows are the reduced axis (dx).
@@ -128,39 +156,334 @@ __global__ __launch_bounds__(256, 2) void k_product(const Args a, const RowsOf<X
                 float v[4];
 #pragma unroll
                 for (int r = 0; r < 4; ++r) v[r] = acc[i][j][4 * g + r];
-                if (tile.expert >= 0) {
-                    if (huge)
-                        for (int r = 0; r < 4; ++r)
-                            if (v[r] != v[r] && r < in) {
-                                const int64_t w0 = (int64_t)tile.expert * (ACROSS ? a.reduced : a.columns), from = place(q);
-                                float s = 0.0f;
-                                for (int k = 0; k < a.reduced; ++k) s = fmaf(x.at(from, k), ACROSS ? w.at(w0 + k, c + r) : w.at(w0 + c + r, k), s);
-                                v[r] = s;
-                            }
-                    if (a.bias)
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) v[r] += r < in ? a.bias[(int64_t)tile.expert * a.columns + c + r] : 0.0f;
-                    if (a.act == MPNN_ACT_SILU)
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) v[r] = silu(v[r]);
-                }
-                if (a.y_bf16) store_four(static_cast<bf16 *>(a.y) + q * a.columns + c, v, in);
-                else store_four(static_cast<float *>(a.y) + q * a.columns + c, v, in);
+                if (huge && tile.expert >= 0)
+                    for (int r = 0; r < 4; ++r)
+                        if (v[r] != v[r] && r < in) {
+                            const int64_t w0 = (int64_t)tile.expert * (ACROSS ? a.reduced : a.columns), from = place(q);
+                            float s = 0.0f;
+                            for (int k = 0; k < a.reduced; ++k) s = fmaf(x.at(from, k), ACROSS ? w.at(w0 + k, c + r) : w.at(w0 + c + r, k), s);
+                            v[r] = s;
+                        }
+                finish(a, tile.expert, q, c, in, v);
             }
     }
 }
 
-template <class X, class W, bool ACROSS>
-Status product_t(Context &cx, Args a, const RowsOf<X> &x, const RowsOf<W> &w) {
-    constexpr int BC = 128, BR = 128;
-    a.tiles_c = (a.columns + BC - 1) / BC;
-    const int64_t blocks = row_tiles(a.n, a.n_experts, BR) * a.tiles_c;
-    return by_launches(blocks, kLaunchBlocks, [&](int64_t from, int64_t count) -> Status {
+// ---- wide tiles ----
+// The product of two 16-byte words that a lane of 32 rows has: 16 steps of bf16, or a group of 32 columns in 4 bits with its
+// scales (byte S of each lane's word of scales).
+typedef int intx8 __attribute__((ext_vector_type(8)));
+template <class T> struct WideOp;
+template <> struct WideOp<bf16> {
+    static constexpr int kPerWord = 8;
+    template <int S> __device__ __forceinline__ static floatx16 multiply(uint4 p, uint4 q, floatx16 c, uint32_t, uint32_t) {
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, p), __builtin_bit_cast(bf16x8, q), c, 0, 0, 0);
+    }
+    __device__ __forceinline__ static const char *bytes(const RowsOf<bf16>::Row &r) { return reinterpret_cast<const char *>(r.p); }
+};
+template <> struct WideOp<Micro> {
+    static constexpr int kPerWord = 32;
+    template <int S> __device__ __forceinline__ static floatx16 multiply(uint4 p, uint4 q, floatx16 c, uint32_t ps, uint32_t qs) {
+        const intx8 a = {(int)p.x, (int)p.y, (int)p.z, (int)p.w, 0, 0, 0, 0}, b = {(int)q.x, (int)q.y, (int)q.z, (int)q.w, 0, 0, 0, 0};
+        return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 4, 4, S, ps, S, qs);
+    }
+    __device__ __forceinline__ static const char *bytes(const RowsOf<Micro>::Row &r) { return reinterpret_cast<const char *>(r.codes); }
+};
+
+// 256 x 256 results at a time, eight waves of 128 columns x 64 rows.  Stages are 64 bytes of every row; they go to LDS without
+// passing through registers, two stages ahead.  A block stays for many tiles: the next one's first stages are on their way
+// while this one's results are stored.  (One block a CU: without that a tile of 2,048 columns takes 29 us of products and
+// 23 us to find its rows, wait for the first of them and store its results.)
+constexpr int kWide = 256, kWideWords = 4, kBuffers = 3, kWideThreads = 512, kCus = 256;
+constexpr int kSegments = 1024 + 2;                // experts and the rows of none
+using WideTile = Along<1, kWide, kWideWords>;
+
+template <class T>
+__global__ __launch_bounds__(kWideThreads, 2) void k_product_wide(const Args a, const RowsOf<T> x, const RowsOf<T> w) {
+    using Op = WideOp<T>;
+    constexpr bool MICRO = std::is_same<T, Micro>::value;
+    constexpr int STAGE = kWideWords * Op::kPerWord;                   // columns of a stage
+    constexpr int SIDE = WideTile::kWords, BOTH = 2 * SIDE;            // words of a stage: rows, then weights
+    constexpr int MT = 4, NT = 2, PITCH = 128 + 16;       // bytes of a line of results and of the way to the next
+    __shared__ uint4 lds[kBuffers * BOTH];
+    __shared__ uint32_t scales[MICRO ? kBuffers : 1][2][MICRO ? kWide : 1];
+    __shared__ uint4 results[kWideThreads / 64][32 * PITCH / 16];
+    __shared__ int first[kSegments + 1], start[kSegments];             // of each segment, its first tile and row
+    typedef const __attribute__((address_space(1))) void *Global;
+    typedef __attribute__((address_space(3))) void *Local;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wm = wave & 1, wn = wave >> 1;
+
+    const int segments = a.n_experts + 2;
+    if (wave == 0) {
+        int before = 0;
+        for (int base = 0; base < segments; base += 64) {
+            int64_t from, to;
+            segment_of(a.offsets, a.n_experts, a.n, base + lane, from, to);
+            const int c = (int)((to - from + kWide - 1) / kWide);
+            int s = c;
+#pragma unroll
+            for (int d = 1; d < 64; d <<= 1) {
+                const int t = __shfl_up(s, d);
+                if (lane >= d) s += t;
+            }
+            if (base + lane < segments) {
+                first[base + lane] = before + s - c;
+                start[base + lane] = (int)from;
+            }
+            before += __builtin_amdgcn_readlane(s, 63);
+        }
+        if (lane == 0) first[segments] = before;
+    }
+    __syncthreads();
+    const int64_t tiles = (int64_t)first[segments] * a.tiles_c;
+
+    const auto place = [&](int64_t q) -> int64_t {
+        if (!a.source) return q;
+        return min((int64_t)((uint32_t)max(a.source[q], 0) / (uint32_t)a.slots), a.n_x - 1);
+    };
+    const int words = (a.reduced + Op::kPerWord - 1) / Op::kPerWord;
+    const int full = MICRO ? words / kWideWords : a.reduced / STAGE, stages = (words + kWideWords - 1) / kWideWords;
+
+    // The tile that is being brought, multiplied and stored.
+    int expert = 0, c0 = 0;
+    int64_t from = 0, to = 0;
+    const char *px[2], *pw[2];
+    const uint8_t *ps_row = nullptr;
+    uint32_t next_scales = 0;
+    int at = 0;                                    // buffer of the tile's first stage
+    const auto w_row = [&](int r) { return w.row((int64_t)expert * a.columns + min(c0 + r, a.columns - 1)); };
+    const auto x_row = [&](int r) { return x.row(place(min(from + r, to - 1))); };
+    const auto buffer_of = [&](int s) { return s % kBuffers; };
+    // A wave brings 32 rows of each side, 16 at once; lane l the word that stands at place l of those rows in LDS.
+    const auto bring = [&](int buffer, int i) {
+        const int words_at = buffer * BOTH + (wave * 32 + i * 16) * kWideWords;
+        __builtin_amdgcn_global_load_lds((Global)px[i], (Local)&lds[words_at], 16, 0, 0);
+        __builtin_amdgcn_global_load_lds((Global)pw[i], (Local)&lds[words_at + SIDE], 16, 0, 0);
+        px[i] += 64;
+        pw[i] += 64;
+    };
+    // Scales: a thread brings the four of a stage of one row, by way of a register (rows of scales start on any byte).  Past
+    // a row's last group they are those of 1, since its codes are zeros there.
+    const auto fetch_scales = [&](int stage) {
+        stage = min(stage, stages - 1);
+        const int left = words - stage * kWideWords;
+        const uint8_t *p = ps_row + stage * kWideWords;
+        uint32_t v = 0;
+        if (left >= kWideWords) __builtin_memcpy(&v, p, 4);
+        else
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v |= (k < left ? (uint32_t)p[k] : 127u) << 8 * k;
+        next_scales = v;
+    };
+    const auto store_scales = [&](int buffer) { scales[buffer][threadIdx.x >> 8][threadIdx.x & 255] = next_scales; };
+    const auto begin = [&](int64_t number) {
+        const int t = (int)(number / a.tiles_c);
+        int low = 0, high = segments - 1;          // the last segment whose first tile is at most t
+        while (low < high) {
+            const int mid = (low + high + 1) / 2;
+            if (first[mid] <= t) low = mid;
+            else high = mid - 1;
+        }
+        expert = __builtin_amdgcn_readfirstlane(low < a.n_experts ? low : -1);
+        c0 = __builtin_amdgcn_readfirstlane((int)(number % a.tiles_c) * kWide);
+        from = __builtin_amdgcn_readfirstlane(start[low] + (t - first[low]) * kWide);
+        int64_t f, e;
+        segment_of(a.offsets, a.n_experts, a.n, low, f, e);
+        to = min((int64_t)__builtin_amdgcn_readfirstlane((int)e), from + kWide);
+        if (expert < 0) return;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int r = wave * 32 + i * 16 + lane / 4, word = (lane & 3) ^ (r >> 2 & 3);
+            px[i] = Op::bytes(x_row(r)) + word * 16;
+            pw[i] = Op::bytes(w_row(r)) + word * 16;
+        }
+        if constexpr (MICRO) {
+            ps_row = wave < 4 ? x_row(threadIdx.x).scales : w_row(threadIdx.x - 256).scales;
+            fetch_scales(0);
+            store_scales(at);
+            fetch_scales(1);
+        }
+        for (int s = 0; s < min(full, kBuffers - 1); ++s) {
+            bring(buffer_of(at + s), 0);
+            bring(buffer_of(at + s), 1);
+        }
+    };
+
+    // blocks of an XCD take neighbouring tiles
+    int64_t number = (int64_t)(blockIdx.x % kXcds) * (gridDim.x / kXcds) + blockIdx.x / kXcds;
+    if (number >= tiles) return;
+    begin(number);
+    while (true) {
+        floatx16 acc[MT][NT];
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int j = 0; j < NT; ++j) acc[i][j] = (floatx16)(0.0f);
+        // Waves whose rows are past the tile's last one bring their share and rest: each SIMD has a wave of the tile's first
+        // half and one of the second, so a tile of up to 128 rows takes half the time.
+        const bool idle = wn * 32 * NT >= to - from;
+        const auto stage = [&](int s, auto more) {
+            const int buffer = buffer_of(at + s);
+            const uint4 *lq = lds + buffer * BOTH, *lp = lq + SIDE;
+            uint4 p[2][MT], q[2][NT];
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+#pragma unroll
+                for (int i = 0; i < MT; ++i) p[t][i] = lp[WideTile::slot((wm * MT + i) * 32 + (lane & 31), 2 * t + (lane >> 5))];
+#pragma unroll
+                for (int j = 0; j < NT; ++j) q[t][j] = lq[WideTile::slot((wn * NT + j) * 32 + (lane & 31), 2 * t + (lane >> 5))];
+            }
+            uint32_t ps[MT] = {}, qs[NT] = {};
+            if constexpr (MICRO) {
+                // of a row's four scales a lane has the words of its half: 0 and 2, or 1 and 3
+                const int shift = 8 * (lane >> 5);
+#pragma unroll
+                for (int i = 0; i < MT; ++i) ps[i] = scales[buffer][1][(wm * MT + i) * 32 + (lane & 31)] >> shift;
+#pragma unroll
+                for (int j = 0; j < NT; ++j) qs[j] = scales[buffer][0][(wn * NT + j) * 32 + (lane & 31)] >> shift;
+                store_scales(buffer_of(at + s + 1));
+                fetch_scales(s + 2);
+            }
+            const auto step = [&](auto t) {
+                if constexpr (more()) bring(buffer_of(at + s + kBuffers - 1), t());
+                if (idle) return;
+#pragma unroll
+                for (int i = 0; i < MT; ++i)
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) acc[i][j] = Op::template multiply<2 * t()>(p[t()][i], q[t()][j], acc[i][j], ps[i], qs[j]);
+                __builtin_amdgcn_sched_barrier(0);
+            };
+            step(std::integral_constant<int, 0>{});
+            step(std::integral_constant<int, 1>{});
+        };
+        if (expert >= 0) {
+            int s = 0;
+            // a stage is there when only the loads of the next one are out, and its buffer's last reads are over when all
+            // waves have come to the stage after them
+            for (; s + kBuffers - 1 < full; ++s) {
+                asm volatile("s_waitcnt vmcnt(4) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+                stage(s, std::true_type{});
+            }
+            for (; s < full; ++s) {
+                if (s + 1 < full) asm volatile("s_waitcnt vmcnt(4) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+                else asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+                stage(s, std::false_type{});
+            }
+            if (s < stages) {
+                // the last columns, short of a stage: by way of registers, zeros after them
+                const int word = threadIdx.x % 4, left = a.reduced - full * STAGE - word * Op::kPerWord;
+                const int64_t bytes = (int64_t)full * kWideWords * 16 + word * 16;
+                const auto last = [&](const char *p, uint4 *side, int r) {
+                    uint4 v = make_uint4(0, 0, 0, 0);
+                    if constexpr (MICRO) {
+                        if (left > 0) __builtin_memcpy(&v, p, 16);     // a group's codes past the last column are zeros
+                    } else if (left > 0) {
+                        Word<T> t;
+                        if (left >= 8) t.load(reinterpret_cast<const T *>(p));
+                        else t.load(reinterpret_cast<const T *>(p), left);
+                        v = make_uint4(t.v[0], t.v[1], t.v[2], t.v[3]);
+                    }
+                    side[WideTile::slot(r, word)] = v;
+                };
+#pragma unroll 1
+                for (int r = threadIdx.x / 4; r < kWide; r += kWideThreads / 4) {
+                    last(Op::bytes(x_row(r)) + bytes, lds + buffer_of(at + s) * BOTH, r);
+                    last(Op::bytes(w_row(r)) + bytes, lds + buffer_of(at + s) * BOTH + SIDE, r);
+                }
+                __syncthreads();
+                stage(s, std::false_type{});
+                ++s;
+            }
+            at = buffer_of(at + s);
+        }
+
+        // the next tile, before this one's results
+        const int this_expert = expert, this_c0 = c0;
+        const int64_t this_from = from, this_to = to;
+        number += gridDim.x;
+        const bool again = number < tiles;
+        if (again) begin(number);
+
+        // Results by way of LDS, 32 rows of 128 bytes of a wave at once, so that whole lines are stored.
+        char *const mine = reinterpret_cast<char *>(results[wave]);
+        const auto out = [&](auto *y) {
+            using Y = std::remove_pointer_t<decltype(y)>;
+            constexpr int V = 16 / sizeof(Y), COLUMNS = 8 * V, GROUPS = COLUMNS / 32;   // columns a lane; of a line, in groups of 32
+            const bool act = a.act == MPNN_ACT_SILU;      // silu(0) = 0: rows of no expert may take it too
+#pragma unroll
+            for (int i = 0; i < MT; i += GROUPS) {
+                Chunk<float, 4> bias[GROUPS][4];
+#pragma unroll
+                for (int u = 0; u < GROUPS; ++u)
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) {
+                        const int c = this_c0 + (wm * MT + i + u) * 32 + 8 * g + 4 * (lane >> 5);
+                        bias[u][g] = {{0.0f, 0.0f, 0.0f, 0.0f}};
+                        if (a.bias && this_expert >= 0) bias[u][g].load(a.bias + (int64_t)this_expert * a.columns + c, a.columns - c);
+                    }
+                const int c = this_c0 + (wm * MT + i) * 32 + lane % 8 * V, in = a.columns - c;
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+#pragma unroll
+                    for (int u = 0; u < GROUPS; ++u)
+#pragma unroll
+                        for (int g = 0; g < 4; ++g) {
+                            Chunk<Y, 4> o;
+#pragma unroll
+                            for (int r = 0; r < 4; ++r) {
+                                const float v = acc[i + u][j][4 * g + r] + bias[u][g].v[r];
+                                o.v[r] = from_f32<Y>(act ? silu(v) : v);
+                            }
+                            __builtin_memcpy(__builtin_assume_aligned(mine + (lane & 31) * PITCH + (u * 32 + 8 * g + 4 * (lane >> 5)) * sizeof(Y), 4 * sizeof(Y)), &o, sizeof o);
+                        }
+                    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+                    for (int r = 0; r < 32; r += 8) {
+                        const int64_t row = this_from + (wn * NT + j) * 32 + r + lane / 8;
+                        Chunk<Y> o;
+                        __builtin_memcpy(&o, __builtin_assume_aligned(mine + (r + lane / 8) * PITCH + lane % 8 * 16, 16), 16);
+                        // (past L2, whose lines the next tiles' rows and weights need: 65,536 rows 2048 -> 1024 332 -> 313 us)
+                        if (row < this_to && in >= V) store_past(y + row * a.columns + c, o);
+                        else if (row < this_to && in > 0) o.store(y + row * a.columns + c, in);
+                    }
+                    __builtin_amdgcn_wave_barrier();
+                }
+            }
+        };
+        if (a.y_bf16) out(static_cast<bf16 *>(a.y));
+        else out(static_cast<float *>(a.y));
+        if (!again) break;
+    }
+}
+
+// Every block of a tiling, in launches of as many as one holds.
+template <class F> Status by_tiles(Args &a, int columns, int rows, F run) {
+    a.tiles_c = (a.columns + columns - 1) / columns;
+    return by_launches(row_tiles(a.n, a.n_experts, rows) * a.tiles_c, kLaunchBlocks, [&](int64_t from, int64_t count) -> Status {
         a.first = from;
-        k_product<X, W, ACROSS, 2, 2, 2, 2><<<grid_xcd(count, 1), 256, 0, cx.stream>>>(a, x, w);
+        run(grid_xcd(count, 1));
         MPNN_HIP(hipGetLastError());
         return Status::ok();
     });
+}
+
+// Rows that start on 16 bytes, as the loads to LDS need them.
+inline bool whole_words(const void *p, int64_t row_bytes) { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && row_bytes % 16 == 0; }
+inline bool wide_fits(const RowsOf<bf16> &x, const RowsOf<bf16> &w) { return whole_words(x.p, 2 * x.ld) && whole_words(w.p, 2 * w.ld); }
+inline bool wide_fits(const RowsOf<Micro> &x, const RowsOf<Micro> &w) { return whole_words(x.codes, 16) && whole_words(w.codes, 16); }
+
+template <class X, class W, bool ACROSS>
+Status product_t(Context &cx, Args a, const RowsOf<X> &x, const RowsOf<W> &w) {
+    if constexpr (!ACROSS && std::is_same<X, W>::value && !std::is_same<X, float>::value) {
+        if (a.columns > 128 && a.n / a.n_experts >= 128 && wide_fits(x, w)) {
+            a.tiles_c = (a.columns + kWide - 1) / kWide;
+            const int64_t tiles = row_tiles(a.n, a.n_experts, kWide) * a.tiles_c;
+            k_product_wide<X><<<(unsigned)std::min<int64_t>(grid_xcd(std::min<int64_t>(tiles, kCus), 1), kCus), kWideThreads, 0, cx.stream>>>(a, x, w);
+            MPNN_HIP(hipGetLastError());
+            return Status::ok();
+        }
+    }
+    return by_tiles(a, 128, 128, [&](unsigned grid) { k_product<X, W, ACROSS, 2, 2, 2, 2><<<grid, 256, 0, cx.stream>>>(a, x, w); });
 }
 
 }  // namespace

@@ -211,21 +211,26 @@ struct Tile {
     int64_t from, to;       // its rows; from >= to: past the last tile
 };
 __device__ __forceinline__ int64_t clamped(int32_t v, int64_t low, int64_t n) { return min(max((int64_t)v, low), n); }
+// Rows of segment e: an expert's, and then those after the last one's and before the first one's.
+__device__ __forceinline__ void segment_of(const int32_t *offsets, int n_experts, int64_t n, int e, int64_t &from, int64_t &to) {
+    from = to = 0;
+    if (e < n_experts) {
+        from = clamped(offsets[e], 0, n);
+        to = clamped(offsets[e + 1], from, n);
+    } else if (e == n_experts) {
+        from = clamped(offsets[n_experts], 0, n);
+        to = n;
+    } else if (e == n_experts + 1) {
+        to = clamped(offsets[0], 0, n);
+    }
+}
 __device__ __forceinline__ Tile find_tile(const int32_t *offsets, int n_experts, int64_t n, int rows, int64_t number) {
     const int lane = threadIdx.x & 63;
     int64_t before = 0;
     for (int base = 0; base < n_experts + 2; base += 64) {
         const int e = base + lane;
-        int64_t from = 0, to = 0;
-        if (e < n_experts) {
-            from = clamped(offsets[e], 0, n);
-            to = clamped(offsets[e + 1], from, n);
-        } else if (e == n_experts) {
-            from = clamped(offsets[n_experts], 0, n);
-            to = n;
-        } else if (e == n_experts + 1) {
-            to = clamped(offsets[0], 0, n);
-        }
+        int64_t from, to;
+        segment_of(offsets, n_experts, n, e, from, to);
         const int c = (int)((to - from + rows - 1) / rows);
         int s = c;
 #pragma unroll
