@@ -456,6 +456,183 @@ __global__ __launch_bounds__(kWideThreads, 2) void k_product_wide(const Args a, 
     }
 }
 
+// ---- few rows ----
+// 16 columns by 16 NT rows a wave, operands straight from memory to registers: what bounds a call of few rows is reading the
+// weights, so each lane reads 64 neighbouring bytes of a weight row at once (32 of 4-bit codes) and the reduced axis is split
+// among the waves of a block, whose sums are added in their order.  A lane's word holds the same steps of the reduced axis for
+// rows and weights; which lane holds which does not matter to the sum.
+typedef float floatx4 __attribute__((ext_vector_type(4)));
+
+// PER steps of a row as loaded, and the products of a lane's word of weights with its word of rows.
+template <class X, class W> struct FewOp;
+template <> struct FewOp<bf16, bf16> {
+    static constexpr int kPer = 8, kWords = 4;
+    struct Raw {
+        Word<bf16> v;
+        template <class R> __device__ __forceinline__ void load(const R &r, int k, int width) { RowsOf<bf16>::load(v, r, k, width); }
+        __device__ __forceinline__ bf16x8 operand() const { return __builtin_bit_cast(bf16x8, make_uint4(v.v[0], v.v[1], v.v[2], v.v[3])); }
+    };
+    using RawX = Raw;
+    using RawW = Raw;
+    __device__ __forceinline__ static floatx4 multiply(const RawW &w, const RawX &x, floatx4 c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(w.operand(), x.operand(), c, 0, 0, 0);
+    }
+};
+template <> struct FewOp<float, float> {       // fp32 matrix cores: few rows leave them time enough
+    static constexpr int kPer = 8, kWords = 4;
+    struct Raw {
+        Word<float> v;
+        template <class R> __device__ __forceinline__ void load(const R &r, int k, int width) { RowsOf<float>::load(v, r, k, width); }
+    };
+    using RawX = Raw;
+    using RawW = Raw;
+    __device__ __forceinline__ static floatx4 multiply(const RawW &w, const RawX &x, floatx4 c) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) c = __builtin_amdgcn_mfma_f32_16x16x4f32(w.v.v[j], x.v.v[j], c, 0, 0, 0);
+        return c;
+    }
+};
+struct FewMicro {                               // a whole group
+    uint4 v;
+    uint32_t scale;
+    __device__ __forceinline__ void load(const RowsOf<Micro>::Row &r, int k, int width) {
+        v = make_uint4(0, 0, 0, 0);
+        scale = 127;
+        if (k >= width) return;
+        __builtin_memcpy(&v, r.codes + k / 2, 16);
+        scale = r.scales[k / kMicroGroup];
+    }
+};
+template <class T> struct FewRows {             // 32 columns of rows that are not held
+    Word<T> v[4];
+    template <class R> __device__ __forceinline__ void load(const R &r, int k, int width) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) RowsOf<T>::load(v[u], r, k + 8 * u, width);
+    }
+};
+template <> struct FewOp<Micro, Micro> {
+    static constexpr int kPer = 32, kWords = 2;
+    using RawX = FewMicro;
+    using RawW = FewMicro;
+    __device__ __forceinline__ static floatx4 multiply(const RawW &w, const RawX &x, floatx4 c) {
+        const intx8 a = {(int)w.v.x, (int)w.v.y, (int)w.v.z, (int)w.v.w, 0, 0, 0, 0}, b = {(int)x.v.x, (int)x.v.y, (int)x.v.z, (int)x.v.w, 0, 0, 0, 0};
+        return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 4, 4, 0, w.scale, 0, x.scale);
+    }
+};
+template <> struct FewOp<bf16, Micro> {
+    static constexpr int kPer = 32, kWords = 2;
+    using RawX = FewRows<bf16>;
+    using RawW = FewMicro;
+    __device__ __forceinline__ static floatx4 multiply(const RawW &w, const RawX &x, floatx4 c) {
+        const uint32_t codes[4] = {w.v.x, w.v.y, w.v.z, w.v.w};
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            Word<Micro> m;
+            m.v = codes[u];
+            m.scale = (uint8_t)w.scale;
+            uint4 t[1];
+            float unused = 0.0f;
+            m.terms(t, unused);
+            c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, t[0]), __builtin_bit_cast(bf16x8, make_uint4(x.v[u].v[0], x.v[u].v[1], x.v[u].v[2], x.v[u].v[3])), c, 0, 0, 0);
+        }
+        return c;
+    }
+};
+template <> struct FewOp<float, Micro> {
+    static constexpr int kPer = 32, kWords = 1;
+    using RawX = FewRows<float>;
+    using RawW = FewMicro;
+    __device__ __forceinline__ static floatx4 multiply(const RawW &w, const RawX &x, floatx4 c) {
+        const uint32_t codes[4] = {w.v.x, w.v.y, w.v.z, w.v.w};
+        const float step = micro_step(w.scale);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const auto two = [&](auto k) {
+                const auto p = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes[u], step, k());
+                c = __builtin_amdgcn_mfma_f32_16x16x4f32(p[0], x.v[u].v[2 * k()], c, 0, 0, 0);
+                c = __builtin_amdgcn_mfma_f32_16x16x4f32(p[1], x.v[u].v[2 * k() + 1], c, 0, 0, 0);
+            };
+            two(std::integral_constant<int, 0>{});
+            two(std::integral_constant<int, 1>{});
+            two(std::integral_constant<int, 2>{});
+            two(std::integral_constant<int, 3>{});
+        }
+        return c;
+    }
+};
+
+// Of the block's eight waves `split` share a tile's reduced axis, so it has 8 / split tiles of 16 columns.
+constexpr int kFewThreads = 512, kFewWaves = kFewThreads / 64;
+template <class X, class W, int NT>
+__global__ __launch_bounds__(kFewThreads) void k_product_few(const Args a, int split, const RowsOf<X> x, const RowsOf<W> w) {
+    using Op = FewOp<X, W>;
+    constexpr int STRIDE = 4 * Op::kWords * Op::kPer;                  // of the reduced axis, a wave at once
+    __shared__ floatx4 sums[kFewWaves][NT][64];
+    const int64_t number = a.first + xcd_block();
+    const Tile tile = find_tile(a.offsets, a.n_experts, a.n, 16 * NT, number / a.tiles_c);
+    if (tile.from >= tile.to) return;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), part = wave % split;
+    const int c0 = ((int)(number % a.tiles_c) * (kFewWaves / split) + wave / split) * 16;
+    floatx4 acc[NT];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) acc[j] = (floatx4)(0.0f);
+    if (tile.expert >= 0 && c0 < a.columns) {
+        const auto place = [&](int64_t q) -> int64_t {
+            if (!a.source) return q;
+            return min((int64_t)((uint32_t)max(a.source[q], 0) / (uint32_t)a.slots), a.n_x - 1);
+        };
+        typename RowsOf<X>::Row xr[NT];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) xr[j] = x.row(place(min(tile.from + 16 * j + (lane & 15), tile.to - 1)));
+        const typename RowsOf<W>::Row wr = w.row((int64_t)tile.expert * a.columns + min(c0 + (lane & 15), a.columns - 1));
+        const int turns = (a.reduced + STRIDE - 1) / STRIDE, each = (turns + split - 1) / split;
+        const int first = part * each, last = min(first + each, turns);
+        typename Op::RawW wv[2][Op::kWords];
+        typename Op::RawX xv[2][NT][Op::kWords];
+        const auto fetch = [&](int turn, int b) {
+            const int k = turn * STRIDE + (lane >> 4) * (Op::kWords * Op::kPer);
+#pragma unroll
+            for (int u = 0; u < Op::kWords; ++u) wv[b][u].load(wr, k + u * Op::kPer, a.reduced);
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int u = 0; u < Op::kWords; ++u) xv[b][j][u].load(xr[j], k + u * Op::kPer, a.reduced);
+        };
+        const auto use = [&](int b) {
+#pragma unroll
+            for (int u = 0; u < Op::kWords; ++u)
+#pragma unroll
+                for (int j = 0; j < NT; ++j) acc[j] = Op::multiply(wv[b][u], xv[b][j][u], acc[j]);
+        };
+        if (first < last) fetch(first, 0);
+        for (int t = first; t < last; t += 2) {
+            if (t + 1 < last) fetch(t + 1, 1);
+            use(0);
+            if (t + 1 < last) {
+                if (t + 2 < last) fetch(t + 2, 0);
+                use(1);
+            }
+        }
+    }
+    if (split > 1) {
+#pragma unroll
+        for (int j = 0; j < NT; ++j) sums[wave][j][lane] = acc[j];
+        __syncthreads();
+        if (part != 0) return;
+        for (int p = 1; p < split; ++p)
+#pragma unroll
+            for (int j = 0; j < NT; ++j) acc[j] += sums[wave + p][j][lane];
+    }
+    // a lane has four neighbouring columns of a row
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+        const int64_t q = tile.from + 16 * j + (lane & 15);
+        const int c = c0 + 4 * (lane >> 4);
+        float v[4] = {acc[j][0], acc[j][1], acc[j][2], acc[j][3]};
+        if (q < tile.to && c < a.columns) finish(a, tile.expert, q, c, a.columns - c, v);
+    }
+}
+
 // Every block of a tiling, in launches of as many as one holds.
 template <class F> Status by_tiles(Args &a, int columns, int rows, F run) {
     a.tiles_c = (a.columns + columns - 1) / columns;
@@ -481,6 +658,21 @@ Status product_t(Context &cx, Args a, const RowsOf<X> &x, const RowsOf<W> &w) {
             k_product_wide<X><<<(unsigned)std::min<int64_t>(grid_xcd(std::min<int64_t>(tiles, kCus), 1), kCus), kWideThreads, 0, cx.stream>>>(a, x, w);
             MPNN_HIP(hipGetLastError());
             return Status::ok();
+        }
+    }
+    if constexpr (!ACROSS) {
+        const int64_t rows = (a.n + std::min<int64_t>(a.n, a.n_experts) - 1) / std::min<int64_t>(a.n, a.n_experts);    // of an expert
+        if (rows <= 64) {
+            int split = 1;
+            while (split < kFewWaves && split * 4 * FewOp<X, W>::kWords * FewOp<X, W>::kPer < a.reduced) split *= 2;
+            const auto few = [&](auto nt) {
+                return by_tiles(a, 16 * (kFewWaves / split), 16 * nt(), [&](unsigned grid) { k_product_few<X, W, nt()><<<grid, kFewThreads, 0, cx.stream>>>(a, split, x, w); });
+            };
+            if (rows <= 16) return few(std::integral_constant<int, 1>{});
+            // four row groups of operands fit the registers where both sides have the same 16-bit or smaller type
+            if constexpr (std::is_same<X, W>::value && !std::is_same<X, float>::value)
+                if (rows > 32) return few(std::integral_constant<int, 4>{});
+            return few(std::integral_constant<int, 2>{});
         }
     }
     return by_tiles(a, 128, 128, [&](unsigned grid) { k_product<X, W, ACROSS, 2, 2, 2, 2><<<grid, 256, 0, cx.stream>>>(a, x, w); });
