@@ -36,12 +36,6 @@ __device__ __forceinline__ float silu(float z) {
     return z >= 0.0f ? z * r : z * a * r;
 }
 
-// 16 bytes that are not read again soon.
-template <class T> __device__ __forceinline__ void store_past(T *p, const Chunk<T> &v) {
-    typedef uint32_t Words __attribute__((ext_vector_type(4), aligned(2)));
-    __builtin_nontemporal_store(__builtin_bit_cast(Words, v), reinterpret_cast<Words *>(p));
-}
-
 template <class T> __device__ __forceinline__ void store_four(T *p, const float (&v)[4], int in) {
     Chunk<T, 4> o;
 #pragma unroll
@@ -198,21 +192,23 @@ constexpr int kWide = 256, kWideWords = 4, kBuffers = 3, kWideThreads = 512, kCu
 constexpr int kSegments = 1024 + 2;                // experts and the rows of none
 using WideTile = Along<1, kWide, kWideWords>;
 
-template <class T>
+// ACROSS (bf16): the weights' rows are the reduced axis; a stage is 32 of them, 512 bytes each.
+template <class T, bool ACROSS>
 __global__ __launch_bounds__(kWideThreads, 2) void k_product_wide(const Args a, const RowsOf<T> x, const RowsOf<T> w) {
     using Op = WideOp<T>;
     constexpr bool MICRO = std::is_same<T, Micro>::value;
     constexpr int STAGE = kWideWords * Op::kPerWord;                   // columns of a stage
-    constexpr int SIDE = WideTile::kWords, BOTH = 2 * SIDE;            // words of a stage: rows, then weights
-    constexpr int MT = 4, NT = 2, PITCH = 128 + 16;       // bytes of a line of results and of the way to the next
+    constexpr int SIDE = WideTile::kWords, BOTH = SIDE + (ACROSS ? Pairs::kWords : SIDE);     // words of a stage: rows, then weights
+    constexpr int MT = 4, NT = 2;
     __shared__ uint4 lds[kBuffers * BOTH];
     __shared__ uint32_t scales[MICRO ? kBuffers : 1][2][MICRO ? kWide : 1];
-    __shared__ uint4 results[kWideThreads / 64][32 * PITCH / 16];
+    __shared__ uint4 results[kWideThreads / 64][kStoreBytes / 16];
     __shared__ int first[kSegments + 1], start[kSegments];             // of each segment, its first tile and row
     typedef const __attribute__((address_space(1))) void *Global;
     typedef __attribute__((address_space(3))) void *Local;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wm = wave & 1, wn = wave >> 1;
 
+    [[maybe_unused]] const Pairs pairs(lane);
     const int segments = a.n_experts + 2;
     if (wave == 0) {
         int before = 0;
@@ -251,16 +247,16 @@ __global__ __launch_bounds__(kWideThreads, 2) void k_product_wide(const Args a, 
     const uint8_t *ps_row = nullptr;
     uint32_t next_scales = 0;
     int at = 0;                                    // buffer of the tile's first stage
-    const auto w_row = [&](int r) { return w.row((int64_t)expert * a.columns + min(c0 + r, a.columns - 1)); };
+    const auto w_row = [&](int r) { return w.row(ACROSS ? (int64_t)expert * a.reduced + r : (int64_t)expert * a.columns + min(c0 + r, a.columns - 1)); };
     const auto x_row = [&](int r) { return x.row(place(min(from + r, to - 1))); };
     const auto buffer_of = [&](int s) { return s % kBuffers; };
     // A wave brings 32 rows of each side, 16 at once; lane l the word that stands at place l of those rows in LDS.
     const auto bring = [&](int buffer, int i) {
-        const int words_at = buffer * BOTH + (wave * 32 + i * 16) * kWideWords;
-        __builtin_amdgcn_global_load_lds((Global)px[i], (Local)&lds[words_at], 16, 0, 0);
-        __builtin_amdgcn_global_load_lds((Global)pw[i], (Local)&lds[words_at + SIDE], 16, 0, 0);
+        const int of = wave * 2 + i;
+        __builtin_amdgcn_global_load_lds((Global)px[i], (Local)&lds[buffer * BOTH + of * 64], 16, 0, 0);
+        __builtin_amdgcn_global_load_lds((Global)pw[i], (Local)&lds[buffer * BOTH + SIDE + of * (ACROSS ? Pairs::kPair : 64)], 16, 0, 0);
         px[i] += 64;
-        pw[i] += 64;
+        pw[i] += ACROSS ? a.columns * (int64_t)64 : 64;       // bytes of 32 rows of weights
     };
     // Scales: a thread brings the four of a stage of one row, by way of a register (rows of scales start on any byte).  Past
     // a row's last group they are those of 1, since its codes are zeros there.
@@ -295,7 +291,13 @@ __global__ __launch_bounds__(kWideThreads, 2) void k_product_wide(const Args a, 
         for (int i = 0; i < 2; ++i) {
             const int r = wave * 32 + i * 16 + lane / 4, word = (lane & 3) ^ (r >> 2 & 3);
             px[i] = Op::bytes(x_row(r)) + word * 16;
-            pw[i] = Op::bytes(w_row(r)) + word * 16;
+            if constexpr (ACROSS) {
+                // words past the last column bring the last one again
+                const int k = (wave * 2 + i) * 2 + Pairs::step_of(lane), at_column = c0 + 8 * Pairs::word_of(lane);
+                pw[i] = Op::bytes(w_row(min(k, a.reduced - 1))) + 2 * min(at_column, a.columns - 8);
+            } else {
+                pw[i] = Op::bytes(w_row(r)) + word * 16;
+            }
         }
         if constexpr (MICRO) {
             ps_row = wave < 4 ? x_row(threadIdx.x).scales : w_row(threadIdx.x - 256).scales;
@@ -329,7 +331,10 @@ __global__ __launch_bounds__(kWideThreads, 2) void k_product_wide(const Args a, 
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
 #pragma unroll
-                for (int i = 0; i < MT; ++i) p[t][i] = lp[WideTile::slot((wm * MT + i) * 32 + (lane & 31), 2 * t + (lane >> 5))];
+                for (int i = 0; i < MT; ++i) {
+                    if constexpr (ACROSS) p[t][i] = __builtin_bit_cast(uint4, pairs.read(lp + wm * 16, i, t));
+                    else p[t][i] = lp[WideTile::slot((wm * MT + i) * 32 + (lane & 31), 2 * t + (lane >> 5))];
+                }
 #pragma unroll
                 for (int j = 0; j < NT; ++j) q[t][j] = lq[WideTile::slot((wn * NT + j) * 32 + (lane & 31), 2 * t + (lane >> 5))];
             }
@@ -388,8 +393,16 @@ __global__ __launch_bounds__(kWideThreads, 2) void k_product_wide(const Args a, 
 #pragma unroll 1
                 for (int r = threadIdx.x / 4; r < kWide; r += kWideThreads / 4) {
                     last(Op::bytes(x_row(r)) + bytes, lds + buffer_of(at + s) * BOTH, r);
-                    last(Op::bytes(w_row(r)) + bytes, lds + buffer_of(at + s) * BOTH + SIDE, r);
+                    if constexpr (!ACROSS) last(Op::bytes(w_row(r)) + bytes, lds + buffer_of(at + s) * BOTH + SIDE, r);
                 }
+                if constexpr (ACROSS)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int r = threadIdx.x / 32 + i * 16, k = full * STAGE + r, column = min(c0 + 8 * (int)(threadIdx.x % 32), a.columns - 8);
+                        uint4 v = make_uint4(0, 0, 0, 0);
+                        if (k < a.reduced) __builtin_memcpy(&v, Op::bytes(w_row(k)) + 2 * column, 16);
+                        lds[buffer_of(at + s) * BOTH + SIDE + Pairs::slot(r, threadIdx.x % 32)] = v;
+                    }
                 __syncthreads();
                 stage(s, std::false_type{});
                 ++s;
@@ -404,51 +417,15 @@ __global__ __launch_bounds__(kWideThreads, 2) void k_product_wide(const Args a, 
         const bool again = number < tiles;
         if (again) begin(number);
 
-        // Results by way of LDS, 32 rows of 128 bytes of a wave at once, so that whole lines are stored.
-        char *const mine = reinterpret_cast<char *>(results[wave]);
         const auto out = [&](auto *y) {
-            using Y = std::remove_pointer_t<decltype(y)>;
-            constexpr int V = 16 / sizeof(Y), COLUMNS = 8 * V, GROUPS = COLUMNS / 32;   // columns a lane; of a line, in groups of 32
-            const bool act = a.act == MPNN_ACT_SILU;      // silu(0) = 0: rows of no expert may take it too
-#pragma unroll
-            for (int i = 0; i < MT; i += GROUPS) {
-                Chunk<float, 4> bias[GROUPS][4];
-#pragma unroll
-                for (int u = 0; u < GROUPS; ++u)
-#pragma unroll
-                    for (int g = 0; g < 4; ++g) {
-                        const int c = this_c0 + (wm * MT + i + u) * 32 + 8 * g + 4 * (lane >> 5);
-                        bias[u][g] = {{0.0f, 0.0f, 0.0f, 0.0f}};
-                        if (a.bias && this_expert >= 0) bias[u][g].load(a.bias + (int64_t)this_expert * a.columns + c, a.columns - c);
-                    }
-                const int c = this_c0 + (wm * MT + i) * 32 + lane % 8 * V, in = a.columns - c;
-#pragma unroll
-                for (int j = 0; j < NT; ++j) {
-#pragma unroll
-                    for (int u = 0; u < GROUPS; ++u)
-#pragma unroll
-                        for (int g = 0; g < 4; ++g) {
-                            Chunk<Y, 4> o;
-#pragma unroll
-                            for (int r = 0; r < 4; ++r) {
-                                const float v = acc[i + u][j][4 * g + r] + bias[u][g].v[r];
-                                o.v[r] = from_f32<Y>(act ? silu(v) : v);
-                            }
-                            __builtin_memcpy(__builtin_assume_aligned(mine + (lane & 31) * PITCH + (u * 32 + 8 * g + 4 * (lane >> 5)) * sizeof(Y), 4 * sizeof(Y)), &o, sizeof o);
-                        }
-                    __builtin_amdgcn_wave_barrier();
-#pragma unroll
-                    for (int r = 0; r < 32; r += 8) {
-                        const int64_t row = this_from + (wn * NT + j) * 32 + r + lane / 8;
-                        Chunk<Y> o;
-                        __builtin_memcpy(&o, __builtin_assume_aligned(mine + (r + lane / 8) * PITCH + lane % 8 * 16, 16), 16);
-                        // (past L2, whose lines the next tiles' rows and weights need: 65,536 rows 2048 -> 1024 332 -> 313 us)
-                        if (row < this_to && in >= V) store_past(y + row * a.columns + c, o);
-                        else if (row < this_to && in > 0) o.store(y + row * a.columns + c, in);
-                    }
-                    __builtin_amdgcn_wave_barrier();
-                }
-            }
+            const bool act = a.act == MPNN_ACT_SILU, biased = a.bias && this_expert >= 0;      // silu(0) = 0: rows of no expert may take it too
+            const auto bias = [&](int c) {
+                Chunk<float, 4> b = {{0.0f, 0.0f, 0.0f, 0.0f}};
+                if (biased) b.load(a.bias + (int64_t)this_expert * a.columns + c, a.columns - c);
+                return b;
+            };
+            store_lines(reinterpret_cast<char *>(results[wave]), acc, lane, y, a.columns, this_from + wn * NT * 32, this_to,
+                        this_c0 + wm * MT * 32, a.columns, bias, [&](float v) { return act ? silu(v) : v; });
         };
         if (a.y_bf16) out(static_cast<bf16 *>(a.y));
         else out(static_cast<float *>(a.y));
@@ -651,17 +628,17 @@ inline bool wide_fits(const RowsOf<Micro> &x, const RowsOf<Micro> &w) { return w
 
 template <class X, class W, bool ACROSS>
 Status product_t(Context &cx, Args a, const RowsOf<X> &x, const RowsOf<W> &w) {
-    if constexpr (!ACROSS && std::is_same<X, W>::value && !std::is_same<X, float>::value) {
-        if (a.columns > 128 && a.n / a.n_experts >= 128 && wide_fits(x, w)) {
+    const int64_t rows = (a.n + std::min<int64_t>(a.n, a.n_experts) - 1) / std::min<int64_t>(a.n, a.n_experts);    // of an expert
+    if constexpr (std::is_same<X, W>::value && !std::is_same<X, float>::value) {
+        if (a.columns > 128 && rows > 32 && wide_fits(x, w)) {
             a.tiles_c = (a.columns + kWide - 1) / kWide;
             const int64_t tiles = row_tiles(a.n, a.n_experts, kWide) * a.tiles_c;
-            k_product_wide<X><<<(unsigned)std::min<int64_t>(grid_xcd(std::min<int64_t>(tiles, kCus), 1), kCus), kWideThreads, 0, cx.stream>>>(a, x, w);
+            k_product_wide<X, ACROSS><<<(unsigned)std::min<int64_t>(grid_xcd(std::min<int64_t>(tiles, kCus), 1), kCus), kWideThreads, 0, cx.stream>>>(a, x, w);
             MPNN_HIP(hipGetLastError());
             return Status::ok();
         }
     }
     if constexpr (!ACROSS) {
-        const int64_t rows = (a.n + std::min<int64_t>(a.n, a.n_experts) - 1) / std::min<int64_t>(a.n, a.n_experts);    // of an expert
         if (rows <= 64) {
             int split = 1;
             while (split < kFewWaves && split * 4 * FewOp<X, W>::kWords * FewOp<X, W>::kPer < a.reduced) split *= 2;

@@ -176,6 +176,31 @@ template <int TERMS, int COLUMNS, int WORDS> struct Across {
     }
 };
 
+// Tiles of 256 columns whose steps come to LDS two at a time without passing through registers (64 lanes, a word each, end up
+// one after another): the odd step of a pair has its groups of four words swapped, and pairs are 128 bytes further apart than
+// their length, so that four steps of a transposing read lie in different banks, at addresses that differ by constants.
+struct Pairs {
+    static constexpr int kPair = 2 * 32 + 8;                            // words
+    static constexpr int kWords = 16 * kPair;                           // of a stage of 32 steps
+    __device__ __forceinline__ static int slot(int step, int word) { return (step >> 1) * kPair + (step & 1) * 32 + (word ^ (step & 1) * 4); }
+    // of the pair's words the one that a lane brings: its step of the two, and its word
+    __device__ __forceinline__ static int step_of(int lane) { return lane >> 5; }
+    __device__ __forceinline__ static int word_of(int lane) { return (lane & 31) ^ (lane >> 5) * 4; }
+    int even, odd;          // byte offsets of the lane's reads of the first and the second 32 columns
+    __device__ __forceinline__ explicit Pairs(int lane) {
+        const int i = lane & 15, step = 8 * (lane >> 5) + i / 4, word = (lane & 16) / 8 + (i >> 1 & 1), low = (i & 1) * 8;
+        even = slot(step, word) * 16 + low;
+        odd = slot(step, word + 4) * 16 + low;
+    }
+    // the operand of 32 columns from 32 i on at step s (16 steps along the reduced axis)
+    __device__ __forceinline__ bf16x8 read(const uint4 *lds, int i, int s) const {
+        typedef __attribute__((address_space(3))) shortx4 *Ptr;
+        const char *p = reinterpret_cast<const char *>(lds) + (i & 1 ? odd : even) + (i >> 1) * 128 + s * (8 * kPair * 16);
+        const shortx4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Ptr)p), b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Ptr)(p + 2 * kPair * 16));
+        return __builtin_bit_cast(bf16x8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+    }
+};
+
 // acc[i][j] += P_i^T Q_j over the WORDS / 2 steps of a stage, P columns of the result and Q its rows: smallest terms first.
 template <class P, class Q, int TP, int TQ, int MT, int NT, int WORDS>
 __device__ __forceinline__ void multiply(const uint4 *p, const uint4 *q, int pfirst, int qfirst, int lane, floatx16 (&acc)[MT][NT]) {
@@ -201,6 +226,54 @@ __device__ __forceinline__ void multiply(const uint4 *p, const uint4 *q, int pfi
 #pragma unroll
                     for (int j = 0; j < NT; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[u][i], b[v][j], acc[i][j], 0, 0, 0);
             }
+    }
+}
+
+// 16 bytes that are not read again soon.
+template <class T> __device__ __forceinline__ void store_past(T *p, const Chunk<T> &v) {
+    typedef uint32_t Words __attribute__((ext_vector_type(4), aligned(2)));
+    __builtin_nontemporal_store(__builtin_bit_cast(Words, v), reinterpret_cast<Words *>(p));
+}
+
+// A wave's results (32 MT columns from col0, 32 NT rows from row0) by way of LDS, 32 rows of 128 bytes at once, so that whole
+// lines are stored, past L2, whose lines the next tiles' operands need (65,536 rows 2048 -> 1024 bf16 332 -> 313 us).
+// mine: the wave's kStoreBytes of LDS; bias(c): what is added to four columns from c on; act(v) then is the result.
+constexpr int kStorePitch = 128 + 16, kStoreBytes = 32 * kStorePitch;
+template <class Y, int MT, int NT, class B, class F>
+__device__ __forceinline__ void store_lines(char *mine, const floatx16 (&acc)[MT][NT], int lane, Y *y, int64_t ld, int64_t row0, int64_t rows,
+                                            int col0, int columns, B bias, F act) {
+    constexpr int V = 16 / sizeof(Y), GROUPS = 8 * V / 32;       // columns a lane; groups of 32 columns a line
+#pragma unroll
+    for (int i = 0; i < MT; i += GROUPS) {
+        const int c = col0 + i * 32 + lane % 8 * V, in = columns - c;
+        Chunk<float, 4> b[GROUPS][4];
+#pragma unroll
+        for (int u = 0; u < GROUPS; ++u)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) b[u][g] = bias(col0 + (i + u) * 32 + 8 * g + 4 * (lane >> 5));
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+#pragma unroll
+            for (int u = 0; u < GROUPS; ++u)
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    Chunk<Y, 4> o;
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) o.v[r] = from_f32<Y>(act(acc[i + u][j][4 * g + r] + b[u][g].v[r]));
+                    __builtin_memcpy(__builtin_assume_aligned(mine + (lane & 31) * kStorePitch + (u * 32 + 8 * g + 4 * (lane >> 5)) * sizeof(Y), 4 * sizeof(Y)), &o,
+                                     sizeof o);
+                }
+            __builtin_amdgcn_wave_barrier();
+#pragma unroll
+            for (int r = 0; r < 32; r += 8) {
+                const int64_t row = row0 + j * 32 + r + lane / 8;
+                Chunk<Y> o;
+                __builtin_memcpy(&o, __builtin_assume_aligned(mine + (r + lane / 8) * kStorePitch + lane % 8 * 16, 16), 16);
+                if (row < rows && in >= V) store_past(y + row * ld + c, o);
+                else if (row < rows && in > 0) o.store(y + row * ld + c, in);
+            }
+            __builtin_amdgcn_wave_barrier();
+        }
     }
 }
 
