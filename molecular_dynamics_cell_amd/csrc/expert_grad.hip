@@ -148,45 +148,61 @@ __global__ __launch_bounds__(256, 2) void k_expert_weight_grad(const Args a, con
 }
 
 // Wide tiles, bf16: 256 columns of x by 256 of dy, eight waves of 128 x 64, stages of 32 rows that go to LDS without passing
-// through registers, two stages ahead; a bias is the product of dy with ones.
-constexpr int kWide = 256, kWideThreads = 512, kBuffers = 3, kWideStage = 32;
+// through registers, two stages ahead; a bias is the product of dy with ones.  A block stays for many tiles: the next one's
+// first stages are on their way while this one's results are stored.
+// Whole pieces are dealt to the blocks first, then what is left of each expert, in turn from the first block to the last and
+// back, so that a block with one tile more has a short one.
+constexpr int kWide = 256, kWideThreads = 512, kBuffers = 3, kWideStage = 32, kCus = 256, kMostExperts = 1024;
 
 __global__ __launch_bounds__(kWideThreads, 2) void k_expert_weight_grad_wide(const Args a, const RowsOf<bf16> dy, const RowsOf<bf16> x) {
     constexpr int MT = 4, NT = 2, SIDE = Pairs::kWords, BOTH = 2 * SIDE;
     __shared__ uint4 lds[kBuffers * BOTH];                             // dy, then x
     __shared__ uint4 results[kWideThreads / 64][kStoreBytes / 16];
+    __shared__ int before[kMostExperts + 1], slot[kMostExperts];       // whole pieces before each expert's; its partial sums
     typedef const __attribute__((address_space(1))) void *Global;
     typedef __attribute__((address_space(3))) void *Local;
-
-    const uint32_t number = (uint32_t)xcd_block();
-    const int tile = (int)(number % (uint32_t)a.tiles);
-    const Piece pc = find_piece(a.offsets, a.n_experts, a.n, a.rows, (int)(number / (uint32_t)a.tiles), -1);
-    if (pc.expert < 0) return;
-    int64_t from, to;
-    pieces_of(a.offsets, pc.expert, a.n, a.rows, from, to);
-    from += pc.piece * a.rows;
-    to = min(to, from + a.rows);
-    const int o0 = tile / a.tiles_c * kWide, c0 = tile % a.tiles_c * kWide;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wm = wave & 1, wn = wave >> 1;
     const Pairs pairs(lane);
+    if (wave == 0) {
+        int wholes = 0, slots = 0;
+        for (int base = 0; base < a.n_experts; base += 64) {
+            const int e = base + lane;
+            int64_t from = 0, to = 0;
+            const int p = e < a.n_experts ? pieces_of(a.offsets, e, a.n, a.rows, from, to) : 0, c = (int)((to - from) / a.rows), m = p > 1 ? p : 0;
+            int s = c, t = m;
+#pragma unroll
+            for (int d = 1; d < 64; d <<= 1) {
+                const int u = __shfl_up(s, d), v = __shfl_up(t, d);
+                if (lane >= d) {
+                    s += u;
+                    t += v;
+                }
+            }
+            if (e < a.n_experts) {
+                before[e] = wholes + s - c;
+                slot[e] = slots + t - m;
+            }
+            wholes += __builtin_amdgcn_readlane(s, 63);
+            slots += __builtin_amdgcn_readlane(t, 63);
+        }
+        if (lane == 0) before[a.n_experts] = wholes;
+    }
+    __syncthreads();
+    const int64_t wholes = (int64_t)before[a.n_experts] * a.tiles, all = wholes + (int64_t)a.n_experts * a.tiles;
+    const int64_t matrix = (int64_t)a.out * a.width;
 
+    // The tile that is being brought, multiplied and stored.
+    float *to_w = nullptr, *to_b = nullptr;        // (null: nothing is stored)
+    int o0 = 0, c0 = 0, full = 0, stages = 0, at = 0;
+    int64_t from = 0, to = 0, next[2];             // next: the row of x that is brought next (by source)
+    const bf16 *px[2], *pd[2];
+    const auto place = [&](int64_t q) -> int64_t { return min((int64_t)((uint32_t)max(a.source[q], 0) / (uint32_t)a.slots), a.n_x - 1); };
     // Lane l of a wave's i-th load of a stage brings one word of step (2 wave + i) 2 + l / 32; words past the last column bring
     // the last one again.
-    const auto place = [&](int64_t q) -> int64_t { return min((int64_t)((uint32_t)max(a.source[q], 0) / (uint32_t)a.slots), a.n_x - 1); };
-    const int step0 = wave * 4 + Pairs::step_of(lane), xc = min(c0 + 8 * Pairs::word_of(lane), a.width - 8), oc = min(o0 + 8 * Pairs::word_of(lane), a.out - 8);
-    const int full = (int)((to - from) / kWideStage), stages = (int)((to - from + kWideStage - 1) / kWideStage);
-    const bf16 *px[2], *pd[2];
-    int64_t next[2];                                // the row of x that is brought next (by source)
+    const int step0 = wave * 4 + Pairs::step_of(lane);
     const auto look_up = [&](int s, int i) { next[i] = place(min(from + (int64_t)s * kWideStage + step0 + i * 2, to - 1)); };
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int64_t q = min(from + step0 + i * 2, max(to - 1, (int64_t)0));
-        pd[i] = dy.p + q * dy.ld + oc;
-        px[i] = x.p + (a.source ? 0 : q * x.ld) + xc;
-        if (a.source && from < to) look_up(0, i);
-    }
     const auto bring = [&](int s, int i) {
-        const int at = s % kBuffers * BOTH + (wave * 2 + i) * Pairs::kPair;
+        const int words = (at + s) % kBuffers * BOTH + (wave * 2 + i) * Pairs::kPair;
         const bf16 *p = px[i];
         if (a.source) {
             p += next[i] * x.ld;
@@ -194,91 +210,146 @@ __global__ __launch_bounds__(kWideThreads, 2) void k_expert_weight_grad_wide(con
         } else {
             px[i] += kWideStage * x.ld;
         }
-        __builtin_amdgcn_global_load_lds((Global)pd[i], (Local)&lds[at], 16, 0, 0);
-        __builtin_amdgcn_global_load_lds((Global)p, (Local)&lds[at + SIDE], 16, 0, 0);
+        __builtin_amdgcn_global_load_lds((Global)pd[i], (Local)&lds[words], 16, 0, 0);
+        __builtin_amdgcn_global_load_lds((Global)p, (Local)&lds[words + SIDE], 16, 0, 0);
         pd[i] += kWideStage * dy.ld;
     };
-
-    floatx16 acc[MT][NT], sum[NT];
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-        sum[j] = (floatx16)(0.0f);
-#pragma unroll
-        for (int i = 0; i < MT; ++i) acc[i][j] = (floatx16)(0.0f);
-    }
-    const bool biased = c0 == 0 && wm == 0 && a.dbias;
-    const uint4 ones = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
-    const auto stage = [&](int s, auto more) {
-        const uint4 *lq = lds + s % kBuffers * BOTH + wn * 8, *lp = lds + s % kBuffers * BOTH + SIDE + wm * 16;
-        bf16x8 p[2][MT], q[2][NT];
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-#pragma unroll
-            for (int i = 0; i < MT; ++i) p[t][i] = pairs.read(lp, i, t);
-#pragma unroll
-            for (int j = 0; j < NT; ++j) q[t][j] = pairs.read(lq, j, t);
+    const auto begin = [&](int64_t number) {
+        const int64_t piece = number / a.tiles;
+        const int tile = (int)(number % a.tiles);
+        int e, k;                                  // expert, and the piece of its pieces
+        if (number < wholes) {
+            int low = 0, high = a.n_experts - 1;   // the last expert with at most `piece` pieces before its own
+            while (low < high) {
+                const int mid = (low + high + 1) / 2;
+                if (before[mid] <= piece) low = mid;
+                else high = mid - 1;
+            }
+            e = low;
+            k = (int)piece - before[low];
+        } else {
+            e = (int)(piece - before[a.n_experts]);
+            k = before[e + 1] - before[e];
         }
-        const auto step = [&](int t) {
-            if constexpr (more()) bring(s + kBuffers - 1, t);
-#pragma unroll
-            for (int i = 0; i < MT; ++i)
-#pragma unroll
-                for (int j = 0; j < NT; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(p[t][i], q[t][j], acc[i][j], 0, 0, 0);
-            if (biased)
-#pragma unroll
-                for (int j = 0; j < NT; ++j) sum[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, ones), q[t][j], sum[j], 0, 0, 0);
-            __builtin_amdgcn_sched_barrier(0);
-        };
-        step(0);
-        step(1);
-    };
-    for (int s = 0; s < min(full, kBuffers - 1); ++s) {
-        bring(s, 0);
-        bring(s, 1);
-    }
-    // a stage is there when only the loads of the next one are out, and its buffer's last reads are over when all waves have
-    // come to the stage after them
-    int s = 0;
-    for (; s + kBuffers - 1 < full; ++s) {
-        asm volatile("s_waitcnt vmcnt(4) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-        stage(s, std::true_type{});
-    }
-    for (; s < full; ++s) {
-        if (s + 1 < full) asm volatile("s_waitcnt vmcnt(4) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-        else asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-        stage(s, std::false_type{});
-    }
-    if (s < stages) {
-        // the last rows, short of a stage: by way of registers, zeros after them
-        const int word = threadIdx.x % 32, oc = min(o0 + 8 * word, a.out - 8), xc = min(c0 + 8 * word, a.width - 8);
-        uint4 *const to_lds = lds + s % kBuffers * BOTH;
+        e = __builtin_amdgcn_readfirstlane(e);
+        k = __builtin_amdgcn_readfirstlane(k);
+        const int pieces = pieces_of(a.offsets, e, a.n, a.rows, from, to);
+        from += k * a.rows;
+        to = min(to, from + a.rows);
+        const int place_of = slot[e] + k;
+        const bool none = k >= pieces || (pieces > 1 && place_of >= a.part_slots);    // (offsets that do not ascend: more pieces than there are)
+        if (none) to = from;
+        to_w = none ? nullptr : pieces == 1 ? a.dweight + e * matrix : a.part + place_of * slot_size(matrix + a.out);
+        to_b = none ? nullptr : pieces == 1 ? (a.dbias ? a.dbias + (int64_t)e * a.out : nullptr) : to_w + matrix;
+        o0 = tile / a.tiles_c * kWide;
+        c0 = tile % a.tiles_c * kWide;
+        full = (int)((to - from) / kWideStage);
+        stages = (int)((to - from + kWideStage - 1) / kWideStage);
+        if (stages == 0) return;
+        const int xc = min(c0 + 8 * Pairs::word_of(lane), a.width - 8), oc = min(o0 + 8 * Pairs::word_of(lane), a.out - 8);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const int step = threadIdx.x / 32 + i * 16;
-            const int64_t q = from + (int64_t)full * kWideStage + step;
-            uint4 d = make_uint4(0, 0, 0, 0), v = d;
-            if (q < to) {
-                __builtin_memcpy(&d, dy.p + q * dy.ld + oc, 16);
-                __builtin_memcpy(&v, x.p + (a.source ? place(q) : q) * x.ld + xc, 16);
-            }
-            to_lds[Pairs::slot(step, word)] = d;
-            to_lds[SIDE + Pairs::slot(step, word)] = v;
+            const int64_t q = min(from + step0 + i * 2, to - 1);
+            pd[i] = dy.p + q * dy.ld + oc;
+            px[i] = x.p + (a.source ? 0 : q * x.ld) + xc;
+            if (a.source) look_up(0, i);
         }
-        __syncthreads();
-        stage(s, std::false_type{});
-    }
+        for (int s = 0; s < min(full, kBuffers - 1); ++s) {
+            bring(s, 0);
+            bring(s, 1);
+        }
+    };
 
-    const int64_t matrix = (int64_t)a.out * a.width;
-    const bool whole = pc.pieces == 1;
-    if (!whole && pc.slot + pc.piece >= a.part_slots) return;     // offsets that do not ascend name more pieces than there are
-    float *to_w = whole ? a.dweight + pc.expert * matrix : a.part + (int64_t)(pc.slot + pc.piece) * slot_size(matrix + a.out);
-    float *to_b = whole ? a.dbias + (int64_t)pc.expert * a.out : to_w + matrix;
-    if (biased && lane < 32)
+    // blocks of an XCD take neighbouring tiles
+    const int block = (int)(blockIdx.x % kXcds * (gridDim.x / kXcds) + blockIdx.x / kXcds);
+    int64_t number = block;
+    if (number >= all) return;
+    begin(number);
+    for (int64_t round = 1;; ++round) {
+        floatx16 acc[MT][NT], sum[NT];
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
-            if (const int o = o0 + (wn * NT + j) * 32 + lane; o < a.out) to_b[o] = sum[j][0];
-    store_lines(reinterpret_cast<char *>(results[wave]), acc, lane, to_w, a.width, o0 + wn * NT * 32, a.out, c0 + wm * MT * 32, a.width,
-                [](int) { return Chunk<float, 4>{{0.0f, 0.0f, 0.0f, 0.0f}}; }, [](float v) { return v; });
+        for (int j = 0; j < NT; ++j) {
+            sum[j] = (floatx16)(0.0f);
+#pragma unroll
+            for (int i = 0; i < MT; ++i) acc[i][j] = (floatx16)(0.0f);
+        }
+        const bool biased = c0 == 0 && wm == 0 && to_b;
+        const uint4 ones = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
+        const auto stage = [&](int s, auto more) {
+            const uint4 *lq = lds + (at + s) % kBuffers * BOTH + wn * 8, *lp = lds + (at + s) % kBuffers * BOTH + SIDE + wm * 16;
+            bf16x8 p[2][MT], q[2][NT];
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+#pragma unroll
+                for (int i = 0; i < MT; ++i) p[t][i] = pairs.read(lp, i, t);
+#pragma unroll
+                for (int j = 0; j < NT; ++j) q[t][j] = pairs.read(lq, j, t);
+            }
+            const auto step = [&](int t) {
+                if constexpr (more()) bring(s + kBuffers - 1, t);
+#pragma unroll
+                for (int i = 0; i < MT; ++i)
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(p[t][i], q[t][j], acc[i][j], 0, 0, 0);
+                if (biased)
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) sum[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, ones), q[t][j], sum[j], 0, 0, 0);
+                __builtin_amdgcn_sched_barrier(0);
+            };
+            step(0);
+            step(1);
+        };
+        // a stage is there when only the loads of the next one are out, and its buffer's last reads are over when all waves have
+        // come to the stage after them
+        int s = 0;
+        for (; s + kBuffers - 1 < full; ++s) {
+            asm volatile("s_waitcnt vmcnt(4) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+            stage(s, std::true_type{});
+        }
+        for (; s < full; ++s) {
+            if (s + 1 < full) asm volatile("s_waitcnt vmcnt(4) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+            else asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+            stage(s, std::false_type{});
+        }
+        if (s < stages) {
+            // the last rows, short of a stage: by way of registers, zeros after them
+            const int word = threadIdx.x % 32, oc = min(o0 + 8 * word, a.out - 8), xc = min(c0 + 8 * word, a.width - 8);
+            uint4 *const to_lds = lds + (at + s) % kBuffers * BOTH;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int step = threadIdx.x / 32 + i * 16;
+                const int64_t q = from + (int64_t)full * kWideStage + step;
+                uint4 d = make_uint4(0, 0, 0, 0), v = d;
+                if (q < to) {
+                    __builtin_memcpy(&d, dy.p + q * dy.ld + oc, 16);
+                    __builtin_memcpy(&v, x.p + (a.source ? place(q) : q) * x.ld + xc, 16);
+                }
+                to_lds[Pairs::slot(step, word)] = d;
+                to_lds[SIDE + Pairs::slot(step, word)] = v;
+            }
+            __syncthreads();
+            stage(s, std::false_type{});
+            ++s;
+        }
+        at = (at + s) % kBuffers;
+
+        // the next tile, before this one's results
+        float *const this_w = to_w, *const this_b = to_b;
+        const int this_o0 = o0, this_c0 = c0;
+        number = round * gridDim.x + (round % 2 ? (int)gridDim.x - 1 - block : block);
+        // a block without a tile in this round has none in a later one: rounds are full but for the last
+        const bool again = number < all;
+        if (again) begin(number);
+        if (this_w) {
+            if (biased && lane < 32)
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+                    if (const int o = this_o0 + (wn * NT + j) * 32 + lane; o < a.out) this_b[o] = sum[j][0];
+            store_lines(reinterpret_cast<char *>(results[wave]), acc, lane, this_w, a.width, this_o0 + wn * NT * 32, a.out, this_c0 + wm * MT * 32,
+                        a.width, [](int) { return Chunk<float, 4>{{0.0f, 0.0f, 0.0f, 0.0f}}; }, [](float v) { return v; });
+        }
+        if (!again) break;
+    }
 }
 
 template <class T>
@@ -298,7 +369,7 @@ Status weight_grad_t(Context &cx, Args a, const RowsOf<T> &dy, const RowsOf<T> &
     MPNN_TRY(cx.rows_scratch(sizeof(float) * (size_t)(a.part_slots * slot_size(matrix + a.out)), &ws));
     a.part = static_cast<float *>(ws);
     if constexpr (std::is_same<T, bf16>::value)
-        if (wide) k_expert_weight_grad_wide<<<grid_xcd(pieces * a.tiles, 1), kWideThreads, 0, cx.stream>>>(a, dy, x);
+        if (wide) k_expert_weight_grad_wide<<<(unsigned)std::min<int64_t>(grid_xcd(std::min<int64_t>(pieces * a.tiles, kCus), 1), kCus), kWideThreads, 0, cx.stream>>>(a, dy, x);
     if (!wide) k_expert_weight_grad<T, 2, 2, 2, 2><<<grid_xcd(pieces * a.tiles, 1), 256, 0, cx.stream>>>(a, dy, x);
     MPNN_HIP(hipGetLastError());
     return a.part_slots ? join_pieces(cx, a.n_experts, a.n, a.rows, a.part_slots, matrix, a.out, a.offsets, a.part, a.dweight, a.dbias) : Status::ok();
