@@ -265,10 +265,7 @@ Status unpermute_rows(Context &cx, const float *sorted, int width, int stride, d
 // ---- routing.hip ----
 Status route_plan(Context &cx, int64_t n, int k, int n_experts, const int32_t *expert, int32_t *offsets, int32_t *source,
                   int32_t *position);
-// the same in scratch that the caller has taken, of so many bytes; position may be null
-size_t route_plan_scratch(int64_t pairs, int n_experts);
-Status route_plan_at(Context &cx, int64_t pairs, int n_experts, const int32_t *expert, int32_t *offsets, int32_t *source,
-                     int32_t *position, void *ws);
+Status embed_plan(Context &cx, int64_t n, int entries, const int32_t *index, int32_t *offsets, int32_t *source);
 Status route_scatter(Context &cx, int dtype, int64_t n, int k, int width, const void *x, int64_t ldx, const int32_t *position,
                      const int32_t *used, void *sorted);
 Status route_combine(Context &cx, int dtype, int64_t n, int k, int width, const void *sorted, const int32_t *position,
@@ -307,7 +304,6 @@ Status micro_save(Context &cx, int dtype, int64_t n, int width, const void *x, i
 Status micro_load(Context &cx, int dtype, int64_t n, int width, const uint8_t *codes, const uint8_t *scales, void *out);
 // ---- embed.hip ----
 Status embed(Context &cx, int dtype, int64_t n, int width, int entries, const int32_t *index, const void *table, float scale, void *out);
-Status embed_plan(Context &cx, int64_t n, int entries, const int32_t *index, int32_t *offsets, int32_t *source);
 Status embed_backward(Context &cx, int dtype, int64_t n, int width, int entries, const void *dout, int64_t ld, const int32_t *offsets,
                       const int32_t *source, float scale, float *dtable);
 

@@ -1,4 +1,4 @@
-// Rows sorted by expert and back (mpnn_route_*).  The pairs p = i k + s of row i and its slot s are ordered by
+// Rows sorted by expert and back (mpnn_route_*), and the order of embedding rows (mpnn_embed_plan).  The pairs p = i k + s of row i and its slot s are ordered by
 // expert with a stable counting sort; pairs whose expert is outside 0 .. E-1 keep a place after the last segment
 // (treated as expert E), so `source` and `position` are inverse permutations of all n k pairs and every index that
 // a kernel reads from them is one it can check against n k.
@@ -21,19 +21,46 @@ namespace {
 constexpr int kPlanThreads = 256;
 constexpr int kPlanWaves = kPlanThreads / 64;
 constexpr int kMaxBins = 1024 + 1;                         // experts and the dropped pairs
+constexpr int kDigit = 10;                                 // bits of an index that one sort takes
 
 __device__ __forceinline__ int bin_of(int e, int n_experts) { return (unsigned)e < (unsigned)n_experts ? e : n_experts; }
 
+// What a counting sort orders by: the experts of the pairs, or a digit of an embedding's indexes, of which `order` has those that
+// an earlier digit has put in order.
+struct ByExpert {
+    const int32_t *expert;
+    __device__ __forceinline__ int key(int64_t p) const { return expert[p]; }
+    __device__ __forceinline__ void placed(int64_t p, int q, int32_t *source, int32_t *position) const {
+        source[q] = (int32_t)p;
+        position[p] = q;
+    }
+};
+struct ByDigit {
+    const int32_t *index, *order;
+    int entries, shift;
+    int32_t *sorted;                       // the indexes in order (entries where one names none), or null
+    __device__ __forceinline__ int64_t row(int64_t p) const { return order ? order[p] : p; }
+    __device__ __forceinline__ int key(int64_t p) const {
+        const int v = index[row(p)];
+        return (unsigned)v < (unsigned)entries ? v >> shift & ((1 << kDigit) - 1) : -1;
+    }
+    __device__ __forceinline__ void placed(int64_t p, int q, int32_t *source, int32_t *) const {
+        const int64_t i = row(p);
+        source[q] = (int32_t)i;
+        if (sorted) sorted[q] = (unsigned)index[i] < (unsigned)entries ? index[i] : entries;
+    }
+};
+
 // counts[block][bin]: pairs of each bin among the block's 256 ITEMS ones (integer adds: the order does not matter)
-template <int ITEMS>
-__global__ __launch_bounds__(kPlanThreads) void k_route_count(const int32_t *__restrict__ expert, int64_t pairs, int n_experts,
+template <int ITEMS, class By>
+__global__ __launch_bounds__(kPlanThreads) void k_route_count(const By by, int64_t pairs, int n_experts,
                                                               int32_t *__restrict__ counts) {
     __shared__ int32_t h[kMaxBins];
     const int bins = n_experts + 1;
     const int64_t base = (int64_t)blockIdx.x * (kPlanThreads * ITEMS);
     int e[ITEMS];
 #pragma unroll
-    for (int j = 0; j < ITEMS; ++j) e[j] = expert[min(base + j * kPlanThreads + threadIdx.x, pairs - 1)];
+    for (int j = 0; j < ITEMS; ++j) e[j] = by.key(min(base + j * kPlanThreads + threadIdx.x, pairs - 1));
     for (int b = threadIdx.x; b < bins; b += kPlanThreads) h[b] = 0;
     __syncthreads();
 #pragma unroll
@@ -91,8 +118,8 @@ __global__ __launch_bounds__(1024) void k_route_scan(int32_t *__restrict__ count
 // The bins' totals and what earlier blocks hold of them: of one block from its own counts, of up to kSumCounts
 // counts from all blocks' counts, which every block adds up for itself (a launch less), else from k_route_scan (`total`).
 constexpr int kSumCounts = 16384;
-template <int ITEMS>
-__global__ __launch_bounds__(kPlanThreads) void k_route_place(const int32_t *__restrict__ expert, int64_t pairs, int n_experts,
+template <int ITEMS, class By>
+__global__ __launch_bounds__(kPlanThreads) void k_route_place(const By by, int64_t pairs, int n_experts,
                                                               const int32_t *__restrict__ counts, const int32_t *__restrict__ total,
                                                               int32_t *__restrict__ offsets, int32_t *__restrict__ source,
                                                               int32_t *__restrict__ position) {
@@ -108,7 +135,7 @@ __global__ __launch_bounds__(kPlanThreads) void k_route_place(const int32_t *__r
 #pragma unroll
     for (int j = 0; j < ITEMS; ++j) {
         const int64_t p = base + j * 64 + lane;
-        bin[j] = pairs > 0 ? expert[min(p, pairs - 1)] : 0;
+        bin[j] = pairs > 0 ? by.key(min(p, pairs - 1)) : 0;
     }
 #pragma unroll
     for (int j = 0; j < ITEMS; ++j) bin[j] = base + j * 64 + lane < pairs ? bin_of(bin[j], n_experts) : -1;
@@ -188,8 +215,7 @@ __global__ __launch_bounds__(kPlanThreads) void k_route_place(const int32_t *__r
         }
         if (bin[j] >= 0) {
             const int q = h[wave][bin[j]] + __popcll(same & ((1ull << lane) - 1));
-            source[q] = (int32_t)p;
-            if (position) position[p] = q;
+            by.placed(p, q, source, position);
             // the highest lane of the bin moves its start past this iteration's pairs
             if ((same >> lane) == 1) h[wave][bin[j]] = q + 1;
         }
@@ -336,15 +362,14 @@ template <int ITEMS> static int64_t plan_blocks(int64_t pairs) {
     return std::max<int64_t>(1, (pairs + kChunk - 1) / kChunk);
 }
 
-template <int ITEMS>
-static Status plan(Context &cx, int64_t pairs, int n_experts, const int32_t *expert, int32_t *offsets, int32_t *source,
-                   int32_t *position, void *ws) {
+template <int ITEMS, class By>
+static Status plan(Context &cx, int64_t pairs, int n_experts, const By &by, int32_t *offsets, int32_t *source, int32_t *position, void *ws) {
     const int64_t blocks = plan_blocks<ITEMS>(pairs);
     const int bins = n_experts + 1;
     int32_t *counts = nullptr, *total = nullptr;
     if (blocks > 1) {
         counts = static_cast<int32_t *>(ws);
-        k_route_count<ITEMS><<<(unsigned)blocks, kPlanThreads, 0, cx.stream>>>(expert, pairs, n_experts, counts);
+        k_route_count<ITEMS><<<(unsigned)blocks, kPlanThreads, 0, cx.stream>>>(by, pairs, n_experts, counts);
         MPNN_HIP(hipGetLastError());
         if (blocks * bins > kSumCounts) {
             total = counts + blocks * bins;
@@ -352,8 +377,7 @@ static Status plan(Context &cx, int64_t pairs, int n_experts, const int32_t *exp
             MPNN_HIP(hipGetLastError());
         }
     }
-    k_route_place<ITEMS><<<(unsigned)blocks, kPlanThreads, 0, cx.stream>>>(expert, pairs, n_experts, counts, total, offsets, source,
-                                                                           position);
+    k_route_place<ITEMS><<<(unsigned)blocks, kPlanThreads, 0, cx.stream>>>(by, pairs, n_experts, counts, total, offsets, source, position);
     MPNN_HIP(hipGetLastError());
     return Status::ok();
 }
@@ -362,22 +386,54 @@ static Status plan(Context &cx, int64_t pairs, int n_experts, const int32_t *exp
 // of them, for fewer counts.
 static bool many_pairs(int64_t pairs) { return pairs > (1 << 20); }
 
-size_t route_plan_scratch(int64_t pairs, int n_experts) {
+static size_t plan_scratch(int64_t pairs, int n_experts) {
     const int64_t blocks = many_pairs(pairs) ? plan_blocks<16>(pairs) : plan_blocks<4>(pairs);
     return blocks > 1 ? sizeof(int32_t) * (size_t)(n_experts + 1) * (size_t)(blocks + 1) : 0;
 }
 
-Status route_plan_at(Context &cx, int64_t pairs, int n_experts, const int32_t *expert, int32_t *offsets, int32_t *source,
-                     int32_t *position, void *ws) {
-    return many_pairs(pairs) ? plan<16>(cx, pairs, n_experts, expert, offsets, source, position, ws)
-                             : plan<4>(cx, pairs, n_experts, expert, offsets, source, position, ws);
+template <class By>
+static Status plan_by(Context &cx, int64_t pairs, int n_experts, const By &by, int32_t *offsets, int32_t *source, int32_t *position, void *ws) {
+    return many_pairs(pairs) ? plan<16>(cx, pairs, n_experts, by, offsets, source, position, ws)
+                             : plan<4>(cx, pairs, n_experts, by, offsets, source, position, ws);
 }
 
 Status route_plan(Context &cx, int64_t n, int k, int n_experts, const int32_t *expert, int32_t *offsets, int32_t *source,
                   int32_t *position) {
     void *ws = nullptr;
-    MPNN_TRY(cx.rows_scratch(route_plan_scratch(n * k, n_experts), &ws));
-    return route_plan_at(cx, n * k, n_experts, expert, offsets, source, position, ws);
+    MPNN_TRY(cx.rows_scratch(plan_scratch(n * k, n_experts), &ws));
+    return plan_by(cx, n * k, n_experts, ByExpert{expert}, offsets, source, position, ws);
+}
+
+// offsets[v]: the first place whose index is at least v
+static __global__ __launch_bounds__(256) void k_embed_offsets(int64_t n, int entries, const int32_t *__restrict__ sorted, int32_t *__restrict__ offsets) {
+    const int v = blockIdx.x * 256 + threadIdx.x;
+    if (v > entries) return;
+    int64_t low = 0, high = n;
+    while (low < high) {
+        const int64_t mid = (low + high) / 2;
+        if (sorted[mid] < v) low = mid + 1;
+        else high = mid;
+    }
+    offsets[v] = (int32_t)low;
+}
+
+// An embedding's order: one counting sort of up to 1,024 entries, else by the low ten bits of the index and then by the high
+// ones, rows of no entry last both times.
+Status embed_plan(Context &cx, int64_t n, int entries, const int32_t *index, int32_t *offsets, int32_t *source) {
+    void *ws = nullptr;
+    if (entries <= 1 << kDigit) {
+        MPNN_TRY(cx.rows_scratch(plan_scratch(n, entries), &ws));
+        return plan_by(cx, n, entries, ByDigit{index, nullptr, entries, 0, nullptr}, offsets, source, nullptr, ws);
+    }
+    const int high = ((entries - 1) >> kDigit) + 1;
+    const size_t counts = std::max(plan_scratch(n, 1 << kDigit), plan_scratch(n, high));
+    MPNN_TRY(cx.rows_scratch(counts + sizeof(int32_t) * (2 * (size_t)n + (1 << kDigit) + 1), &ws));
+    int32_t *const low = reinterpret_cast<int32_t *>(static_cast<char *>(ws) + counts), *const sorted = low + n, *const ends = sorted + n;
+    MPNN_TRY(plan_by(cx, n, 1 << kDigit, ByDigit{index, nullptr, entries, 0, nullptr}, ends, low, nullptr, ws));
+    MPNN_TRY(plan_by(cx, n, high, ByDigit{index, low, entries, kDigit, sorted}, ends, source, nullptr, ws));
+    k_embed_offsets<<<grid_for((int64_t)entries + 1), 256, 0, cx.stream>>>(n, entries, sorted, offsets);
+    MPNN_HIP(hipGetLastError());
+    return Status::ok();
 }
 
 // Slots that a kernel takes together, as a constant.
