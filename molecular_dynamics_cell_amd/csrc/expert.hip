@@ -99,14 +99,28 @@ __global__ __launch_bounds__(256, 2) void k_product(const Args a, const RowsOf<X
 
         Word<X> xv[XQ];
         Word<W> wv[XP];
+        // Loads of a stage have no conditions beside them but in the last stage, and in the last tile of weights across whose
+        // columns are no whole words.
+        const bool columns_whole = !ACROSS || c0 + BC <= a.columns || a.columns % 8 == 0;
+        const int at_column = ACROSS ? (columns_whole ? min(c0 + tid % WIDE * 8, a.columns - 8) : c0 + tid % WIDE * 8) : 0;
         auto fetch = [&](int k0) {
+            if (columns_whole && k0 + 8 * WORDS <= a.reduced) {
+#pragma unroll
+                for (int i = 0; i < XQ; ++i) RowsOf<X>::load(xv[i], xr[i], k0 + word * 8);
+#pragma unroll
+                for (int i = 0; i < XP; ++i) {
+                    if constexpr (ACROSS) RowsOf<W>::load(wv[i], w.row(w0 + k0 + tid / WIDE + i * AT_ONCE), at_column);
+                    else RowsOf<W>::load(wv[i], wr[i], k0 + word * 8);
+                }
+                return;
+            }
 #pragma unroll
             for (int i = 0; i < XQ; ++i) RowsOf<X>::load(xv[i], xr[i], k0 + word * 8, a.reduced);
 #pragma unroll
             for (int i = 0; i < XP; ++i) {
                 if constexpr (ACROSS) {
                     const int k = k0 + tid / WIDE + i * AT_ONCE;
-                    if (k < a.reduced) RowsOf<W>::load(wv[i], w.row(w0 + k), c0 + tid % WIDE * 8, a.columns);
+                    if (k < a.reduced) RowsOf<W>::load(wv[i], w.row(w0 + k), at_column, a.columns);
                     else wv[i].clear();
                 } else {
                     RowsOf<W>::load(wv[i], wr[i], k0 + word * 8, a.reduced);

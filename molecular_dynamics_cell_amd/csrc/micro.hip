@@ -17,7 +17,8 @@ namespace {
 
 constexpr int kLeast = 127 - 100;
 
-template <class T>
+// WHOLE: rows of whole chunks of eight columns, whose loads and stores then have no condition beside them.
+template <class T, bool WHOLE>
 __global__ __launch_bounds__(256) void k_micro_save(Items it, int width, const T *__restrict__ x, int64_t ld, uint8_t *__restrict__ codes,
                                                     uint8_t *__restrict__ scales) {
     constexpr int W = 8;
@@ -31,7 +32,8 @@ __global__ __launch_bounds__(256) void k_micro_save(Items it, int width, const T
     for (int u = 0; u < kUnroll; ++u) {
         if (u >= many) break;
         item_at<4>(it, block, u, row[u], c[u]);
-        v[u].load(x + row[u] * ld + c[u] * W, width - c[u] * W);
+        if (WHOLE) v[u].load(x + row[u] * ld + min(c[u] * W, width - W));
+        else v[u].load(x + row[u] * ld + c[u] * W, width - c[u] * W);
     }
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
@@ -40,7 +42,7 @@ __global__ __launch_bounds__(256) void k_micro_save(Items it, int width, const T
         float f[W];
 #pragma unroll
         for (int j = 0; j < W; ++j) {
-            f[j] = to_f32(v[u].v[j]);
+            f[j] = !WHOLE || c[u] * W < width ? to_f32(v[u].v[j]) : 0.0f;
             m = max(m, __float_as_uint(f[j]) & 0x7fffffffu);      // magnitudes order as integers, a NaN above infinity
         }
         m = max(m, __float_as_uint(dpp<0xb1>(__uint_as_float(m))));
@@ -59,7 +61,7 @@ __global__ __launch_bounds__(256) void k_micro_save(Items it, int width, const T
     }
 }
 
-template <class T>
+template <class T, bool WHOLE>
 __global__ __launch_bounds__(256) void k_micro_load(Items it, int width, const uint8_t *__restrict__ codes, const uint8_t *__restrict__ scales,
                                                     T *__restrict__ out) {
     const int64_t block = xcd_block();
@@ -91,7 +93,8 @@ __global__ __launch_bounds__(256) void k_micro_load(Items it, int width, const u
         two(std::integral_constant<int, 1>{});
         two(std::integral_constant<int, 2>{});
         two(std::integral_constant<int, 3>{});
-        o.store(out + row[u] * width + c[u] * 8, width - c[u] * 8);
+        if (WHOLE) o.store(out + row[u] * width + c[u] * 8);
+        else o.store(out + row[u] * width + c[u] * 8, width - c[u] * 8);
     }
 }
 
@@ -99,7 +102,8 @@ template <class T> Status save_t(Context &cx, int64_t n, int width, const T *x, 
     const int groups = (width + kMicroGroup - 1) / kMicroGroup;
     return by_launches(n, kLaunchBlocks * items_of(n, groups * 4).rows, [&](int64_t from, int64_t rows) -> Status {
         const Items it = items_of(rows, groups * 4);
-        k_micro_save<T><<<grid_of(it), 256, 0, cx.stream>>>(it, width, x + from * ld, ld, codes + from * groups * (kMicroGroup / 2),
+        auto *kernel = width % 8 ? k_micro_save<T, false> : k_micro_save<T, true>;
+        kernel<<<grid_of(it), 256, 0, cx.stream>>>(it, width, x + from * ld, ld, codes + from * groups * (kMicroGroup / 2),
                                                            scales + from * groups);
         MPNN_HIP(hipGetLastError());
         return Status::ok();
@@ -110,7 +114,8 @@ template <class T> Status load_t(Context &cx, int64_t n, int width, const uint8_
     const int groups = (width + kMicroGroup - 1) / kMicroGroup, per = (width + 7) / 8;
     return by_launches(n, kLaunchBlocks * items_of(n, per).rows, [&](int64_t from, int64_t rows) -> Status {
         const Items it = items_of(rows, per);
-        k_micro_load<T><<<grid_of(it), 256, 0, cx.stream>>>(it, width, codes + from * groups * (kMicroGroup / 2), scales + from * groups,
+        auto *kernel = width % 8 ? k_micro_load<T, false> : k_micro_load<T, true>;
+        kernel<<<grid_of(it), 256, 0, cx.stream>>>(it, width, codes + from * groups * (kMicroGroup / 2), scales + from * groups,
                                                            out + from * width);
         MPNN_HIP(hipGetLastError());
         return Status::ok();

@@ -108,6 +108,8 @@ template <class T> struct RowsOf {
         const T *p;
     };
     __device__ __forceinline__ Row row(int64_t i) const { return {p + i * ld}; }
+    // a word that is all the row's
+    __device__ __forceinline__ static void load(Word<T> &w, const Row &r, int c) { w.load(r.p + c); }
     // the word at column c of a row that has `width` of them (zeros past the end)
     __device__ __forceinline__ static void load(Word<T> &w, const Row &r, int c, int width) {
         const int in = width - c;
@@ -125,6 +127,9 @@ template <> struct RowsOf<Micro> {
     __device__ __forceinline__ Row row(int64_t i) const { return {codes + i * groups * (kMicroGroup / 2), scales + i * groups}; }
     __device__ __forceinline__ static void load(Word<Micro> &w, const Row &r, int c, int width) {
         if (c >= width) return w.clear();
+        load(w, r, c);
+    }
+    __device__ __forceinline__ static void load(Word<Micro> &w, const Row &r, int c) {
         __builtin_memcpy(&w.v, r.codes + c / 2, 4);
         w.scale = r.scales[c / kMicroGroup];
     }
