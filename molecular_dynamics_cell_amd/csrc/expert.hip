@@ -12,6 +12,8 @@ namespace mpnn {
 
 namespace {
 
+constexpr int kCus = 256;
+
 struct Args {
     int64_t n, first;               // rows; the launch's first block
     int reduced, columns;           // length of the products' sums; columns of the result
@@ -57,123 +59,150 @@ __device__ __forceinline__ void finish(const Args &a, int expert, int64_t q, int
     else store_four(static_cast<float *>(a.y) + q * a.columns + c, v, in);
 }
 
-// Tiles of 32 MT WM columns by 32 NT WN rows.  ACROSS: the weights' rows are the reduced axis (dx).
-template <class X, class W, bool ACROSS, int MT, int NT, int WM, int WN>
+// 128 x 128 results at a time, four waves of 64 x 64, any types, strides and alignments: words go through registers, where
+// fp32 is cut into terms and 4-bit codes become bf16.  A block stays for many tiles: the next one's first words are on
+// their way while this one's results are stored.  ACROSS: the weights' rows are the reduced axis (dx).
+constexpr int kTile = 128;
+template <class X, class W, bool ACROSS>
 __global__ __launch_bounds__(256, 2) void k_product(const Args a, const RowsOf<X> x, const RowsOf<W> w) {
-    constexpr int TP = kTerms<W>, TQ = kTerms<X>, WORDS = TP * TQ > 3 ? 4 : 8;
-    constexpr int BC = 32 * MT * WM, BR = 32 * NT * WN;
-    using P = std::conditional_t<ACROSS, Across<TP, BC, WORDS>, Along<TP, BC, WORDS>>;
-    using Q = Along<TQ, BR, WORDS>;
+    constexpr int TP = kTerms<W>, TQ = kTerms<X>, WORDS = TP * TQ > 1 ? 4 : 8, STAGE = 8 * WORDS, MT = 2, NT = 2;
+    using P = std::conditional_t<ACROSS, Across<TP, kTile, WORDS>, Along<TP, kTile, WORDS>>;
+    using Q = Along<TQ, kTile, WORDS>;
     __shared__ uint4 lds[P::kWords + Q::kWords];
+    __shared__ uint4 results[4][kStoreBytes / 16];
+    __shared__ Segments table;
     uint4 *const lp = lds, *const lq = lds + P::kWords;
-
-    const int64_t number = a.first + xcd_block();
-    const Tile tile = find_tile(a.offsets, a.n_experts, a.n, BR, number / a.tiles_c);
-    if (tile.from >= tile.to) return;
-    const int c0 = (int)(number % a.tiles_c) * BC;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, wm = wave / WN, wn = wave % WN;
-
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), wm = wave >> 1, wn = wave & 1;
+    if (wave == 0) table.fill(a.offsets, a.n_experts, a.n, kTile);
+    __syncthreads();
+    const int64_t tiles = table.tiles(a.n_experts) * a.tiles_c;
     const auto place = [&](int64_t q) -> int64_t {
         if (!a.source) return q;
         return min((int64_t)((uint32_t)max(a.source[q], 0) / (uint32_t)a.slots), a.n_x - 1);
     };
-    floatx16 acc[MT][NT];
-#pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int j = 0; j < NT; ++j) acc[i][j] = (floatx16)(0.0f);
-    float largest = 0.0f;
-    if (tile.expert >= 0) {
-        constexpr int XQ = BR * WORDS / 256, XP = BC * WORDS / 256;
-        typename RowsOf<X>::Row xr[XQ];
-        typename RowsOf<W>::Row wr[ACROSS ? 1 : XP];
-        const int word = tid % WORDS, row = tid / WORDS;
-        constexpr int STEP = 256 / WORDS;
-#pragma unroll
-        for (int i = 0; i < XQ; ++i) xr[i] = x.row(place(min(tile.from + row + i * STEP, tile.to - 1)));
-        const int64_t w0 = (int64_t)tile.expert * (ACROSS ? a.reduced : a.columns);
-        if constexpr (!ACROSS)
-#pragma unroll
-            for (int i = 0; i < XP; ++i) wr[i] = w.row(w0 + min(c0 + row + i * STEP, a.columns - 1));
-        constexpr int WIDE = BC / 8, AT_ONCE = 256 / WIDE;      // words of a weight row, weight rows at once
 
-        Word<X> xv[XQ];
-        Word<W> wv[XP];
-        // Loads of a stage have no conditions beside them but in the last stage, and in the last tile of weights across whose
-        // columns are no whole words.
-        const bool columns_whole = !ACROSS || c0 + BC <= a.columns || a.columns % 8 == 0;
-        const int at_column = ACROSS ? (columns_whole ? min(c0 + tid % WIDE * 8, a.columns - 8) : c0 + tid % WIDE * 8) : 0;
-        auto fetch = [&](int k0) {
-            if (columns_whole && k0 + 8 * WORDS <= a.reduced) {
+    // The tile whose words are being loaded.
+    constexpr int EACH = kTile * WORDS / 256, STEP = 256 / WORDS, WIDE = kTile / 8, AT_ONCE = 256 / WIDE;   // (of weight rows across: words, rows at once)
+    const int word = tid % WORDS, row = tid / WORDS;
+    Tile tile;
+    int c0 = 0, at_column = 0;
+    bool columns_whole = true;
+    int64_t w0 = 0;
+    typename RowsOf<X>::Row xr[EACH];
+    typename RowsOf<W>::Row wr[ACROSS ? 1 : EACH];
+    Word<X> xv[EACH];
+    Word<W> wv[EACH];
+    // Loads of a stage have no conditions beside them but in the last stage, and in the last tile of weights across whose
+    // columns are no whole words.
+    const auto fetch = [&](int k0) {
+        if (columns_whole && k0 + STAGE <= a.reduced) {
 #pragma unroll
-                for (int i = 0; i < XQ; ++i) RowsOf<X>::load(xv[i], xr[i], k0 + word * 8);
+            for (int i = 0; i < EACH; ++i) RowsOf<X>::load(xv[i], xr[i], k0 + word * 8);
 #pragma unroll
-                for (int i = 0; i < XP; ++i) {
-                    if constexpr (ACROSS) RowsOf<W>::load(wv[i], w.row(w0 + k0 + tid / WIDE + i * AT_ONCE), at_column);
-                    else RowsOf<W>::load(wv[i], wr[i], k0 + word * 8);
-                }
-                return;
+            for (int i = 0; i < EACH; ++i) {
+                if constexpr (ACROSS) RowsOf<W>::load(wv[i], w.row(w0 + k0 + tid / WIDE + i * AT_ONCE), at_column);
+                else RowsOf<W>::load(wv[i], wr[i], k0 + word * 8);
             }
+            return;
+        }
 #pragma unroll
-            for (int i = 0; i < XQ; ++i) RowsOf<X>::load(xv[i], xr[i], k0 + word * 8, a.reduced);
+        for (int i = 0; i < EACH; ++i) RowsOf<X>::load(xv[i], xr[i], k0 + word * 8, a.reduced);
 #pragma unroll
-            for (int i = 0; i < XP; ++i) {
-                if constexpr (ACROSS) {
-                    const int k = k0 + tid / WIDE + i * AT_ONCE;
-                    if (k < a.reduced) RowsOf<W>::load(wv[i], w.row(w0 + k), at_column, a.columns);
-                    else wv[i].clear();
-                } else {
-                    RowsOf<W>::load(wv[i], wr[i], k0 + word * 8, a.reduced);
-                }
+        for (int i = 0; i < EACH; ++i) {
+            if constexpr (ACROSS) {
+                const int k = k0 + tid / WIDE + i * AT_ONCE;
+                if (k < a.reduced) RowsOf<W>::load(wv[i], w.row(w0 + k), at_column, a.columns);
+                else wv[i].clear();
+            } else {
+                RowsOf<W>::load(wv[i], wr[i], k0 + word * 8, a.reduced);
             }
-        };
+        }
+    };
+    const auto begin = [&](int64_t number) {
+        tile = table.find(a.offsets, a.n_experts, a.n, kTile, (int)(number / a.tiles_c));
+        c0 = (int)(number % a.tiles_c) * kTile;
+        if (tile.expert < 0) return;
+        w0 = (int64_t)tile.expert * (ACROSS ? a.reduced : a.columns);
+#pragma unroll
+        for (int i = 0; i < EACH; ++i) xr[i] = x.row(place(min(tile.from + row + i * STEP, tile.to - 1)));
+        if constexpr (ACROSS) {
+            columns_whole = c0 + kTile <= a.columns || a.columns % 8 == 0;
+            at_column = c0 + tid % WIDE * 8;
+            if (columns_whole) at_column = min(at_column, a.columns - 8);
+        } else {
+#pragma unroll
+            for (int i = 0; i < EACH; ++i) wr[i] = w.row(w0 + min(c0 + row + i * STEP, a.columns - 1));
+        }
         fetch(0);
-        for (int k0 = 0; k0 < a.reduced; k0 += 8 * WORDS) {
+    };
+
+    // blocks of an XCD take neighbouring tiles
+    int64_t number = (int64_t)(blockIdx.x % kXcds) * (gridDim.x / kXcds) + blockIdx.x / kXcds;
+    if (number >= tiles) return;
+    begin(number);
+    while (true) {
+        floatx16 acc[MT][NT];
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int j = 0; j < NT; ++j) acc[i][j] = (floatx16)(0.0f);
+        float largest = 0.0f;
+        for (int k0 = 0; k0 < a.reduced && tile.expert >= 0; k0 += STAGE) {
             __syncthreads();
 #pragma unroll
-            for (int i = 0; i < XQ; ++i) {
+            for (int i = 0; i < EACH; ++i) {
                 uint4 t[TQ];
                 xv[i].terms(t, largest);
                 Q::store(lq, row + i * STEP, word, t);
             }
 #pragma unroll
-            for (int i = 0; i < XP; ++i) {
+            for (int i = 0; i < EACH; ++i) {
                 uint4 t[TP];
                 wv[i].terms(t, largest);
                 if constexpr (ACROSS) P::store(lp, tid / WIDE + i * AT_ONCE, tid % WIDE, t);
                 else P::store(lp, row + i * STEP, word, t);
             }
             __syncthreads();
-            if (k0 + 8 * WORDS < a.reduced) fetch(k0 + 8 * WORDS);
+            if (k0 + STAGE < a.reduced) fetch(k0 + STAGE);
             multiply<P, Q, TP, TQ, MT, NT, WORDS>(lp, lq, wm * MT * 32, wn * NT * 32, lane, acc);
         }
-    }
-    const bool huge = TP + TQ > 2 && __syncthreads_or(largest >= kHuge);
+        const bool huge = TP + TQ > 2 && __syncthreads_or(largest >= kHuge);
 
-    // a lane has four neighbouring columns of a row in four registers
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-        const int64_t q = tile.from + (wn * NT + j) * 32 + (lane & 31);
-        if (q >= tile.to) continue;
-#pragma unroll
-        for (int i = 0; i < MT; ++i)
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                const int c = c0 + (wm * MT + i) * 32 + 8 * g + 4 * (lane >> 5), in = a.columns - c;
-                if (in <= 0) continue;
-                float v[4];
-#pragma unroll
-                for (int r = 0; r < 4; ++r) v[r] = acc[i][j][4 * g + r];
-                if (huge && tile.expert >= 0)
-                    for (int r = 0; r < 4; ++r)
-                        if (v[r] != v[r] && r < in) {
-                            const int64_t w0 = (int64_t)tile.expert * (ACROSS ? a.reduced : a.columns), from = place(q);
-                            float s = 0.0f;
-                            for (int k = 0; k < a.reduced; ++k) s = fmaf(x.at(from, k), ACROSS ? w.at(w0 + k, c + r) : w.at(w0 + c + r, k), s);
-                            v[r] = s;
-                        }
-                finish(a, tile.expert, q, c, in, v);
+        // the next tile, before this one's results
+        const Tile done = tile;
+        const int done_c0 = c0;
+        number += gridDim.x;
+        const bool again = number < tiles;
+        if (again) begin(number);
+
+        const bool act = a.act == MPNN_ACT_SILU, biased = a.bias && done.expert >= 0;      // silu(0) = 0: rows of no expert may take it too
+        const auto out = [&](auto *y) {
+            const auto bias = [&](int c) {
+                Chunk<float, 4> b = {{0.0f, 0.0f, 0.0f, 0.0f}};
+                if (biased) b.load(a.bias + (int64_t)done.expert * a.columns + c, a.columns - c);
+                return b;
+            };
+            store_lines(reinterpret_cast<char *>(results[wave]), acc, lane, y, a.columns, done.from + wn * NT * 32, done.to, done_c0 + wm * MT * 32,
+                        a.columns, bias, [&](float v) { return act ? silu(v) : v; });
+            if (!huge) return;
+            // results that are not numbers, once more without terms
+            __syncthreads();
+            for (int e = tid; e < kTile * kTile; e += 256) {
+                const int64_t q = done.from + e / kTile;
+                const int c = done_c0 + e % kTile;
+                if (q >= done.to || c >= a.columns) continue;
+                const float was = to_f32(y[q * a.columns + c]);
+                if (was == was) continue;
+                const int64_t weights = (int64_t)done.expert * (ACROSS ? a.reduced : a.columns), from = place(q);
+                float s = 0.0f;
+                for (int k = 0; k < a.reduced; ++k) s = fmaf(x.at(from, k), ACROSS ? w.at(weights + k, c) : w.at(weights + c, k), s);
+                if (biased) s += a.bias[(int64_t)done.expert * a.columns + c];
+                y[q * a.columns + c] = from_f32<std::remove_pointer_t<decltype(y)>>(act ? silu(s) : s);
             }
+        };
+        if (a.y_bf16) out(static_cast<bf16 *>(a.y));
+        else out(static_cast<float *>(a.y));
+        if (!again) break;
     }
 }
 
@@ -202,8 +231,7 @@ template <> struct WideOp<Micro> {
 // passing through registers, two stages ahead.  A block stays for many tiles: the next one's first stages are on their way
 // while this one's results are stored.  (One block a CU: without that a tile of 2,048 columns takes 29 us of products and
 // 23 us to find its rows, wait for the first of them and store its results.)
-constexpr int kWide = 256, kWideWords = 4, kBuffers = 3, kWideThreads = 512, kCus = 256;
-constexpr int kSegments = 1024 + 2;                // experts and the rows of none
+constexpr int kWide = 256, kWideWords = 4, kBuffers = 3, kWideThreads = 512;
 using WideTile = Along<1, kWide, kWideWords>;
 
 // ACROSS (bf16): the weights' rows are the reduced axis; a stage is 32 of them, 512 bytes each.
@@ -217,35 +245,15 @@ __global__ __launch_bounds__(kWideThreads, 2) void k_product_wide(const Args a, 
     __shared__ uint4 lds[kBuffers * BOTH];
     __shared__ uint32_t scales[MICRO ? kBuffers : 1][2][MICRO ? kWide : 1];
     __shared__ uint4 results[kWideThreads / 64][kStoreBytes / 16];
-    __shared__ int first[kSegments + 1], start[kSegments];             // of each segment, its first tile and row
+    __shared__ Segments table;
     typedef const __attribute__((address_space(1))) void *Global;
     typedef __attribute__((address_space(3))) void *Local;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wm = wave & 1, wn = wave >> 1;
 
     [[maybe_unused]] const Pairs pairs(lane);
-    const int segments = a.n_experts + 2;
-    if (wave == 0) {
-        int before = 0;
-        for (int base = 0; base < segments; base += 64) {
-            int64_t from, to;
-            segment_of(a.offsets, a.n_experts, a.n, base + lane, from, to);
-            const int c = (int)((to - from + kWide - 1) / kWide);
-            int s = c;
-#pragma unroll
-            for (int d = 1; d < 64; d <<= 1) {
-                const int t = __shfl_up(s, d);
-                if (lane >= d) s += t;
-            }
-            if (base + lane < segments) {
-                first[base + lane] = before + s - c;
-                start[base + lane] = (int)from;
-            }
-            before += __builtin_amdgcn_readlane(s, 63);
-        }
-        if (lane == 0) first[segments] = before;
-    }
+    if (wave == 0) table.fill(a.offsets, a.n_experts, a.n, kWide);
     __syncthreads();
-    const int64_t tiles = (int64_t)first[segments] * a.tiles_c;
+    const int64_t tiles = table.tiles(a.n_experts) * a.tiles_c;
 
     const auto place = [&](int64_t q) -> int64_t {
         if (!a.source) return q;
@@ -287,19 +295,11 @@ __global__ __launch_bounds__(kWideThreads, 2) void k_product_wide(const Args a, 
     };
     const auto store_scales = [&](int buffer) { scales[buffer][threadIdx.x >> 8][threadIdx.x & 255] = next_scales; };
     const auto begin = [&](int64_t number) {
-        const int t = (int)(number / a.tiles_c);
-        int low = 0, high = segments - 1;          // the last segment whose first tile is at most t
-        while (low < high) {
-            const int mid = (low + high + 1) / 2;
-            if (first[mid] <= t) low = mid;
-            else high = mid - 1;
-        }
-        expert = __builtin_amdgcn_readfirstlane(low < a.n_experts ? low : -1);
-        c0 = __builtin_amdgcn_readfirstlane((int)(number % a.tiles_c) * kWide);
-        from = __builtin_amdgcn_readfirstlane(start[low] + (t - first[low]) * kWide);
-        int64_t f, e;
-        segment_of(a.offsets, a.n_experts, a.n, low, f, e);
-        to = min((int64_t)__builtin_amdgcn_readfirstlane((int)e), from + kWide);
+        const Tile tile = table.find(a.offsets, a.n_experts, a.n, kWide, (int)(number / a.tiles_c));
+        expert = tile.expert;
+        from = tile.from;
+        to = tile.to;
+        c0 = (int)(number % a.tiles_c) * kWide;
         if (expert < 0) return;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -635,6 +635,9 @@ template <class F> Status by_tiles(Args &a, int columns, int rows, F run) {
     });
 }
 
+// Blocks that stay for many tiles: as many as run at once, or as there are tiles.
+inline unsigned resident(int64_t tiles, int64_t most) { return grid_xcd(std::min(tiles, most), 1); }
+
 // Rows that start on 16 bytes, as the loads to LDS need them.
 inline bool whole_words(const void *p, int64_t row_bytes) { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && row_bytes % 16 == 0; }
 inline bool wide_fits(const RowsOf<bf16> &x, const RowsOf<bf16> &w) { return whole_words(x.p, 2 * x.ld) && whole_words(w.p, 2 * w.ld); }
@@ -646,8 +649,7 @@ Status product_t(Context &cx, Args a, const RowsOf<X> &x, const RowsOf<W> &w) {
     if constexpr (std::is_same<X, W>::value && !std::is_same<X, float>::value) {
         if (a.columns > 128 && rows > 32 && wide_fits(x, w)) {
             a.tiles_c = (a.columns + kWide - 1) / kWide;
-            const int64_t tiles = row_tiles(a.n, a.n_experts, kWide) * a.tiles_c;
-            k_product_wide<X, ACROSS><<<(unsigned)std::min<int64_t>(grid_xcd(std::min<int64_t>(tiles, kCus), 1), kCus), kWideThreads, 0, cx.stream>>>(a, x, w);
+            k_product_wide<X, ACROSS><<<resident(row_tiles(a.n, a.n_experts, kWide) * a.tiles_c, kCus), kWideThreads, 0, cx.stream>>>(a, x, w);
             MPNN_HIP(hipGetLastError());
             return Status::ok();
         }
@@ -666,7 +668,10 @@ Status product_t(Context &cx, Args a, const RowsOf<X> &x, const RowsOf<W> &w) {
             return few(std::integral_constant<int, 2>{});
         }
     }
-    return by_tiles(a, 128, 128, [&](unsigned grid) { k_product<X, W, ACROSS, 2, 2, 2, 2><<<grid, 256, 0, cx.stream>>>(a, x, w); });
+    a.tiles_c = (a.columns + kTile - 1) / kTile;
+    k_product<X, W, ACROSS><<<resident(row_tiles(a.n, a.n_experts, kTile) * a.tiles_c, 2 * kCus), 256, 0, cx.stream>>>(a, x, w);
+    MPNN_HIP(hipGetLastError());
+    return Status::ok();
 }
 
 }  // namespace

@@ -328,6 +328,47 @@ __device__ __forceinline__ Tile find_tile(const int32_t *offsets, int n_experts,
     }
     return Tile{-1, 0, 0};
 }
+// The same for blocks that take many tiles: of each segment its first tile and row, in LDS.
+constexpr int kSegments = 1024 + 2;
+struct Segments {
+    int first[kSegments + 1], start[kSegments];
+    // by the first wave; the others see it after a barrier
+    __device__ __forceinline__ void fill(const int32_t *offsets, int n_experts, int64_t n, int rows) {
+        const int lane = threadIdx.x & 63, segments = n_experts + 2;
+        int before = 0;
+        for (int base = 0; base < segments; base += 64) {
+            int64_t from, to;
+            segment_of(offsets, n_experts, n, base + lane, from, to);
+            const int c = (int)((to - from + rows - 1) / rows);
+            int s = c;
+#pragma unroll
+            for (int d = 1; d < 64; d <<= 1) {
+                const int t = __shfl_up(s, d);
+                if (lane >= d) s += t;
+            }
+            if (base + lane < segments) {
+                first[base + lane] = before + s - c;
+                start[base + lane] = (int)from;
+            }
+            before += __builtin_amdgcn_readlane(s, 63);
+        }
+        if (lane == 0) first[segments] = before;
+    }
+    __device__ __forceinline__ int64_t tiles(int n_experts) const { return first[n_experts + 2]; }
+    __device__ __forceinline__ Tile find(const int32_t *offsets, int n_experts, int64_t n, int rows, int tile) const {
+        int low = 0, high = n_experts + 1;         // the last segment whose first tile is at most this one
+        while (low < high) {
+            const int mid = (low + high + 1) / 2;
+            if (first[mid] <= tile) low = mid;
+            else high = mid - 1;
+        }
+        low = __builtin_amdgcn_readfirstlane(low);
+        const int64_t from = __builtin_amdgcn_readfirstlane(start[low] + (tile - first[low]) * rows);
+        int64_t f, e;
+        segment_of(offsets, n_experts, n, low, f, e);
+        return Tile{low < n_experts ? low : -1, from, min(e, from + rows)};
+    }
+};
 // At most so many row tiles: one short one for each expert that has rows, and for the two outer segments.
 inline int64_t row_tiles(int64_t n, int n_experts, int rows) { return n / rows + std::min<int64_t>(n, n_experts) + 2; }
 
