@@ -136,11 +136,10 @@ __global__ __launch_bounds__(256, 2) void k_product(const Args a, const RowsOf<X
         fetch(0);
     };
 
-    // blocks of an XCD take neighbouring tiles
-    int64_t number = (int64_t)(blockIdx.x % kXcds) * (gridDim.x / kXcds) + blockIdx.x / kXcds;
-    if (number >= tiles) return;
+    int64_t number = tile_in_round(0, blockIdx.x, tiles);
+    if (number < 0) return;
     begin(number);
-    while (true) {
+    for (int64_t round = 1;; ++round) {
         floatx16 acc[MT][NT];
 #pragma unroll
         for (int i = 0; i < MT; ++i)
@@ -171,8 +170,8 @@ __global__ __launch_bounds__(256, 2) void k_product(const Args a, const RowsOf<X
         // the next tile, before this one's results
         const Tile done = tile;
         const int done_c0 = c0;
-        number += gridDim.x;
-        const bool again = number < tiles;
+        number = tile_in_round(round, blockIdx.x, tiles);
+        const bool again = number >= 0;
         if (again) begin(number);
 
         const bool act = a.act == MPNN_ACT_SILU, biased = a.bias && done.expert >= 0;      // silu(0) = 0: rows of no expert may take it too
@@ -325,11 +324,10 @@ __global__ __launch_bounds__(kWideThreads, 2) void k_product_wide(const Args a, 
         }
     };
 
-    // blocks of an XCD take neighbouring tiles
-    int64_t number = (int64_t)(blockIdx.x % kXcds) * (gridDim.x / kXcds) + blockIdx.x / kXcds;
-    if (number >= tiles) return;
+    int64_t number = tile_in_round(0, blockIdx.x, tiles);
+    if (number < 0) return;
     begin(number);
-    while (true) {
+    for (int64_t round = 1;; ++round) {
         floatx16 acc[MT][NT];
 #pragma unroll
         for (int i = 0; i < MT; ++i)
@@ -427,8 +425,8 @@ __global__ __launch_bounds__(kWideThreads, 2) void k_product_wide(const Args a, 
         // the next tile, before this one's results
         const int this_expert = expert, this_c0 = c0;
         const int64_t this_from = from, this_to = to;
-        number += gridDim.x;
-        const bool again = number < tiles;
+        number = tile_in_round(round, blockIdx.x, tiles);
+        const bool again = number >= 0;
         if (again) begin(number);
 
         const auto out = [&](auto *y) {
@@ -460,6 +458,7 @@ template <> struct FewOp<bf16, bf16> {
     static constexpr int kPer = 8, kWords = 4;
     struct Raw {
         Word<bf16> v;
+        template <class R> __device__ __forceinline__ void load(const R &r, int k) { RowsOf<bf16>::load(v, r, k); }
         template <class R> __device__ __forceinline__ void load(const R &r, int k, int width) { RowsOf<bf16>::load(v, r, k, width); }
         __device__ __forceinline__ bf16x8 operand() const { return __builtin_bit_cast(bf16x8, make_uint4(v.v[0], v.v[1], v.v[2], v.v[3])); }
     };
@@ -473,6 +472,7 @@ template <> struct FewOp<float, float> {       // fp32 matrix cores: few rows le
     static constexpr int kPer = 8, kWords = 4;
     struct Raw {
         Word<float> v;
+        template <class R> __device__ __forceinline__ void load(const R &r, int k) { RowsOf<float>::load(v, r, k); }
         template <class R> __device__ __forceinline__ void load(const R &r, int k, int width) { RowsOf<float>::load(v, r, k, width); }
     };
     using RawX = Raw;
@@ -489,7 +489,9 @@ struct FewMicro {                               // a whole group
     __device__ __forceinline__ void load(const RowsOf<Micro>::Row &r, int k, int width) {
         v = make_uint4(0, 0, 0, 0);
         scale = 127;
-        if (k >= width) return;
+        if (k < width) load(r, k);
+    }
+    __device__ __forceinline__ void load(const RowsOf<Micro>::Row &r, int k) {
         __builtin_memcpy(&v, r.codes + k / 2, 16);
         scale = r.scales[k / kMicroGroup];
     }
@@ -499,6 +501,10 @@ template <class T> struct FewRows {             // 32 columns of rows that are n
     template <class R> __device__ __forceinline__ void load(const R &r, int k, int width) {
 #pragma unroll
         for (int u = 0; u < 4; ++u) RowsOf<T>::load(v[u], r, k + 8 * u, width);
+    }
+    template <class R> __device__ __forceinline__ void load(const R &r, int k) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) RowsOf<T>::load(v[u], r, k + 8 * u);
     }
 };
 template <> struct FewOp<Micro, Micro> {
@@ -559,7 +565,7 @@ __global__ __launch_bounds__(kFewThreads) void k_product_few(const Args a, int s
     using Op = FewOp<X, W>;
     constexpr int STRIDE = 4 * Op::kWords * Op::kPer;                  // of the reduced axis, a wave at once
     __shared__ floatx4 sums[kFewWaves][NT][64];
-    const int64_t number = a.first + xcd_block();
+    const int64_t number = a.first + blockIdx.x;       // (the last row tiles may be none: all XCDs have their share of the others)
     const Tile tile = find_tile(a.offsets, a.n_experts, a.n, 16 * NT, number / a.tiles_c);
     if (tile.from >= tile.to) return;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), part = wave % split;
@@ -582,6 +588,15 @@ __global__ __launch_bounds__(kFewThreads) void k_product_few(const Args a, int s
         typename Op::RawX xv[2][NT][Op::kWords];
         const auto fetch = [&](int turn, int b) {
             const int k = turn * STRIDE + (lane >> 4) * (Op::kWords * Op::kPer);
+            if ((turn + 1) * STRIDE <= a.reduced) {      // whole words, no conditions beside the loads
+#pragma unroll
+                for (int u = 0; u < Op::kWords; ++u) wv[b][u].load(wr, k + u * Op::kPer);
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                    for (int u = 0; u < Op::kWords; ++u) xv[b][j][u].load(xr[j], k + u * Op::kPer);
+                return;
+            }
 #pragma unroll
             for (int u = 0; u < Op::kWords; ++u) wv[b][u].load(wr, k + u * Op::kPer, a.reduced);
 #pragma unroll

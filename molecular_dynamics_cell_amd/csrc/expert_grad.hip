@@ -271,10 +271,8 @@ __global__ __launch_bounds__(kWideThreads, 2) void k_expert_weight_grad_wide(con
         }
     };
 
-    // blocks of an XCD take neighbouring tiles
-    const int block = (int)(blockIdx.x % kXcds * (gridDim.x / kXcds) + blockIdx.x / kXcds);
-    int64_t number = block;
-    if (number >= all) return;
+    int64_t number = tile_in_round(0, blockIdx.x, all);
+    if (number < 0) return;
     begin(number);
     for (int64_t round = 1;; ++round) {
         floatx16 acc[MT][NT], sum[NT];
@@ -347,9 +345,8 @@ __global__ __launch_bounds__(kWideThreads, 2) void k_expert_weight_grad_wide(con
         // the next tile, before this one's results
         float *const this_w = to_w, *const this_b = to_b;
         const int this_o0 = o0, this_c0 = c0;
-        number = round * gridDim.x + (round % 2 ? (int)gridDim.x - 1 - block : block);
-        // a block without a tile in this round has none in a later one: rounds are full but for the last
-        const bool again = number < all;
+        number = tile_in_round(round, round % 2 ? gridDim.x - 1 - blockIdx.x : blockIdx.x, all);
+        const bool again = number >= 0;            // a block without a tile in this round has none in a later one
         if (again) begin(number);
         if (this_w) {
             if (biased && lane < 32)

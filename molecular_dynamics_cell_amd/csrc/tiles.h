@@ -369,6 +369,13 @@ struct Segments {
         return Tile{low < n_experts ? low : -1, from, min(e, from + rows)};
     }
 };
+// The tile that block `block` of a grid of whole eighths takes in a round, or -1: neighbouring tiles on one XCD, and those of a
+// round that is not full on all XCDs alike.
+__device__ __forceinline__ int64_t tile_in_round(int64_t round, int block, int64_t tiles) {
+    const int64_t base = round * gridDim.x;
+    const int left = (int)min(tiles - base, (int64_t)gridDim.x), per = (left + kXcds - 1) / kXcds, i = block / kXcds, at = block % kXcds * per + i;
+    return left > 0 && i < per && at < left ? base + at : -1;
+}
 // At most so many row tiles: one short one for each expert that has rows, and for the two outer segments.
 inline int64_t row_tiles(int64_t n, int n_experts, int rows) { return n / rows + std::min<int64_t>(n, n_experts) + 2; }
 
