@@ -660,27 +660,31 @@ inline bool wide_fits(const RowsOf<Micro> &x, const RowsOf<Micro> &w) { return w
 
 template <class X, class W, bool ACROSS>
 Status product_t(Context &cx, Args a, const RowsOf<X> &x, const RowsOf<W> &w) {
-    const int64_t rows = (a.n + std::min<int64_t>(a.n, a.n_experts) - 1) / std::min<int64_t>(a.n, a.n_experts);    // of an expert
-    if constexpr (std::is_same<X, W>::value && !std::is_same<X, float>::value) {
-        if (a.columns > 128 && rows > 32 && wide_fits(x, w)) {
-            a.tiles_c = (a.columns + kWide - 1) / kWide;
-            k_product_wide<X, ACROSS><<<resident(row_tiles(a.n, a.n_experts, kWide) * a.tiles_c, kCus), kWideThreads, 0, cx.stream>>>(a, x, w);
-            MPNN_HIP(hipGetLastError());
-            return Status::ok();
-        }
-    }
+    // Few results: straight from memory.  Its time goes with the rows that every 16 columns read again, a tile's with the length
+    // of its sums, so the sides meet at a number of results: 512 rows of eight experts 2048 -> 1024 bf16 30 us and 40 in tiles,
+    // 640 rows 46 and 41; fp32 73 and 118, 800 rows 126 and 118; 200 rows 4096 -> 4096 fp32 199 and 227, 400 rows 370 and 233.
     if constexpr (!ACROSS) {
-        if (rows <= 64) {
+        constexpr bool both32 = std::is_same<X, float>::value && std::is_same<W, float>::value;
+        if (a.n * a.columns <= (both32 ? 768 << 10 : 512 << 10)) {
             int split = 1;
             while (split < kFewWaves && split * 4 * FewOp<X, W>::kWords * FewOp<X, W>::kPer < a.reduced) split *= 2;
             const auto few = [&](auto nt) {
                 return by_tiles(a, 16 * (kFewWaves / split), 16 * nt(), [&](unsigned grid) { k_product_few<X, W, nt()><<<grid, kFewThreads, 0, cx.stream>>>(a, split, x, w); });
             };
+            const int64_t rows = (a.n + std::min<int64_t>(a.n, a.n_experts) - 1) / std::min<int64_t>(a.n, a.n_experts);    // of an expert
             if (rows <= 16) return few(std::integral_constant<int, 1>{});
             // four row groups of operands fit the registers where both sides have the same 16-bit or smaller type
             if constexpr (std::is_same<X, W>::value && !std::is_same<X, float>::value)
                 if (rows > 32) return few(std::integral_constant<int, 4>{});
             return few(std::integral_constant<int, 2>{});
+        }
+    }
+    if constexpr (std::is_same<X, W>::value && !std::is_same<X, float>::value) {
+        if (a.columns > kTile && wide_fits(x, w)) {
+            a.tiles_c = (a.columns + kWide - 1) / kWide;
+            k_product_wide<X, ACROSS><<<resident(row_tiles(a.n, a.n_experts, kWide) * a.tiles_c, kCus), kWideThreads, 0, cx.stream>>>(a, x, w);
+            MPNN_HIP(hipGetLastError());
+            return Status::ok();
         }
     }
     a.tiles_c = (a.columns + kTile - 1) / kTile;
