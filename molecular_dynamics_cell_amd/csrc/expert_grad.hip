@@ -56,28 +56,36 @@ __global__ __launch_bounds__(256, 2) void k_expert_weight_grad(const Args a, con
             at[i] = a.source ? (int32_t)min((int64_t)((uint32_t)max(a.source[q], 0) / (uint32_t)a.slots), a.n_x - 1) : (int32_t)q;
         }
     };
-    // Loads of a stage have no conditions beside them but in a piece's last stage, and in the last tiles of columns that are no
-    // whole words.
+    // A stage of whole words has no conditions beside its loads; nor has another one where eight rows follow those that a wave
+    // loads, so that words may be loaded past a row's end.
     const bool columns_whole = (c0 + BC <= a.width || a.width % 8 == 0) && (o0 + BO <= a.out || a.out % 8 == 0);
     const int pc0 = c0 + tid % WP * 8, qc0 = o0 + tid % WQ * 8, pc1 = min(pc0, a.width - 8), qc1 = min(qc0, a.out - 8);
     const auto fetch = [&](int64_t q0) {
+        bool over = q0 + STEPS <= to && q0 + STEPS + 8 <= a.n;
+#pragma unroll
+        for (int i = 0; i < XP; ++i) over = over && at[i] + 8 < a.n_x;
         if (columns_whole && q0 + STEPS <= to) {
 #pragma unroll
             for (int i = 0; i < XP; ++i) RowsOf<T>::load(pv[i], x.row(at[i]), pc1);
 #pragma unroll
             for (int i = 0; i < XQ; ++i) RowsOf<T>::load(qv[i], dy.row(q0 + tid / WQ + i * (256 / WQ)), qc1);
-            return;
-        }
+        } else if (__all(over)) {
 #pragma unroll
-        for (int i = 0; i < XP; ++i) {
-            if (q0 + tid / WP + i * (256 / WP) < to) RowsOf<T>::load(pv[i], x.row(at[i]), pc0, a.width);
-            else pv[i].clear();
-        }
+            for (int i = 0; i < XP; ++i) RowsOf<T>::load_over(pv[i], x.row(at[i]), pc0, a.width);
 #pragma unroll
-        for (int i = 0; i < XQ; ++i) {
-            const int64_t q = q0 + tid / WQ + i * (256 / WQ);
-            if (q < to) RowsOf<T>::load(qv[i], dy.row(q), qc0, a.out);
-            else qv[i].clear();
+            for (int i = 0; i < XQ; ++i) RowsOf<T>::load_over(qv[i], dy.row(q0 + tid / WQ + i * (256 / WQ)), qc0, a.out);
+        } else {
+#pragma unroll
+            for (int i = 0; i < XP; ++i) {
+                if (q0 + tid / WP + i * (256 / WP) < to) RowsOf<T>::load(pv[i], x.row(at[i]), pc0, a.width);
+                else pv[i].clear();
+            }
+#pragma unroll
+            for (int i = 0; i < XQ; ++i) {
+                const int64_t q = q0 + tid / WQ + i * (256 / WQ);
+                if (q < to) RowsOf<T>::load(qv[i], dy.row(q), qc0, a.out);
+                else qv[i].clear();
+            }
         }
     };
     floatx16 acc[MT][NT];

@@ -48,6 +48,10 @@ template <> struct Word<float> {
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] = j < in ? p[j] : 0.0f;
     }
+    __device__ __forceinline__ void keep(int in) {       // the first `in` values, zeros after them
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = j < in ? v[j] : 0.0f;
+    }
     __device__ __forceinline__ float at(int j) const { return v[j]; }
     __device__ __forceinline__ void terms(uint4 (&w)[3], float &largest) const {
         float a[8];
@@ -71,16 +75,21 @@ template <> struct Word<float> {
         }
     }
 };
+typedef uint32_t uintx4 __attribute__((ext_vector_type(4)));
 template <> struct Word<bf16> {
-    uint32_t v[4];
-    __device__ __forceinline__ void clear() { v[0] = v[1] = v[2] = v[3] = 0; }
-    __device__ __forceinline__ void load(const bf16 *p) { __builtin_memcpy(v, p, 16); }
+    uintx4 v;
+    __device__ __forceinline__ void clear() { v = (uintx4)(0u); }
+    __device__ __forceinline__ void load(const bf16 *p) { __builtin_memcpy(&v, p, 16); }
     __device__ __forceinline__ void load(const bf16 *p, int in) {
         const uint16_t *u = reinterpret_cast<const uint16_t *>(p);
-        uint16_t s[8];
+        uint32_t s[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) s[j] = j < in ? u[j] : (uint16_t)0;
-        __builtin_memcpy(v, s, 16);
+        for (int j = 0; j < 8; ++j) s[j] = j < in ? (uint32_t)u[j] : 0u;
+        v = (uintx4){s[0] | s[1] << 16, s[2] | s[3] << 16, s[4] | s[5] << 16, s[6] | s[7] << 16};
+    }
+    __device__ __forceinline__ void keep(int in) {
+        const auto mask = [&](int j) { return (2 * j < in ? 0xffffu : 0u) | (2 * j + 1 < in ? 0xffff0000u : 0u); };
+        v &= (uintx4){mask(0), mask(1), mask(2), mask(3)};
     }
     __device__ __forceinline__ float at(int j) const { return __uint_as_float(j & 1 ? v[j >> 1] & 0xffff0000u : v[j >> 1] << 16); }
     __device__ __forceinline__ void terms(uint4 (&w)[1], float &) const { w[0] = make_uint4(v[0], v[1], v[2], v[3]); }
@@ -110,7 +119,13 @@ template <class T> struct RowsOf {
     __device__ __forceinline__ Row row(int64_t i) const { return {p + i * ld}; }
     // a word that is all the row's
     __device__ __forceinline__ static void load(Word<T> &w, const Row &r, int c) { w.load(r.p + c); }
-    // the word at column c of a row that has `width` of them (zeros past the end)
+    // the word at column c of a row that has `width` of them (zeros past the end), without a condition beside the load: eight
+    // further rows come after this one, so that what is read past its end is of theirs (zeros alone where not `any`)
+    __device__ __forceinline__ static void load_over(Word<T> &w, const Row &r, int c, int width, bool any = true) {
+        w.load(r.p + min(c, width - 1));
+        w.keep(any ? width - c : 0);
+    }
+    // the same for any row
     __device__ __forceinline__ static void load(Word<T> &w, const Row &r, int c, int width) {
         const int in = width - c;
         if (in >= 8) w.load(r.p + c);
@@ -129,6 +144,7 @@ template <> struct RowsOf<Micro> {
         if (c >= width) return w.clear();
         load(w, r, c);
     }
+    __device__ __forceinline__ static void load_over(Word<Micro> &w, const Row &r, int c, int width) { load(w, r, c, width); }
     __device__ __forceinline__ static void load(Word<Micro> &w, const Row &r, int c) {
         __builtin_memcpy(&w.v, r.codes + c / 2, 4);
         w.scale = r.scales[c / kMicroGroup];
