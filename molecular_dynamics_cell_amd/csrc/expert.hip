@@ -657,6 +657,110 @@ __global__ __launch_bounds__(kFewThreads) void k_product_few(const Args a, int s
     }
 }
 
+// The same across (dx): a lane has four neighbouring columns of a weight row and four steps of a gradient row, which are fp32
+// operands whatever their type; a wave has 64 columns, a lane's results are sixteen neighbouring ones.
+template <class T> struct FewAcross {
+    T v[4];
+    __device__ __forceinline__ void load(const T *p) { __builtin_memcpy(v, p, 4 * sizeof(T)); }
+    // `in` of them are the row's: one value at least lies at or before p
+    __device__ __forceinline__ void load(const T *p, int in) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = p[min(j, in - 1)];
+    }
+    __device__ __forceinline__ void keep(int in) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = j < in ? v[j] : from_f32<T>(0.0f);
+    }
+};
+template <class T, int NT>
+__global__ __launch_bounds__(kFewThreads) void k_input_grad_few(const Args a, int split, const RowsOf<T> dy, const RowsOf<T> w) {
+    constexpr int STRIDE = 16;
+    __shared__ floatx4 sums[kFewWaves][4 * NT][64];
+    const int64_t number = a.first + blockIdx.x;
+    const Tile tile = find_tile(a.offsets, a.n_experts, a.n, 16 * NT, number / a.tiles_c);
+    if (tile.from >= tile.to) return;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), part = wave % split;
+    const int c0 = ((int)(number % a.tiles_c) * (kFewWaves / split) + wave / split) * 64;
+    floatx4 acc[NT][4];
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[j][i] = (floatx4)(0.0f);
+    if (tile.expert >= 0 && c0 < a.columns) {
+        const T *yr[NT];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) yr[j] = dy.row(min(tile.from + 16 * j + (lane & 15), tile.to - 1)).p + 4 * (lane >> 4);
+        const int c = c0 + 4 * (lane & 15), in = a.columns - c;
+        const bool whole = c0 + 64 <= a.columns;
+        const T *const wr = w.row((int64_t)tile.expert * a.reduced).p + (in > 0 ? c : 0);       // columns past the last are not stored
+        const int turns = (a.reduced + STRIDE - 1) / STRIDE, each = (turns + split - 1) / split;
+        const int first = part * each, last = min(first + each, turns);
+        FewAcross<T> wv[2][4], yv[2][NT];
+        const auto fetch = [&](int turn, int b) {
+            const int k = turn * STRIDE, mine = k + 4 * (lane >> 4);
+            if (whole && k + STRIDE <= a.reduced) {
+#pragma unroll
+                for (int u = 0; u < 4; ++u) wv[b][u].load(wr + (int64_t)(mine + u) * w.ld);
+#pragma unroll
+                for (int j = 0; j < NT; ++j) yv[b][j].load(yr[j] + k);
+                return;
+            }
+            const int steps = a.reduced - mine;          // steps past the last are zeros on both sides
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                wv[b][u].load(wr + (int64_t)min(mine + u, a.reduced - 1) * w.ld, in > 0 ? in : 1);
+                wv[b][u].keep(u < steps ? 4 : 0);
+            }
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                yv[b][j].load(yr[j] + k, steps);
+                yv[b][j].keep(steps);
+            }
+        };
+        const auto use = [&](int b) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        acc[j][i] = __builtin_amdgcn_mfma_f32_16x16x4f32(to_f32(wv[b][u].v[i]), to_f32(yv[b][j].v[u]), acc[j][i], 0, 0, 0);
+        };
+        if (first < last) fetch(first, 0);
+        for (int t = first; t < last; t += 2) {
+            if (t + 1 < last) fetch(t + 1, 1);
+            use(0);
+            if (t + 1 < last) {
+                if (t + 2 < last) fetch(t + 2, 0);
+                use(1);
+            }
+        }
+    }
+    if (split > 1) {
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sums[wave][4 * j + i][lane] = acc[j][i];
+        __syncthreads();
+        if (part != 0) return;
+        for (int p = 1; p < split; ++p)
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[j][i] += sums[wave + p][4 * j + i][lane];
+    }
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+        const int64_t q = tile.from + 16 * j + (lane & 15);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int c = c0 + 16 * (lane >> 4) + 4 * r;
+            float v[4] = {acc[j][0][r], acc[j][1][r], acc[j][2][r], acc[j][3][r]};
+            if (q < tile.to && c < a.columns) finish(a, tile.expert, q, c, a.columns - c, v);
+        }
+    }
+}
+
 // Every block of a tiling, in launches of as many as one holds.
 template <class F> Status by_tiles(Args &a, int columns, int rows, F run) {
     a.tiles_c = (a.columns + columns - 1) / columns;
@@ -695,6 +799,20 @@ Status product_t(Context &cx, Args a, const RowsOf<X> &x, const RowsOf<W> &w) {
             if constexpr (std::is_same<X, W>::value && !std::is_same<X, float>::value)
                 if (rows > 32) return few(std::integral_constant<int, 4>{});
             return few(std::integral_constant<int, 2>{});
+        }
+    }
+    // Few results across likewise, in groups of 64 columns: eight experts' 2048 -> 1024 take 64 rows of dx fp32 16 us (tiles 70),
+    // 1,024 rows 66 (71); bf16 64 rows 14 (25), 256 rows 20 (25), 512 rows 31 (25); 400 rows 4096 -> 4096 fp32 215 (256);
+    // 1,000 rows 256 -> 4096 fp32 47 (254), bf16 57 (104); 40,000 rows 15 -> 500 of twenty fp32 72 (63).
+    if constexpr (ACROSS) {
+        if (a.n * ((a.columns + 63) / 64 * 64) <= (std::is_same<X, float>::value ? 1536 << 10 : 512 << 10)) {
+            int split = 1;
+            while (split < kFewWaves && split * 32 < a.reduced) split *= 2;
+            const auto few = [&](auto nt) {
+                return by_tiles(a, 64 * (kFewWaves / split), 16 * nt(), [&](unsigned grid) { k_input_grad_few<X, nt()><<<grid, kFewThreads, 0, cx.stream>>>(a, split, x, w); });
+            };
+            const int64_t rows = (a.n + std::min<int64_t>(a.n, a.n_experts) - 1) / std::min<int64_t>(a.n, a.n_experts);    // of an expert
+            return rows <= 16 ? few(std::integral_constant<int, 1>{}) : few(std::integral_constant<int, 2>{});
         }
     }
     if constexpr (std::is_same<X, W>::value && !std::is_same<X, float>::value) {

@@ -121,6 +121,36 @@ def test_product_backward(m, n, width, out, counts, first, dtype):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("n,width,out,counts,first", [(6000, 300, 129, [2000, 0, 3990], 3), (6500, 257, 40, [6500], 0), (13000, 100, 65, [1, 12000], 7), (26000, 33, 31, [50] * 500, 0),
+                                                      (4000, 520, 7, [1300] * 3, 100), (3500, 1000, 300, [50] * 70, 0), (7000, 264, 1, [3000, 4000], 0), (9000, 192, 96, [4500] * 2, 0),
+                                                      (24000, 64, 17, [24000], 0), (6400, 128, 64, [130] * 49, 5)])
+def test_input_gradient_in_tiles(m, n, width, out, counts, first, dtype):
+    g = rng(n + width + 5 * out)
+    w, dy, offsets = normal(g, len(counts), out, width, dtype=dtype, size=width ** -0.5), rows(g, n, out, dtype), ends(counts, first)
+    dx = m.expert_product_backward(dy, None, w, offsets)[0]
+    want, size = P.input_grad(dy, w, offsets)
+    check("dx", dx, want, bound(out, size, dtype, dtype), dtype)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("n,width,out", [(6, 70, 13), (6, 64, 16), (40, 5, 130), (30000, 65, 21), (9000, 264, 40)])
+def test_input_gradient_of_weights_not_finite(m, n, width, out, dtype):
+    """An infinite weight in the last step gives an infinite result, a NaN one reaches its own column and expert alone."""
+    g = rng(n + width + out)
+    w, dy = normal(g, 3, out, width, dtype=dtype), rows(g, n, out, dtype).abs() + 0.5
+    cuts = [0, n // 3, 2 * (n // 3), n]
+    w[0, out - 1, 0], w[0, out - 1, width - 1] = float("inf"), float("-inf")
+    w[1], w[2, 0, width // 2] = float("nan"), float("nan")
+    dx = m.expert_product_backward(dy, None, w, torch.tensor(cuts, dtype=torch.int32, device=DEV))[0].float().cpu()
+    first, second, third = (dx[a:b] for a, b in zip(cuts, cuts[1:]))
+    assert (first[:, 0] == float("inf")).all() and (first[:, -1] == float("-inf")).all() and first[:, 1:-1].isfinite().all()
+    assert second.isnan().all()
+    nan = torch.zeros(width, dtype=torch.bool)
+    nan[width // 2] = True
+    assert third[:, nan].isnan().all() and third[:, ~nan].isfinite().all()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("n,out,width,counts", [(40000, 64, 108, [30000, 10000]), (20000, 130, 40, [19000, 1, 0, 999]), (9000, 1, 1000, [9000]),
                                                 (12000, 1000, 3, [6000, 6000]), (30000, 260, 24, [300] * 100)])
 def test_weight_gradient_of_many_rows(m, n, out, width, counts, dtype):
