@@ -390,7 +390,8 @@ mpnn_status mpnn_checkpoint_weight_grad(mpnn_ctx *ctx, int32_t dtype, int64_t n,
  * x has the n rows, s(q) = q.  With source (device [n], as mpnn_route_plan writes it) x has n_x rows before they are
  * sorted, n = n_x k with 1 <= k <= 64, and s(q) = source[q] / k, kept in 0 .. n_x - 1: sorted rows are not written.
  * weight [n_experts][n_out][width] has the rows' type, bias (fp32, [n_experts][n_out]) may be NULL.  Sums are fp32, and
- * as accurate as fp32 products and sums for both types; they are rounded once, after the activation.  width, n_out <= 65,536. */
+ * as accurate as fp32 products and sums for both types (but what lies below 2^-126 of a value or of a product may count as
+ * zero); they are rounded once, after the activation.  width, n_out <= 65,536. */
 typedef enum { MPNN_ACT_NONE = 0, MPNN_ACT_SILU = 1 } mpnn_act;
 mpnn_status mpnn_expert_product(mpnn_ctx *ctx, int32_t dtype, int64_t n, int32_t width, int32_t n_out, int32_t n_experts,
                                 const int32_t *offsets, const void *x, int64_t ldx, const int32_t *source, int64_t n_x,

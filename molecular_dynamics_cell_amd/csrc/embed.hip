@@ -3,6 +3,9 @@
 // An entry's rows are added in their order, in fp32, by a few lanes where there are at most `window` of them.  Longer
 // ones are split at the multiples of `window` places, whose sums are added afterwards: a window has the end of at most one
 // long entry and the start of at most one other, so two partial sums a window are enough whatever the entries' lengths.
+// Bound by HBM: 400,002 rows of 128 fp32 40 us (5.2 TB/s, all but the table is written); gradients of 128,000 x 312 fp32 of five
+// entries 44 us (windows 30, 5.4 TB/s; their sums 8), of 65,536 x 1,024 bf16 of 32,000, a few frequent, without the order 96 us
+// (windows 18, their sums 17, the other entries 49: 131 MB of fp32 gradients are written).
 #include <algorithm>
 #include <type_traits>
 

@@ -7,6 +7,8 @@
 // 2 * 2^-9 * 2^-18 = 2^-26 of the product, less than fp32's own rounding of it.  A value of 0x1.ffp127 and more rounds to an
 // infinity, whose other terms are not numbers: kernels keep the largest magnitude they have met and compute the results
 // that are not numbers again, one by one, where it is that large.
+// The matrix cores take terms below 2^-126 as zero, so that at most as much is lost of a value (its third term is that small
+// from 2^-109 down).
 //
 // Layouts in LDS (a word is 16 bytes: eight bf16 values).  For rows along the reduced axis [row][word], for a reduced
 // axis across the rows [step along it][word of eight columns], which the transposing reads turn.  Words are permuted inside

@@ -151,6 +151,58 @@ def test_input_gradient_of_weights_not_finite(m, n, width, out, dtype):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("n,width,out", [(900, 16, 40), (12000, 16, 264), (9000, 264, 136)])
+def test_as_many_experts_as_there_may_be(m, n, width, out, dtype):
+    """1,024 experts, three of four without rows, rows of none before the first and after the last."""
+    g = rng(n + width)
+    sizes = torch.randint(1, max(2, n // 300), (1024,), generator=g) * (torch.arange(1024) % 4 == 1)
+    offsets = ends(sizes.tolist(), 3)
+    assert int(offsets[-1]) < n
+    x, w, bias = rows(g, n, width, dtype), normal(g, 1024, out, width, dtype=dtype, size=width ** -0.5), normal(g, 1024, out)
+    dy = rows(g, n, out, dtype)
+    y = m.expert_product(x, w, offsets, bias)
+    want, size = P.product(x, w, offsets, bias, "none", n)
+    check("y", y, want, bound(width, size, dtype, dtype), dtype)
+    dx, dw, db = m.expert_product_backward(dy, x, w, offsets)
+    want, size = P.input_grad(dy, w, offsets)
+    check("dx", dx, want, bound(out, size, dtype, dtype), dtype)
+    dw64, dws, db64, dbs, count = P.weight_grad(dy, x, offsets)
+    most = int(sizes.max())
+    check("dweight", dw, dw64, bound(most, dws, dtype, dtype))
+    check("dbias", db, db64, (most + 2) * U * dbs)
+    held = m.micro_save(w.reshape(1024 * out, width))
+    y = m.micro_product(x, held, offsets, bias, dtype=torch.float32)
+    want, size = P.product(x, f64(m.micro_load(held)).reshape(1024, out, width), offsets, bias, "none", n)
+    check("y", y, want, bound(width, size, dtype, torch.bfloat16))
+
+
+@pytest.mark.parametrize("power", [-100, -112, -118, -126])
+@pytest.mark.parametrize("n,width,out", [(7000, 128, 256), (24, 100, 60)])
+def test_values_near_the_least(m, n, width, out, power):
+    """fp32 rows of values near 2^power.  A value's bf16 terms below 2^-126 count as zero (at most 1.01 times that is lost of each
+    value), and so may each of a product's six products below it."""
+    g = rng(n + power)
+    x, w, offsets = rows(g, n, width) * 2.0 ** power, normal(g, 2, out, width), ends([n // 2, n - n // 2])
+    dy = normal(g, n, out)
+    least = 2.0 ** -126
+
+    def near(name, got, want, size, K, *lost):
+        b = bound(K, size, torch.float32, torch.float32) + least * (1.01 * sum(lost) + 6 * K)
+        assert ((f64(got) - want).abs() <= b).all(), name
+
+    want, size = P.product(x, w, offsets, None, "none", n)
+    lost = P.product(torch.ones_like(x), w, offsets, None, "none", n)[1]
+    near("y", m.expert_product(x, w, offsets), want, size, width, lost, f64(x).abs().sum(1, keepdim=True))
+    small = dy * 2.0 ** power
+    want, size = P.input_grad(small, w, offsets)
+    near("dx", m.expert_product_backward(small, None, w, offsets)[0], want, size, out, P.input_grad(torch.ones_like(dy), w, offsets)[1],
+         f64(small).abs().sum(1, keepdim=True))
+    dw, dws, _, _, count = P.weight_grad(dy, x, offsets)
+    lost = P.weight_grad(dy, torch.ones_like(x), offsets)[1] + P.weight_grad(torch.ones_like(dy), x, offsets)[1]
+    near("dweight", m.expert_product_backward(dy, x, None, offsets)[1], dw, dws, max(count), lost)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("n,out,width,counts", [(40000, 64, 108, [30000, 10000]), (20000, 130, 40, [19000, 1, 0, 999]), (9000, 1, 1000, [9000]),
                                                 (12000, 1000, 3, [6000, 6000]), (30000, 260, 24, [300] * 100)])
 def test_weight_gradient_of_many_rows(m, n, out, width, counts, dtype):
