@@ -380,7 +380,12 @@ Status weight_grad_t(Context &cx, Args a, const RowsOf<T> &dy, const RowsOf<T> &
     a.tiles_c = (a.width + tile - 1) / tile;
     a.tiles = a.tiles_c * ((a.out + tile - 1) / tile);
     const int64_t want = wide ? std::max<int64_t>(1, 256 / a.tiles) : std::max<int64_t>(1, 512 / a.tiles - a.n_experts);
-    a.rows = std::max<int64_t>(512, ((a.n + want - 1) / want + 63) / 64 * 64);
+    // The least rows of a piece: few, as a piece's time is that of its stages one after another where there are too few pieces for
+    // the GPU (30,000 rows 64 -> 64 x 4 fp32 43 us with 512, 30 with 256, 23 with 128, bf16 21, 17, 17; 3,000 rows fp32 42 and 19);
+    // more where a stage is longer (20,000 rows 256 -> 256 x 8 bf16 27 us with 256, 30 with 128) and where tiles are wide (4,000 rows
+    // 1024 -> 1024 x 8 32 us with 512, 53 with 256); and up to 512 rows are not cut, which spares a launch (454 rows 11 and 15 us).
+    const int64_t least = wide || a.n <= 512 ? 512 : std::is_same<T, float>::value ? 128 : 256;
+    a.rows = std::max<int64_t>(least, ((a.n + want - 1) / want + 63) / 64 * 64);
     const int64_t pieces = a.n / a.rows + a.n_experts;
     const int64_t matrix = (int64_t)a.out * a.width;
     a.part_slots = a.n > a.rows ? 2 * (a.n / a.rows) : 0;

@@ -1,4 +1,5 @@
-// Rows sorted by expert and back (mpnn_route_*), and the order of embedding rows (mpnn_embed_plan).  The pairs p = i k + s of row i and its slot s are ordered by
+// Rows sorted by expert and back (mpnn_route_*), and the order of embedding rows (mpnn_embed_plan).  The pairs p = i k + s of row
+// i and its slot s are ordered by
 // expert with a stable counting sort; pairs whose expert is outside 0 .. E-1 keep a place after the last segment
 // (treated as expert E), so `source` and `position` are inverse permutations of all n k pairs and every index that
 // a kernel reads from them is one it can check against n k.
