@@ -62,9 +62,9 @@ __device__ __forceinline__ void finish(const Args &a, int expert, int64_t q, int
 // 128 x 128 results at a time, four waves of 64 x 64, any types, strides and alignments: words go through registers, where
 // fp32 is cut into terms and 4-bit codes become bf16.  A block stays for many tiles: the next one's first words are on
 // their way while this one's results are stored.  ACROSS: the weights' rows are the reduced axis (dx).
-// Two blocks a CU take turns at cutting and multiplying: fp32 128,000 rows 312 -> 128 x 5 with SiLU 85 us (47 at a large bf16
-// product's rate) with the matrix cores, vector issue and LDS busy 40 % of the time each, dx 110-119 us; 32,768 rows
-// 1024 -> 1024 x 8 fp32 360 us, 1.14 PFLOP/s of bf16 products; bf16 312 -> 128 30 us (HBM, 5.4 TB/s) and dx 54 us.
+// Two blocks a CU take turns at cutting and multiplying: fp32 128,000 rows 312 -> 128 x 5 with SiLU 78-90 us (47 at a large bf16
+// product's rate) with the matrix cores, vector issue and LDS busy 40 % of the time each, dx 95-98 us; 32,768 rows
+// 1024 -> 1024 x 8 fp32 355 us, 1.16 PFLOP/s of bf16 products; bf16 312 -> 128 30 us and dx 38 us.
 constexpr int kTile = 128;
 template <class X, class W, bool ACROSS>
 __global__ __launch_bounds__(256, 2) void k_product(const Args a, const RowsOf<X> x, const RowsOf<W> w) {
@@ -97,7 +97,7 @@ __global__ __launch_bounds__(256, 2) void k_product(const Args a, const RowsOf<X
     Word<W> wv[EACH];
     // A stage of whole words has no conditions beside its loads; nor has another one where eight rows follow the tile's rows and
     // the expert's weights (`over`), so that words may be loaded past a row's end (128,000 rows 311 -> 127 x 5 in bf16 42 us; with
-    // 312 -> 128 30 us). bf16 across does without: its words would leave the registers (195 us in place of 60).
+    // 312 -> 128 30 us). bf16 across does without: its words would leave the registers (195 us in place of 52).
     constexpr bool kOver = !ACROSS || sizeof(X) == 4;
     const auto fetch = [&](int k0) {
         const int k = k0 + word * 8;
@@ -137,8 +137,8 @@ __global__ __launch_bounds__(256, 2) void k_product(const Args a, const RowsOf<X
         tile = table.find(a.offsets, a.n_experts, a.n, kTile, (int)(number / a.tiles_c));
         c0 = (int)(number % a.tiles_c) * kTile;
         // Across in bf16 the last tile ends with the row (its first columns are then the one's before too, the same bits), so that
-        // no word of weights is cut: 361 rows 2639 -> 2910 59 us in place of 158, 128,000 rows 127 -> 311 x 5 60 in place of 66
-        // (fp32, whose words go past their row's end, 151 in place of 141).
+        // no word of weights is cut: 361 rows 2639 -> 2910 59 us in place of 158, 128,000 rows 127 -> 311 x 5 52 in place of 66
+        // (fp32, whose words go past their row's end, gains nothing).
         if (!kOver) c0 = min(c0, max(a.columns - kTile, 0));
         if (tile.expert < 0) return;
         w0 = (int64_t)tile.expert * (ACROSS ? a.reduced : a.columns);
@@ -255,8 +255,8 @@ template <> struct WideOp<Micro> {
 // passing through registers, two stages ahead.  A block stays for many tiles: the next one's first stages are on their way
 // while this one's results are stored.  (One block a CU: without that a tile of 2,048 columns takes 29 us of products and
 // 23 us to find its rows, wait for the first of them and store its results.)
-// 65,536 rows 2048 -> 1024 x 64 bf16 260 us with equal shares (1.06 PFLOP/s) and 330-372 with a router's, whose tiles are not
-// all full; 16,384 rows 2048 -> 4096 x 8 in 4 bits 149 us (1.84 PFLOP/s); dx of 32,768 rows 1024 -> 1024 x 8 78 us.  The card's
+// 65,536 rows 2048 -> 1024 x 64 bf16 260-286 us with equal shares (up to 1.06 PFLOP/s) and 321-372 with a router's, whose tiles are not
+// all full; 16,384 rows 2048 -> 4096 x 8 in 4 bits 149 us (1.84 PFLOP/s); dx of 32,768 rows 1024 -> 1024 x 8 68-78 us.  The card's
 // power bounds it: the bf16 products alone, of random data from registers, run at 1.75 PFLOP/s, of zeros at 2.47.
 constexpr int kWide = 256, kWideWords = 4, kBuffers = 3, kWideThreads = 512;
 using WideTile = Along<1, kWide, kWideWords>;

@@ -258,13 +258,14 @@ template <class T> __device__ __forceinline__ void store_past(T *p, const Chunk<
     __builtin_nontemporal_store(__builtin_bit_cast(Words, v), reinterpret_cast<Words *>(p));
 }
 
-// A wave's results (32 MT columns from col0, 32 NT rows from row0) by way of LDS, 32 rows of 128 bytes at once, so that whole
-// lines are stored, past L2, whose lines the next tiles' operands need (65,536 rows 2048 -> 1024 bf16 332 -> 313 us).
+// A wave's results (32 MT columns from col0, 32 NT rows from row0) by way of LDS, 32 rows of 128 bytes at once, so that lines are
+// stored whole, and past L2 where rows are whole lines (279,184 rows 32 -> 512 bf16 55 us, by L2 72).  Others' parts of lines have
+// to meet in L2 (32 -> 463 bf16 130 us, past it 217; 128,000 rows 128 -> 312 bf16 38 and 53; fp32 98 and 113).
 // mine: the wave's kStoreBytes of LDS; bias(c): what is added to four columns from c on; act(v) then is the result.
 constexpr int kStorePitch = 128 + 16, kStoreBytes = 32 * kStorePitch;
-template <class Y, int MT, int NT, class B, class F>
-__device__ __forceinline__ void store_lines(char *mine, const floatx16 (&acc)[MT][NT], int lane, Y *y, int64_t ld, int64_t row0, int64_t rows,
-                                            int col0, int columns, B bias, F act) {
+template <bool PAST, class Y, int MT, int NT, class B, class F>
+__device__ __forceinline__ void store_lines_to(char *mine, const floatx16 (&acc)[MT][NT], int lane, Y *y, int64_t ld, int64_t row0, int64_t rows,
+                                               int col0, int columns, B bias, F act) {
     constexpr int V = 16 / sizeof(Y), GROUPS = 8 * V / 32;       // columns a lane; groups of 32 columns a line
 #pragma unroll
     for (int i = 0; i < MT; i += GROUPS) {
@@ -292,12 +293,22 @@ __device__ __forceinline__ void store_lines(char *mine, const floatx16 (&acc)[MT
                 const int64_t row = row0 + j * 32 + r + lane / 8;
                 Chunk<Y> o;
                 __builtin_memcpy(&o, __builtin_assume_aligned(mine + (r + lane / 8) * kStorePitch + lane % 8 * 16, 16), 16);
-                if (row < rows && in >= V) store_past(y + row * ld + c, o);
-                else if (row < rows && in > 0) o.store(y + row * ld + c, in);
+                if (row < rows && in >= V) {
+                    if constexpr (PAST) store_past(y + row * ld + c, o);
+                    else o.store(y + row * ld + c);
+                } else if (row < rows && in > 0) {
+                    o.store(y + row * ld + c, in);
+                }
             }
             __builtin_amdgcn_wave_barrier();
         }
     }
+}
+template <class Y, int MT, int NT, class B, class F>
+__device__ __forceinline__ void store_lines(char *mine, const floatx16 (&acc)[MT][NT], int lane, Y *y, int64_t ld, int64_t row0, int64_t rows,
+                                            int col0, int columns, B bias, F act) {
+    if (ld % (128 / (int)sizeof(Y)) == 0) store_lines_to<true>(mine, acc, lane, y, ld, row0, rows, col0, columns, bias, act);
+    else store_lines_to<false>(mine, acc, lane, y, ld, row0, rows, col0, columns, bias, act);
 }
 
 // Row tiles of the experts' segments, and of the rows that no expert has (before the first segment and after the last;
