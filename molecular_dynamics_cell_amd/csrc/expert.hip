@@ -63,7 +63,7 @@ __device__ __forceinline__ void finish(const Args &a, int expert, int64_t q, int
 // fp32 is cut into terms and 4-bit codes become bf16.  A block stays for many tiles: the next one's first words are on
 // their way while this one's results are stored.  ACROSS: the weights' rows are the reduced axis (dx).
 // Two blocks a CU take turns at cutting and multiplying: fp32 128,000 rows 312 -> 128 x 5 with SiLU 78-90 us (47 at a large bf16
-// product's rate) with the matrix cores, vector issue and LDS busy 40 % of the time each, dx 95-98 us; 32,768 rows
+// product's rate) with the matrix cores, vector issue and LDS busy 40 % of the time each, dx 95-117 us; 32,768 rows
 // 1024 -> 1024 x 8 fp32 355 us, 1.16 PFLOP/s of bf16 products; bf16 312 -> 128 30 us and dx 38 us.
 constexpr int kTile = 128;
 template <class X, class W, bool ACROSS>

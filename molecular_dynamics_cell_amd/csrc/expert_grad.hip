@@ -173,7 +173,7 @@ __global__ __launch_bounds__(256, 2) void k_expert_weight_grad(const Args a, con
 // first stages are on their way while this one's results are stored.
 // Whole pieces are dealt to the blocks first, then what is left of each expert, in turn from the first block to the last and
 // back, so that a block with one tile more has a short one.
-// 32,768 rows 1024 -> 1024 x 8: 93-120 us by the experts' shares (46 at a large product's rate), and 24 to add the pieces.
+// 32,768 rows 1024 -> 1024 x 8: 93-135 us by the experts' shares (46 at a large product's rate), and 21 to add the pieces.
 constexpr int kWide = 256, kWideThreads = 512, kBuffers = 3, kWideStage = 32, kCus = 256, kMostExperts = 1024;
 
 __global__ __launch_bounds__(kWideThreads, 2) void k_expert_weight_grad_wide(const Args a, const RowsOf<bf16> dy, const RowsOf<bf16> x) {
