@@ -110,7 +110,8 @@ template <int W> __device__ __forceinline__ void store_sums(float *p, const floa
 }
 
 // A window's rows of entries that are longer than it: blockIdx.x a window, blockIdx.y a stripe of `chunks` chunks, of which each
-// thread has one and every slices-th row.  owner: the long entry that begins in the window, or -1.
+// thread has one and every slices-th row.  The sum of the entry that begins inside the window is its second one, that of an
+// entry that has its first place the first one.  owner: the long entry that begins in the window, at its first place or inside, or -1.
 template <class T, bool SHORT>
 __global__ __launch_bounds__(256) void k_embed_windows(int64_t n, int width, int entries, int64_t window, int chunks, const int32_t *__restrict__ offsets,
                                                        const int32_t *__restrict__ source, const T *__restrict__ dout, int64_t ld,
@@ -119,20 +120,16 @@ __global__ __launch_bounds__(256) void k_embed_windows(int64_t n, int width, int
     constexpr int W = P::W;
     __shared__ float sums[256][W];
     const int64_t used = min(max((int64_t)offsets[entries], (int64_t)0), n), from = (int64_t)blockIdx.x * window, to = min(from + window, used);
-    const bool writes = blockIdx.y == 0 && threadIdx.x == 0;
-    if (from >= to) {
-        if (writes) owner[blockIdx.x] = -1;
-        return;
-    }
+    int begins = -1;
     const int slices = 256 / chunks, slice = threadIdx.x / chunks, lc = threadIdx.x % chunks, c = blockIdx.y * chunks + lc;
-    int entry[2];
-    entries_of(offsets, entries, from, to - 1, entry[0], entry[1]);
-    for (int side = 0; side < 2; ++side) {
-        const int e = entry[side];
+    int entry[2] = {0, 0};
+    if (from < to) entries_of(offsets, entries, from, to - 1, entry[0], entry[1]);
+    for (int k = 0; k < 2 && from < to; ++k) {
+        const int e = entry[k];
         const int64_t start = max((int64_t)offsets[e], (int64_t)0), end = min((int64_t)offsets[e + 1], used);
-        const bool is_long = end - start > window;
-        if (side && writes) owner[blockIdx.x] = is_long && start >= from ? e : -1;
-        if ((side && (entry[0] == e || start <= from)) || !is_long) continue;
+        // (the first entry stands for places before its own too)
+        if ((k && entry[0] == e) || end - start <= window || start >= to) continue;
+        if (start >= from) begins = e;
         float s[W] = {};
         const bool in = slice < slices && c * W < width;
         if (in) add_rows<T, SHORT, 8>(dout, ld, source, (int)n, (int)max(start, from) + slice, (int)min(end, to), slices, P::start(c, width), s);
@@ -141,11 +138,12 @@ __global__ __launch_bounds__(256) void k_embed_windows(int64_t n, int width, int
         for (int j = 0; j < W; ++j) sums[threadIdx.x][j] = s[j];
         __syncthreads();
         if (!in || slice != 0) continue;
-        for (int k = 1; k < slices; ++k)
+        for (int i = 1; i < slices; ++i)
 #pragma unroll
-            for (int j = 0; j < W; ++j) s[j] += sums[k * chunks + lc][j];
-        store_sums<W>(part + (2 * (int64_t)blockIdx.x + side) * width + P::start(c, width), s, 1.0f);
+            for (int j = 0; j < W; ++j) s[j] += sums[i * chunks + lc][j];
+        store_sums<W>(part + (2 * (int64_t)blockIdx.x + (start > from ? 1 : 0)) * width + P::start(c, width), s, 1.0f);
     }
+    if (blockIdx.y == 0 && threadIdx.x == 0) owner[blockIdx.x] = begins;
 }
 
 // The windows' sums of each long entry, in their order: 16 columns by 64 slices of the windows a block, which takes every

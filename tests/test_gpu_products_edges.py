@@ -1,0 +1,73 @@
+"""Products by expert, 4-bit rows and embedding rows on the GPU where they go wrong most easily, against plain 64-bit
+implementations.  The bounds are those of test_gpu_products.py."""
+import pytest
+import torch
+
+from molecular_dynamics_cell_amd import binding
+from molecular_dynamics_cell_amd import inputs as I
+from tests.rows_util import U, check, f64
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda:0"
+TYPES = [torch.float32, torch.bfloat16]
+
+
+@pytest.fixture(scope="module")
+def m():
+    ctx = binding.MPNN(I.make_params(1), DEV)
+    yield ctx
+    torch.cuda.synchronize()
+    ctx.close()
+
+
+@pytest.fixture(autouse=True)
+def say_name(request):
+    print(f"[products] {request.node.name}", flush=True)
+    yield
+    torch.cuda.synchronize()
+
+
+def rng(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def normal(g, *shape, dtype=torch.float32, size=1.0):
+    return (torch.randn(*shape, generator=g) * size).to(dtype).to(DEV)
+
+
+# ---------------------------------------------------------------------------------------------------------------
+# embedding rows
+# ---------------------------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("width", [1, 5, 40, 136])
+@pytest.mark.parametrize("ends", [[10, 500, 1000], [30, 31, 31, 900], [64, 1000], [200, 1000], [63, 129, 700], [65, 130, 140], [700, 1000], [960, 1000],
+                                  [999, 1000], [1000, 1000], [300, 600, 2000], [-5, -3, 70, 800], [64, 128, 193, 193, 1000]])
+def test_embed_gradient_of_entries_from_later_places_on(m, ends, width, dtype):
+    """Rows before the first entry's are no entry's, wherever it starts in a window of 64 places; what earlier calls left in the
+    scratch reaches nothing."""
+    g, n = rng(width + ends[0]), 1000
+    source = torch.randperm(n, generator=g).to(torch.int32).to(DEV)
+    dout = normal(g, n, width, dtype=dtype)
+    whole = torch.tensor([0, n // 3, n], dtype=torch.int32, device=DEV)
+    m.embed_backward(torch.full_like(dout, float("nan")), whole, source)
+    cut = [min(max(v, 0), n) for v in ends]
+    kept = dout.clone()
+    dout[source[:cut[0]].long()], dout[source[cut[-1]:].long()] = float("nan"), float("nan")
+    got = m.embed_backward(dout, torch.tensor(ends, dtype=torch.int32, device=DEV), source, -0.5)
+    d = f64(kept)[source.cpu().long()]
+    want, size = (torch.stack([v[a:b].sum(0) for a, b in zip(cut, cut[1:])]) * s for v, s in ((d, -0.5), (d.abs(), 0.5)))
+    check("dtable", got, want, (n + 2) * U * size)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_embed_gradient_of_a_shard(m, dtype):
+    """A slice of the plan's offsets gives those entries' gradients, the same bits."""
+    g, n, entries = rng(4), 30000, 40
+    index = (torch.rand(n, generator=g) ** 3 * (entries + 2) - 1).floor().to(torch.int32).to(DEV)
+    offsets, source = m.embed_plan(index, entries)
+    dout = normal(g, n, 72, dtype=dtype)
+    whole = m.embed_backward(dout, offsets, source, 1.5)
+    for a, b in ((0, 1), (1, 2), (1, 40), (2, 9), (7, 40), (39, 40)):
+        m.embed_backward(torch.full_like(dout, float("nan")), offsets, source)
+        assert torch.equal(m.embed_backward(dout, offsets[a:b + 1], source, 1.5), whole[a:b]), (a, b)
