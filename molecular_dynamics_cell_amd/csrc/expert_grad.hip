@@ -404,6 +404,7 @@ Status weight_grad_t(Context &cx, Args a, const RowsOf<T> &dy, const RowsOf<T> &
 
 Status expert_weight_grad(Context &cx, int dtype, int64_t n, int width, int n_out, int n_experts, const int32_t *offsets, const void *dy,
                           int64_t ld_dy, const void *x, int64_t ldx, const int32_t *source, int64_t n_x, float *dweight, float *dbias) {
+    if (n == 0) source = nullptr;       // no places to look up, and n_x may be zero
     const Args a{n, 0, n_out, width, n_experts, 0, 0, offsets, source, source ? n_x : n, source ? (int)(n / n_x) : 1, 0, nullptr, dweight, dbias};
     if (dtype == MPNN_BF16) return weight_grad_t<bf16>(cx, a, {(const bf16 *)dy, ld_dy}, {(const bf16 *)x, ldx});
     return weight_grad_t<float>(cx, a, {(const float *)dy, ld_dy}, {(const float *)x, ldx});

@@ -37,6 +37,26 @@ def normal(g, *shape, dtype=torch.float32, size=1.0):
 
 
 # ---------------------------------------------------------------------------------------------------------------
+# products by expert
+# ---------------------------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("n_x", [0, 5])
+@pytest.mark.parametrize("dtype", [0, 1])
+def test_no_rows_with_a_source(m, dtype, n_x):
+    """A batch without rows whose source is an array all the same: gradients of zeros, nothing else written."""
+    L = binding.lib()
+    offsets, source = (torch.zeros(9, dtype=torch.int32, device=DEV) for _ in range(2))
+    x, dw, db, y = (torch.full((600,), 7.0, device=DEV) for _ in range(4))
+    o, s, p = offsets.data_ptr(), source.data_ptr(), x.data_ptr()
+    assert L.mpnn_expert_weight_grad(m.h, dtype, 0, 16, 8, 2, o, p, 8, p, 16, s, n_x, dw.data_ptr(), db.data_ptr()) == 0
+    assert L.mpnn_expert_weight_grad(m.h, dtype, 0, 16, 8, 2, o, None, 8, None, 16, s, n_x, dw[300:].data_ptr(), None) == 0
+    assert L.mpnn_expert_product(m.h, dtype, 0, 16, 8, 2, o, p, 16, s, n_x, p, None, 0, y.data_ptr()) == 0
+    assert L.mpnn_micro_product(m.h, dtype, 0, 0, 16, 8, 2, o, p, 16, None, s, n_x, p, p, None, 0, y.data_ptr()) == 0
+    torch.cuda.synchronize()
+    assert (dw[:256] == 0).all() and (dw[256:300] == 7).all() and (dw[300:556] == 0).all() and (dw[556:] == 7).all()
+    assert (db[:16] == 0).all() and (db[16:] == 7).all() and (y == 7).all() and (x == 7).all()
+
+
+# ---------------------------------------------------------------------------------------------------------------
 # embedding rows
 # ---------------------------------------------------------------------------------------------------------------
 @pytest.mark.parametrize("dtype", TYPES)
