@@ -77,17 +77,18 @@ __device__ __forceinline__ void entries_of(const int32_t *offsets, int entries, 
     last = __builtin_amdgcn_readfirstlane(low[1]);
 }
 
-// s += the rows at places from, from + by .. below `to`, one chunk of columns, AHEAD rows in flight.  (Places and rows are below
-// 2^31; where they are the same for a whole wave, so are a row's address and the loads of its place.)
+// s += the rows at places from, from + by .. below `to`, one chunk of columns, AHEAD rows in flight.  (Places are below 2^31 and
+// those that are looked ahead to below 2^32: 32 bits without a sign hold them.  Where they are the same for a whole wave, so are a
+// row's address and the loads of its place.)
 template <class T, bool SHORT, int AHEAD>
-__device__ __forceinline__ void add_rows(const T *dout, int64_t ld, const int32_t *source, int n, int from, int to, int by, int column,
+__device__ __forceinline__ void add_rows(const T *dout, int64_t ld, const int32_t *source, uint32_t n, uint32_t from, uint32_t to, uint32_t by, int column,
                                          float (&s)[Part<T, SHORT>::W]) {
     using P = Part<T, SHORT>;
-    for (int q = from; q < to; q += AHEAD * by) {
+    for (uint32_t q = from; q < to; q += AHEAD * by) {
         P v[AHEAD];
 #pragma unroll
         for (int u = 0; u < AHEAD; ++u) {
-            const uint32_t i = min((uint32_t)source[min(q + u * by, to - 1)], (uint32_t)n - 1);
+            const uint32_t i = min((uint32_t)source[min(q + u * by, to - 1)], n - 1);
             v[u].load(dout + (int64_t)i * ld + column);
         }
 #pragma unroll
@@ -132,7 +133,7 @@ __global__ __launch_bounds__(256) void k_embed_windows(int64_t n, int width, int
         if (start >= from) begins = e;
         float s[W] = {};
         const bool in = slice < slices && c * W < width;
-        if (in) add_rows<T, SHORT, 8>(dout, ld, source, (int)n, (int)max(start, from) + slice, (int)min(end, to), slices, P::start(c, width), s);
+        if (in) add_rows<T, SHORT, 8>(dout, ld, source, (uint32_t)n, (uint32_t)max(start, from) + slice, (uint32_t)min(end, to), slices, P::start(c, width), s);
         __syncthreads();
 #pragma unroll
         for (int j = 0; j < W; ++j) sums[threadIdx.x][j] = s[j];
@@ -235,9 +236,9 @@ __global__ __launch_bounds__(256) void k_embed_entries(int64_t n, int width, int
     if (c * W >= width) return;
     float s[W] = {};
     const int many = end - start, column = P::start(c, width);
-    if (many > 6) add_rows<T, SHORT, 16>(dout, ld, source, (int)n, start, end, 1, column, s);
-    else if (many > 2) add_rows<T, SHORT, 6>(dout, ld, source, (int)n, start, end, 1, column, s);
-    else if (many > 0) add_rows<T, SHORT, 2>(dout, ld, source, (int)n, start, end, 1, column, s);
+    if (many > 6) add_rows<T, SHORT, 16>(dout, ld, source, (uint32_t)n, start, end, 1, column, s);
+    else if (many > 2) add_rows<T, SHORT, 6>(dout, ld, source, (uint32_t)n, start, end, 1, column, s);
+    else if (many > 0) add_rows<T, SHORT, 2>(dout, ld, source, (uint32_t)n, start, end, 1, column, s);
     store_sums<W>(dtable + e * width + column, s, scale);
 }
 

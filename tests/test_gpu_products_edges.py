@@ -91,3 +91,27 @@ def test_embed_gradient_of_a_shard(m, dtype):
     for a, b in ((0, 1), (1, 2), (1, 40), (2, 9), (7, 40), (39, 40)):
         m.embed_backward(torch.full_like(dout, float("nan")), offsets, source)
         assert torch.equal(m.embed_backward(dout, offsets[a:b + 1], source, 1.5), whole[a:b]), (a, b)
+
+
+def test_embed_of_as_many_rows_as_there_may_be(m):
+    """2^31 - 1 rows: places next to the end of 32 bits, sums of small whole numbers (exact)."""
+    n, tail = 2 ** 31 - 1, 200000
+    index = torch.full((n,), -1, dtype=torch.int32, device=DEV)
+    last = torch.zeros(tail, dtype=torch.int32)
+    last[-60:-1], last[-1] = 1, 2
+    index[-tail:] = last.to(DEV)
+    table = torch.tensor([[2.0], [3.0], [5.0]], dtype=torch.bfloat16, device=DEV)
+    out = m.embed(index, table)
+    assert torch.equal(out[-tail:].cpu(), table.cpu()[last.long()]) and float(out[:1000].abs().max()) == 0
+    # the plan puts the rows of no entry last; offsets of the same rows in their own order put the entries last
+    offsets, source = m.embed_plan(index, 3)
+    assert offsets.tolist() == [0, tail - 60, tail - 1, tail]
+    assert torch.equal(source[:tail], torch.arange(n - tail, n, dtype=torch.int32, device=DEV)) and int(source[-1]) == n - tail - 1
+    out.zero_()
+    values = (torch.arange(tail) % 7 - 2).to(torch.bfloat16)
+    out[-tail:] = values.to(DEV).unsqueeze(1)
+    want = torch.stack([v.double().sum() for v in (values[:-60], values[-60:-1], values[-1:])])
+    assert torch.equal(f64(m.embed_backward(out, offsets, source))[:, 0], want)
+    torch.arange(n, out=source)
+    late = torch.tensor([n - tail, n - 60, n - 1, n], dtype=torch.int32, device=DEV)
+    assert torch.equal(f64(m.embed_backward(out, late, source))[:, 0], want)
