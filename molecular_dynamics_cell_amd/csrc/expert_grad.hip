@@ -65,7 +65,7 @@ __global__ __launch_bounds__(256, 2) void k_expert_weight_grad(const Args a, con
     const auto fetch = [&](int64_t q0) {
         bool over = q0 + STEPS <= to && q0 + STEPS + 8 <= a.n;
 #pragma unroll
-        for (int i = 0; i < XP; ++i) over = over && at[i] + 8 < a.n_x;
+        for (int i = 0; i < XP; ++i) over = over && at[i] < a.n_x - 8;
         if (columns_whole && q0 + STEPS <= to) {
 #pragma unroll
             for (int i = 0; i < XP; ++i) RowsOf<T>::load(pv[i], x.row(at[i]), pc1);

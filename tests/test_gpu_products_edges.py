@@ -56,6 +56,35 @@ def test_no_rows_with_a_source(m, dtype, n_x):
     assert (db[:16] == 0).all() and (db[16:] == 7).all() and (y == 7).all() and (x == 7).all()
 
 
+def test_as_many_rows_as_there_may_be(m):
+    """2^31 - 1 rows of one column, the last rows' places first: small whole numbers, whose sums are exact."""
+    n, some = 2 ** 31 - 1, 100000
+    whole = torch.full((n + 16, 1), float("nan"), dtype=torch.bfloat16, device=DEV)
+    x = whole[:n]
+    x.zero_()
+    mine, other = (torch.arange(some) % 7 - 2).bfloat16(), (torch.arange(some) % 5 - 1).bfloat16()
+    x[-some:] = mine.to(DEV).unsqueeze(1)
+    dy = torch.zeros(n, 1, dtype=torch.bfloat16, device=DEV)
+    dy[:some] = other.to(DEV).unsqueeze(1)
+    source = torch.arange(n, dtype=torch.int32, device=DEV)
+    source.neg_().add_(n - 1)
+    offsets = torch.tensor([0, 1000, n], dtype=torch.int32, device=DEV)
+    w = torch.tensor([3.0, -2.0], dtype=torch.bfloat16, device=DEV).reshape(2, 1, 1)
+    _, dw, db = m.expert_product_backward(dy, x, None, offsets, source=source)
+    pairs = mine.flip(0).double() * other.double()
+    assert f64(dw).reshape(-1).tolist() == [float(pairs[:1000].sum()), float(pairs[1000:].sum())]
+    assert f64(db).reshape(-1).tolist() == [float(other[:1000].double().sum()), float(other[1000:].double().sum())]
+    factor = torch.where(torch.arange(some) < 1000, 3.0, -2.0).double()
+    y = m.expert_product(x, w, offsets, source=source)
+    assert torch.equal(f64(y[:some])[:, 0], factor * mine.flip(0).double()) and float(y[-1000:].float().abs().max()) == 0
+    del y
+    y = m.expert_product(x, w, offsets)
+    assert torch.equal(f64(y[-some:])[:, 0], -2.0 * mine.double()) and float(y[:1000].float().abs().max()) == 0
+    del y
+    dx = m.expert_product_backward(x, None, w, offsets)[0]
+    assert torch.equal(f64(dx[-some:])[:, 0], -2.0 * mine.double())
+
+
 # ---------------------------------------------------------------------------------------------------------------
 # embedding rows
 # ---------------------------------------------------------------------------------------------------------------
