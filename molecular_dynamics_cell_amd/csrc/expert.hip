@@ -190,7 +190,7 @@ __global__ __launch_bounds__(256, 2) void k_product(const Args a, const RowsOf<X
             if (k0 + STAGE < a.reduced) fetch(k0 + STAGE);
             multiply<P, Q, TP, TQ, MT, NT, WORDS>(lp, lq, wm * MT * 32, wn * NT * 32, lane, acc);
         }
-        const bool huge = TP + TQ > 2 && __syncthreads_or(largest >= kHuge);
+        const bool large = TP + TQ > 2 && __syncthreads_or(largest >= kLarge);
 
         // the next tile, before this one's results
         const Tile done = tile;
@@ -208,15 +208,24 @@ __global__ __launch_bounds__(256, 2) void k_product(const Args a, const RowsOf<X
             };
             store_lines(reinterpret_cast<char *>(results[wave]), acc, lane, y, a.columns, done.from + wn * NT * 32, done.to, done_c0 + wm * MT * 32,
                         a.columns, bias, [&](float v) { return act ? silu(v) : v; });
-            if (!huge) return;
-            // results that are not numbers, once more without terms
+            if (!large) return;
+            // (sums that are all finite are right: 128,000 rows of values near 1e15 take no longer than of 1, and 141 us in place of 83
+            // where results are looked through for it)
+            float zero = 0.0f;
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) zero = fmaf(acc[i][j][r], 0.0f, zero);
+            if (!__syncthreads_or(zero != 0.0f)) return;
+            // results that are not finite, once more without terms
             __syncthreads();
             for (int e = tid; e < kTile * kTile; e += 256) {
                 const int64_t q = done.from + e / kTile;
                 const int c = done_c0 + e % kTile;
                 if (q >= done.to || c >= a.columns) continue;
-                const float was = to_f32(y[q * a.columns + c]);
-                if (was == was) continue;
+                if (isfinite(to_f32(y[q * a.columns + c]))) continue;
                 const int64_t weights = (int64_t)done.expert * (ACROSS ? a.reduced : a.columns), from = place(q);
                 float s = 0.0f;
                 for (int k = 0; k < a.reduced; ++k) s = fmaf(x.at(from, k), ACROSS ? w.at(weights + k, c) : w.at(weights + c, k), s);

@@ -122,7 +122,7 @@ __global__ __launch_bounds__(256, 2) void k_expert_weight_grad(const Args a, con
         if (q0 + STEPS < to) fetch(q0 + STEPS);
         multiply<P, Q, TERMS, TERMS, MT, NT, WORDS>(lp, lq, wm * MT * 32, wn * NT * 32, lane, acc);
     }
-    const bool huge = TERMS > 1 && __syncthreads_or(largest >= kHuge);
+    const bool large = TERMS > 1 && __syncthreads_or(largest >= kLarge);       // then results that are not finite, once more without terms
 
     const int64_t matrix = (int64_t)a.out * a.width;
     const bool whole = pc.pieces == 1;
@@ -142,9 +142,9 @@ __global__ __launch_bounds__(256, 2) void k_expert_weight_grad(const Args a, con
                 Chunk<float, 4> v;
 #pragma unroll
                 for (int r = 0; r < 4; ++r) v.v[r] = acc[i][j][4 * g + r];
-                if (huge)
+                if (large)
                     for (int r = 0; r < 4; ++r)
-                        if (v.v[r] != v.v[r] && r < in) {
+                        if (!isfinite(v.v[r]) && r < in) {
                             float s = 0.0f;
                             for (int64_t q = from; q < to; ++q) {
                                 const int64_t at = a.source ? min((int64_t)((uint32_t)max(a.source[q], 0) / (uint32_t)a.slots), a.n_x - 1) : q;

@@ -4,9 +4,11 @@
 // Operands.  A bf16 value is one as it stands, and so is a 4-bit value times its power-of-two step.  An fp32 value is cut
 // into three bf16 terms by rounding, each to nearest: the second is at most 2^-9 of the value, the third 2^-18, and the three add
 // up to it exactly.  Of the nine products of two such values the six largest are taken; what is left out is below
-// 2 * 2^-9 * 2^-18 = 2^-26 of the product, less than fp32's own rounding of it.  A value of 0x1.ffp127 and more rounds to an
-// infinity, whose other terms are not numbers: kernels keep the largest magnitude they have met and compute the results
-// that are not numbers again, one by one, where it is that large.
+// 2 * 2^-9 * 2^-18 = 2^-26 of the product, less than fp32's own rounding of it.  Terms overflow where their values do not: a
+// value of 0x1.ffp127 and more rounds to an infinity, whose other terms are not numbers, products of first terms may be 2^-8 larger
+// than those of the values, and the remainders' products may overflow with the other sign.  Kernels keep the largest magnitude
+// they have met and compute the results that are not finite again from the values, one by one, where it is large enough for any
+// of it: below 2^48 products are below 2^96, and 2^31 of them below 2^127.
 // The matrix cores take terms below 2^-126 as zero, so that at most as much is lost of a value (its third term is that small
 // from 2^-109 down).
 //
@@ -31,7 +33,7 @@ typedef short shortx4 __attribute__((ext_vector_type(4)));
 struct Micro {};                             // values in 4 bits: 16 bytes of codes and a scale byte for 32 columns
 constexpr int kMicroGroup = 32;
 
-constexpr float kHuge = 0x1.ffp127f;         // rounds to an infinity in bf16
+constexpr float kLarge = 0x1p48f;            // sums of products of smaller values do not overflow
 
 template <class T> constexpr int kTerms = std::is_same<T, float>::value ? 3 : 1;
 
@@ -103,8 +105,9 @@ template <> struct Word<Micro> {
         v = 0;
         scale = 127;
     }
-    __device__ __forceinline__ void terms(uint4 (&w)[1], float &) const {
+    __device__ __forceinline__ void terms(uint4 (&w)[1], float &largest) const {
         const float s = micro_step(scale);
+        largest = fmaxf(largest, 8.0f * s);
         const auto two = [&](auto k) { return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(v, s, k())); };
         w[0] = make_uint4(two(std::integral_constant<int, 0>{}), two(std::integral_constant<int, 1>{}),
                           two(std::integral_constant<int, 2>{}), two(std::integral_constant<int, 3>{}));

@@ -5,7 +5,9 @@ import torch
 
 from molecular_dynamics_cell_amd import binding
 from molecular_dynamics_cell_amd import inputs as I
+from tests import products_util as P
 from tests.rows_util import U, check, f64
+from tests.test_gpu_products import act_bound, bound, ends, rows
 
 pytestmark = pytest.mark.gpu
 
@@ -83,6 +85,84 @@ def test_as_many_rows_as_there_may_be(m):
     del y
     dx = m.expert_product_backward(x, None, w, offsets)[0]
     assert torch.equal(f64(dx[-some:])[:, 0], -2.0 * mine.double())
+
+
+TOP = torch.finfo(torch.float32).max
+# straight from memory, tiles, and wide tiles where the type has them
+SIZES = [(24, 100, 60), (3000, 33, 600), (7000, 128, 256), (5000, 264, 392)]
+
+
+def agrees(name, got, want, b, dtype):
+    """Within the bound, and infinite exactly where a 64-bit result does not fit the type, with its sign."""
+    want = torch.where(want.abs() > torch.finfo(dtype).max, torch.sign(want) * float("inf"), want)
+    assert torch.equal(f64(got).isinf(), want.isinf()), name
+    check(name, got, want, torch.where(want.isinf(), 0.0, b), dtype)
+
+
+def large(g, *shape, at, dtype):
+    """Positive values between `at` and twice it, whose roundings to fewer bits are off either way."""
+    return ((1 + torch.rand(*shape, generator=g)) * at).to(dtype).to(DEV)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("at", [1e25, 2.0 ** 66])
+@pytest.mark.parametrize("n,width,out", SIZES)
+def test_products_that_overflow(m, n, width, out, at, dtype):
+    """Finite values whose product does not fit: an infinity with the product's sign, not a NaN; their neighbours stay."""
+    g, c, o = rng(n + out), width - 1, out // 3
+    x, w, dy = rows(g, n, width, dtype), normal(g, 2, out, width, dtype=dtype), rows(g, n, out, dtype)
+    offsets, few = ends([n // 2, n - n // 2]), slice(0, n, 3)
+    x[few, c], dy[few, o] = large(g, len(x[few]), at=at, dtype=dtype), large(g, len(x[few]), at=at, dtype=dtype)
+    w[:, :out // 2, c] = large(g, 2, out // 2, at=at, dtype=dtype)
+    for act in ("none", "silu"):
+        bias = None if act == "none" else normal(g, 2, out)
+        want, size = P.product(x, w, offsets, bias, act, n)
+        agrees("y", m.expert_product(x, w, offsets, bias, act=act), want, act_bound(bound(width, size, dtype, dtype), want, act), dtype)
+    w[:, :out // 4, c] *= -1
+    want, size = P.product(x, w, offsets, None, "none", n)
+    agrees("y of either sign", m.expert_product(x, w, offsets), want, bound(width, size, dtype, dtype), dtype)
+    dx, dw, db = m.expert_product_backward(dy, x, w, offsets)
+    want, size = P.input_grad(dy, w, offsets)
+    agrees("dx", dx, want, bound(out, size, dtype, dtype), dtype)
+    want, size, db64, dbs, count = P.weight_grad(dy, x, offsets)
+    agrees("dweight", dw, want, bound(max(count), size, dtype, dtype), torch.float32)
+    check("dbias", db, db64, (max(count) + 2) * U * dbs)
+
+
+@pytest.mark.parametrize("n,width,out", SIZES)
+def test_products_just_below_the_largest(m, n, width, out):
+    """Two values whose first terms' product is 2^128, but not their own."""
+    g, c, o, r = rng(n + out), width // 2, out - 1, n // 3
+    x, w, dy = rows(g, n, width), normal(g, 2, out, width), rows(g, n, out)
+    near = (2 - 2.0 ** -12) * 2.0 ** 63
+    x[r, c], w[:, o, c], dy[r, o] = near, near, near
+    offsets, b = ends([n // 2, n - n // 2]), normal(g, 2, out)
+    f32 = torch.float32
+    for act in ("none", "silu"):
+        want, size = P.product(x, w, offsets, b, act, n)
+        assert 0.999 * TOP < want[r, o] < TOP
+        agrees("y", m.expert_product(x, w, offsets, b, act=act), want, act_bound(bound(width, size, f32, f32), want, act), f32)
+    dx, dw, _ = m.expert_product_backward(dy, x, w, offsets)
+    want, size = P.input_grad(dy, w, offsets)
+    agrees("dx", dx, want, bound(out, size, f32, f32), f32)
+    want, size, _, _, count = P.weight_grad(dy, x, offsets)
+    agrees("dweight", dw, want, bound(max(count), size, f32, f32), f32)
+
+
+@pytest.mark.parametrize("kind", ["float32", "bfloat16", "micro"])
+@pytest.mark.parametrize("rows_at,weights_at", [(1e25, 1e25), (1e10, 2.0 ** 110), (2.0 ** 110, 1e10)])
+@pytest.mark.parametrize("n,width,out", SIZES)
+def test_products_by_held_weights_that_overflow(m, n, width, out, rows_at, weights_at, kind):
+    g, c = rng(n + out), width - 1
+    dtype = torch.float32 if kind == "float32" else torch.bfloat16
+    x, w = rows(g, n, width, dtype), normal(g, 2 * out, width)
+    x[::3, c], w[:out // 2, c] = large(g, len(x[::3]), at=rows_at, dtype=dtype), -large(g, out // 2, at=weights_at, dtype=torch.float32)
+    held, offsets = m.micro_save(w), ends([n // 2, n - n // 2])
+    taken = m.micro_save(x) if kind == "micro" else x
+    x64 = P.micro_load(taken.codes, taken.scales, width) if kind == "micro" else f64(x)
+    want, size = P.product(x64, P.micro_load(held.codes, held.scales, width).reshape(2, out, width), offsets, None, "none", n)
+    for t in TYPES:
+        agrees("y", m.micro_product(taken, held, offsets, dtype=t), want, bound(width, size, dtype, torch.bfloat16), t)
 
 
 # ---------------------------------------------------------------------------------------------------------------
