@@ -165,6 +165,76 @@ def test_products_by_held_weights_that_overflow(m, n, width, out, rows_at, weigh
         agrees("y", m.micro_product(taken, held, offsets, dtype=t), want, bound(width, size, dtype, torch.bfloat16), t)
 
 
+def same_places(name, got, want, b, dtype=torch.float32):
+    """Not-a-numbers and infinities where 64 bits have them, the others within the bound."""
+    got64, fine = f64(got), want.isfinite()
+    assert torch.equal(got64.isnan(), want.isnan()) and torch.equal(got64[want.isinf()], want[want.isinf()]), name
+    check(name, torch.where(fine, got64, 0.0), torch.where(fine, want, 0.0), torch.where(fine, b, 0.0), dtype)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("by_source", [False, True])
+@pytest.mark.parametrize("n,width,out", SIZES + [(2000, 264, 136), (2200, 136, 800)])
+def test_values_that_are_not_finite_in_tiles(m, n, width, out, by_source, dtype):
+    """Infinities and NaN in an expert's first and last rows, in last columns and weights: where the formula has them (0 times an
+    infinity is not a number), in their rows, columns and experts alone."""
+    g, inf, nan = rng(n + width), float("inf"), float("nan")
+    x, w, dy = rows(g, n, width, dtype), normal(g, 3, out, width, dtype=dtype), rows(g, n, out, dtype)
+    cut = [2, 2 + n // 3, 2 + n // 3, n - 5]
+    offsets = torch.tensor(cut, dtype=torch.int32, device=DEV)
+    x[:2], x[-5:], dy[:2], dy[-5:] = nan, inf, inf, nan              # rows of no expert
+    source = torch.randperm(n, generator=g).to(torch.int32).to(DEV) if by_source else torch.arange(n, dtype=torch.int32, device=DEV)
+    xs = x.clone()                                                   # sorted
+    xs[cut[0], width - 1], xs[cut[1] - 1, 0], xs[cut[3] - 1, width // 2] = inf, nan, -inf
+    xs[cut[2] + 1, 3] = 0.0
+    w[0, out - 1, 1], w[2, 4, width - 1], w[2, 5, 3] = -inf, nan, inf
+    w[1] = nan                                                       # of the expert without rows
+    dy[cut[0], 7], dy[cut[1] - 1, out - 1], dy[cut[3] - 1, 0] = inf, -inf, nan
+    x[source.long()] = xs
+    given = {"source": source} if by_source else {}
+    x64, w64, dy64 = f64(xs), f64(w), f64(dy)
+    y64, dx64, b64 = torch.zeros(n, out, dtype=torch.float64), torch.zeros(n, width, dtype=torch.float64), [torch.zeros(n, v, dtype=torch.float64) for v in (out, width)]
+    dw64, db64, dws, dbs = [], [], [], []
+    for e, r in P.segments(offsets, n):
+        y64[r], b64[0][r] = x64[r] @ w64[e].T, x64[r].abs() @ w64[e].abs().T
+        dx64[r], b64[1][r] = dy64[r] @ w64[e], dy64[r].abs() @ w64[e].abs()
+        dw64.append(dy64[r].T @ x64[r]), dws.append(dy64[r].abs().T @ x64[r].abs())
+        db64.append(dy64[r].sum(0)), dbs.append(dy64[r].abs().sum(0))
+    same_places("y", m.expert_product(x, w, offsets, **given), y64, bound(width, b64[0], dtype, dtype), dtype)
+    dx, dw, db = m.expert_product_backward(dy, x, w, offsets, **given)
+    same_places("dx", dx, dx64, bound(out, b64[1], dtype, dtype), dtype)
+    same_places("dweight", dw, torch.stack(dw64), bound(n, torch.stack(dws), dtype, dtype))
+    same_places("dbias", db, torch.stack(db64), (n + 2) * U * torch.stack(dbs))
+
+
+@pytest.mark.parametrize("act", ["none", "silu"])
+@pytest.mark.parametrize("n,width,out", SIZES)
+def test_values_that_round_to_an_infinity(m, n, width, out, act):
+    """fp32 values above bf16's largest, in sums that fit: their results, with bias and activation, and both gradients."""
+    g, f32, huge = rng(3 * n + out), torch.float32, 3.395e38
+    x, w, dy = rows(g, n, width), (torch.rand(2, out, width, generator=g) * 1.8 - 0.9).to(DEV), rows(g, n, out)
+    offsets, bias = ends([n // 2, n - n // 2]), normal(g, 2, out)
+    for r, q in ((1, 3), (n - 1, n - 4)):
+        x[r, width - 1], dy[q, out // 2] = huge, -huge
+        dy[r], x[q] = (torch.rand(out, generator=g) * 1.8 - 0.9).to(DEV), (torch.rand(width, generator=g) * 1.8 - 0.9).to(DEV)
+    want, size = P.product(x, w, offsets, bias, act, n)
+    assert int((want.abs() > 1e37).sum()) > out // 4
+    agrees("y", m.expert_product(x, w, offsets, bias, act=act), want, act_bound(bound(width, size, f32, f32), want, act), f32)
+    held = m.micro_save(w.reshape(-1, width))
+    w64 = P.micro_load(held.codes, held.scales, width).reshape(w.shape)
+    want, size = P.product(x, w64, offsets, bias, act, n)
+    b = act_bound(bound(width, size, f32, torch.bfloat16), want, act)
+    for t in TYPES:
+        agrees("y by held weights", m.micro_product(x, held, offsets, bias, act=act, dtype=t), want, b, t)
+    dx, dw, _ = m.expert_product_backward(dy, x, w, offsets)
+    want, size = P.input_grad(dy, w, offsets)
+    assert int((want.abs() > 1e37).sum()) > width // 4
+    agrees("dx", dx, want, bound(out, size, f32, f32), f32)
+    want, size, _, _, count = P.weight_grad(dy, x, offsets)
+    assert int((want.abs() > 1e37).sum()) > (width + out) // 4
+    agrees("dweight", dw, want, bound(max(count), size, f32, f32), f32)
+
+
 # ---------------------------------------------------------------------------------------------------------------
 # embedding rows
 # ---------------------------------------------------------------------------------------------------------------
