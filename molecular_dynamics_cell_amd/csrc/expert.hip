@@ -62,9 +62,10 @@ __device__ __forceinline__ void finish(const Args &a, int expert, int64_t q, int
 // 128 x 128 results at a time, four waves of 64 x 64, any types, strides and alignments: words go through registers, where
 // fp32 is cut into terms and 4-bit codes become bf16.  A block stays for many tiles: the next one's first words are on
 // their way while this one's results are stored.  ACROSS: the weights' rows are the reduced axis (dx).
-// Two blocks a CU take turns at cutting and multiplying: fp32 128,000 rows 312 -> 128 x 5 with SiLU 78-90 us (47 at a large bf16
-// product's rate) with the matrix cores, vector issue and LDS busy 40 % of the time each, dx 95-117 us; 32,768 rows
-// 1024 -> 1024 x 8 fp32 355 us, 1.16 PFLOP/s of bf16 products; bf16 312 -> 128 30 us and dx 38 us.
+// Two blocks a CU take turns at cutting and multiplying: fp32 128,000 rows 312 -> 128 x 5 with SiLU 78-92 us (47 at a large bf16
+// product's rate), dx 95-117 us.  No unit bounds it: of a CU's cycles the matrix cores are busy 39 %, vector issue 49 %, LDS 22 %; of
+// its waves' 39 % go by waiting for an issue slot and 24 % for memory or a barrier, so the turns do not fill each other's gaps.
+// 32,768 rows 1024 -> 1024 x 8 fp32 355 us, 1.16 PFLOP/s of bf16 products; bf16 312 -> 128 30 us and dx 38 us.
 constexpr int kTile = 128;
 template <class X, class W, bool ACROSS>
 __global__ __launch_bounds__(256, 2) void k_product(const Args a, const RowsOf<X> x, const RowsOf<W> w) {
@@ -264,9 +265,11 @@ template <> struct WideOp<Micro> {
 // passing through registers, two stages ahead.  A block stays for many tiles: the next one's first stages are on their way
 // while this one's results are stored.  (One block a CU: without that a tile of 2,048 columns takes 29 us of products and
 // 23 us to find its rows, wait for the first of them and store its results.)
-// 65,536 rows 2048 -> 1024 x 64 bf16 260-286 us with equal shares (up to 1.06 PFLOP/s) and 321-372 with a router's, whose tiles are not
-// all full; 16,384 rows 2048 -> 4096 x 8 in 4 bits 149 us (1.84 PFLOP/s); dx of 32,768 rows 1024 -> 1024 x 8 68-78 us.  The card's
-// power bounds it: the bf16 products alone, of random data from registers, run at 1.75 PFLOP/s, of zeros at 2.47.
+// 65,536 rows 2048 -> 1024 x 64 bf16 260-318 us with equal shares (up to 1.06 PFLOP/s) and 321-372 with a router's, whose tiles are not
+// all full; 16,384 rows 2048 -> 4096 x 8 in 4 bits 149 us (1.84 PFLOP/s), of which SiLU at the ends of tiles is 24-32 and uneven shares
+// 15-24; dx of 32,768 rows 1024 -> 1024 x 8 68-78 us.  No unit bounds it: of a CU's cycles the matrix cores are busy 45 % (in 4 bits
+// 26 %), vector issue 28 % (50 %), LDS 21 % (18 %), and 39 % (33 %) of the waves' go by waiting for loads and barriers; the clock is
+// 2.0 GHz meanwhile.  (The bf16 products alone, of random data from registers, run at 1.75 PFLOP/s, of zeros at 2.47.)
 constexpr int kWide = 256, kWideWords = 4, kBuffers = 3, kWideThreads = 512;
 using WideTile = Along<1, kWide, kWideWords>;
 
@@ -486,8 +489,9 @@ __global__ __launch_bounds__(kWideThreads, 2) void k_product_wide(const Args a, 
 // 16 columns by 16 NT rows a wave, operands straight from memory to registers: what bounds a call of few rows is reading the
 // weights, so each lane reads 64 neighbouring bytes of a weight row at once (32 of 4-bit codes) and the reduced axis is split
 // among the waves of a block, whose sums are added in their order.  A lane's word holds the same steps of the reduced axis for
-// rows and weights; which lane holds which does not matter to the sum.  8 rows of eight experts 2048 -> 1024 bf16 10 us, 4 rows
-// 4096 -> 4096 by 4-bit weights 10 us, of which the launch and the binding are 8.
+// rows and weights; which lane holds which does not matter to the sum.  8 rows of eight experts 2048 -> 1024 bf16 9.1 us, 4 rows
+// 4096 -> 4096 by 4-bit weights 8.0 us, 216 rows of four 64 -> 128 fp32 10.4 us (a tile's rows found, loads, products and the waves'
+// sums one after another); the host needs 10-11 us for such a call.
 typedef float floatx4 __attribute__((ext_vector_type(4)));
 
 // PER steps of a row as loaded, and the products of a lane's word of weights with its word of rows.
