@@ -229,7 +229,7 @@ __global__ __launch_bounds__(256, 2) void k_product(const Args a, const RowsOf<X
                 if (isfinite(to_f32(y[q * a.columns + c]))) continue;
                 const int64_t weights = (int64_t)done.expert * (ACROSS ? a.reduced : a.columns), from = place(q);
                 float s = 0.0f;
-                for (int k = 0; k < a.reduced; ++k) s = fmaf(x.at(from, k), ACROSS ? w.at(weights + k, c) : w.at(weights + c, k), s);
+                for (int k = 0; k < a.reduced && s == s; ++k) s = fmaf(x.at(from, k), ACROSS ? w.at(weights + k, c) : w.at(weights + c, k), s);
                 if (biased) s += a.bias[(int64_t)done.expert * a.columns + c];
                 y[q * a.columns + c] = from_f32<std::remove_pointer_t<decltype(y)>>(act ? silu(s) : s);
             }

@@ -146,7 +146,7 @@ __global__ __launch_bounds__(256, 2) void k_expert_weight_grad(const Args a, con
                     for (int r = 0; r < 4; ++r)
                         if (!isfinite(v.v[r]) && r < in) {
                             float s = 0.0f;
-                            for (int64_t q = from; q < to; ++q) {
+                            for (int64_t q = from; q < to && s == s; ++q) {
                                 const int64_t at = a.source ? min((int64_t)((uint32_t)max(a.source[q], 0) / (uint32_t)a.slots), a.n_x - 1) : q;
                                 s = fmaf(dy.at(q, o), x.at(at, c + r), s);
                             }
